@@ -328,6 +328,130 @@ moe_status moe_route_noalloc(const void* x_bf16, int T, int H, const void* wr_bf
  * plan NULL. */
 moe_status moe_debug_fail_next_forward(moe_plan* plan);
 
+/* ------------------------------------------------------------------ 4-bit key/value cache
+ *
+ * The attention next to an MoE layer: a paged key/value cache held in 4 bits,
+ * the hot KV that "763B MoE in two 96 GB cards" keeps in VRAM (KV side-box of
+ * section "Where the VRAM gap comes from") at 4.5 bits per value (groups of
+ * 64), beside the experts that compete for the same HBM.
+ *
+ * Caller-owned device memory:
+ *   pages   [layer][page][kv head][page bytes per head]; a stored value is
+ *           c + s (u - 8) with u in 0..15 and, per token, kv head and group of
+ *           group_size channels, a step s and a centre c in the cache's type:
+ *           s = rn((max - min) / 15), c = rn(min + 8 s),
+ *           u = clamp(rint((x - c) / s) + 8, 0, 15), or 8 where s = 0.  A group
+ *           that holds an infinity or a NaN reads as NaN (s = 0, c = NaN).
+ *           Per head a page is page_size / 16 blocks of
+ *           K codes [16][D/2] | V codes [16][D/2] | K params [16][D/G][s, c] |
+ *           V params [16][D/G][s, c]   (order of the codes: csrc/kv_common.cuh).
+ *   bounds  [layer][page][kv head][max, min][D] of the cache's type, or NULL:
+ *           the extremes of each page's stored keys, which moe_kv_append
+ *           maintains and moe_kv_select reads.
+ * moe_kv_sizes gives the bytes.  The pages of a sequence are named by a block
+ * table shared by the layers. */
+typedef struct moe_kv_cache moe_kv_cache;
+
+typedef enum moe_kv_dtype { MOE_KV_BF16 = 0, MOE_KV_F16 = 1 } moe_kv_dtype;
+
+typedef struct moe_kv_desc {
+  uint32_t struct_size; /* sizeof(moe_kv_desc) */
+  int32_t device;       /* CUDA device ordinal */
+  int32_t dtype;        /* moe_kv_dtype: keys, values, queries, outputs, params and bounds */
+  int32_t num_layers;   /* >= 1 */
+  int32_t kv_heads;     /* 1..1024 */
+  int32_t head_dim;     /* D: 64 or 128 */
+  int32_t group_size;   /* G: 32, 64 or 128, dividing D */
+  int32_t page_size;    /* tokens per page: 16, 32, 64, 128 or 256 */
+  int64_t num_pages;    /* 1 .. 2^31 - 1 */
+  void* pages;          /* 16-byte aligned device memory */
+  void* bounds;         /* 16-byte aligned device memory, or NULL */
+  int64_t reserved[2];  /* must be zero */
+} moe_kv_desc;
+
+/* A batch of sequences.  Sequence s has lens[s] tokens in the cache, its page
+ * j is table[s * table_stride + j], and its rows (queries, or the keys and
+ * values being written or read) are the last ones of these tokens: max_new of
+ * them, or where `starts` is given starts[s + 1] - starts[s], rows starts[s] ..
+ * of tensors that hold the sequences' rows one after the other.  lens, table
+ * and starts are device memory and are not read on the host: lengths below 0
+ * count as 0, rows before a sequence's first token are dropped by a write, read
+ * as zero and attend to nothing, tokens beyond table_pages pages and tokens
+ * whose table entry names no page are neither written nor attended to (and read
+ * as zero), starts are cut to [0, rows], a sequence's rows to max_new. */
+typedef struct moe_kv_batch {
+  uint32_t struct_size; /* sizeof(moe_kv_batch) */
+  int32_t batch;        /* sequences, >= 0 */
+  int32_t max_new;      /* rows per sequence (starts given: at most this many), >= 0 */
+  int32_t table_pages;  /* entries of a table row, >= 1 */
+  int64_t table_stride; /* >= table_pages */
+  int64_t rows;         /* rows in all (starts NULL: batch * max_new) */
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* starts; /* [batch + 1] or NULL */
+} moe_kv_batch;
+
+/* A tensor of rows by heads by head_dim in the cache's type: strides in
+ * elements (multiples of 8; the channels contiguous), data 16-byte aligned.
+ * Row i of sequence s is at s * batch_stride + i * row_stride, or where starts
+ * is given at (starts[s] + i) * row_stride. */
+typedef struct moe_kv_tensor {
+  void* data;
+  int64_t batch_stride, row_stride, head_stride;
+} moe_kv_tensor;
+
+/* Bytes of one layer's pages and bounds for desc (pages and bounds not read). */
+moe_status moe_kv_sizes(const moe_kv_desc* desc, int64_t* page_bytes_per_layer, int64_t* bounds_bytes_per_layer);
+
+/* Create a handle on caller-owned pages: validates the shapes and allocates
+ * the workspace of attention and selection (nothing is allocated later).  The
+ * pages need no initialisation.  A handle is used by one host thread at a
+ * time; a call that uses the workspace on another stream than the last such
+ * call first waits for it (calls inside a stream capture take no part in
+ * that).  Ordering writes to the pages before reads of them is the caller's,
+ * as for any device memory. */
+moe_status moe_kv_create(const moe_kv_desc* desc, moe_kv_cache** out);
+/* Waits for the last call that used the workspace and frees it. */
+moe_status moe_kv_destroy(moe_kv_cache* kv);
+
+/* Quantise the rows k, v into the pages of `layer`, and with bounds update the
+ * bounds of the pages written to: a page whose first token is among the rows
+ * starts anew, any other is widened.  Pages written to must not be shared
+ * between the sequences of a call. */
+moe_status moe_kv_append(moe_kv_cache* kv, int layer, const moe_kv_batch* batch, const moe_kv_tensor* k,
+                         const moe_kv_tensor* v, void* stream);
+
+/* The stored values of the rows, rounded to the cache's type. */
+moe_status moe_kv_read(moe_kv_cache* kv, int layer, const moe_kv_batch* batch, const moe_kv_tensor* k,
+                       const moe_kv_tensor* v, void* stream);
+
+/* Attention: out = softmax(scale q k^T) v over the stored keys and values.
+ * Query head h reads kv head h / (q_heads / kv_heads); a row at position p sees
+ * the tokens 0..p (causal) or all of its sequence's (causal = 0).  A row that
+ * sees nothing gets zeros.  pages: NULL, or [rows][kv_heads][budget] int32
+ * (device) of distinct page indices (entries outside the sequence's pages are
+ * skipped): only the tokens of these pages are attended to.  lse: NULL, or
+ * [rows][q_heads] fp32, the natural logarithm of the sum of exponentials (-inf
+ * where a row sees nothing).  q and out must not overlap.  Rows that are no
+ * sequence's are not written. */
+moe_status moe_kv_attention(moe_kv_cache* kv, int layer, const moe_kv_batch* batch, const moe_kv_tensor* q,
+                            int q_heads, float scale, int causal, const moe_kv_tensor* out, float* lse,
+                            const int32_t* pages, int budget, void* stream);
+
+/* Choose `budget` pages per row and kv head: the first keep_first and the last
+ * keep_last pages up to the row's position, then those of the highest score
+ *     sum over d of max(qs[d] max[d], qs[d] min[d]),
+ * qs the sum of the group's query heads (fp32, ascending), the products and
+ * their sum in fp32, the sum by adjacent pairs level by level; ties go to the
+ * lower page, a NaN score counts as -infinity.  pages_out [rows][kv_heads]
+ * [budget]: page indices ascending, -1 after them where the row sees fewer.
+ * keep_first + keep_last <= budget, keep_last >= 1; needs bounds. */
+moe_status moe_kv_select(moe_kv_cache* kv, int layer, const moe_kv_batch* batch, const moe_kv_tensor* q,
+                         int q_heads, int budget, int keep_first, int keep_last, int32_t* pages_out, void* stream);
+
+/* Last error text of `kv` (or of the last call that had no handle, for NULL). */
+const char* moe_kv_last_error(const moe_kv_cache* kv);
+
 const char* moe_status_string(moe_status s);
 /* Last error text of `plan` (or of the last call that had no plan, for NULL). */
 const char* moe_last_error(const moe_plan* plan);

@@ -13,6 +13,9 @@ import os
 
 import numpy as np
 
+from . import kv as _kv
+from .kv import KVCache
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoe_gb300.so")
 
@@ -29,7 +32,9 @@ EXPORTS = ["moe_plan_create", "moe_plan_destroy", "moe_set_router", "moe_update_
            "moe_place_experts", "moe_layer_forward", "moe_layer_forward_residual", "moe_prefill_forward", "moe_layer_forward_host",
            "moe_step_end",
            "moe_cache_stats", "moe_residence_table", "moe_quantize", "moe_probe_bandwidth",
-           "moe_route_noalloc", "moe_status_string", "moe_last_error"]
+           "moe_route_noalloc", "moe_status_string", "moe_last_error",
+           "moe_kv_sizes", "moe_kv_create", "moe_kv_destroy", "moe_kv_append", "moe_kv_read", "moe_kv_attention",
+           "moe_kv_select", "moe_kv_last_error"]
 
 _P = ctypes.c_void_p
 
@@ -101,6 +106,7 @@ def lib():
         L.moe_status_string.argtypes = [i32]
         L.moe_last_error.restype = ctypes.c_char_p
         L.moe_last_error.argtypes = [_P]
+        _kv.declare(L)
         _lib = L
     return _lib
 

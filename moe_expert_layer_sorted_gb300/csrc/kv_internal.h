@@ -1,0 +1,71 @@
+// The 4-bit key/value cache's handle and the launchers of its kernels.
+#pragma once
+
+#include <atomic>
+#include <string>
+
+#include "internal.h"
+#include "kv_common.cuh"
+
+namespace moe {
+
+struct Kv {
+  moe_kv_desc d{};
+  int sms = 0;
+  int64_t block_bytes = 0, head_bytes = 0, page_bytes = 0, layer_bytes = 0, bounds_layer = 0;  // bounds_layer: elements
+  uint8_t* ws = nullptr;  // workspace of attention and selection
+  static constexpr size_t kScoreBytes = size_t(16) << 20;
+  cudaEvent_t ev_done = nullptr;  // end of the last call that used the workspace
+  cudaStream_t last_stream = nullptr;
+  bool have_last = false;
+  std::atomic<int> busy{0};
+  std::string last_error;
+};
+
+struct KvAttnArgs {
+  KvView c;
+  KvBatch b;
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;  // [rows][q_heads] or nullptr
+  KvRows qs, os;
+  int q_heads;
+  float scale;
+  int causal;
+  const int32_t* sel;  // [rows][heads][budget] page indices, or nullptr: every page
+  int budget;
+};
+
+struct KvSelectArgs {
+  KvView c;
+  KvBatch b;
+  const uint16_t* q;
+  KvRows qs;
+  int q_heads, budget, first, last;
+  int32_t* out;  // [rows][heads][budget]
+};
+
+cudaError_t kv_append(const Kv& kv, const KvView& c, const KvBatch& b, const uint16_t* k, const KvRows& ks,
+                      const uint16_t* v, const KvRows& vs, cudaStream_t s);
+cudaError_t kv_read(const Kv& kv, const KvView& c, const KvBatch& b, uint16_t* k, const KvRows& ks, uint16_t* v,
+                    const KvRows& vs, cudaStream_t s);
+cudaError_t kv_attention(Kv& kv, const KvAttnArgs& a, cudaStream_t s);
+cudaError_t kv_select(Kv& kv, const KvSelectArgs& a, cudaStream_t s);
+
+// Calls f with (T, D, G) of the cache as compile-time constants.
+#define KV_DISPATCH(desc, ...)                                                            \
+  do {                                                                                    \
+    auto run_ = [&](auto tag_) {                                                          \
+      using T = decltype(tag_);                                                           \
+      const int dg_ = (desc).head_dim * 1000 + (desc).group_size;                         \
+      if (dg_ == 64032) { constexpr int D = 64, G = 32; __VA_ARGS__ }                     \
+      else if (dg_ == 64064) { constexpr int D = 64, G = 64; __VA_ARGS__ }                \
+      else if (dg_ == 128032) { constexpr int D = 128, G = 32; __VA_ARGS__ }              \
+      else if (dg_ == 128064) { constexpr int D = 128, G = 64; __VA_ARGS__ }              \
+      else { constexpr int D = 128, G = 128; __VA_ARGS__ }                                \
+    };                                                                                    \
+    if ((desc).dtype == MOE_KV_BF16) run_(__nv_bfloat16());                               \
+    else run_(__half());                                                                  \
+  } while (0)
+
+}  // namespace moe
