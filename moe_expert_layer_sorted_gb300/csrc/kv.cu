@@ -127,6 +127,7 @@ cudaError_t order_after(Kv* kv, cudaStream_t s, bool capturing) {
 
 void release(Kv* kv) {
   if (kv->ws) cudaFree(kv->ws);
+  if (kv->err_host) cudaFreeHost(const_cast<uint32_t*>(kv->err_host));
   if (kv->ev_done) cudaEventDestroy(kv->ev_done);
   delete kv;
 }
@@ -193,7 +194,16 @@ extern "C" moe_status moe_kv_create(const moe_kv_desc* desc, moe_kv_cache** out)
     kv->d = *desc;
     set_sizes(kv);
     cudaDeviceGetAttribute(&kv->sms, cudaDevAttrMultiProcessorCount, desc->device);
-    cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&kv->ws), Kv::kScoreBytes);
+    cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&kv->ws), Kv::kWorkspace);
+    if (e == cudaSuccess) e = cudaMemset(kv->counters(), 0, Kv::kCounterBytes);
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();  // the memset is done before any stream's first call
+    void* word = nullptr;
+    if (e == cudaSuccess) e = cudaHostAlloc(&word, 64, cudaHostAllocMapped);
+    if (e == cudaSuccess) {
+      kv->err_host = static_cast<volatile uint32_t*>(word);
+      *kv->err_host = 0;
+      e = cudaHostGetDevicePointer(reinterpret_cast<void**>(&kv->err_dev), word, 0);
+    }
     if (e == cudaSuccess) e = cudaEventCreateWithFlags(&kv->ev_done, cudaEventDisableTiming);
     if (e != cudaSuccess) {
       cudaGetLastError();
@@ -263,6 +273,12 @@ extern "C" moe_status moe_kv_attention(moe_kv_cache* h, int layer, const moe_kv_
                  pages, pages ? budget : 0};
     bool capturing = false;
     cudaError_t e = order_before(kv, s, capturing);
+    if (e == cudaSuccess && *kv->err_host) {  // reported once; the counters start afresh behind the failed call
+      *kv->err_host = 0;
+      e = cudaMemsetAsync(kv->counters(), 0, Kv::kCounterBytes, s);
+      if (e == cudaSuccess) e = order_after(kv, s, capturing);
+      if (e == cudaSuccess) return fail(kv, MOE_ERR_TIMEOUT, "a bounded wait of an earlier moe_kv_attention gave up: its results are wrong");
+    }
     if (e == cudaSuccess) e = kv_attention(*kv, a, s);
     if (e == cudaSuccess) e = order_after(kv, s, capturing);
     return e == cudaSuccess ? MOE_OK : cuda_fail(kv, e, "moe_kv_attention");

@@ -89,6 +89,8 @@ __global__ void __launch_bounds__(128) kv_attention_kernel(KvAttnArgs a) {
 }  // namespace
 
 cudaError_t moe::kv_attention(Kv& kv, const KvAttnArgs& a, cudaStream_t s) {
+  if (a.sel || (int64_t)a.b.max_new * (a.q_heads / a.c.heads) <= 32)
+    return kv.d.dtype == MOE_KV_BF16 ? kv_decode_bf16(kv, a, s) : kv_decode_f16(kv, a, s);
   const int64_t warps = (int64_t)a.b.batch * a.b.max_new * a.q_heads;
   if (warps / 4 + 1 > 0x7fffffff) return cudaErrorInvalidConfiguration;
   cudaError_t e = cudaSuccess;

@@ -13,8 +13,19 @@ struct Kv {
   moe_kv_desc d{};
   int sms = 0;
   int64_t block_bytes = 0, head_bytes = 0, page_bytes = 0, layer_bytes = 0, bounds_layer = 0;  // bounds_layer: elements
-  uint8_t* ws = nullptr;  // workspace of attention and selection
+  // workspace: the selection's scores; partial results of attention items that are cut
+  // between CTAs (two per CTA); their counters, zero between calls
+  uint8_t* ws = nullptr;
   static constexpr size_t kScoreBytes = size_t(16) << 20;
+  static constexpr int kMaxParts = 1024;                                // CTAs
+  static constexpr size_t kPartBytes = size_t(16) * (128 + 2) * 4;      // 16 columns of (O, max, sum)
+  static constexpr size_t kPartsBytes = 2 * kMaxParts * kPartBytes;
+  static constexpr size_t kCounterBytes = kMaxParts * sizeof(unsigned);
+  static constexpr size_t kWorkspace = kScoreBytes + kPartsBytes + kCounterBytes;
+  float* parts() const { return reinterpret_cast<float*>(ws + kScoreBytes); }
+  unsigned* counters() const { return reinterpret_cast<unsigned*>(ws + kScoreBytes + kPartsBytes); }
+  volatile uint32_t* err_host = nullptr;  // mapped pinned word: set by a kernel whose bounded wait gave up
+  uint32_t* err_dev = nullptr;
   cudaEvent_t ev_done = nullptr;  // end of the last call that used the workspace
   cudaStream_t last_stream = nullptr;
   bool have_last = false;
@@ -49,8 +60,15 @@ cudaError_t kv_append(const Kv& kv, const KvView& c, const KvBatch& b, const uin
                       const uint16_t* v, const KvRows& vs, cudaStream_t s);
 cudaError_t kv_read(const Kv& kv, const KvView& c, const KvBatch& b, uint16_t* k, const KvRows& ks, uint16_t* v,
                     const KvRows& vs, cudaStream_t s);
+// Attention of few rows, or over chosen pages.
+cudaError_t kv_decode_bf16(Kv& kv, const KvAttnArgs& a, cudaStream_t s);
+cudaError_t kv_decode_f16(Kv& kv, const KvAttnArgs& a, cudaStream_t s);
 cudaError_t kv_attention(Kv& kv, const KvAttnArgs& a, cudaStream_t s);
 cudaError_t kv_select(Kv& kv, const KvSelectArgs& a, cudaStream_t s);
+
+// Blocks in flight per warp of the decode kernel: 3 to 8, so that two CTAs of eight warps share an SM.
+template <int D, int G>
+constexpr int kDecStages = 9216 / KvGeom<D, G>::kBytes;
 
 // Calls f with (T, D, G) of the cache as compile-time constants.
 #define KV_DISPATCH(desc, ...)                                                            \
