@@ -14,7 +14,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
 SOURCES = ["plan.cu", "decode.cu", "prefill.cu", "cache.cu", "noalloc.cu", "kv.cu", "kv_append.cu",
-           "kv_attention.cu", "kv_select.cu", "kv_decode_bf16.cu", "kv_decode_f16.cu"]
+           "kv_attention.cu", "kv_select.cu", "kv_decode_bf16.cu", "kv_decode_f16.cu",
+           "kv_prompt_bf16.cu", "kv_prompt_f16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -63,6 +63,9 @@ cudaError_t kv_read(const Kv& kv, const KvView& c, const KvBatch& b, uint16_t* k
 // Attention of few rows, or over chosen pages.
 cudaError_t kv_decode_bf16(Kv& kv, const KvAttnArgs& a, cudaStream_t s);
 cudaError_t kv_decode_f16(Kv& kv, const KvAttnArgs& a, cudaStream_t s);
+// Attention of prompts.
+cudaError_t kv_prompt_bf16(Kv& kv, const KvAttnArgs& a, cudaStream_t s);
+cudaError_t kv_prompt_f16(Kv& kv, const KvAttnArgs& a, cudaStream_t s);
 cudaError_t kv_attention(Kv& kv, const KvAttnArgs& a, cudaStream_t s);
 cudaError_t kv_select(Kv& kv, const KvSelectArgs& a, cudaStream_t s);
 

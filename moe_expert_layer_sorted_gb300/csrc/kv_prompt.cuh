@@ -1,0 +1,657 @@
+// Attention of prompts over the 4-bit cache: many rows per kv head, on the
+// tcgen05 tensor cores.  Included by kv_prompt_bf16.cu and kv_prompt_f16.cu.
+//
+// One CTA takes 256 rows x of one sequence and kv head (x = row * (heads per
+// kv head) + head, so that the heads that share keys share a tile) as two tiles
+// of 128, and walks over the tokens in tiles of 128:
+//   S_t = Q_t K^T   (Q, K in shared memory, S fp32 in TMEM),
+//   P_t = 2^(S_t scale log2 e - m) in 16 bits over S_t's columns of TMEM,
+//   O_t += P_t V    (P as the TMEM operand, V token-major in shared memory).
+// The two tiles alternate: while the tensor cores work for one, the softmax
+// warps work for the other.  Roles:
+//   warps 0-3, 4-7  softmax of tile 0, 1: a thread owns a row (a TMEM lane);
+//                   the running reference m is raised, and O rescaled in TMEM,
+//                   only where a score passes it by 2^8;
+//   warps 8-11      stored codes -> 16-bit K and V tiles: a thread owns a
+//                   token, its code words and params loaded a tile ahead;
+//   warp 12         tcgen05.mma issue, TMEM allocation.
+// Rounding: k, v and P to fp16, in caches of both types, k and v from c + s (u - 8)
+// by one fma on exact operands; the sums are fp32.  (bf16's 2^-9 would be seen: in a
+// score of several hundred, and in P and v as much as in a bf16 output.)  So that
+// nothing leaves fp16's range, powers of two are taken out and put back: of a query
+// row, to its largest element (back in the row's factor scale log2 e); of a token
+// whose keys are all tiny or huge (back on its column, in tiles that hold one); of
+// all values, 2^E with E raised when a token needs it (O is rescaled as for m).
+//
+// Masks: a score that its row may not see becomes -infinity.  A masked weight
+// is an exact zero, but zero times a NaN value is not: values of a poisoned
+// group enter the tile as zeros and its groups are remembered per row that sees
+// the token.
+#pragma once
+
+#include "kv_internal.h"
+
+using namespace moe;
+
+namespace {
+
+#include "device_common.cuh"
+#include "kv_operand.cuh"
+
+constexpr int kPrSoft = 8, kPrDequant = 4, kPrMma = kPrSoft + kPrDequant;
+constexpr int kPrThreads = 512;  // four warpgroups; warps 13-15 only fill theirs
+// Registers: the launch's 128 per thread are dealt out again between the warpgroups,
+// 128 threads x (168 + 168 + 112 + 64) = 512 x 128.
+constexpr int kPrRegs = 128, kPrSoftRegs = 168, kPrDequantRegs = 112, kPrMmaRegs = 64;
+static_assert(2 * kPrSoftRegs + kPrDequantRegs + kPrMmaRegs == 4 * kPrRegs, "a split above the launch's registers never ends");
+template <int R, bool Inc>
+__device__ __forceinline__ void set_registers() {
+  if constexpr (Inc) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+constexpr int kPrTile = 128;  // rows of a row tile, tokens of a token tile
+// weights are 2^(score - reference): set kPrDrop below the largest score, raised when one
+// passes it by kPrSlack; so weights reach 2^15 at most and fp16 holds 2^-25 of them
+constexpr float kPrDrop = 7.0f, kPrSlack = 15.0f;
+
+// K-major operand, 128-byte swizzle: 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3fffu) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+         (uint64_t)2 << 61;
+}
+// Token-major (MN-major) operand, 128-byte swizzle: rows of 64 channels, 8-token
+// groups 1024 bytes apart, the next 64 channels one slab (16 KB) on.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3fffu) | (uint64_t)((kPrTile * 128) >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+__device__ __forceinline__ constexpr uint32_t idesc(int N, bool b_mn) {  // fp16 operands, fp32 sums
+  return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(kPrTile >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 32 columns of the warp's 32 TMEM lanes
+__device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// two fp32 in one register pair
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void split2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
+// 2^e, e in -126..127
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+
+// The eight stored values of a word in channel order, in fp16; par: step and centre as fp16.
+__device__ __forceinline__ uint4 values8(uint32_t w, uint32_t par) {
+  using F = Frag<__half>;
+  const uint32_t s2 = __byte_perm(par, par, 0x1010), c2 = __byte_perm(par, par, 0x3232);
+  return make_uint4(fma_half2(F::template value<0>(w), s2, c2), fma_half2(F::template value<1>(w), s2, c2),
+                    fma_half2(F::template value<2>(w), s2, c2), fma_half2(F::template value<3>(w), s2, c2));
+}
+
+struct PromptArgs {
+  KvAttnArgs a;
+  int per;        // query heads per kv head
+  int tiles;      // row-tile pairs per sequence and head, at most
+  uint32_t* err;
+};
+
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_constant__ PromptArgs p) {
+  using Geo = KvGeom<D, G>;
+  constexpr int NG = D / G;
+  constexpr uint32_t kSlab = kPrTile * 128;          // 128 rows of 64 channels
+  constexpr uint32_t kTileBytes = kSlab * (D / 64);  // a Q, K or V tile
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t kFull[2], kEmpty[2], vFull[2], vEmpty[2], sFull[2], pFull[2], oFull;
+  __shared__ uint32_t tmem_base;
+  // per token tile (ring of 4): tokens that exist, tokens with a poisoned value, tokens with scaled keys
+  __shared__ uint4 sh_valid[4], sh_poison[4], sh_scaled[4];
+  __shared__ float sh_kscale[4][kPrTile];      // what the scaled keys' scores are multiplied by
+  __shared__ int sh_vtop[4][kPrDequant];       // exponents of the tile's largest values, one per warp
+  __shared__ int sh_vexp[4];                   // E of the tile
+  __shared__ float sh_qscale[2 * kPrTile];     // what a query row's scores are multiplied by
+  __shared__ uint8_t sh_pgroups[4][kPrTile];   // the poisoned groups of a token
+  const KvAttnArgs& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  // heavy tiles first: the last rows of every sequence see the most
+  const int hs = blockIdx.x % (a.c.heads * a.b.batch);
+  const int rt = p.tiles - 1 - blockIdx.x / (a.c.heads * a.b.batch);
+  const int h = hs % a.c.heads, s = hs / a.c.heads;
+  const KvSeq q = kv_seq(a.b, s);
+  const int64_t nx = (int64_t)q.rows * p.per;  // rows x of this sequence and head
+  const int64_t x0 = (int64_t)rt * 2 * kPrTile;
+  if (x0 >= nx) return;
+  const int cap = kv_capacity(a.c, a.b);
+  const int64_t first = (int64_t)q.len - q.rows;  // position of row 0
+  auto seen_of = [&](int64_t x) {  // tokens that row x sees
+    return (int)min(max(a.causal ? first + x / p.per + 1 : (int64_t)q.len, (int64_t)0), (int64_t)cap);
+  };
+  const int most = seen_of(min(x0 + 2 * kPrTile, nx) - 1);
+  const int ntiles = (most + kPrTile - 1) / kPrTile;
+  const bool two = nx > x0 + kPrTile;  // the second row tile has rows
+  const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  const uint32_t sq = smem, sk = smem + 2 * kTileBytes, sv = sk + 2 * kTileBytes;
+  uint8_t* gen = smem_raw + (smem - smem_addr(smem_raw));  // the same places as a generic pointer
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&kFull[i]), kPrDequant);
+      mbar_init(smem_addr(&kEmpty[i]), 1);
+      mbar_init(smem_addr(&vFull[i]), kPrDequant);
+      mbar_init(smem_addr(&vEmpty[i]), 1);
+      mbar_init(smem_addr(&sFull[i]), 1);
+      mbar_init(smem_addr(&pFull[i]), 4);
+    }
+    mbar_init(smem_addr(&oFull), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kPrMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_base)), "n"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  // Q: both tiles, rows past the last as zeros; D / 8 neighbouring lanes hold a row
+  for (int i = tid; i < 2 * kPrTile * (D / 8); i += kPrThreads) {
+    const int row = i / (D / 8), ch = i % (D / 8);
+    const int64_t x = x0 + row;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (x < nx)
+      v = *reinterpret_cast<const uint4*>(a.q + kv_row_offset(a.b, a.qs, s, q.row0, (int)(x / p.per)) +
+                                          (int64_t)(h * p.per + (int)(x % p.per)) * a.qs.head + 8 * ch);
+    float back = 1.0f;
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      uint32_t top = 0;  // largest magnitude's bits
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = max(top, max(w[e] << 16 & 0x7fff0000u, w[e] & 0x7fff0000u));
+#pragma unroll
+      for (int o = 1; o < D / 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int ex = (int)(top >> 23) - 127;  // to 2^14; an infinity or a NaN stays what it is
+      const int by = top == 0u || ex > 127 ? 0 : min(max(14 - ex, -113), 113);
+      back = pow2(-by);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = KvType<__half>::pack(KvType<T>::lo(w[e]) * pow2(by), KvType<T>::hi(w[e]) * pow2(by));
+      v = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    if (ch == 0) sh_qscale[row] = back;
+    *reinterpret_cast<uint4*>(gen + (row / kPrTile) * kTileBytes + (ch / 8) * kSlab + (row % kPrTile) * 128 +
+                              ((ch % 8) ^ (row & 7)) * 16) = v;
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tm = tmem_base;
+
+  if (warp < kPrSoft) {
+    // ------------------------------------------------------------------ softmax
+    set_registers<kPrSoftRegs, true>();
+    const int t = warp >> 2, quad = warp & 3;
+    const int64_t x = x0 + t * kPrTile + quad * 32 + lane;
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    const uint32_t ts = tm + t * kPrTile + lanes, to = tm + 2 * kPrTile + t * D + lanes;
+    const int seen = x < nx ? seen_of(x) : 0;
+    const float kappa = a.scale * 1.4426950408889634f * sh_qscale[t * kPrTile + quad * 32 + lane];
+    const uint64_t kappa2 = pair2(kappa, kappa);
+    float m = kNone;
+    uint64_t l2 = 0;        // the two halves of the row's sum
+    uint32_t poisoned = 0;  // groups with a NaN value that the row sees
+    int vexp = 0;           // E so far
+    for (int j = 0; j < (t == 0 || two ? ntiles : 0); ++j) {
+      mbar_wait<false>(smem_addr(&sFull[t]), (uint32_t)j & 1u, p.err);
+      fence_after();
+      const uint4 valid4 = sh_valid[j & 3], poison4 = sh_poison[j & 3], scaled4 = sh_scaled[j & 3];
+      const bool scaled = (scaled4.x | scaled4.y | scaled4.z | scaled4.w) != 0;
+      const uint32_t valid[4] = {valid4.x, valid4.y, valid4.z, valid4.w};
+      const uint32_t poison[4] = {poison4.x, poison4.y, poison4.z, poison4.w};
+      uint32_t pr[kPrTile / 2];
+      auto mask_of = [&](int k) {  // tokens of the k-th 32 that the row sees
+        const int n = seen - (j * kPrTile + 32 * k);
+        return valid[k] & (n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u);
+      };
+      auto load = [&](int k, uint32_t (&v)[32]) {  // the k-th 32 scores
+        tmem_ld32(ts + 32 * k, v);
+        tmem_wait_ld();
+        if (scaled) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * sh_kscale[j & 3][32 * k + i]);
+        }
+      };
+      uint64_t sum;
+      bool raise = j == 0 || sh_vexp[j & 3] != vexp;
+      if (!raise) {
+        // weights against the reference as it stands; top: the largest exponent
+        auto pass = [&](float& top) {
+          const uint64_t neg = pair2(-m, -m);
+          sum = 0;
+          top = kNone;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t v[32];
+            const uint32_t mask = mask_of(k);
+            load(k, v);
+            float e[32];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              split2(fma2(pair2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), kappa2, neg), e[i], e[i + 1]);
+            if (!__all_sync(0xffffffffu, mask == 0xffffffffu)) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!((mask >> i) & 1u)) e[i] = -__int_as_float(0x7f800000);
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              top = fmaxf(top, fmaxf(e[i], e[i + 1]));
+              const float p0 = exp2_fast(e[i]), p1 = exp2_fast(e[i + 1]);
+              sum = add2(sum, pair2(p0, p1));
+              pr[16 * k + i / 2] = KvType<__half>::pack(p0, p1);
+            }
+          }
+        };
+        float top;
+        pass(top);
+        raise = __any_sync(0xffffffffu, top > kPrSlack);
+      }
+      if (raise) {
+        // the row's largest score of this tile becomes its reference; what was summed so far shrinks
+        float best = kNone;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t v[32];
+          const uint32_t mask = mask_of(k);
+          load(k, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if ((mask >> i) & 1u) best = fmaxf(best, __uint_as_float(v[i]) * kappa);
+        }
+        best = fmaxf(best - kPrDrop, m);
+        const float f = exp2_fast(m - best), fo = f * pow2(max(vexp - sh_vexp[j & 3], -126));
+        m = best;
+        vexp = sh_vexp[j & 3];
+        float s0, s1;
+        split2(l2, s0, s1);
+        l2 = pair2(s0 * f, s1 * f);
+        if (j > 0) {
+#pragma unroll 1
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t v[32];
+            tmem_ld32(to + 32 * k, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * fo);
+            tmem_st32(to + 32 * k, v);
+          }
+          tmem_wait_st();
+        }
+        const uint64_t neg = pair2(-m, -m);
+        sum = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t v[32];
+          const uint32_t mask = mask_of(k);
+          load(k, v);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            float e0, e1;
+            split2(fma2(pair2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), kappa2, neg), e0, e1);
+            if (!((mask >> i) & 1u)) e0 = -__int_as_float(0x7f800000);
+            if (!((mask >> (i + 1)) & 1u)) e1 = -__int_as_float(0x7f800000);
+            const float p0 = exp2_fast(e0), p1 = exp2_fast(e1);
+            sum = add2(sum, pair2(p0, p1));
+            pr[16 * k + i / 2] = KvType<__half>::pack(p0, p1);
+          }
+        }
+      }
+      l2 = add2(l2, sum);
+      tmem_st32(ts, pr);
+      tmem_st32(ts + 32, pr + 32);
+      if (poison[0] | poison[1] | poison[2] | poison[3]) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          for (uint32_t b = poison[k] & mask_of(k); b; b &= b - 1) poisoned |= sh_pgroups[j & 3][32 * k + __ffs(b) - 1];
+      }
+      tmem_wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&pFull[t]));
+    }
+    // ---- output
+    if (ntiles > 0) {
+      mbar_wait<false>(smem_addr(&oFull), 0, p.err);
+      fence_after();
+    }
+    float s0, s1;
+    split2(l2, s0, s1);
+    const float l = s0 + s1, inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int i = (int)(x / p.per), hq = h * p.per + (int)(x % p.per);
+    const float back = pow2(vexp);
+    uint16_t* dst = x < nx ? a.out + kv_row_offset(a.b, a.os, s, q.row0, i) + (int64_t)hq * a.os.head : nullptr;
+    if (t == 0 || two) {
+#pragma unroll 1
+      for (int k = 0; k < D / 32; ++k) {
+        uint32_t v[32];
+        if (ntiles > 0) {
+          tmem_ld32(to + 32 * k, v);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = 0;
+        }
+        // a row that sees nothing is zero; the groups of a poisoned value are NaN
+        const float f = (poisoned >> (32 * k / G)) & 1u ? __int_as_float(0x7fffffff) : inv;
+        if (dst) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t o[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              o[y] = KvType<T>::pack(__uint_as_float(v[e + 2 * y]) * f * back, __uint_as_float(v[e + 2 * y + 1]) * f * back);
+            *reinterpret_cast<uint4*>(dst + 32 * k + e) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+      }
+      if (dst && a.lse)
+        a.lse[kv_row_index(a.b, s, q.row0, i) * a.q_heads + hq] =
+            l == 0.0f ? -__int_as_float(0x7f800000) : (m + log2f(l)) * 0.6931471805599453f;
+    }
+  } else if (warp < kPrMma) {
+    // ------------------------------------------------------------------ codes to K and V tiles
+    set_registers<kPrDequantRegs, false>();
+    const int t = tid - kPrSoft * 32;  // token of the tile
+    const int dw = warp - kPrSoft;
+    uint4 kq[D / 32], vq[D / 32];
+    uint32_t kp[NG], vp[NG], vpn[NG];  // params of the keys, the values, the next tile's values
+    bool ok = false;       // token of the K words in hand exists
+    bool okv = false;
+    const uint8_t* at = nullptr;  // its block
+    constexpr int kNoExp = -1000;
+    int vexp = kNoExp;            // E
+    int64_t pid = -1;             // page of the token one tile on
+    auto page_of = [&](int j) {
+      const int pos = j * kPrTile + t;
+      pid = j < ntiles && pos < most ? kv_page(a.c, a.b, s, pos >> a.c.page_shift) : -1;
+    };
+    const int row = t & 15;
+    const uint32_t flip = (uint32_t)((t >> 2) & 1) * (D / 4);
+    auto load_k = [&](int j) {
+      const int pos = j * kPrTile + t;
+      ok = pid >= 0;
+      at = a.c.pages + pid * a.c.page_stride + h * a.c.head_stride +
+           ((pos & (a.c.page_size - 1)) >> 4) * (int64_t)Geo::kBytes;
+      if (ok) {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) kq[i] = *reinterpret_cast<const uint4*>(at + row * Geo::kRow + 16 * i);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          kp[g] = *reinterpret_cast<const uint32_t*>(at + Geo::kKPar + row * Geo::kParRow + 4 * g);
+          vpn[g] = *reinterpret_cast<const uint32_t*>(at + Geo::kVPar + row * Geo::kParRow + 4 * g);
+        }
+      }
+    };
+    const uint8_t* atv = nullptr;
+    auto load_v = [&]() {
+      if (okv) {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+          vq[i] = *reinterpret_cast<const uint4*>(atv + Geo::kVOff + kv_v_row(row) * Geo::kRow + ((16 * i) ^ flip));
+      }
+    };
+    auto put = [&](uint8_t* tile, int ch, uint4 v) {  // channels ch .. ch + 7 of token t
+      *reinterpret_cast<uint4*>(tile + (ch / 64) * kSlab + t * 128 + ((ch % 64 / 8) ^ (t & 7)) * 16) = v;
+    };
+    if (ntiles > 0) {
+      page_of(0);
+      load_k(0);
+      page_of(1);
+    }
+    for (int j = 0; j < ntiles; ++j) {
+      const int st = j & 1;
+      const uint32_t free_parity = ((uint32_t)(j >> 1) & 1u) ^ 1u;
+      // this tile's values can be asked for now: their words arrive while the keys are turned
+      okv = ok;
+      atv = at;
+      load_v();
+#pragma unroll
+      for (int g = 0; g < NG; ++g) vp[g] = vpn[g];
+      mbar_wait<false>(smem_addr(&kEmpty[st]), free_parity, p.err);
+      uint8_t* tk = gen + 2 * kTileBytes + st * kTileBytes;
+      uint32_t bad = 0;  // the token's poisoned groups
+      float kscale = 1.0f, vbig = 0.0f;
+      if (ok) {
+        float kbig = 0.0f;  // bound of the token's keys
+#pragma unroll
+        for (int g = 0; g < NG; ++g) kbig = fmaxf(kbig, fabsf(KvType<T>::hi(kp[g])) + 8.0f * KvType<T>::lo(kp[g]));
+        float to = 1.0f;
+        if (!(kbig >= 0x1p-8f && kbig <= 0x1p14f) && kbig > 0.0f) {
+          const int by = min(max(13 - ((int)(__float_as_uint(kbig) >> 23) - 127), -126), 126);
+          to = pow2(by);
+          kscale = pow2(-by);
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const float big = fabsf(KvType<T>::hi(vp[g])) + 8.0f * KvType<T>::lo(vp[g]);
+          vbig = fmaxf(vbig, big);
+          if (big != big) {
+            bad |= 1u << g;
+            vp[g] = 0;  // enters as zeros
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g)  // params as fp16
+          kp[g] = KvType<__half>::pack(KvType<T>::lo(kp[g]) * to, KvType<T>::hi(kp[g]) * to);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const uint32_t w[4] = {kq[i].x, kq[i].y, kq[i].z, kq[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int n = 4 * i + e, quarter = n / (D / 32), rest = n % (D / 32), g = rest / (G / 32);
+            put(tk, g * G + quarter * (G / 4) + rest % (G / 32) * 8,
+                values8(w[e], kp[g]));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int ch = 0; ch < D; ch += 8) put(tk, ch, make_uint4(0, 0, 0, 0));
+      }
+      const uint32_t bv = __ballot_sync(0xffffffffu, ok), bp = __ballot_sync(0xffffffffu, bad != 0);
+      const uint32_t bs = __ballot_sync(0xffffffffu, kscale != 1.0f);
+      sh_kscale[j & 3][t] = kscale;
+      if (lane == 0) {
+        reinterpret_cast<uint32_t*>(&sh_scaled[j & 3])[dw] = bs;
+        reinterpret_cast<uint32_t*>(&sh_valid[j & 3])[dw] = bv;
+        reinterpret_cast<uint32_t*>(&sh_poison[j & 3])[dw] = bp;
+      }
+      if (bp) sh_pgroups[j & 3][t] = (uint8_t)bad;
+      // E: first so that the tile's largest value is about 2^7, then raised where one would pass 2^15
+      const uint32_t vtop = __reduce_max_sync(0xffffffffu, __float_as_uint(vbig));
+      if (lane == 0) sh_vtop[j & 3][dw] = vtop == 0 ? -1000 : (int)(vtop >> 23) - 127;
+      asm volatile("bar.sync 1, %0;" ::"n"(kPrDequant * 32) : "memory");
+      int e = sh_vtop[j & 3][0];
+#pragma unroll
+      for (int i = 1; i < kPrDequant; ++i) e = max(e, sh_vtop[j & 3][i]);
+      if (e > -1000 && (vexp == kNoExp || e > vexp + 14)) vexp = min(max(e - 7, -110), 120);
+      if (t == 0) sh_vexp[j & 3] = vexp == kNoExp ? 0 : vexp;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&kFull[st]));
+      // the next tile's keys
+      load_k(j + 1);
+      page_of(j + 2);
+      mbar_wait<false>(smem_addr(&vEmpty[st]), free_parity, p.err);
+      uint8_t* tv = gen + 4 * kTileBytes + st * kTileBytes;
+      if (okv) {
+        const float to = pow2(vexp == kNoExp ? 0 : -vexp);
+        uint32_t w[D / 8];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) vp[g] = KvType<__half>::pack(KvType<T>::lo(vp[g]) * to, KvType<T>::hi(vp[g]) * to);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          w[4 * i] = vq[i].x;
+          w[4 * i + 1] = vq[i].y;
+          w[4 * i + 2] = vq[i].z;
+          w[4 * i + 3] = vq[i].w;
+        }
+#pragma unroll
+        for (int o = 0; o < D / 8; ++o) {  // channels 8 o ..
+          put(tv, 8 * o, values8(kv_v_codes<D, G>(w, o, 0), vp[8 * o / G]));
+        }
+      } else {
+#pragma unroll
+        for (int ch = 0; ch < D; ch += 8) put(tv, ch, make_uint4(0, 0, 0, 0));
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&vFull[st]));
+    }
+  } else {
+    set_registers<kPrMmaRegs, false>();
+    // ------------------------------------------------------------------ MMA issue
+    const uint32_t ids = idesc(kPrTile, false), ido = idesc(D, true);
+    const int nt = two ? 2 : 1;
+    auto scores = [&](int t, int j) {
+      if (lane == 0) {
+        const uint32_t qa = sq + t * kTileBytes, kb = sk + (j & 1) * kTileBytes;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma_ss(tm + t * kPrTile, desc_k(qa + (k / 4) * kSlab + (k % 4) * 32), desc_k(kb + (k / 4) * kSlab + (k % 4) * 32),
+                 ids, k ? 1u : 0u);
+        commit(&sFull[t]);
+        if (t == nt - 1) commit(&kEmpty[j & 1]);
+      }
+      __syncwarp();
+    };
+    if (warp == kPrMma && ntiles > 0) {
+      mbar_wait<false>(smem_addr(&kFull[0]), 0, p.err);
+      fence_after();
+      for (int t = 0; t < nt; ++t) scores(t, 0);
+      for (int j = 0; j < ntiles; ++j) {
+        for (int t = 0; t < nt; ++t) {
+          if (t == 0) mbar_wait<false>(smem_addr(&vFull[j & 1]), (uint32_t)(j >> 1) & 1u, p.err);
+          mbar_wait<false>(smem_addr(&pFull[t]), (uint32_t)j & 1u, p.err);
+          fence_after();
+          if (lane == 0) {
+            const uint32_t vb = sv + (j & 1) * kTileBytes;
+#pragma unroll
+            for (int k = 0; k < kPrTile / 16; ++k)
+              mma_ts(tm + 2 * kPrTile + t * D, tm + t * kPrTile + 8 * k, desc_mn(vb + k * 2048), ido, (j | k) ? 1u : 0u);
+            if (t == nt - 1) commit(&vEmpty[j & 1]);
+          }
+          __syncwarp();
+          if (j + 1 < ntiles) {
+            if (t == 0) {
+              mbar_wait<false>(smem_addr(&kFull[(j + 1) & 1]), (uint32_t)((j + 1) >> 1) & 1u, p.err);
+              fence_after();
+            }
+            scores(t, j + 1);
+          }
+        }
+      }
+      if (lane == 0) commit(&oFull);
+      __syncwarp();
+      mbar_drain(smem_addr(&oFull), 0);
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == kPrMma) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(512));
+  }
+}
+
+template <typename T, int D, int G>
+cudaError_t launch_prompt(Kv& kv, const PromptArgs& p, unsigned ctas, cudaStream_t s) {
+  const size_t smem = 1024 + (size_t)6 * kPrTile * D * 2;
+  const auto kernel = kv_prompt_kernel<T, D, G>;
+  static const bool registers_fit = [&] {  // what the split needs is what a launch brings
+    cudaFuncAttributes f{};
+    return cudaFuncGetAttributes(&f, reinterpret_cast<const void*>(kernel)) == cudaSuccess && f.numRegs == kPrRegs;
+  }();
+  if (!registers_fit) return cudaErrorInvalidKernelImage;
+  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<ctas, kPrThreads, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t prompt(Kv& kv, const KvAttnArgs& a, cudaStream_t s) {
+  PromptArgs p{a, a.q_heads / a.c.heads, 0, kv.err_dev};
+  const int64_t tiles = ((int64_t)a.b.max_new * p.per + 2 * kPrTile - 1) / (2 * kPrTile);
+  const int64_t ctas = tiles * a.c.heads * a.b.batch;
+  if (ctas > 0x7fffffff || (int64_t)a.c.heads * a.b.batch > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  p.tiles = (int)tiles;
+  cudaError_t e = cudaErrorInvalidValue;
+  const int dg = kv.d.head_dim * 1000 + kv.d.group_size;
+#define KV_CASE(DD, GG) \
+  if (dg == DD * 1000 + GG) e = launch_prompt<T, DD, GG>(kv, p, (unsigned)ctas, s);
+  KV_CASE(64, 32)
+  KV_CASE(64, 64)
+  KV_CASE(128, 32)
+  KV_CASE(128, 64)
+  KV_CASE(128, 128)
+#undef KV_CASE
+  return e;
+}
+
+}  // namespace

@@ -276,6 +276,30 @@ def test_large_scores(counts):
     run_attention(w, counts, 4, scale=0.0)
 
 
+@pytest.mark.parametrize("dtype,big,small", [(BF, 1e9, 1e-9), (FP, 6e4, 1e-4)])
+@pytest.mark.parametrize("n", [1, 3, 80])
+def test_keys_and_queries_of_any_size(dtype, big, small, n):
+    """Tiny and huge keys beside ordinary ones, values up to the type's largest, tiny and huge
+    queries: scores of ordinary size throughout."""
+    w = World(128, 64, 32, dtype, 2, [300, 300, 300], seed=n)
+    w.k[0][5:200:7] *= small
+    w.k[0][9] = 0.0
+    w.k[1] = (w.k[1].float().clamp(-1, 1) * big).to(dtype)
+    w.k[2] = (w.k[2].float() * small).to(dtype)
+    w.v[2][::3] = (w.v[2][::3].float().clamp(-1, 1) * torch.finfo(dtype).max).to(dtype)
+    w.v[2][::3, :, ::2] = -torch.finfo(dtype).max
+    w.fill()
+    q = w.rand(3, n, 8, 128)
+    q[1] = (q[1].float() / big).to(dtype)
+    q[2] = (q[2].float() / small).to(dtype)
+    out = torch.empty_like(q)
+    w.cache.attention(q, out, **w.batch)
+    for i in range(3):
+        seen = torch.arange(300, device="cuda")[None] <= torch.arange(300 - n, 300, device="cuda")[:, None]
+        want, _, tol, _ = ref.attention(q[i], *w.values(i), seen, 1 / math.sqrt(128))
+        check(out[i], want, tol, f"sequence {i}")
+
+
 def test_long_sequences_are_split_and_joined():
     run_attention(World(128, 64, 64, BF, 2, [20011], seed=5).fill(), [1], 16, ragged=False)
     run_attention(World(64, 32, 16, FP, 1, [9000, 40], seed=6).fill(), [1, 1], 4, ragged=False)
