@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -17,19 +18,15 @@ class KVDesc(ctypes.Structure):
                 ("pages", _P), ("bounds", _P), ("reserved", _I64 * 2)]
 
 
-class KVBatch(ctypes.Structure):
-    _fields_ = [("struct_size", ctypes.c_uint32), ("batch", ctypes.c_int32), ("max_new", ctypes.c_int32),
-                ("table_pages", ctypes.c_int32), ("table_stride", _I64), ("rows", _I64),
-                ("table", _P), ("lens", _P), ("starts", _P)]
-
-
-class KVTensor(ctypes.Structure):
-    _fields_ = [("data", _P), ("batch_stride", _I64), ("row_stride", _I64), ("head_stride", _I64)]
+# moe_kv_batch and moe_kv_tensor, packed
+_BATCH = struct.Struct("=I3i2q3Q")
+_BATCH_SIZE = _BATCH.size
+_TENSOR = struct.Struct("=Q3q")
 
 
 def declare(L):
     """Argument types of the library's moe_kv_* functions."""
-    i32, B, X = ctypes.c_int, ctypes.POINTER(KVBatch), ctypes.POINTER(KVTensor)
+    i32, B, X = ctypes.c_int, ctypes.c_char_p, ctypes.c_char_p  # packed structures
     L.moe_kv_sizes.argtypes = [ctypes.POINTER(KVDesc), ctypes.POINTER(_I64), ctypes.POINTER(_I64)]
     L.moe_kv_create.argtypes = [ctypes.POINTER(KVDesc), ctypes.POINTER(_P)]
     L.moe_kv_destroy.argtypes = [_P]
@@ -87,6 +84,7 @@ class KVCache:
         import torch
         from . import MoeError
         self._h = None
+        self._lib = _lib()
         dtype = torch.bfloat16 if dtype is None else dtype
         if not (pages.is_cuda and pages.dtype == torch.uint8 and pages.dim() in (4, 5) and pages.is_contiguous()):
             _bad("pages: contiguous uint8 CUDA tensor [layers,] num_pages, kv_heads, blocks, block bytes")
@@ -105,14 +103,16 @@ class KVCache:
         d.pages = pages.data_ptr()
         d.bounds = None if bounds is None else bounds.data_ptr()
         h = _P()
-        rc = _lib().moe_kv_create(ctypes.byref(d), ctypes.byref(h))
+        rc = self._lib.moe_kv_create(ctypes.byref(d), ctypes.byref(h))
         if rc:
-            raise MoeError(rc, _lib().moe_kv_last_error(None).decode())
+            raise MoeError(rc, self._lib.moe_kv_last_error(None).decode())
         self._h, self.pages, self.bounds, self.desc = h, pages, bounds, d
         self.dtype, self.device = dtype, pages.device
         self.layers, self.kv_heads, self.head_dim = layers, kv_heads, head_dim
         self.page_size, self.group_size = page_size, group_size
         self._scale = 1.0 / math.sqrt(head_dim)
+        self._index, self._i32 = pages.device.index, torch.int32
+        self._current_stream = torch._C._cuda_getCurrentRawStream
 
     @staticmethod
     def _block_shape(head_dim, group_size, page_size):
@@ -133,7 +133,7 @@ class KVCache:
 
     def close(self):
         if getattr(self, "_h", None):
-            _lib().moe_kv_destroy(self._h)
+            self._lib.moe_kv_destroy(self._h)
             self._h = None
 
     def __del__(self):
@@ -143,113 +143,129 @@ class KVCache:
             pass
 
     # ------------------------------------------------------------------ marshalling
+    # A decode step's calls are a few microseconds of GPU work each, so the host's share
+    # counts: the C structures are packed in one step each, and tensors are asked for
+    # nothing twice.
 
     def _int(self, t, name, dim):
-        import torch
-        if not (t.device == self.device and t.dtype == torch.int32 and t.dim() == dim and (t.shape[-1] < 2 or t.stride(-1) == 1)):
-            _bad(f"{name}: int32 tensor of {dim} axes on {self.device}, its last axis contiguous")
+        if not (t.dtype is self._i32 and t.is_cuda and t.get_device() == self._index and t.dim() == dim):
+            _bad(f"{name}: int32 tensor of {dim} axes on {self.device}")
         return t.data_ptr()
 
     def _batch(self, shape, table, lens, starts, max_new):
-        b = KVBatch()
-        b.struct_size = ctypes.sizeof(KVBatch)
-        b.table, b.lens = self._int(table, "table", 2), self._int(lens, "lens", 1)
-        b.batch = lens.shape[0]
-        if table.shape[0] != b.batch:
+        tp, lp, sp = self._int(table, "table", 2), self._int(lens, "lens", 1), 0
+        n, (sequences, cols) = len(shape), table.shape
+        batch = lens.shape[0]
+        if sequences != batch:
             _bad("table and lens name different numbers of sequences")
-        b.table_pages = table.shape[1]
-        b.table_stride = table.stride(0) if b.batch > 1 else table.shape[1]
+        stride, step = table.stride()
+        if (step != 1 and cols > 1) or (batch > 1 and lens.stride(0) != 1):
+            _bad("table's rows and lens must be contiguous")
+        if batch <= 1:
+            stride = cols
         if starts is None:
-            if len(shape) != 4 or shape[0] != b.batch:
+            if n != 4 or shape[0] != batch:
                 _bad("row tensors without starts: [sequences, rows, heads, head_dim]")
             if max_new is not None and max_new != shape[1]:
                 _bad("max_new belongs to starts")
-            b.max_new, b.rows = shape[1], shape[0] * shape[1]
+            max_new = shape[1]
+            rows = batch * max_new
         else:
-            if len(shape) != 3:
+            if n != 3:
                 _bad("row tensors with starts: [rows, heads, head_dim]")
-            b.starts = self._int(starts, "starts", 1)
-            if starts.shape[0] != b.batch + 1:
-                _bad("starts: one entry more than sequences")
-            b.rows = shape[0]
-            b.max_new = shape[0] if max_new is None else max_new
-        return b
+            sp = self._int(starts, "starts", 1)
+            if starts.shape[0] != batch + 1 or starts.stride(0) != 1:
+                _bad("starts: contiguous, one entry more than sequences")
+            rows = shape[0]
+            if max_new is None:
+                max_new = rows
+        if not (0 <= max_new < 1 << 31 and rows < 1 << 62 and batch < 1 << 31 and cols < 1 << 31):
+            _bad("max_new, the sequences or the table's pages are out of range")
+        return rows, _BATCH.pack(_BATCH_SIZE, batch, max_new, cols, stride, rows, tp, lp, sp)
 
-    def _rows(self, t, name, shape=None, written=False):
-        if not (t.device == self.device and t.dtype == self.dtype and t.dim() in (3, 4) and t.shape[-1] == self.head_dim
-                and t.stride(-1) == 1):
-            _bad(f"{name}: {self.dtype} on {self.device}, [..., heads, {self.head_dim}] with contiguous channels")
-        if shape is not None and t.shape != shape:
-            _bad(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    def _rows(self, t, name, shape, written=False):
+        if not (t.dtype is self.dtype and t.is_cuda and t.get_device() == self._index and t.shape == shape):
+            _bad(f"{name}: {self.dtype} on {self.device}, expected shape {tuple(shape)}")
         st = t.stride()
-        if written and any(n > 1 and d == 0 for n, d in zip(t.shape, st)):
+        if written and 0 in st and any(n > 1 and d == 0 for n, d in zip(shape, st)):
             _bad(f"{name}: an expanded tensor cannot be written to")
-        x = KVTensor()
-        # axes of length 1 have no stride that matters
-        x.data, x.head_stride = t.data_ptr(), st[-2] if t.shape[-2] > 1 else 0
-        x.row_stride = st[-3] if t.shape[-3] > 1 else 0
-        x.batch_stride = st[0] if t.dim() == 4 and t.shape[0] > 1 else 0
-        return x
+        if st[-1] != 1:
+            _bad(f"{name}: the channels must be contiguous")
+        if len(shape) == 4:
+            b, r, h, _ = st
+            nb, nr, nh, _ = shape
+            # axes of length 1 have no stride that matters
+            return _TENSOR.pack(t.data_ptr(), b if nb > 1 else 0, r if nr > 1 else 0, h if nh > 1 else 0)
+        r, h, _ = st
+        return _TENSOR.pack(t.data_ptr(), 0, r if shape[0] > 1 else 0, h if shape[1] > 1 else 0)
 
-    def _call(self, rc):
-        if rc:
-            from . import MoeError
-            # a busy handle's text is the running call's
-            raise MoeError(rc, "the cache is in use by another thread" if rc == 5 else
-                           _lib().moe_kv_last_error(self._h).decode())
+    def _heads(self, shape, name, kv):
+        if not (3 <= len(shape) <= 4 and shape[-1] == self.head_dim and (not kv or shape[-2] == self.kv_heads)):
+            _bad(f"{name}: [..., {self.kv_heads if kv else 'heads'}, {self.head_dim}] with 3 or 4 axes, got {tuple(shape)}")
+        return shape[-2]
+
+    def _failed(self, rc):
+        from . import MoeError
+        # a busy handle's text is the running call's
+        raise MoeError(rc, "the cache is in use by another thread" if rc == 5 else
+                       self._lib.moe_kv_last_error(self._h).decode())
 
     def _stream(self, stream):
         if stream is None:
-            import torch
-            return torch.cuda.current_stream(self.device).cuda_stream
+            return self._current_stream(self._index)
         return stream if isinstance(stream, int) else stream.cuda_stream
 
     # ------------------------------------------------------------------------- calls
 
     def append(self, k, v, *, table, lens, starts=None, max_new=None, layer=0, stream=None):
         """Quantise the rows k, v into the sequences' pages and update the pages' bounds."""
-        if k.shape[-2] != self.kv_heads:
-            _bad(f"k: {k.shape[-2]} heads, the cache has {self.kv_heads}")
-        b = self._batch(k.shape, table, lens, starts, max_new)
-        kt, vt = self._rows(k, "k"), self._rows(v, "v", k.shape)
-        self._call(_lib().moe_kv_append(self._h, layer, ctypes.byref(b), ctypes.byref(kt), ctypes.byref(vt),
-                                        self._stream(stream)))
+        shape = k.shape
+        self._heads(shape, "k", True)
+        _, b = self._batch(shape, table, lens, starts, max_new)
+        rc = self._lib.moe_kv_append(self._h, layer, b, self._rows(k, "k", shape), self._rows(v, "v", shape),
+                                     self._stream(stream))
+        if rc:
+            self._failed(rc)
 
     def read(self, k, v, *, table, lens, starts=None, max_new=None, layer=0, stream=None):
         """The stored keys and values of the rows, into k and v."""
-        if k.shape[-2] != self.kv_heads:
-            _bad(f"k: {k.shape[-2]} heads, the cache has {self.kv_heads}")
-        b = self._batch(k.shape, table, lens, starts, max_new)
-        kt, vt = self._rows(k, "k", written=True), self._rows(v, "v", k.shape, written=True)
-        self._call(_lib().moe_kv_read(self._h, layer, ctypes.byref(b), ctypes.byref(kt), ctypes.byref(vt),
-                                      self._stream(stream)))
+        shape = k.shape
+        self._heads(shape, "k", True)
+        _, b = self._batch(shape, table, lens, starts, max_new)
+        rc = self._lib.moe_kv_read(self._h, layer, b, self._rows(k, "k", shape, True), self._rows(v, "v", shape, True),
+                                   self._stream(stream))
+        if rc:
+            self._failed(rc)
 
     def attention(self, q, out, *, table, lens, starts=None, max_new=None, scale=None, causal=True, lse=None,
                   pages=None, layer=0, stream=None):
         """out = softmax(scale q k^T) v of the rows q (scale None: 1 / sqrt(head_dim)).
         pages: None, or `select`'s choice, the only pages then attended to.  lse: None, or
         float32 [rows, heads] for the logarithm of each row's sum of exponentials."""
-        import torch
-        b = self._batch(q.shape, table, lens, starts, max_new)
-        qt, ot = self._rows(q, "q"), self._rows(out, "out", q.shape, written=True)
+        shape = q.shape
+        heads = self._heads(shape, "q", False)
+        rows, b = self._batch(shape, table, lens, starts, max_new)
         lp = pp = None
         budget = 0
         if lse is not None:
+            import torch
             if not (lse.device == self.device and lse.dtype == torch.float32 and lse.is_contiguous()
-                    and lse.numel() == b.rows * q.shape[-2]):
+                    and lse.numel() == rows * heads):
                 _bad("lse: contiguous float32, one value per row and query head")
             lp = lse.data_ptr()
         if pages is not None:
-            budget = self._choice(pages, b)
+            budget = self._choice(pages, rows)
             pp = pages.data_ptr()
-        self._call(_lib().moe_kv_attention(self._h, layer, ctypes.byref(b), ctypes.byref(qt), q.shape[-2],
-                                           self._scale if scale is None else scale, int(causal), ctypes.byref(ot), lp,
-                                           pp, budget, self._stream(stream)))
+        rc = self._lib.moe_kv_attention(self._h, layer, b, self._rows(q, "q", shape), heads,
+                                        self._scale if scale is None else scale, 1 if causal else 0,
+                                        self._rows(out, "out", shape, True), lp, pp, budget, self._stream(stream))
+        if rc:
+            self._failed(rc)
 
-    def _choice(self, pages, b):
-        import torch
-        if not (pages.device == self.device and pages.dtype == torch.int32 and pages.is_contiguous() and pages.dim() >= 3
-                and pages.shape[-2] == self.kv_heads and pages.numel() == b.rows * self.kv_heads * pages.shape[-1]):
+    def _choice(self, pages, rows):
+        if not (pages.dtype is self._i32 and pages.is_cuda and pages.get_device() == self._index and pages.is_contiguous()
+                and pages.dim() >= 3 and pages.shape[-2] == self.kv_heads
+                and pages.numel() == rows * self.kv_heads * pages.shape[-1]):
             _bad("pages: contiguous int32 [rows, kv_heads, budget]")
         return pages.shape[-1]
 
@@ -258,8 +274,10 @@ class KVCache:
         """Choose pages.shape[-1] pages for each row and kv head into pages (int32 [rows,
         kv_heads, budget], ascending, -1 where a row sees fewer): the first keep_first, the
         last keep_last, then those whose bounds promise the largest q . k."""
-        b = self._batch(q.shape, table, lens, starts, max_new)
-        qt = self._rows(q, "q")
-        budget = self._choice(pages, b)
-        self._call(_lib().moe_kv_select(self._h, layer, ctypes.byref(b), ctypes.byref(qt), q.shape[-2], budget,
-                                        keep_first, keep_last, pages.data_ptr(), self._stream(stream)))
+        shape = q.shape
+        heads = self._heads(shape, "q", False)
+        rows, b = self._batch(shape, table, lens, starts, max_new)
+        rc = self._lib.moe_kv_select(self._h, layer, b, self._rows(q, "q", shape), heads, self._choice(pages, rows),
+                                     keep_first, keep_last, pages.data_ptr(), self._stream(stream))
+        if rc:
+            self._failed(rc)
