@@ -41,8 +41,8 @@ namespace {
 constexpr int kPrSoft = 8, kPrDequant = 4, kPrMma = kPrSoft + kPrDequant;
 constexpr int kPrThreads = 512;  // four warpgroups; warps 13-15 only fill theirs
 // Registers: the launch's 128 per thread are dealt out again between the warpgroups,
-// 128 threads x (168 + 168 + 112 + 64) = 512 x 128.
-constexpr int kPrRegs = 128, kPrSoftRegs = 168, kPrDequantRegs = 112, kPrMmaRegs = 64;
+// 128 threads x (176 + 176 + 112 + 48) = 512 x 128.
+constexpr int kPrRegs = 128, kPrSoftRegs = 176, kPrDequantRegs = 112, kPrMmaRegs = 48;
 static_assert(2 * kPrSoftRegs + kPrDequantRegs + kPrMmaRegs == 4 * kPrRegs, "a split above the launch's registers never ends");
 template <int R, bool Inc>
 __device__ __forceinline__ void set_registers() {
@@ -50,9 +50,10 @@ __device__ __forceinline__ void set_registers() {
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 constexpr int kPrTile = 128;  // rows of a row tile, tokens of a token tile
-// weights are 2^(score - reference): set kPrDrop below the largest score, raised when one
-// passes it by kPrSlack; so weights reach 2^15 at most and fp16 holds 2^-25 of them
-constexpr float kPrDrop = 7.0f, kPrSlack = 15.0f;
+// weights are 2^(score - reference): the reference is set kPrDrop below the largest score and
+// raised when a tile's weights sum to kPrLimit; so no weight passes 2^15 and fp16 holds those
+// 2^-31 of the largest
+constexpr float kPrDrop = 7.0f, kPrLimit = 32768.0f;
 
 // K-major operand, 128-byte swizzle: 8-row groups 1024 bytes apart.
 __device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
@@ -69,20 +70,33 @@ __device__ __forceinline__ constexpr uint32_t idesc(int N, bool b_mn) {  // fp16
   return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(kPrTile >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+// The whole warp runs these, one lane (`leader`, from elect.sync) acts: without a branch around
+// them the descriptors stay in uniform registers, where the instruction wants them.
+__device__ __forceinline__ uint32_t elect_leader() {
+  uint32_t d;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(d));
+  return d;
+}
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(acc)
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc), "r"(leader)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(acc)
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc), "r"(leader)
       : "memory");
 }
-__device__ __forceinline__ void commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+__device__ __forceinline__ void commit(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_addr(bar)),
+      "r"(leader)
+      : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -264,65 +278,81 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
       const bool scaled = (scaled4.x | scaled4.y | scaled4.z | scaled4.w) != 0;
       const uint32_t valid[4] = {valid4.x, valid4.y, valid4.z, valid4.w};
       const uint32_t poison[4] = {poison4.x, poison4.y, poison4.z, poison4.w};
+      // a tile that every row of the warp sees in full takes no masks
+      const bool plain = __all_sync(0xffffffffu, seen >= (j + 1) * kPrTile) &&
+                         (valid4.x & valid4.y & valid4.z & valid4.w) == 0xffffffffu && !scaled;
       uint32_t pr[kPrTile / 2];
       auto mask_of = [&](int k) {  // tokens of the k-th 32 that the row sees
         const int n = seen - (j * kPrTile + 32 * k);
         return valid[k] & (n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u);
       };
-      auto load = [&](int k, uint32_t (&v)[32]) {  // the k-th 32 scores
+      auto load = [&](int k, uint32_t (&v)[32]) {  // the k-th 32 scores, masked ones -infinity (in the sign of scale)
         tmem_ld32(ts + 32 * k, v);
         tmem_wait_ld();
+        const uint32_t mask = mask_of(k);
         if (scaled) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * sh_kscale[j & 3][32 * k + i]);
         }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = (mask >> i) & 1u ? __float_as_uint(__uint_as_float(v[i]) * kappa) : 0xff800000u;
       };
-      uint64_t sum;
+      uint64_t sum = 0;
+      auto weights = [&](const uint32_t (&v)[32], int k, uint64_t factor, uint64_t neg) {
+        uint64_t more = 0;
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          float e[4];
+          split2(fma2(pair2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), factor, neg), e[0], e[1]);
+          split2(fma2(pair2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), factor, neg), e[2], e[3]);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) e[y] = exp2_fast(e[y]);
+          sum = add2(sum, pair2(e[0], e[1]));
+          more = add2(more, pair2(e[2], e[3]));
+          pr[16 * k + i / 2] = KvType<__half>::pack(e[0], e[1]);
+          pr[16 * k + i / 2 + 1] = KvType<__half>::pack(e[2], e[3]);
+        }
+        sum = add2(sum, more);
+      };
+      auto masked_pass = [&]() {
+        const uint64_t neg = pair2(-m, -m), one = pair2(1.0f, 1.0f);
+        sum = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t v[32];
+          load(k, v);
+          weights(v, k, one, neg);
+        }
+      };
       bool raise = j == 0 || sh_vexp[j & 3] != vexp;
-      if (!raise) {
-        // weights against the reference as it stands; top: the largest exponent
-        auto pass = [&](float& top) {
+      if (!raise) {  // weights against the reference as it stands
+        if (plain) {
           const uint64_t neg = pair2(-m, -m);
-          sum = 0;
-          top = kNone;
+          uint32_t v[2][32];
+          tmem_ld32(ts, v[0]);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t v[32];
-            const uint32_t mask = mask_of(k);
-            load(k, v);
-            float e[32];
-#pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              split2(fma2(pair2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), kappa2, neg), e[i], e[i + 1]);
-            if (!__all_sync(0xffffffffu, mask == 0xffffffffu)) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((mask >> i) & 1u)) e[i] = -__int_as_float(0x7f800000);
-            }
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              top = fmaxf(top, fmaxf(e[i], e[i + 1]));
-              const float p0 = exp2_fast(e[i]), p1 = exp2_fast(e[i + 1]);
-              sum = add2(sum, pair2(p0, p1));
-              pr[16 * k + i / 2] = KvType<__half>::pack(p0, p1);
-            }
+          for (int k = 0; k < 4; ++k) {  // the next 32 scores arrive while these are worked on
+            tmem_wait_ld();
+            if (k < 3) tmem_ld32(ts + 32 * (k + 1), v[(k + 1) & 1]);
+            weights(v[k & 1], k, kappa2, neg);
           }
-        };
-        float top;
-        pass(top);
-        raise = __any_sync(0xffffffffu, top > kPrSlack);
+        } else {
+          masked_pass();
+        }
+        // a weight above the limit shows in the sum (which may reach it without one: no harm)
+        float s0, s1;
+        split2(sum, s0, s1);
+        raise = __any_sync(0xffffffffu, fmaxf(s0, s1) > kPrLimit);
       }
       if (raise) {
         // the row's largest score of this tile becomes its reference; what was summed so far shrinks
         float best = kNone;
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < 4; ++k) {
           uint32_t v[32];
-          const uint32_t mask = mask_of(k);
           load(k, v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if ((mask >> i) & 1u) best = fmaxf(best, __uint_as_float(v[i]) * kappa);
+          for (int i = 0; i < 32; ++i) best = fmaxf(best, __uint_as_float(v[i]));
         }
         best = fmaxf(best - kPrDrop, m);
         const float f = exp2_fast(m - best), fo = f * pow2(max(vexp - sh_vexp[j & 3], -126));
@@ -343,24 +373,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
           }
           tmem_wait_st();
         }
-        const uint64_t neg = pair2(-m, -m);
-        sum = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t v[32];
-          const uint32_t mask = mask_of(k);
-          load(k, v);
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            float e0, e1;
-            split2(fma2(pair2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), kappa2, neg), e0, e1);
-            if (!((mask >> i) & 1u)) e0 = -__int_as_float(0x7f800000);
-            if (!((mask >> (i + 1)) & 1u)) e1 = -__int_as_float(0x7f800000);
-            const float p0 = exp2_fast(e0), p1 = exp2_fast(e1);
-            sum = add2(sum, pair2(p0, p1));
-            pr[16 * k + i / 2] = KvType<__half>::pack(p0, p1);
-          }
-        }
+        masked_pass();
       }
       l2 = add2(l2, sum);
       tmem_st32(ts, pr);
@@ -568,17 +581,15 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
     // ------------------------------------------------------------------ MMA issue
     const uint32_t ids = idesc(kPrTile, false), ido = idesc(D, true);
     const int nt = two ? 2 : 1;
+    const uint32_t leader = elect_leader();
     auto scores = [&](int t, int j) {
-      if (lane == 0) {
-        const uint32_t qa = sq + t * kTileBytes, kb = sk + (j & 1) * kTileBytes;
+      const uint32_t qa = sq + t * kTileBytes, kb = sk + (j & 1) * kTileBytes;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ss(tm + t * kPrTile, desc_k(qa + (k / 4) * kSlab + (k % 4) * 32), desc_k(kb + (k / 4) * kSlab + (k % 4) * 32),
-                 ids, k ? 1u : 0u);
-        commit(&sFull[t]);
-        if (t == nt - 1) commit(&kEmpty[j & 1]);
-      }
-      __syncwarp();
+      for (int k = 0; k < D / 16; ++k)
+        mma_ss(leader, tm + t * kPrTile, desc_k(qa + (k / 4) * kSlab + (k % 4) * 32),
+               desc_k(kb + (k / 4) * kSlab + (k % 4) * 32), ids, k ? 1u : 0u);
+      commit(leader, &sFull[t]);
+      if (t == nt - 1) commit(leader, &kEmpty[j & 1]);
     };
     if (warp == kPrMma && ntiles > 0) {
       mbar_wait<false>(smem_addr(&kFull[0]), 0, p.err);
@@ -589,14 +600,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
           if (t == 0) mbar_wait<false>(smem_addr(&vFull[j & 1]), (uint32_t)(j >> 1) & 1u, p.err);
           mbar_wait<false>(smem_addr(&pFull[t]), (uint32_t)j & 1u, p.err);
           fence_after();
-          if (lane == 0) {
-            const uint32_t vb = sv + (j & 1) * kTileBytes;
+          const uint32_t vb = sv + (j & 1) * kTileBytes;
 #pragma unroll
-            for (int k = 0; k < kPrTile / 16; ++k)
-              mma_ts(tm + 2 * kPrTile + t * D, tm + t * kPrTile + 8 * k, desc_mn(vb + k * 2048), ido, (j | k) ? 1u : 0u);
-            if (t == nt - 1) commit(&vEmpty[j & 1]);
-          }
-          __syncwarp();
+          for (int k = 0; k < kPrTile / 16; ++k)
+            mma_ts(leader, tm + 2 * kPrTile + t * D, tm + t * kPrTile + 8 * k, desc_mn(vb + k * 2048), ido, (j | k) ? 1u : 0u);
+          if (t == nt - 1) commit(leader, &vEmpty[j & 1]);
           if (j + 1 < ntiles) {
             if (t == 0) {
               mbar_wait<false>(smem_addr(&kFull[(j + 1) & 1]), (uint32_t)((j + 1) >> 1) & 1u, p.err);
@@ -606,8 +614,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
           }
         }
       }
-      if (lane == 0) commit(&oFull);
-      __syncwarp();
+      commit(leader, &oFull);
       mbar_drain(smem_addr(&oFull), 0);
     }
   }
