@@ -79,7 +79,7 @@ __device__ __forceinline__ int64_t kv_row_index(const KvBatch& b, int s, int64_t
 }
 // Tokens the table can hold: positions beyond are neither written nor read.
 __device__ __forceinline__ int kv_capacity(const KvView& c, const KvBatch& b) {
-  return (int)min((int64_t)b.table_pages << c.page_shift, (int64_t)0x7fffffff);
+  return (int)min((int64_t)b.table_pages << c.page_shift, (int64_t)0x7ffff000);  // a block past it still has a position
 }
 // Page id of a sequence's page j, or -1 where the entry names no page of the pool.
 __device__ __forceinline__ int64_t kv_page(const KvView& c, const KvBatch& b, int s, int j) {

@@ -7,26 +7,29 @@
 // the 16 rows of mma.m16n8k16 and up to 8 columns as its n, so a group of
 // query heads costs what one head costs.  The operand is the code itself, not
 // the stored value: with stored value c + s (u - 8) per token and group,
-//     S[t][col] = sum over groups g of  s_g (u - 8)_g . q_g + c_g sum(q_g),
-// the products are exact, and s and c enter in fp32 on the accumulators.
-// (bf16 takes 128 + u, one mask, and corrects by 136 sum(q_g) s_g; fp16, whose
-// 1024 + u would cost three more bits of the accumulator, takes u - 8.)
-// O^T = V^T P^T is the second product, the channels as rows: P s_g per group is
-// rounded to 16 bits (the one rounding before the output's: relative 2^-9 or
-// 2^-12 of a weight, independent from token to token), u - 8 is exact, and the
-// centres' part sum over t of P c_g is summed apart in fp32.
+//     S[t][col] = sum over groups g of  s_g (u_g . q_g) + (c_g - 8 s_g) sum(q_g),
+// where u enters as its four bits in an fp16 subnormal (one mask, exact), q as
+// fp16 times a power of two that brings its largest element to 2^14, and s and
+// c in fp32 on the accumulators.  O^T = V^T P^T is the second product, the
+// channels as rows: P s_g per group is rounded to fp16 (the one rounding before
+// the output's, 2^-12 of a weight and independent from token to token); the
+// centres' part is summed apart in fp32.  bf16 outputs take the values' codes
+// as they are too (their offset of 8 s makes that rounding three times larger,
+// far below bf16's); fp16 outputs take u - 8.  Values are carried times 2^-E,
+// E raised when a token's values need it, so that no size of value leaves
+// fp16's or, summed, fp32's range.
 //
-// Softmax: running reference per column, raised only when a score exceeds it by
-// more than kSlack, so that most blocks rescale nothing; weights are at most
-// 2^kSlack and the sums are fp32.  A column that sees no token keeps the sum 0.
+// Softmax: running reference per column, raised only when a score passes it by
+// 4 (in powers of two), so that most blocks rescale nothing; sums are fp32.  A
+// column that sees no token keeps the sum 0.
 //
-// Work split: all blocks (16 tokens of one kv head and column tile) of the
-// batch in one line, cut into equal runs, one per CTA; a run covers any number
-// of items (sequence, head, column tile) or part of one.  Warp w of 8 takes
-// every eighth block of the run through a ring of its own, each block one bulk
-// copy.  At the end of an item's stretch the warps' (max, sum, O) are joined in
-// shared memory; an item cut between CTAs is joined by the CTA that finishes
-// last, in the order of the CTAs, so results do not depend on timing.
+// Work split: all rounds (8 blocks of 16 tokens of one kv head and column tile)
+// of the batch in one line, cut into equal shares, one per CTA; a share covers
+// any number of items (sequence, head, column tile) or part of one.  In a round
+// each of the 8 warps takes one block, through a ring of its own, each block
+// one bulk copy.  At the end of an item's stretch the warps' (max, sum, O) are
+// joined in shared memory; an item cut between CTAs is joined by the CTA that
+// finishes last, in the order of the CTAs, so results do not depend on timing.
 #pragma once
 
 #include "kv_internal.h"
@@ -39,172 +42,218 @@ namespace {
 #include "kv_operand.cuh"
 
 constexpr int kDecWarps = 8;
+constexpr float kDecSlack = 4.0f;      // weights reach 2^4
+constexpr float kDecValues = 8192.0f;  // bound of |c| + 8 s times 2^-E
+// O leaves a warp times 2^-32: sums of 2^28 weights times bf16's largest value stay finite
+constexpr int kDecDown = 32;
 
-// What the work is divided into.  A unit is 16 tokens of an item; an item is a
-// (group, head, column tile); a group is a sequence, or with chosen pages one
-// of its rows.  Unit numbers run over the groups, inside them over the items,
-// inside them over the tokens.
-struct DecPlan {
-  int groups;     // sequences, or batch * max_new rows
-  int items;      // items per group: heads * column tiles
-  int ctiles;     // column tiles
-  int per;        // query heads per kv head
-  int min_units;  // a CTA's share is not made smaller than this
-};
-
-__device__ __forceinline__ int group_units(const KvAttnArgs& a, int gi) {
-  if (a.sel) {
-    const int s = gi / a.b.max_new, i = gi % a.b.max_new;
-    return i < kv_seq(a.b, s).rows ? a.budget << (a.c.page_shift - 4) : 0;
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
+  return d;
+}
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t* p) {  // 4 N contiguous, aligned bytes
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
   }
-  const KvSeq q = kv_seq(a.b, gi);
-  return q.rows > 0 ? (min(q.len, kv_capacity(a.c, a.b)) + 15) >> 4 : 0;
 }
 
-// First CTA whose share [total c / n, total (c + 1) / n) holds unit u.
-__device__ __forceinline__ int owner(int64_t u, int64_t total, int n) { return (int)(((u + 1) * n - 1) / total); }
+// What the work is divided into.  A round is 8 blocks of an item; an item is a
+// (group, head, column tile); a group is a sequence, or with chosen pages one
+// of its rows.  Round numbers run over the groups, inside them over the items,
+// inside them over the tokens.
+struct DecPlan {
+  int groups;      // sequences, or batch * max_new rows
+  int items;       // items per group: heads * column tiles
+  int ctiles;      // column tiles
+  int per;         // query heads per kv head
+  int min_rounds;  // a CTA's share is not made smaller than this
+};
 
-// A place in the line of units.
+__device__ __forceinline__ int group_rounds(const KvAttnArgs& a, int gi) {
+  if (a.sel) {
+    const int s = gi / a.b.max_new, i = gi % a.b.max_new;
+    return i < kv_seq(a.b, s).rows ? ((a.budget << (a.c.page_shift - 4)) + kDecWarps - 1) / kDecWarps : 0;
+  }
+  const KvSeq q = kv_seq(a.b, gi);
+  return q.rows > 0 ? (min(q.len, kv_capacity(a.c, a.b)) + 16 * kDecWarps - 1) / (16 * kDecWarps) : 0;
+}
+
+// First CTA whose share [total c / n, total (c + 1) / n) holds round u.
+__device__ __forceinline__ int owner(int u, int total, int n) { return (int)((((int64_t)u + 1) * n - 1) / total); }
+__device__ __forceinline__ int share(int total, int c, int n) { return (int)((int64_t)total * c / n); }
+
+// A place in the line of rounds.
 struct Cursor {
-  int group;           // its group
-  int64_t base, end;   // units of the group
-  int units;           // units of each of the group's items
-  // the current item
-  int64_t item0, item_end;
-  int item;
+  int group, end, rounds;  // the group, its end, the rounds of each of its items
+  int item, item0, item_end;
 
-  __device__ __forceinline__ void enter(const KvAttnArgs& a, const DecPlan& p, int64_t u) {
+  __device__ __forceinline__ void enter(const KvAttnArgs& a, const DecPlan& p, int u) {
+    int base = end - rounds * p.items;
     while (u >= end) {
       base = end;
-      units = group_units(a, ++group);
-      end = base + (int64_t)units * p.items;
+      rounds = group_rounds(a, ++group);
+      end = base + rounds * p.items;
     }
-    item = (int)((u - base) / units);
-    item0 = base + (int64_t)item * units;
-    item_end = item0 + units;
+    item = (u - base) / rounds;
+    item0 = base + item * rounds;
+    item_end = item0 + rounds;
   }
 };
 
 template <typename T, int D, int G, int NT>
 __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
-    kv_decode_kernel(KvAttnArgs a, DecPlan p, float* __restrict__ ws, unsigned* __restrict__ counters, uint32_t* err) {
+    kv_decode_kernel(const __grid_constant__ KvAttnArgs a, const __grid_constant__ DecPlan p, float* __restrict__ ws,
+                     unsigned* __restrict__ counters, uint32_t* err) {
   using Geo = KvGeom<D, G>;
-  using F = Frag<T>;
+  constexpr bool kCentred = std::is_same<T, __half>::value;
   constexpr int C = 8 * NT, NG = D / G;
   constexpr int kStages = kDecStages<D, G>;
   constexpr int kSlot = C * (D + 2);  // floats of one partial result: O [C][D], max [C], sum [C]
   extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t* ring = smem;                                                         // [warp][stage][block]
-  float* mo = reinterpret_cast<float*>(smem + kDecWarps * kStages * Geo::kBytes);  // [warp][C][D + 4]
+  float* mo = reinterpret_cast<float*>(smem + kDecWarps * kStages * Geo::kBytes);  // [warp][C][D + 4]; below: [warp][stage][block]
   float* mm = mo + kDecWarps * C * (D + 4);                                     // [warp][C] max, then sums
   float* ml = mm + kDecWarps * C;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ml + kDecWarps * C);             // [warp][stage]
-  int* spos = reinterpret_cast<int*>(bars + kDecWarps * kStages);               // [warp][stage] position of a block, -1: none
-  __shared__ int64_t sh_sum[kDecWarps];
-  __shared__ int64_t sh_base;
-  __shared__ int sh_group;
+  uint64_t* bars_all = reinterpret_cast<uint64_t*>(ml + kDecWarps * C);         // [warp][stage]
+  int* spos_all = reinterpret_cast<int*>(bars_all + kDecWarps * kStages);       // [warp][stage] position of a block, -1: none
+  __shared__ int sh_sum[kDecWarps];
+  __shared__ int sh_base, sh_group;
   __shared__ unsigned sh_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
+  uint8_t* ring = smem + (size_t)warp * kStages * Geo::kBytes;
+  uint64_t* bars = bars_all + warp * kStages;
+  volatile int* spos = spos_all + warp * kStages;
 
-  if (lane < kStages) mbar_init(smem_addr(&bars[warp * kStages + lane]), 1);
+  if (lane < kStages) mbar_init(smem_addr(&bars[lane]), 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 
-  // ---- the CTA's share: the sum of all units, then the group its first unit lies in
-  auto block_sum = [&](int64_t v) {
+  // ---- the CTA's share: the sum of all rounds, and the group its first round lies in
+  auto scan = [&](int v, int& all) {  // inclusive prefix over the CTA's threads, and the sum
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
     __syncthreads();
-    if (lane == 0) sh_sum[warp] = v;
+    if (lane == 31) sh_sum[warp] = v;
     __syncthreads();
-    int64_t s = 0;
+    all = 0;
 #pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) s += sh_sum[w];
-    return s;
+    for (int w = 0; w < kDecWarps; ++w) {
+      if (w < warp) v += sh_sum[w];
+      all += sh_sum[w];
+    }
+    return v;
   };
-  int64_t total = 0;
+  int total = 0, mine = 0, upto = 0;  // the last 256 groups' (for up to 256 groups: the only) prefix
   for (int g0 = 0; g0 < p.groups; g0 += kDecWarps * 32) {
     const int gi = g0 + tid;
-    total += block_sum(gi < p.groups ? (int64_t)group_units(a, gi) * p.items : 0);
+    int all;
+    mine = gi < p.groups ? group_rounds(a, gi) * p.items : 0;
+    upto = scan(mine, all);
+    total += all;
   }
-  // rows that see nothing at all (no unit in their group) are written by the last loop below
-  const int n = (int)min((int64_t)gridDim.x, max((total + p.min_units - 1) / p.min_units, (int64_t)1));
+  const int n = max(min((int)gridDim.x, (total + p.min_rounds - 1) / p.min_rounds), 1);
   const int me = blockIdx.x;
-  const int64_t first = me < n ? total * me / n : total, last = me < n ? total * (me + 1) / n : total;
+  const int first = me < n ? share(total, me, n) : total, last = me < n ? share(total, me + 1, n) : total;
   if (first < last) {
-    int64_t before = 0;
-    for (int g0 = 0; g0 < p.groups; g0 += kDecWarps * 32) {  // the group that holds unit `first`
-      const int gi = g0 + tid;
-      const int64_t v = gi < p.groups ? (int64_t)group_units(a, gi) * p.items : 0;
-      int64_t x = v;  // inclusive prefix over the CTA
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+    if (p.groups <= kDecWarps * 32) {
+      if (upto - mine <= first && first < upto) {
+        sh_group = tid;
+        sh_base = upto - mine;
       }
-      __syncthreads();
-      if (lane == 31) sh_sum[warp] = x;
-      __syncthreads();
-      int64_t all = 0;
-      for (int w = 0; w < kDecWarps; ++w) {
-        if (w < warp) x += sh_sum[w];
-        all += sh_sum[w];
+    } else {
+      int before = 0;
+      for (int g0 = 0; g0 < p.groups && before <= first; g0 += kDecWarps * 32) {
+        const int gi = g0 + tid;
+        int all;
+        mine = gi < p.groups ? group_rounds(a, gi) * p.items : 0;
+        upto = before + scan(mine, all);
+        if (upto - mine <= first && first < upto) {
+          sh_group = gi;
+          sh_base = upto - mine;
+        }
+        before += all;
       }
-      if (before + x - v <= first && first < before + x) {
-        sh_group = gi;
-        sh_base = before + x - v;
-      }
-      before += all;
-      if (before > first) break;
     }
     __syncthreads();
     Cursor seed;
     seed.group = sh_group - 1;
     seed.end = sh_base;
+    seed.rounds = 0;
 
-    // ---- the producer side: this warp's units first + warp, + 8, ...
+    // ---- the producer side: block `warp` of each round
     Cursor pc = seed;
-    int64_t pu = first + warp;
-    int64_t pid = -1;       // page of unit pu (requested one step ahead of its copy)
-    int ppos = -1, pblk = 0;  // its position in the sequence (-1: nothing to read), its block of the page
     pc.item_end = 0;
+    const int per_page = a.c.page_shift - 4;
+    int pu = first;
+    int ppos = -1;                     // position of round pu's block (-1: nothing to read)
+    int pid = -1;                      // its page, requested a round ahead of its copy
+    int pblk = 0;                      // its block of the page
+    const int32_t* ptable = nullptr;   // the sequence's table
+    const int32_t* plist = nullptr;    // the chosen pages
+    const uint8_t* phead = nullptr;
+    int pseen = 0;                     // positions from here on are not read
     auto locate = [&]() {
-      if (pu >= last) return;
-      if (pu >= pc.item_end) pc.enter(a, p, pu);
-      const int ub = (int)(pu - pc.item0);
-      const int per_page = a.c.page_shift - 4;
+      if (pu >= pc.item_end) {
+        if (pu >= last) return;
+        pc.enter(a, p, pu);
+        const int h = pc.item / p.ctiles;
+        int s = pc.group;
+        if (a.sel) {
+          s = pc.group / a.b.max_new;
+          const KvSeq q = kv_seq(a.b, s);
+          const int i = pc.group % a.b.max_new;
+          plist = a.sel + (kv_row_index(a.b, s, q.row0, i) * a.c.heads + h) * a.budget;
+          pseen = (int)min(a.causal ? (int64_t)q.len - q.rows + i + 1 : (int64_t)q.len, (int64_t)kv_capacity(a.c, a.b));
+        } else {
+          pseen = min(kv_seq(a.b, s).len, kv_capacity(a.c, a.b));
+        }
+        ptable = a.b.table + (int64_t)s * a.b.table_stride;
+        phead = a.c.pages + h * a.c.head_stride;
+      }
+      const int ub = (pu - pc.item0) * kDecWarps + warp;
       int j = ub >> per_page;
       pblk = ub & ((1 << per_page) - 1);
-      int s = pc.group;
+      ppos = ub * 16;
       if (a.sel) {
-        s = pc.group / a.b.max_new;
-        const KvSeq q = kv_seq(a.b, s);
-        const int i = pc.group % a.b.max_new;
-        const int64_t row = kv_row_index(a.b, s, q.row0, i);
-        j = a.sel[(row * a.c.heads + pc.item / p.ctiles) * a.budget + j];
-        const int64_t seen = min(a.causal ? (int64_t)q.len - q.rows + i + 1 : (int64_t)q.len, (int64_t)kv_capacity(a.c, a.b));
-        const int64_t pos = ((int64_t)j << a.c.page_shift) + 16 * pblk;
-        ppos = j >= 0 && pos < seen ? (int)pos : -1;
-        if (ppos < 0) j = 0;
-      } else {
-        ppos = ub * 16;
+        j = j < a.budget ? plist[j] : -1;
+        // pages beyond the row's are skipped (compared as pages: positions could wrap)
+        if (j < 0 || j > (pseen - 1) >> a.c.page_shift) j = -1;
+        ppos = (j << a.c.page_shift) + 16 * pblk;
+        if (j < 0) ppos = 0x7fffffff;
       }
-      pid = kv_page(a.c, a.b, s, j);
+      pid = -1;
+      if (ppos < pseen) pid = ptable[j];
     };
     auto issue = [&](int slot) {
       if (pu >= last) return;
+      const bool ok = ppos < pseen && (uint32_t)pid < (uint32_t)a.c.num_pages;
       if (lane == 0) {
-        const bool ok = ppos >= 0 && pid >= 0;
-        spos[warp * kStages + slot] = ok ? ppos : -1;
+        spos[slot] = ok ? ppos : -1;
         if (ok) {
-          const uint32_t bar = smem_addr(&bars[warp * kStages + slot]);
+          const uint32_t bar = smem_addr(&bars[slot]);
           mbar_arrive_expect_tx(bar, Geo::kBytes);
-          bulk_g2s(smem_addr(ring + (size_t)(warp * kStages + slot) * Geo::kBytes),
-                   a.c.pages + pid * a.c.page_stride + (pc.item / p.ctiles) * a.c.head_stride + (int64_t)pblk * Geo::kBytes,
-                   Geo::kBytes, bar);
+          bulk_g2s(smem_addr(ring + slot * Geo::kBytes),
+                   phead + (int64_t)pid * a.c.page_stride + pblk * Geo::kBytes, Geo::kBytes, bar);
         }
       }
-      pu += kDecWarps;
+      ++pu;
       locate();
     };
     locate();
@@ -214,10 +263,9 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
     uint32_t phases = 0;  // bit q: the parity slot q's next copy completes
 
     Cursor cc = seed;
-    int64_t cu = first + warp;  // this warp's next unit
-    for (int64_t seg = first; seg < last;) {
+    for (int seg = first; seg < last;) {
       cc.enter(a, p, seg);
-      const int64_t seg_end = min(cc.item_end, last);
+      const int seg_end = min(cc.item_end, last);
       // ---- the item's columns
       int s = cc.group, row_lo = 0, ncols;
       const int h = cc.item / p.ctiles, ct = cc.item % p.ctiles;
@@ -228,53 +276,70 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
       const KvSeq q = kv_seq(a.b, s);
       ncols = (a.sel ? 1 : q.rows) * p.per;
       const int cap = kv_capacity(a.c, a.b);
-      auto col_seen = [&](int col) {  // tokens that column `col` of the tile sees
-        const int x = ct * C + col;
-        if (x >= ncols) return 0x7fffffff;  // a column of nobody: zeros times anything, never written
-        const int64_t pos = (int64_t)q.len - q.rows + row_lo + x / p.per;
-        return (int)min(max(a.causal ? pos + 1 : (int64_t)q.len, (int64_t)0), (int64_t)cap);
-      };
-      uint32_t qf[NT][D / 8];   // this lane's query operand: column 8 nt + r, its quarter of every group
-      float qsum[NT][NG][2];    // sums over a group's channels, columns 8 nt + 2c, + 1 (times scale log2 e)
-      int seen[NT][2];
-      const float kappa = a.scale * 1.4426950408889634f;
+      uint32_t qf[NT][D / 8];    // this lane's query operand: column 8 nt + r, its quarter of every group
+      float qsum[NT][NG][2];     // 2^-24 sums over a group's channels, columns 8 nt + 2c, + 1
+      float factor[NT][2];       // what makes the columns' sums scores (log2)
+      int seen[NT][2];           // tokens that the columns see
+      int least = 0x7fffffff, most = 0;  // over the columns
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const int x = ct * C + nt * 8 + r;
-        const uint16_t* src = nullptr;
-        if (x < ncols)
-          src = a.q + kv_row_offset(a.b, a.qs, s, q.row0, row_lo + x / p.per) + (int64_t)(h * p.per + x % p.per) * a.qs.head;
+        const int x = ct * C + nt * 8 + r;  // column 8 nt + r; a column of nobody is zeros, never written
+        const bool real = x < ncols;
+        const int i = row_lo + (real ? x / p.per : 0);
+        const uint16_t* src = a.q + kv_row_offset(a.b, a.qs, s, q.row0, i) + (int64_t)(h * p.per + x % p.per) * a.qs.head;
+        uint4 raw[D / 32];
+        uint32_t top = 0;
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
           const int ch = w / (G / 32) * G + c * (G / 4) + w % (G / 32) * 8;
-          const uint4 v = src ? *reinterpret_cast<const uint4*>(src + ch) : make_uint4(0, 0, 0, 0);
-          qf[nt][4 * w] = v.x;
-          qf[nt][4 * w + 1] = v.y;
-          qf[nt][4 * w + 2] = v.z;
-          qf[nt][4 * w + 3] = v.w;
+          raw[w] = real ? *reinterpret_cast<const uint4*>(src + ch) : make_uint4(0, 0, 0, 0);
+          const uint32_t v[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            top = max(top, max(__float_as_uint(fabsf(KvType<T>::lo(v[e]))), __float_as_uint(fabsf(KvType<T>::hi(v[e])))));
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int ex = (int)(top >> 23) - 127;  // the largest element to 2^14; an infinity or a NaN stays what it is
+        const int by = top == 0u || ex > 127 ? 0 : min(max(14 - ex, -102), 113);
+        const float up = pow2(by), up16 = pow2(by - 4);  // the odd fields are 16 u
+        float sum[NG];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) sum[g] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          const uint32_t v[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float lo = KvType<T>::lo(v[e]), hi = KvType<T>::hi(v[e]), f = e % 2 ? up16 : up;
+            qf[nt][4 * w + e] = KvType<__half>::pack(lo * f, hi * f);
+            sum[w / (G / 32)] += lo * (up * 0x1p-24f) + hi * (up * 0x1p-24f);
+          }
         }
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          float t = 0.0f;
+          sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+          sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
 #pragma unroll
-          for (int i = g * (G / 8); i < (g + 1) * (G / 8); ++i) t += KvType<T>::lo(qf[nt][i]) + KvType<T>::hi(qf[nt][i]);
-          t += __shfl_xor_sync(0xffffffffu, t, 1);
-          t += __shfl_xor_sync(0xffffffffu, t, 2);  // column 8 nt + r
-#pragma unroll
-          for (int e = 0; e < 2; ++e) qsum[nt][g][e] = kappa * __shfl_sync(0xffffffffu, t, 4 * (2 * c + e));
+          for (int e = 0; e < 2; ++e) qsum[nt][g][e] = __shfl_sync(0xffffffffu, sum[g], 4 * (2 * c + e));
         }
-        seen[nt][0] = col_seen(nt * 8 + 2 * c);
-        seen[nt][1] = col_seen(nt * 8 + 2 * c + 1);
-      }
-      int least = seen[0][0];  // blocks that end by here need no mask
+        const int64_t pos = (int64_t)q.len - q.rows + i;
+        const int see = (int)min(max(a.causal ? pos + 1 : (int64_t)q.len, (int64_t)0), (int64_t)cap);
+        const float back = a.scale * 1.4426950408889634f * pow2(24 - by);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) least = min(least, min(seen[nt][0], seen[nt][1]));
-      least = min(least, __shfl_xor_sync(0xffffffffu, least, 1));
-      least = min(least, __shfl_xor_sync(0xffffffffu, least, 2));
+        for (int e = 0; e < 2; ++e) {
+          factor[nt][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * c + e));
+          seen[nt][e] = __shfl_sync(0xffffffffu, see, 4 * (2 * c + e));
+        }
+        least = min(least, __reduce_min_sync(0xffffffffu, see));
+        most = max(most, __reduce_max_sync(0xffffffffu, see));
+      }
 
       float acc[D / 16][NT][4];  // O^T: channel tiles by columns
-      float oc[NT][NG][2];       // this lane's tokens' part of sum P c
+      float oc[NT][NG][2];       // this lane's tokens' part of sum P (c - 8 s), or of sum P c
       float m[NT][2], l[NT][2];
+      int vexp = 0;              // E
+      float vdown = 0.0f;        // 2^-E; 0 before the first block
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -290,32 +355,31 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
         }
       }
 
-      for (; cu < seg_end; cu += kDecWarps) {
+      for (int cu = seg; cu < seg_end; ++cu) {
         __syncwarp();
-        const int pos = *reinterpret_cast<volatile int*>(&spos[warp * kStages + slot]);
+        const int pos = spos[slot];
         if (pos >= 0) {
-          const uint32_t bar = smem_addr(&bars[warp * kStages + slot]);
+          const uint32_t bar = smem_addr(&bars[slot]);
           if (!mbar_wait(bar, (phases >> slot) & 1u, err)) mbar_drain(bar, (phases >> slot) & 1u);
           phases ^= 1u << slot;
-          const uint8_t* blk = ring + (size_t)(warp * kStages + slot) * Geo::kBytes;
+          const uint8_t* blk = ring + slot * Geo::kBytes;
+          const bool part = pos + 16 > least;  // some column does not see some token
           // ---- scores of tokens r and r + 8, columns 2c and 2c + 1
-          uint32_t kw[2][D / 32];
+          uint32_t kw[2][D / 32], kp[2][NG], vp[2][NG];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const uint8_t* src = blk + (r + 8 * e) * Geo::kRow + c * (D / 8);
-            if constexpr (D == 128) {
-              const uint4 v = *reinterpret_cast<const uint4*>(src);
-              kw[e][0] = v.x, kw[e][1] = v.y, kw[e][2] = v.z, kw[e][3] = v.w;
-            } else {
-              const uint2 v = *reinterpret_cast<const uint2*>(src);
-              kw[e][0] = v.x, kw[e][1] = v.y;
-            }
+            load_words(kw[e], blk + (r + 8 * e) * Geo::kRow + c * (D / 8));
+            load_words(kp[e], blk + Geo::kKPar + (r + 8 * e) * Geo::kParRow);
+            load_words(vp[e], blk + Geo::kVPar + (r + 8 * e) * Geo::kParRow);
+          }
+          if (part) {  // what no column sees may be anything
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (pos + r + 8 * e >= most)
+#pragma unroll
+                for (int g = 0; g < NG; ++g) kp[e][g] = vp[e][g] = 0;
           }
           float sc[NT][4];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[nt][e] = 0.0f;
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
             float d[NT][4];
@@ -325,121 +389,145 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
               for (int e = 0; e < 4; ++e) d[nt][e] = 0.0f;
 #pragma unroll
             for (int w = g * (G / 32); w < (g + 1) * (G / 32); ++w) {
-              const uint32_t a0[4] = {F::template key<0>(kw[0][w]), F::template key<0>(kw[1][w]),
-                                      F::template key<1>(kw[0][w]), F::template key<1>(kw[1][w])};
-              const uint32_t a1[4] = {F::template key<2>(kw[0][w]), F::template key<2>(kw[1][w]),
-                                      F::template key<3>(kw[0][w]), F::template key<3>(kw[1][w])};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                F::mma(d[nt], a0, qf[nt][4 * w], qf[nt][4 * w + 1]);
-                F::mma(d[nt], a1, qf[nt][4 * w + 2], qf[nt][4 * w + 3]);
+                mma_f16(d[nt], raw_pair<0>(kw[0][w]), raw_pair<0>(kw[1][w]), raw_pair<1>(kw[0][w]), raw_pair<1>(kw[1][w]),
+                        qf[nt][4 * w], qf[nt][4 * w + 1]);
+                mma_f16(d[nt], raw_pair<2>(kw[0][w]), raw_pair<2>(kw[1][w]), raw_pair<3>(kw[0][w]), raw_pair<3>(kw[1][w]),
+                        qf[nt][4 * w + 2], qf[nt][4 * w + 3]);
               }
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const uint32_t par = *reinterpret_cast<const uint32_t*>(blk + Geo::kKPar + (r + 8 * e) * Geo::kParRow + 4 * g);
-              const float ks = KvType<T>::lo(par), kc = fmaf(-F::kOffset, ks, KvType<T>::hi(par)), kk = ks * kappa;
+              const float ks = KvType<T>::lo(kp[e][g]), kc = fmaf(-8.0f, ks, KvType<T>::hi(kp[e][g]));
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
-                  sc[nt][2 * e + x] = fmaf(kk, d[nt][2 * e + x], fmaf(kc, qsum[nt][g][x], sc[nt][2 * e + x]));
+                for (int x = 0; x < 2; ++x) {
+                  const float z = g ? fmaf(kc, qsum[nt][g][x], sc[nt][2 * e + x]) : kc * qsum[nt][g][x];
+                  sc[nt][2 * e + x] = fmaf(ks, d[nt][2 * e + x], z);
+                }
             }
           }
-          if (pos + 16 > least) {
+          // exponents against the reference; it and E are raised where one passes it
+          float ex[NT][4];
+          auto exponents = [&]() {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (pos + r + 8 * (e >> 1) >= seen[nt][e & 1]) sc[nt][e] = -__int_as_float(0x7f800000);
-          }
-          // ---- the reference, raised where a score is far above it
-          bool raise = false;
+              for (int e = 0; e < 4; ++e) {
+                ex[nt][e] = fmaf(sc[nt][e], factor[nt][e & 1], -m[nt][e & 1]);
+                if (part && pos + r + 8 * (e >> 1) >= seen[nt][e & 1]) ex[nt][e] = -__int_as_float(0x7f800000);
+              }
+          };
+          exponents();
+          float vs[2][NG], vc[2][NG], big = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+              vs[e][g] = KvType<T>::lo(vp[e][g]);
+              vc[e][g] = KvType<T>::hi(vp[e][g]);
+              big = fmaxf(big, fmaf(8.0f, vs[e][g], fabsf(vc[e][g])));
+              if constexpr (!kCentred) vc[e][g] = fmaf(-8.0f, vs[e][g], vc[e][g]);
+            }
+          float top = big * vdown > kDecValues || vdown == 0.0f ? __int_as_float(0x7f800000) : ex[0][0];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) raise |= fmaxf(sc[nt][x], sc[nt][2 + x]) > m[nt][x] + F::kSlack;
-          if (__any_sync(0xffffffffu, raise)) {
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, ex[nt][e]);
+          if (__any_sync(0xffffffffu, top > kDecSlack)) {
+            const uint32_t vtop = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
+            const int need = (int)(vtop >> 23) - 127;
+            float fv = 1.0f;
+            if (vdown == 0.0f || need > vexp + 12) {  // about 2^5, room for 2^13
+              const int to = min(max(need - 5, -90), 120);
+              fv = vdown == 0.0f ? 0.0f : pow2(max(vexp - to, -126));
+              vexp = to;
+              vdown = pow2(-to);
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
-                float t = fmaxf(sc[nt][x], sc[nt][2 + x]);
+                float t = kNone;
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (!part || pos + r + 8 * e < seen[nt][x]) t = fmaxf(t, sc[nt][2 * e + x] * factor[nt][x]);
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-                t = fmaxf(t + F::kLift, m[nt][x]);
-                const float f = exp2_fast(m[nt][x] - t);
+                t = fmaxf(t, m[nt][x]);
+                const float f = exp2_fast(m[nt][x] - t), g2 = f * fv;
                 m[nt][x] = t;
                 l[nt][x] *= f;
 #pragma unroll
-                for (int g = 0; g < NG; ++g) oc[nt][g][x] *= f;
+                for (int g = 0; g < NG; ++g) oc[nt][g][x] *= g2;
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) {
-                  acc[j][nt][x] *= f;
-                  acc[j][nt][2 + x] *= f;
+                  acc[j][nt][x] *= g2;
+                  acc[j][nt][2 + x] *= g2;
                 }
               }
+            exponents();
           }
           // ---- weights, their sums, and P s as the second product's operand
           uint32_t pf[NT][NG][2];
-          float vs[2][NG], vc[2][NG];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
+          for (int e = 0; e < 2; ++e)
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-              const uint32_t par = *reinterpret_cast<const uint32_t*>(blk + Geo::kVPar + (r + 8 * e) * Geo::kParRow + 4 * g);
-              vs[e][g] = KvType<T>::lo(par);
-              vc[e][g] = KvType<T>::hi(par);
+              vs[e][g] *= vdown;
+              vc[e][g] *= vdown;
             }
-          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float pr[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) pr[e] = exp2_fast(sc[nt][e] - m[nt][e & 1]);
+            for (int e = 0; e < 4; ++e) pr[e] = exp2_fast(ex[nt][e]);
             l[nt][0] += pr[0] + pr[2];
             l[nt][1] += pr[1] + pr[3];
-            // a masked token's weight is 0, but its params may be anything: not multiplied
-            const bool part = pos + 16 > least;
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
               float y[4];
+              if (!part) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                y[e] = pr[e] * vs[e >> 1][g];
-                float z = pr[e] * vc[e >> 1][g];
-                if (part && pos + r + 8 * (e >> 1) >= seen[nt][e & 1]) y[e] = z = 0.0f;
-                oc[nt][g][e & 1] += z;
+                for (int e = 0; e < 4; ++e) {
+                  y[e] = pr[e] * vs[e >> 1][g];
+                  oc[nt][g][e & 1] = fmaf(pr[e], vc[e >> 1][g], oc[nt][g][e & 1]);
+                }
+              } else {  // zero times a poisoned centre is not zero: masked tokens are left out
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const bool sees = pos + r + 8 * (e >> 1) < seen[nt][e & 1];
+                  y[e] = sees ? pr[e] * vs[e >> 1][g] : 0.0f;
+                  if (sees) oc[nt][g][e & 1] = fmaf(pr[e], vc[e >> 1][g], oc[nt][g][e & 1]);
+                }
               }
-              pf[nt][g][0] = transpose8x8(KvType<T>::pack(y[0], y[1]));
-              pf[nt][g][1] = transpose8x8(KvType<T>::pack(y[2], y[3]));
+              pf[nt][g][0] = transpose8x8(KvType<__half>::pack(y[0], y[1]));
+              pf[nt][g][1] = transpose8x8(KvType<__half>::pack(y[2], y[3]));
             }
           }
           // ---- O^T += V^T P^T
-          const uint8_t* vb = blk + Geo::kVOff + c * Geo::kRow;
-          const int piece = (r ^ ((c >> 1) << 2)) * (D / 16);
+          const uint8_t* vb = blk + Geo::kVOff + c * Geo::kRow + (r ^ ((c >> 1) << 2)) * (D / 16);
           uint32_t vw[4][D / 64];  // tokens 2c, 2c + 1, 2c + 8, 2c + 9
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const uint8_t* src = vb + t * 4 * Geo::kRow + piece;
-            if constexpr (D == 128) {
-              const uint2 v = *reinterpret_cast<const uint2*>(src);
-              vw[t][0] = v.x, vw[t][1] = v.y;
-            } else {
-              vw[t][0] = *reinterpret_cast<const uint32_t*>(src);
-            }
-          }
+          for (int t = 0; t < 4; ++t) load_words(vw[t], vb + t * 4 * Geo::kRow);
 #pragma unroll
           for (int w = 0; w < D / 64; ++w) {
             const uint32_t lo0 = __byte_perm(vw[0][w], vw[1][w], 0x5410), hi0 = __byte_perm(vw[0][w], vw[1][w], 0x7632);
             const uint32_t lo1 = __byte_perm(vw[2][w], vw[3][w], 0x5410), hi1 = __byte_perm(vw[2][w], vw[3][w], 0x7632);
             auto tile = [&](auto k_) {
               constexpr int K = decltype(k_)::value;
-              const uint32_t av[4] = {F::template value<K>(lo0), F::template value<K>(hi0), F::template value<K>(lo1),
-                                      F::template value<K>(hi1)};
               const int j = 4 * w + K, g = j / (G / 16);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) F::mma(acc[j][nt], av, pf[nt][g][0], pf[nt][g][1]);
+              for (int nt = 0; nt < NT; ++nt) {
+                if constexpr (kCentred)
+                  mma_f16(acc[j][nt], centred_pair<K>(lo0), centred_pair<K>(hi0), centred_pair<K>(lo1), centred_pair<K>(hi1),
+                          pf[nt][g][0], pf[nt][g][1]);
+                else
+                  mma_f16(acc[j][nt], raw_pair<K>(lo0), raw_pair<K>(hi0), raw_pair<K>(lo1), raw_pair<K>(hi1), pf[nt][g][0],
+                          pf[nt][g][1]);
+              }
             };
             tile(std::integral_constant<int, 0>());
             tile(std::integral_constant<int, 1>());
@@ -453,6 +541,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
       }
 
       // ---- join the warps: O of this warp with its centres' part, then all of them
+      const float mid = pow2(vexp - kDecDown), even = mid * (kCentred ? 1.0f : 0x1p24f), odd = even * (kCentred ? 1.0f : 0.0625f);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -461,9 +550,11 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], o);
 #pragma unroll
-          for (int g = 0; g < NG; ++g)
+          for (int g = 0; g < NG; ++g) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) oc[nt][g][x] += __shfl_xor_sync(0xffffffffu, oc[nt][g][x], o);
+            oc[nt][g][x] *= mid;
+          }
           if (r == 0) {
             mm[warp * C + col] = m[nt][x];
             ml[warp * C + col] = l[nt][x];
@@ -472,7 +563,9 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
             const int g = j / (G / 16), ch = g * G + r * (G / 8) + 2 * j % (G / 8);
-            *reinterpret_cast<float2*>(dst + ch) = make_float2(acc[j][nt][x] + oc[nt][g][x], acc[j][nt][2 + x] + oc[nt][g][x]);
+            const float f = j % 2 ? odd : even;
+            *reinterpret_cast<float2*>(dst + ch) =
+                make_float2(fmaf(acc[j][nt][x], f, oc[nt][g][x]), fmaf(acc[j][nt][2 + x], f, oc[nt][g][x]));
           }
         }
       __syncthreads();
@@ -483,7 +576,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
         const int x = ct * C + col;
         if (x >= ncols) return;
         const int i = row_lo + x / p.per, hq = h * p.per + x % p.per;
-        const float inv = L == 0.0f ? 0.0f : 1.0f / L;  // a row that sees nothing is zero
+        const float inv = L == 0.0f ? 0.0f : pow2(kDecDown) / L;  // a row that sees nothing is zero
         *reinterpret_cast<uint2*>(a.out + kv_row_offset(a.b, a.os, s, q.row0, i) + (int64_t)hq * a.os.head + 4 * d4) =
             make_uint2(KvType<T>::pack(o.x * inv, o.y * inv), KvType<T>::pack(o.z * inv, o.w * inv));
         if (a.lse && d4 == 0)
@@ -526,11 +619,12 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
         if (sh_last == (unsigned)(c1 - c0)) {
           __threadfence();
           // the item began c0's last stretch: its only one if the item begins c0's share
-          const int head = 2 * c0 + (cc.item0 == total * c0 / n ? 0 : 1);
+          const int head = 2 * c0 + (cc.item0 == share(total, c0, n) ? 0 : 1);
           for (int x = tid; x < C * (D / 4); x += kDecWarps * 32) {
             const int col = x / (D / 4), d4 = x % (D / 4);
             float M = kNone, L = 0.0f;
             float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
             for (int y = c0; y <= c1; ++y) M = fmaxf(M, __ldcg(ws + (int64_t)(y == c0 ? head : 2 * y) * kSlot + C * D + col));
 #pragma unroll 4
             for (int y = c0; y <= c1; ++y) {
@@ -553,9 +647,9 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
     }
   }
 
-  // ---- groups without a unit: their rows see nothing
+  // ---- groups without a round: their rows see nothing
   for (int gi = me; gi < p.groups; gi += gridDim.x) {
-    if (group_units(a, gi)) continue;
+    if (group_rounds(a, gi)) continue;
     const int s = a.sel ? gi / a.b.max_new : gi;
     const KvSeq q = kv_seq(a.b, s);
     const int lo = a.sel ? gi % a.b.max_new : 0, hi = a.sel ? min(lo + 1, q.rows) : q.rows;
@@ -593,9 +687,12 @@ cudaError_t decode(Kv& kv, const KvAttnArgs& a, cudaStream_t s) {
   const int nt = cols > 8 ? 2 : 1;
   p.groups = (int)groups;
   p.ctiles = (int)((cols + 8 * nt - 1) / (8 * nt));
-  if ((int64_t)p.ctiles * a.c.heads > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  p.items = p.ctiles * a.c.heads;
-  p.min_units = 8;
+  const int64_t items = (int64_t)p.ctiles * a.c.heads;
+  const int64_t blocks = (int64_t)(a.sel ? a.budget : a.b.table_pages) << (a.c.page_shift - 4);
+  if (items > 0x7fffffff || groups * items > 0x7fffffff / ((blocks + kDecWarps - 1) / kDecWarps))
+    return cudaErrorInvalidConfiguration;  // rounds are numbered in 32 bits
+  p.items = (int)items;
+  p.min_rounds = 1;
   cudaError_t e = cudaErrorInvalidValue;
   const int dg = kv.d.head_dim * 1000 + kv.d.group_size;
 #define KV_CASE(DD, GG)                                                        \

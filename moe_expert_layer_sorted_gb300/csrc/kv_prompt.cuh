@@ -151,15 +151,11 @@ __device__ __forceinline__ uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c
   return d;
 }
 
-// 2^e, e in -126..127
-__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
-
 // The eight stored values of a word in channel order, in fp16; par: step and centre as fp16.
 __device__ __forceinline__ uint4 values8(uint32_t w, uint32_t par) {
-  using F = Frag<__half>;
   const uint32_t s2 = __byte_perm(par, par, 0x1010), c2 = __byte_perm(par, par, 0x3232);
-  return make_uint4(fma_half2(F::template value<0>(w), s2, c2), fma_half2(F::template value<1>(w), s2, c2),
-                    fma_half2(F::template value<2>(w), s2, c2), fma_half2(F::template value<3>(w), s2, c2));
+  return make_uint4(fma_half2(centred_pair<0>(w), s2, c2), fma_half2(centred_pair<1>(w), s2, c2),
+                    fma_half2(centred_pair<2>(w), s2, c2), fma_half2(centred_pair<3>(w), s2, c2));
 }
 
 struct PromptArgs {
@@ -264,7 +260,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
     const int64_t x = x0 + t * kPrTile + quad * 32 + lane;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const uint32_t ts = tm + t * kPrTile + lanes, to = tm + 2 * kPrTile + t * D + lanes;
-    const int seen = x < nx ? seen_of(x) : 0;
+    const int seen = x < nx ? seen_of(x) : most;  // rows past the last (zeros, not written) ask for no masks
     const float kappa = a.scale * 1.4426950408889634f * sh_qscale[t * kPrTile + quad * 32 + lane];
     const uint64_t kappa2 = pair2(kappa, kappa);
     float m = kNone;
@@ -274,6 +270,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
     for (int j = 0; j < (t == 0 || two ? ntiles : 0); ++j) {
       mbar_wait<false>(smem_addr(&sFull[t]), (uint32_t)j & 1u, p.err);
       fence_after();
+      uint32_t v[2][32];  // asked for before what the tile needs is known: nearly always the unmasked pass
+      tmem_ld32(ts, v[0]);
       const uint4 valid4 = sh_valid[j & 3], poison4 = sh_poison[j & 3], scaled4 = sh_scaled[j & 3];
       const bool scaled = (scaled4.x | scaled4.y | scaled4.z | scaled4.w) != 0;
       const uint32_t valid[4] = {valid4.x, valid4.y, valid4.z, valid4.w};
@@ -328,8 +326,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
       if (!raise) {  // weights against the reference as it stands
         if (plain) {
           const uint64_t neg = pair2(-m, -m);
-          uint32_t v[2][32];
-          tmem_ld32(ts, v[0]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {  // the next 32 scores arrive while these are worked on
             tmem_wait_ld();
@@ -596,8 +592,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
       fence_after();
       for (int t = 0; t < nt; ++t) scores(t, 0);
       for (int j = 0; j < ntiles; ++j) {
+        // both operands of this round are usually there long before the weights
+        mbar_wait<false>(smem_addr(&vFull[j & 1]), (uint32_t)(j >> 1) & 1u, p.err);
+        if (j + 1 < ntiles) mbar_wait<false>(smem_addr(&kFull[(j + 1) & 1]), (uint32_t)((j + 1) >> 1) & 1u, p.err);
         for (int t = 0; t < nt; ++t) {
-          if (t == 0) mbar_wait<false>(smem_addr(&vFull[j & 1]), (uint32_t)(j >> 1) & 1u, p.err);
           mbar_wait<false>(smem_addr(&pFull[t]), (uint32_t)j & 1u, p.err);
           fence_after();
           const uint32_t vb = sv + (j & 1) * kTileBytes;
@@ -605,13 +603,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
           for (int k = 0; k < kPrTile / 16; ++k)
             mma_ts(leader, tm + 2 * kPrTile + t * D, tm + t * kPrTile + 8 * k, desc_mn(vb + k * 2048), ido, (j | k) ? 1u : 0u);
           if (t == nt - 1) commit(leader, &vEmpty[j & 1]);
-          if (j + 1 < ntiles) {
-            if (t == 0) {
-              mbar_wait<false>(smem_addr(&kFull[(j + 1) & 1]), (uint32_t)((j + 1) >> 1) & 1u, p.err);
-              fence_after();
-            }
-            scores(t, j + 1);
-          }
+          if (j + 1 < ntiles) scores(t, j + 1);
         }
       }
       commit(leader, &oFull);
