@@ -6,12 +6,22 @@
 // run and can be checked to the bit.  The first and the last pages are always
 // taken, then the highest scores, ties to the lower page; a NaN score counts
 // as minus infinity.
+//
+// Scoring streams the bounds (2 D values per page and head); picking works on
+// the scores' order-preserving keys: the value of the last key that is taken by
+// bisection, then one ordered pass.  Rows with few pages do both in one CTA per
+// row and head (keys in shared memory); otherwise the pages of a row are spread
+// over CTAs first and a second kernel picks.
 #include "kv_internal.h"
 
 using namespace moe;
 
 namespace {
 
+constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
+constexpr int kSelPages = 64;     // pages per scoring CTA
+constexpr int kSelHeads = 16;     // kv heads per scoring CTA
+constexpr int kSelOwn = 512;      // rows with at most this many pages are scored and picked by one CTA
 constexpr uint32_t kAlways = 0xffffffffu;  // above the key of +infinity
 
 // Order-preserving key of a score (-0 and +0 equal), NaN as -infinity.
@@ -26,123 +36,261 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
-// One CTA of 256 threads per (row, head) of the rows first_row ..: scores into
-// keys, the budget-th largest key by four 8-bit radix passes, then the list in
-// ascending page order.
+struct Row {
+  int s, i;
+  KvSeq q;
+  int pages;  // pages the row sees
+};
+__device__ __forceinline__ Row row_of(const KvSelectArgs& a, int64_t r) {
+  Row w;
+  w.s = (int)(r / a.b.max_new);
+  w.i = (int)(r % a.b.max_new);
+  w.q = kv_seq(a.b, w.s);
+  const int64_t pos = min((int64_t)w.q.len - w.q.rows + w.i, (int64_t)kv_capacity(a.c, a.b) - 1);
+  w.pages = w.i >= w.q.rows || pos < 0 ? 0 : (int)(pos >> a.c.page_shift) + 1;
+  return w;
+}
+
+// qs[d] of one head.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) kv_select_kernel(KvSelectArgs a, int64_t first_row, uint32_t* keys_all) {
-  constexpr int C = D / 32;  // channels per lane
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t sh_prefix, sh_need;
-  __shared__ int wsum[2][8];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.x % a.c.heads;
-  const int64_t r = first_row + blockIdx.x / a.c.heads;
-  const int s = (int)(r / a.b.max_new), i = (int)(r % a.b.max_new);
-  const KvSeq q = kv_seq(a.b, s);
-  if (i >= q.rows) return;
-  const int64_t pos = min((int64_t)q.len - q.rows + i, (int64_t)kv_capacity(a.c, a.b) - 1);
-  const int n = pos < 0 ? 0 : (int)(pos >> a.c.page_shift) + 1;  // pages the row sees
-  int32_t* out = a.out + (kv_row_index(a.b, s, q.row0, i) * a.c.heads + h) * a.budget;
-  if (n <= a.budget) {
-    for (int x = tid; x < a.budget; x += 256) out[x] = x < n ? x : -1;
-    return;
-  }
-  uint32_t* keys = keys_all + (int64_t)blockIdx.x * a.b.table_pages;
+__device__ __forceinline__ void head_sum(const KvSelectArgs& a, const Row& w, int h, int d, float* qs) {
   const int per = a.q_heads / a.c.heads;
-  const uint16_t* qr = a.q + kv_row_offset(a.b, a.qs, s, q.row0, i) + (int64_t)h * per * a.qs.head + C * lane;
-  float qs[C];
+  const uint16_t* src = a.q + kv_row_offset(a.b, a.qs, w.s, w.q.row0, w.i) + (int64_t)h * per * a.qs.head + d;
+  float v = KvType<T>::to_f(src[0]);
+#pragma unroll 4
+  for (int x = 1; x < per; ++x) v = __fadd_rn(v, KvType<T>::to_f(src[x * a.qs.head]));
+  qs[d] = v;
+}
+
+// Score of a page and head by D / 8 neighbouring lanes, eight channels each.
+template <typename T, int D>
+__device__ __forceinline__ float page_score(const float* qs, uint4 hi, uint4 lo) {
+  constexpr int L = D / 8;
+  const int l = threadIdx.x % L;
+  const float4 q0 = *reinterpret_cast<const float4*>(qs + 8 * l), q1 = *reinterpret_cast<const float4*>(qs + 8 * l + 4);
+  const float q[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+  const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, o[4] = {lo.x, lo.y, lo.z, lo.w};
+  float v[8];
 #pragma unroll
-  for (int c = 0; c < C; ++c) qs[c] = KvType<T>::to_f(qr[c]);
-  for (int x = 1; x < per; ++x)
-#pragma unroll
-    for (int c = 0; c < C; ++c) qs[c] = __fadd_rn(qs[c], KvType<T>::to_f(qr[x * a.qs.head + c]));
-  for (int j = warp; j < n; j += 8) {
-    uint32_t key = kAlways;
-    if (j >= a.first && j < n - a.last) {
-      float sc = -__int_as_float(0x7f800000);
-      const int64_t pid = kv_page(a.c, a.b, s, j);
-      if (pid >= 0) {
-        const uint16_t* ends = a.c.bounds + (pid * a.c.heads + h) * (2 * D) + C * lane;
-        float v[C];
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-          v[c] = max_nan(__fmul_rn(qs[c], KvType<T>::to_f(ends[c])), __fmul_rn(qs[c], KvType<T>::to_f(ends[D + c])));
-#pragma unroll
-        for (int st = 1; st < C; st <<= 1)
-#pragma unroll
-          for (int c = 0; c < C; c += 2 * st) v[c] = __fadd_rn(v[c], v[c + st]);
-        sc = v[0];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) sc = __fadd_rn(sc, __shfl_xor_sync(0xffffffffu, sc, o));
-      }
-      key = score_key(sc);
-    }
-    if (lane == 0) keys[j] = key;
+  for (int e = 0; e < 4; ++e) {
+    v[2 * e] = max_nan(__fmul_rn(q[2 * e], KvType<T>::lo(h[e])), __fmul_rn(q[2 * e], KvType<T>::lo(o[e])));
+    v[2 * e + 1] = max_nan(__fmul_rn(q[2 * e + 1], KvType<T>::hi(h[e])), __fmul_rn(q[2 * e + 1], KvType<T>::hi(o[e])));
   }
-  if (tid == 0) {
-    sh_prefix = 0;
-    sh_need = (uint32_t)a.budget;
+  float s = __fadd_rn(__fadd_rn(__fadd_rn(v[0], v[1]), __fadd_rn(v[2], v[3])),
+                      __fadd_rn(__fadd_rn(v[4], v[5]), __fadd_rn(v[6], v[7])));
+#pragma unroll
+  for (int x = 1; x < L; x <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, x));
+  return s;
+}
+
+// Keys of pages [j0, j1) and heads [h0, h1) of a row: units (page, head), heads
+// fastest as the bounds lie, D / 8 lanes a unit, four units of each asked for at once.
+// qs: [head - h0][D]; keys[(head - h0) * stride + page - j0].
+template <typename T, int D>
+__device__ __forceinline__ void score_pages(const KvSelectArgs& a, const Row& w, int j0, int j1, int h0, int h1,
+                                            const float* qs, uint32_t* keys, int64_t stride) {
+  constexpr int L = D / 8, kGroups = kSelThreads / L, kUnroll = 4;
+  const int l = threadIdx.x % L, grp = threadIdx.x / L, nh = h1 - h0;
+  const int units = (j1 - j0) * nh;
+  for (int u0 = 0; u0 < units; u0 += kGroups * kUnroll) {
+    uint4 hi[kUnroll], lo[kUnroll];
+    bool ok[kUnroll];
+#pragma unroll
+    for (int x = 0; x < kUnroll; ++x) {
+      const int u = u0 + x * kGroups + grp;
+      ok[x] = false;
+      if (u < units) {
+        const int j = j0 + u / nh, h = h0 + u % nh;
+        const int64_t pid = kv_page(a.c, a.b, w.s, j);
+        ok[x] = pid >= 0;
+        if (ok[x]) {
+          const uint4* ends = reinterpret_cast<const uint4*>(a.c.bounds + (pid * a.c.heads + h) * (2 * D));
+          hi[x] = __ldg(ends + l);
+          lo[x] = __ldg(ends + L + l);
+        }
+      }
+      if (!ok[x]) hi[x] = lo[x] = make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int x = 0; x < kUnroll; ++x) {
+      const int u = u0 + x * kGroups + grp;
+      const int j = j0 + u / nh, h = u % nh;
+      const float s = page_score<T, D>(qs + h * D, hi[x], lo[x]);
+      if (l == 0 && u < units)
+        keys[h * stride + j - j0] =
+            j < a.first || j >= w.pages - a.last ? kAlways : score_key(ok[x] ? s : -__int_as_float(0x7f800000));
+    }
+  }
+}
+
+// Inclusive prefix sum of v over the CTA.
+__device__ __forceinline__ int cta_scan(int v, int* sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
   }
   __syncthreads();
-  for (int shift = 24; shift >= 0; shift -= 8) {  // the budget-th largest key, byte by byte
-    hist[tid] = 0;
-    __syncthreads();
-    const uint32_t prefix = sh_prefix, mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-    for (int j = tid; j < n; j += 256)
-      if ((keys[j] & mask) == prefix) atomicAdd(&hist[(keys[j] >> shift) & 255u], 1u);
-    __syncthreads();
-    if (tid == 0) {
-      uint32_t need = sh_need;
-      int bin = 255;
-      while (bin > 0 && hist[bin] < need) need -= hist[bin--];
-      sh_prefix = prefix | (uint32_t)bin << shift;
-      sh_need = need;
+  if (lane == 31) sh[warp] = v;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w)
+    if (w < warp) v += sh[w];
+  return v;
+}
+
+// The list of a row and head from its n > budget keys.
+__device__ __forceinline__ void pick(const KvSelectArgs& a, const uint32_t* keys, int n, int32_t* out) {
+  __shared__ uint32_t sh_lo[kSelWarps], sh_hi[kSelWarps];
+  __shared__ int sh_cnt[2][kSelWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int need = a.budget - a.first - a.last;  // pages to take by score
+  uint32_t tau = kAlways - 1;              // keys above are taken, and `need` of those equal, lowest pages first
+  if (need > 0) {
+    uint32_t lo = kAlways, hi = 0;  // of the keys that count
+    for (int j = tid; j < n; j += kSelThreads) {
+      const uint32_t k = keys[j];
+      if (k != kAlways) {
+        lo = min(lo, k);
+        hi = max(hi, k);
+      }
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+      sh_lo[warp] = lo;
+      sh_hi[warp] = hi;
     }
     __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w) {
+      lo = min(lo, sh_lo[w]);
+      hi = max(hi, sh_hi[w]);
+    }
+    // at least `need` keys are >= lo, fewer are > hi; above: how many are > hi
+    int above = 0;
+    for (int it = 0; lo < hi; it ^= 1) {
+      const uint32_t mid = lo + (hi - lo + 1) / 2;
+      int c = 0;
+#pragma unroll 4
+      for (int j = tid; j < n; j += kSelThreads) {
+        const uint32_t k = keys[j];
+        c += k >= mid && k != kAlways;
+      }
+      c = __reduce_add_sync(0xffffffffu, c);
+      if (lane == 0) sh_cnt[it][warp] = c;  // two buffers: one barrier per step
+      __syncthreads();
+      c = 0;
+#pragma unroll
+      for (int w = 0; w < kSelWarps; ++w) c += sh_cnt[it][w];
+      if (c >= need) {
+        lo = mid;
+        if (c == need) {  // exactly the keys from mid on
+          above = need;
+          hi = lo = mid - 1;
+        }
+      } else {
+        hi = mid - 1;
+        above = c;
+      }
+    }
+    tau = lo;
+    need -= above;
   }
-  const uint32_t tau = sh_prefix;
-  int left = (int)sh_need, done = 0;  // keys equal to tau still to take; entries written
-  for (int base = 0; base < n; base += 256) {
-    const int j = base + tid;
-    const uint32_t key = j < n ? keys[j] : 0u;
-    const bool eq = j < n && key == tau;
-    const uint32_t beq = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) wsum[0][warp] = __popc(beq);
-    __syncthreads();
-    int before = __popc(beq & ((1u << lane) - 1u)), all = 0;
-    for (int x = 0; x < 8; ++x) {
-      before += x < warp ? wsum[0][x] : 0;
-      all += wsum[0][x];
-    }
-    const bool take = j < n && (key > tau || (eq && before < left));
-    const uint32_t bt = __ballot_sync(0xffffffffu, take);
-    if (lane == 0) wsum[1][warp] = __popc(bt);
-    __syncthreads();
-    int at = done + __popc(bt & ((1u << lane) - 1u)), sum = 0;
-    for (int x = 0; x < 8; ++x) {
-      at += x < warp ? wsum[1][x] : 0;
-      sum += wsum[1][x];
-    }
-    if (take) out[at] = j;
-    done += sum;
-    left = max(left - all, 0);
+  // every thread takes a run of pages: ranks of the keys equal to tau, then places in the list
+  const int run = (n + kSelThreads - 1) / kSelThreads;
+  const int b = min(tid * run, n), e = min(b + run, n);
+  int eq = 0, gt = 0;
+  for (int j = b; j < e; ++j) {
+    eq += keys[j] == tau;
+    gt += keys[j] > tau;
   }
+  int rank = cta_scan(eq, sh_cnt[0]) - eq;
+  const int taken = gt + min(eq, max(need - rank, 0));
+  int at = cta_scan(taken, sh_cnt[1]) - taken;
+  for (int j = b; j < e; ++j) {
+    const uint32_t k = keys[j];
+    if (k > tau || (k == tau && rank++ < need)) out[at++] = j;
+  }
+}
+
+__device__ __forceinline__ int32_t* list_of(const KvSelectArgs& a, const Row& w, int h) {
+  return a.out + (kv_row_index(a.b, w.s, w.q.row0, w.i) * a.c.heads + h) * a.budget;
+}
+// All pages, where they are no more than the budget.
+__device__ __forceinline__ void list_all(const KvSelectArgs& a, const Row& w, int32_t* out) {
+  for (int x = threadIdx.x; x < a.budget; x += kSelThreads) out[x] = x < w.pages ? x : -1;
+}
+
+// One CTA per (row, head): scores and choice.
+template <typename T, int D>
+__global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_constant__ KvSelectArgs a) {
+  __shared__ __align__(16) float qs[D];
+  __shared__ uint32_t keys[kSelOwn];
+  const int h = blockIdx.x % a.c.heads;
+  const Row w = row_of(a, blockIdx.x / a.c.heads);
+  if (w.i >= w.q.rows) return;
+  int32_t* out = list_of(a, w, h);
+  if (w.pages <= a.budget) return list_all(a, w, out);
+  if (threadIdx.x < D) head_sum<T, D>(a, w, h, threadIdx.x, qs);
+  __syncthreads();
+  score_pages<T, D>(a, w, 0, w.pages, h, h + 1, qs, keys, 0);
+  __syncthreads();
+  pick(a, keys, w.pages, out);
+}
+
+// Scores: one CTA per (row, kSelPages pages, kSelHeads heads).
+template <typename T, int D>
+__global__ void __launch_bounds__(kSelThreads) kv_score_kernel(const __grid_constant__ KvSelectArgs a, int64_t first_row,
+                                                               int chunks, uint32_t* __restrict__ keys) {
+  __shared__ __align__(16) float qs[kSelHeads * D];
+  const int64_t r = blockIdx.x / chunks;
+  const Row w = row_of(a, first_row + r);
+  const int j0 = blockIdx.x % chunks * kSelPages, j1 = min(j0 + kSelPages, w.pages);
+  if (w.pages <= a.budget || j0 >= j1) return;
+  const int h0 = blockIdx.y * kSelHeads, h1 = min(h0 + kSelHeads, a.c.heads);
+  for (int x = threadIdx.x; x < (h1 - h0) * D; x += kSelThreads) head_sum<T, D>(a, w, h0 + x / D, x % D, qs + x / D * D);
+  __syncthreads();
+  score_pages<T, D>(a, w, j0, j1, h0, h1, qs, keys + (r * a.c.heads + h0) * a.b.table_pages + j0, a.b.table_pages);
+}
+// ... and the choice: one CTA per (row, head).
+__global__ void __launch_bounds__(kSelThreads) kv_pick_kernel(const __grid_constant__ KvSelectArgs a, int64_t first_row,
+                                                              const uint32_t* __restrict__ keys) {
+  const int h = blockIdx.x % a.c.heads;
+  const Row w = row_of(a, first_row + blockIdx.x / a.c.heads);
+  if (w.i >= w.q.rows) return;
+  if (w.pages <= a.budget) return list_all(a, w, list_of(a, w, h));
+  pick(a, keys + (int64_t)blockIdx.x * a.b.table_pages, w.pages, list_of(a, w, h));
+}
+
+template <typename T, int D>
+cudaError_t select(Kv& kv, const KvSelectArgs& a, cudaStream_t s) {
+  const int64_t rows = (int64_t)a.b.batch * a.b.max_new;
+  if (a.b.table_pages <= kSelOwn) {
+    if (rows * a.c.heads > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    kv_select_kernel<T, D><<<(unsigned)(rows * a.c.heads), kSelThreads, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+  uint32_t* keys = reinterpret_cast<uint32_t*>(kv.ws);
+  const int chunks = (a.b.table_pages + kSelPages - 1) / kSelPages;
+  const int64_t step = std::min<int64_t>((int64_t)(Kv::kScoreBytes / 4) / ((int64_t)a.c.heads * a.b.table_pages),
+                                         0x7fffffff / std::max(chunks, a.c.heads));
+  const unsigned head_tiles = (unsigned)((a.c.heads + kSelHeads - 1) / kSelHeads);
+  for (int64_t r = 0; r < rows; r += step) {  // as many rows at a time as the workspace holds scores for
+    const int64_t n = std::min(step, rows - r);
+    kv_score_kernel<T, D><<<dim3((unsigned)(n * chunks), head_tiles), kSelThreads, 0, s>>>(a, r, chunks, keys);
+    kv_pick_kernel<<<(unsigned)(n * a.c.heads), kSelThreads, 0, s>>>(a, r, keys);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
 
 cudaError_t moe::kv_select(Kv& kv, const KvSelectArgs& a, cudaStream_t s) {
-  const int64_t per_row = (int64_t)a.c.heads * a.b.table_pages;  // keys
-  const int64_t rows = (int64_t)a.b.batch * a.b.max_new;
-  const int64_t step = std::min<int64_t>((int64_t)(Kv::kScoreBytes / 4) / per_row, 0x7fffffff / a.c.heads);
-  for (int64_t r = 0; r < rows; r += step) {
-    const unsigned ctas = (unsigned)(std::min(step, rows - r) * a.c.heads);
-    KV_DISPATCH(kv.d, {
-      kv_select_kernel<T, D><<<ctas, 256, 0, s>>>(a, r, reinterpret_cast<uint32_t*>(kv.ws));
-    });
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  if (kv.d.dtype == MOE_KV_BF16)
+    return kv.d.head_dim == 128 ? select<__nv_bfloat16, 128>(kv, a, s) : select<__nv_bfloat16, 64>(kv, a, s);
+  return kv.d.head_dim == 128 ? select<__half, 128>(kv, a, s) : select<__half, 64>(kv, a, s);
 }
