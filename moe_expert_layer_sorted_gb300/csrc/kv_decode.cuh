@@ -25,9 +25,11 @@
 //
 // Work split: all rounds (8 blocks of 16 tokens of one kv head and column tile)
 // of the batch in one line, cut into equal shares, one per CTA; a share covers
-// any number of items (sequence, head, column tile) or part of one.  In a round
-// each of the 8 warps takes one block, through a ring of its own, each block
-// one bulk copy.  At the end of an item's stretch the warps' (max, sum, O) are
+// any number of items (sequence, head, column tile) or part of one.  Rounds come
+// through a ring in shared memory, one bulk copy per page (or its 128 tokens);
+// each of the 8 warps takes one block of a round.  The warps fetch in turn, warp
+// w every eighth round, its page numbers asked for eight rounds ahead: what a
+// fetch costs is paid once per 8 blocks, and no warp is set aside for it.  At the end of an item's stretch the warps' (max, sum, O) are
 // joined in shared memory; an item cut between CTAs is joined by the CTA that
 // finishes last, in the order of the CTAs, so results do not depend on timing.
 #pragma once
@@ -125,21 +127,22 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
   constexpr int kStages = kDecStages<D, G>;
   constexpr int kSlot = C * (D + 2);  // floats of one partial result: O [C][D], max [C], sum [C]
   extern __shared__ __align__(128) uint8_t smem[];
-  float* mo = reinterpret_cast<float*>(smem + kDecWarps * kStages * Geo::kBytes);  // [warp][C][D + 4]; below: [warp][stage][block]
+  float* mo = reinterpret_cast<float*>(smem + kDecWarps * kStages * Geo::kBytes);  // [warp][C][D + 4]; below: [stage][block]
   float* mm = mo + kDecWarps * C * (D + 4);                                     // [warp][C] max, then sums
   float* ml = mm + kDecWarps * C;
-  uint64_t* bars_all = reinterpret_cast<uint64_t*>(ml + kDecWarps * C);         // [warp][stage]
-  int* spos_all = reinterpret_cast<int*>(bars_all + kDecWarps * kStages);       // [warp][stage] position of a block, -1: none
+  uint64_t* full = reinterpret_cast<uint64_t*>(ml + kDecWarps * C);             // [stage]
+  uint64_t* empty = full + kStages;                                             // [stage]
+  int* spos = reinterpret_cast<int*>(empty + kStages);                          // [stage][block] its position, -1: not there
   __shared__ int sh_sum[kDecWarps];
   __shared__ int sh_base, sh_group;
   __shared__ unsigned sh_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
-  uint8_t* ring = smem + (size_t)warp * kStages * Geo::kBytes;
-  uint64_t* bars = bars_all + warp * kStages;
-  volatile int* spos = spos_all + warp * kStages;
 
-  if (lane < kStages) mbar_init(smem_addr(&bars[lane]), 1);
+  if (tid < kStages) {
+    mbar_init(smem_addr(&full[tid]), 1);
+    mbar_init(smem_addr(&empty[tid]), kDecWarps);
+  }
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 
   // ---- the CTA's share: the sum of all rounds, and the group its first round lies in
@@ -197,70 +200,68 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
     seed.end = sh_base;
     seed.rounds = 0;
 
-    // ---- the producer side: block `warp` of each round
+    // ---- fetching: this warp's rounds are first + warp, + 8, ...; lane b < 8 looks after block b
     Cursor pc = seed;
     pc.item_end = 0;
     const int per_page = a.c.page_shift - 4;
-    int pu = first;
-    int ppos = -1;                     // position of round pu's block (-1: nothing to read)
-    int pid = -1;                      // its page, requested a round ahead of its copy
-    int pblk = 0;                      // its block of the page
-    const int32_t* ptable = nullptr;   // the sequence's table
-    const int32_t* plist = nullptr;    // the chosen pages
-    const uint8_t* phead = nullptr;
-    int pseen = 0;                     // positions from here on are not read
-    auto locate = [&]() {
+    const int run = min(1 << per_page, kDecWarps);  // blocks per copy
+    int pu = first + warp;
+    int ppos = 0, pid = -1;           // position and page of the block
+    int pseen = 0;                    // positions from here on are not read
+    const int32_t* ptable = nullptr;  // the sequence's table
+    const int32_t* plist = nullptr;   // the chosen pages
+    int phead = 0;
+    auto look = [&]() {  // asks for the pages of round pu
+      if (pu >= last) return;
       if (pu >= pc.item_end) {
-        if (pu >= last) return;
         pc.enter(a, p, pu);
-        const int h = pc.item / p.ctiles;
+        phead = pc.item / p.ctiles;
         int s = pc.group;
         if (a.sel) {
           s = pc.group / a.b.max_new;
           const KvSeq q = kv_seq(a.b, s);
           const int i = pc.group % a.b.max_new;
-          plist = a.sel + (kv_row_index(a.b, s, q.row0, i) * a.c.heads + h) * a.budget;
+          plist = a.sel + (kv_row_index(a.b, s, q.row0, i) * a.c.heads + phead) * a.budget;
           pseen = (int)min(a.causal ? (int64_t)q.len - q.rows + i + 1 : (int64_t)q.len, (int64_t)kv_capacity(a.c, a.b));
         } else {
           pseen = min(kv_seq(a.b, s).len, kv_capacity(a.c, a.b));
         }
         ptable = a.b.table + (int64_t)s * a.b.table_stride;
-        phead = a.c.pages + h * a.c.head_stride;
       }
-      const int ub = (pu - pc.item0) * kDecWarps + warp;
+      const int ub = (pu - pc.item0) * kDecWarps + lane;
       int j = ub >> per_page;
-      pblk = ub & ((1 << per_page) - 1);
       ppos = ub * 16;
       if (a.sel) {
         j = j < a.budget ? plist[j] : -1;
         // pages beyond the row's are skipped (compared as pages: positions could wrap)
-        if (j < 0 || j > (pseen - 1) >> a.c.page_shift) j = -1;
-        ppos = (j << a.c.page_shift) + 16 * pblk;
-        if (j < 0) ppos = 0x7fffffff;
+        const bool in = j >= 0 && j <= (pseen - 1) >> a.c.page_shift;
+        ppos = in ? (j << a.c.page_shift) + 16 * (ub & ((1 << per_page) - 1)) : 0x7fffffff;
       }
-      pid = -1;
-      if (ppos < pseen) pid = ptable[j];
+      pid = lane < kDecWarps && ppos < pseen ? ptable[j] : -1;
     };
-    auto issue = [&](int slot) {
+    auto fetch = [&](int stage) {  // copies round pu into a free stage
       if (pu >= last) return;
-      const bool ok = ppos < pseen && (uint32_t)pid < (uint32_t)a.c.num_pages;
-      if (lane == 0) {
-        spos[slot] = ok ? ppos : -1;
-        if (ok) {
-          const uint32_t bar = smem_addr(&bars[slot]);
-          mbar_arrive_expect_tx(bar, Geo::kBytes);
-          bulk_g2s(smem_addr(ring + slot * Geo::kBytes),
-                   phead + (int64_t)pid * a.c.page_stride + pblk * Geo::kBytes, Geo::kBytes, bar);
-        }
-      }
-      ++pu;
-      locate();
+      const bool ok = lane < kDecWarps && ppos < pseen && (uint32_t)pid < (uint32_t)a.c.num_pages;
+      const uint32_t there = __ballot_sync(0xffffffffu, ok);
+      if (lane < kDecWarps) spos[stage * kDecWarps + lane] = ok ? ppos : -1;
+      __syncwarp();
+      const uint32_t bar = smem_addr(&full[stage]);
+      if (lane == 0) mbar_arrive_expect_tx(bar, __popc(there) * Geo::kBytes);
+      __syncwarp();
+      // the blocks of a page that are there are its first ones: one copy
+      const int count = __popc(there >> lane & ((1u << run) - 1u));
+      if (ok && lane % run == 0)
+        bulk_g2s(smem_addr(smem) + (stage * kDecWarps + lane) * Geo::kBytes,
+                 a.c.pages + (int64_t)pid * a.c.page_stride + phead * a.c.head_stride +
+                     (int64_t)((ppos & (a.c.page_size - 1)) >> 4) * Geo::kBytes,
+                 count * Geo::kBytes, bar);
+      pu += kDecWarps;
+      look();
     };
-    locate();
-#pragma unroll 1
-    for (int q = 0; q < kStages; ++q) issue(q);
-    int slot = 0;
-    uint32_t phases = 0;  // bit q: the parity slot q's next copy completes
+    look();
+    if (warp < kStages - 1) fetch(warp);
+    int stage = 0;         // of the round at hand
+    uint32_t parity = 0;   // of its fill
 
     Cursor cc = seed;
     for (int seg = first; seg < last;) {
@@ -356,13 +357,11 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
       }
 
       for (int cu = seg; cu < seg_end; ++cu) {
-        __syncwarp();
-        const int pos = spos[slot];
+        const uint32_t bar = smem_addr(&full[stage]);
+        if (!mbar_wait<false>(bar, parity, err)) mbar_drain(bar, parity);
+        const int pos = spos[stage * kDecWarps + warp];
         if (pos >= 0) {
-          const uint32_t bar = smem_addr(&bars[slot]);
-          if (!mbar_wait(bar, (phases >> slot) & 1u, err)) mbar_drain(bar, (phases >> slot) & 1u);
-          phases ^= 1u << slot;
-          const uint8_t* blk = ring + slot * Geo::kBytes;
+          const uint8_t* blk = smem + (size_t)(stage * kDecWarps + warp) * Geo::kBytes;
           const bool part = pos + 16 > least;  // some column does not see some token
           // ---- scores of tokens r and r + 8, columns 2c and 2c + 1
           uint32_t kw[2][D / 32], kp[2][NG], vp[2][NG];
@@ -535,9 +534,19 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
             tile(std::integral_constant<int, 3>());
           }
         }
-        __syncwarp();  // every lane is done with the slot
-        issue(slot);
-        slot = slot + 1 == kStages ? 0 : slot + 1;
+        __syncwarp();  // every lane is done with the stage
+        if (lane == 0) mbar_arrive(smem_addr(&empty[stage]));
+        // the round kStages - 1 on goes where the last one was, once every warp is done with that
+        const int next = cu + kStages - 1;
+        if (next < last && (next - first) % kDecWarps == warp) {
+          const int to = stage == 0 ? kStages - 1 : stage - 1;
+          if (cu > first) mbar_wait<false>(smem_addr(&empty[to]), parity ^ (stage == 0 ? 1u : 0u), err);
+          fetch(to);
+        }
+        if (++stage == kStages) {
+          stage = 0;
+          parity ^= 1u;
+        }
       }
 
       // ---- join the warps: O of this warp with its centres' part, then all of them
@@ -666,7 +675,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
 template <typename T, int D, int G, int NT>
 cudaError_t launch_decode(Kv& kv, const KvAttnArgs& a, const DecPlan& p, cudaStream_t s) {
   constexpr int C = 8 * NT;
-  const size_t smem = (size_t)kDecWarps * kDecStages<D, G> * (KvGeom<D, G>::kBytes + 12) +
+  const size_t smem = (size_t)kDecStages<D, G> * (kDecWarps * (KvGeom<D, G>::kBytes + 4) + 16) +
                       (size_t)kDecWarps * C * (D + 6) * sizeof(float);
   const auto kernel = kv_decode_kernel<T, D, G, NT>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
