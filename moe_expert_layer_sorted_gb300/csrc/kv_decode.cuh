@@ -51,8 +51,7 @@ constexpr int kDecDown = 32;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -263,6 +262,9 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
     int stage = 0;         // of the round at hand
     uint32_t parity = 0;   // of its fill
 
+    // where this lane's words lie in a block
+    const int at_k = r * Geo::kRow + c * (D / 8), at_p = Geo::kKPar + r * Geo::kParRow;
+    const int at_v = Geo::kVOff + c * Geo::kRow + (r ^ ((c >> 1) << 2)) * (D / 16);
     Cursor cc = seed;
     for (int seg = first; seg < last;) {
       cc.enter(a, p, seg);
@@ -340,7 +342,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
       float oc[NT][NG][2];       // this lane's tokens' part of sum P (c - 8 s), or of sum P c
       float m[NT][2], l[NT][2];
       int vexp = 0;              // E
-      float vdown = 0.0f;        // 2^-E; 0 before the first block
+      float vdown = 0.0f;        // 2^-E
+      float vlimit = -1.0f;      // the values' bound for this E; negative before the first block
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -356,183 +359,195 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
         }
       }
 
+      // One block; part: some column does not see some of its tokens.
+      auto block = [&](const uint8_t* blk, int pos, auto part_) {
+        constexpr bool part = decltype(part_)::value;
+        // codes and params of tokens r and r + 8 (keys, params) and 2c, 2c + 1, 2c + 8, 2c + 9 (values)
+        uint32_t kw[2][D / 32], kp[2][NG], vp[2][NG], vw[4][D / 64];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          load_words(kw[e], blk + at_k + 8 * e * Geo::kRow);
+          load_words(kp[e], blk + at_p + 8 * e * Geo::kParRow);
+          load_words(vp[e], blk + at_p + Geo::kVPar - Geo::kKPar + 8 * e * Geo::kParRow);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) load_words(vw[t], blk + at_v + t * 4 * Geo::kRow);
+        bool hidden[NT][4];  // scores that their column does not see
+        if constexpr (part) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (pos + r + 8 * e >= most)  // what no column sees may be anything
+#pragma unroll
+              for (int g = 0; g < NG; ++g) kp[e][g] = vp[e][g] = 0;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) hidden[nt][e] = pos + r + 8 * (e >> 1) >= seen[nt][e & 1];
+        }
+        // ---- scores of tokens r and r + 8, columns 2c and 2c + 1
+        float sc[NT][4];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          float d[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[nt][e] = 0.0f;
+#pragma unroll
+          for (int w = g * (G / 32); w < (g + 1) * (G / 32); ++w) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_f16(d[nt], raw_pair<0>(kw[0][w]), raw_pair<0>(kw[1][w]), raw_pair<1>(kw[0][w]), raw_pair<1>(kw[1][w]),
+                      qf[nt][4 * w], qf[nt][4 * w + 1]);
+              mma_f16(d[nt], raw_pair<2>(kw[0][w]), raw_pair<2>(kw[1][w]), raw_pair<3>(kw[0][w]), raw_pair<3>(kw[1][w]),
+                      qf[nt][4 * w + 2], qf[nt][4 * w + 3]);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float ks = KvType<T>::lo(kp[e][g]), kc = fmaf(-8.0f, ks, KvType<T>::hi(kp[e][g]));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const float z = g ? fmaf(kc, qsum[nt][g][x], sc[nt][2 * e + x]) : kc * qsum[nt][g][x];
+                sc[nt][2 * e + x] = fmaf(ks, d[nt][2 * e + x], z);
+              }
+          }
+        }
+        // exponents against the reference; it and E are raised where one passes it
+        float ex[NT][4];
+        auto exponents = [&]() {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              ex[nt][e] = fmaf(sc[nt][e], factor[nt][e & 1], -m[nt][e & 1]);
+              if constexpr (part)
+                if (hidden[nt][e]) ex[nt][e] = -__int_as_float(0x7f800000);
+            }
+        };
+        exponents();
+        float vs[2][NG], vc[2][NG], big = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            vs[e][g] = KvType<T>::lo(vp[e][g]);
+            vc[e][g] = KvType<T>::hi(vp[e][g]);
+            big = fmaxf(big, fmaf(8.0f, vs[e][g], fabsf(vc[e][g])));
+            if constexpr (!kCentred) vc[e][g] = fmaf(-8.0f, vs[e][g], vc[e][g]);
+          }
+        float top = ex[0][0];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, ex[nt][e]);
+        if (__any_sync(0xffffffffu, top > kDecSlack || big > vlimit)) {
+          const uint32_t vtop = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
+          float fv = 1.0f;
+          if (__uint_as_float(vtop) > vlimit) {  // to about 2^5, room for 2^13
+            const int to = min(max((int)(vtop >> 23) - 127 - 5, -90), 120);
+            fv = vlimit < 0.0f ? 0.0f : pow2(max(vexp - to, -126));
+            vexp = to;
+            vdown = pow2(-to);
+            vlimit = kDecValues * pow2(min(to, 113));
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float t = kNone;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float y = sc[nt][2 * e + x] * factor[nt][x];
+                if constexpr (part)
+                  if (hidden[nt][2 * e + x]) y = kNone;
+                t = fmaxf(t, y);
+              }
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+              t = fmaxf(t, m[nt][x]);
+              const float f = exp2_fast(m[nt][x] - t), g2 = f * fv;
+              m[nt][x] = t;
+              l[nt][x] *= f;
+#pragma unroll
+              for (int g = 0; g < NG; ++g) oc[nt][g][x] *= g2;
+#pragma unroll
+              for (int j = 0; j < D / 16; ++j) {
+                acc[j][nt][x] *= g2;
+                acc[j][nt][2 + x] *= g2;
+              }
+            }
+          exponents();
+        }
+        // ---- weights, their sums, and P s as the second product's operand
+        uint32_t pf[NT][NG][2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            vs[e][g] *= vdown;
+            vc[e][g] *= vdown;
+          }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float pr[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) pr[e] = exp2_fast(ex[nt][e]);
+          l[nt][0] += pr[0] + pr[2];
+          l[nt][1] += pr[1] + pr[3];
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              y[e] = pr[e] * vs[e >> 1][g];
+              float z = fmaf(pr[e], vc[e >> 1][g], oc[nt][g][e & 1]);
+              if constexpr (part)  // zero times a poisoned centre is not zero: masked tokens are left out
+                if (hidden[nt][e]) {
+                  y[e] = 0.0f;
+                  z = oc[nt][g][e & 1];
+                }
+              oc[nt][g][e & 1] = z;
+            }
+            pf[nt][g][0] = transpose8x8(KvType<__half>::pack(y[0], y[1]));
+            pf[nt][g][1] = transpose8x8(KvType<__half>::pack(y[2], y[3]));
+          }
+        }
+        // ---- O^T += V^T P^T
+#pragma unroll
+        for (int w = 0; w < D / 64; ++w) {
+          const uint32_t lo0 = __byte_perm(vw[0][w], vw[1][w], 0x5410), hi0 = __byte_perm(vw[0][w], vw[1][w], 0x7632);
+          const uint32_t lo1 = __byte_perm(vw[2][w], vw[3][w], 0x5410), hi1 = __byte_perm(vw[2][w], vw[3][w], 0x7632);
+          auto tile = [&](auto k_) {
+            constexpr int K = decltype(k_)::value;
+            const int j = 4 * w + K, g = j / (G / 16);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if constexpr (kCentred)
+                mma_f16(acc[j][nt], centred_pair<K>(lo0), centred_pair<K>(hi0), centred_pair<K>(lo1), centred_pair<K>(hi1),
+                        pf[nt][g][0], pf[nt][g][1]);
+              else
+                mma_f16(acc[j][nt], raw_pair<K>(lo0), raw_pair<K>(hi0), raw_pair<K>(lo1), raw_pair<K>(hi1), pf[nt][g][0],
+                        pf[nt][g][1]);
+            }
+          };
+          tile(std::integral_constant<int, 0>());
+          tile(std::integral_constant<int, 1>());
+          tile(std::integral_constant<int, 2>());
+          tile(std::integral_constant<int, 3>());
+        }
+      };
+
       for (int cu = seg; cu < seg_end; ++cu) {
         const uint32_t bar = smem_addr(&full[stage]);
         if (!mbar_wait<false>(bar, parity, err)) mbar_drain(bar, parity);
         const int pos = spos[stage * kDecWarps + warp];
         if (pos >= 0) {
-          const uint8_t* blk = smem + (size_t)(stage * kDecWarps + warp) * Geo::kBytes;
-          const bool part = pos + 16 > least;  // some column does not see some token
-          // ---- scores of tokens r and r + 8, columns 2c and 2c + 1
-          uint32_t kw[2][D / 32], kp[2][NG], vp[2][NG];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            load_words(kw[e], blk + (r + 8 * e) * Geo::kRow + c * (D / 8));
-            load_words(kp[e], blk + Geo::kKPar + (r + 8 * e) * Geo::kParRow);
-            load_words(vp[e], blk + Geo::kVPar + (r + 8 * e) * Geo::kParRow);
-          }
-          if (part) {  // what no column sees may be anything
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (pos + r + 8 * e >= most)
-#pragma unroll
-                for (int g = 0; g < NG; ++g) kp[e][g] = vp[e][g] = 0;
-          }
-          float sc[NT][4];
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            float d[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) d[nt][e] = 0.0f;
-#pragma unroll
-            for (int w = g * (G / 32); w < (g + 1) * (G / 32); ++w) {
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                mma_f16(d[nt], raw_pair<0>(kw[0][w]), raw_pair<0>(kw[1][w]), raw_pair<1>(kw[0][w]), raw_pair<1>(kw[1][w]),
-                        qf[nt][4 * w], qf[nt][4 * w + 1]);
-                mma_f16(d[nt], raw_pair<2>(kw[0][w]), raw_pair<2>(kw[1][w]), raw_pair<3>(kw[0][w]), raw_pair<3>(kw[1][w]),
-                        qf[nt][4 * w + 2], qf[nt][4 * w + 3]);
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float ks = KvType<T>::lo(kp[e][g]), kc = fmaf(-8.0f, ks, KvType<T>::hi(kp[e][g]));
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                  const float z = g ? fmaf(kc, qsum[nt][g][x], sc[nt][2 * e + x]) : kc * qsum[nt][g][x];
-                  sc[nt][2 * e + x] = fmaf(ks, d[nt][2 * e + x], z);
-                }
-            }
-          }
-          // exponents against the reference; it and E are raised where one passes it
-          float ex[NT][4];
-          auto exponents = [&]() {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                ex[nt][e] = fmaf(sc[nt][e], factor[nt][e & 1], -m[nt][e & 1]);
-                if (part && pos + r + 8 * (e >> 1) >= seen[nt][e & 1]) ex[nt][e] = -__int_as_float(0x7f800000);
-              }
-          };
-          exponents();
-          float vs[2][NG], vc[2][NG], big = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-              vs[e][g] = KvType<T>::lo(vp[e][g]);
-              vc[e][g] = KvType<T>::hi(vp[e][g]);
-              big = fmaxf(big, fmaf(8.0f, vs[e][g], fabsf(vc[e][g])));
-              if constexpr (!kCentred) vc[e][g] = fmaf(-8.0f, vs[e][g], vc[e][g]);
-            }
-          float top = big * vdown > kDecValues || vdown == 0.0f ? __int_as_float(0x7f800000) : ex[0][0];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = fmaxf(top, ex[nt][e]);
-          if (__any_sync(0xffffffffu, top > kDecSlack)) {
-            const uint32_t vtop = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
-            const int need = (int)(vtop >> 23) - 127;
-            float fv = 1.0f;
-            if (vdown == 0.0f || need > vexp + 12) {  // about 2^5, room for 2^13
-              const int to = min(max(need - 5, -90), 120);
-              fv = vdown == 0.0f ? 0.0f : pow2(max(vexp - to, -126));
-              vexp = to;
-              vdown = pow2(-to);
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                float t = kNone;
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  if (!part || pos + r + 8 * e < seen[nt][x]) t = fmaxf(t, sc[nt][2 * e + x] * factor[nt][x]);
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-                t = fmaxf(t, m[nt][x]);
-                const float f = exp2_fast(m[nt][x] - t), g2 = f * fv;
-                m[nt][x] = t;
-                l[nt][x] *= f;
-#pragma unroll
-                for (int g = 0; g < NG; ++g) oc[nt][g][x] *= g2;
-#pragma unroll
-                for (int j = 0; j < D / 16; ++j) {
-                  acc[j][nt][x] *= g2;
-                  acc[j][nt][2 + x] *= g2;
-                }
-              }
-            exponents();
-          }
-          // ---- weights, their sums, and P s as the second product's operand
-          uint32_t pf[NT][NG][2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-              vs[e][g] *= vdown;
-              vc[e][g] *= vdown;
-            }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float pr[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) pr[e] = exp2_fast(ex[nt][e]);
-            l[nt][0] += pr[0] + pr[2];
-            l[nt][1] += pr[1] + pr[3];
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-              float y[4];
-              if (!part) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  y[e] = pr[e] * vs[e >> 1][g];
-                  oc[nt][g][e & 1] = fmaf(pr[e], vc[e >> 1][g], oc[nt][g][e & 1]);
-                }
-              } else {  // zero times a poisoned centre is not zero: masked tokens are left out
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const bool sees = pos + r + 8 * (e >> 1) < seen[nt][e & 1];
-                  y[e] = sees ? pr[e] * vs[e >> 1][g] : 0.0f;
-                  if (sees) oc[nt][g][e & 1] = fmaf(pr[e], vc[e >> 1][g], oc[nt][g][e & 1]);
-                }
-              }
-              pf[nt][g][0] = transpose8x8(KvType<__half>::pack(y[0], y[1]));
-              pf[nt][g][1] = transpose8x8(KvType<__half>::pack(y[2], y[3]));
-            }
-          }
-          // ---- O^T += V^T P^T
-          const uint8_t* vb = blk + Geo::kVOff + c * Geo::kRow + (r ^ ((c >> 1) << 2)) * (D / 16);
-          uint32_t vw[4][D / 64];  // tokens 2c, 2c + 1, 2c + 8, 2c + 9
-#pragma unroll
-          for (int t = 0; t < 4; ++t) load_words(vw[t], vb + t * 4 * Geo::kRow);
-#pragma unroll
-          for (int w = 0; w < D / 64; ++w) {
-            const uint32_t lo0 = __byte_perm(vw[0][w], vw[1][w], 0x5410), hi0 = __byte_perm(vw[0][w], vw[1][w], 0x7632);
-            const uint32_t lo1 = __byte_perm(vw[2][w], vw[3][w], 0x5410), hi1 = __byte_perm(vw[2][w], vw[3][w], 0x7632);
-            auto tile = [&](auto k_) {
-              constexpr int K = decltype(k_)::value;
-              const int j = 4 * w + K, g = j / (G / 16);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                if constexpr (kCentred)
-                  mma_f16(acc[j][nt], centred_pair<K>(lo0), centred_pair<K>(hi0), centred_pair<K>(lo1), centred_pair<K>(hi1),
-                          pf[nt][g][0], pf[nt][g][1]);
-                else
-                  mma_f16(acc[j][nt], raw_pair<K>(lo0), raw_pair<K>(hi0), raw_pair<K>(lo1), raw_pair<K>(hi1), pf[nt][g][0],
-                          pf[nt][g][1]);
-              }
-            };
-            tile(std::integral_constant<int, 0>());
-            tile(std::integral_constant<int, 1>());
-            tile(std::integral_constant<int, 2>());
-            tile(std::integral_constant<int, 3>());
-          }
+          const uint8_t* blk = smem + (stage * kDecWarps + warp) * Geo::kBytes;
+          if (pos + 16 <= least) block(blk, pos, std::false_type());
+          else block(blk, pos, std::true_type());
         }
         __syncwarp();  // every lane is done with the stage
         if (lane == 0) mbar_arrive(smem_addr(&empty[stage]));
