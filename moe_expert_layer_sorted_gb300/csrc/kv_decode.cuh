@@ -15,13 +15,17 @@
 // the output's, 2^-12 of a weight and independent from token to token); the
 // centres' part is summed apart in fp32.  bf16 outputs take the values' codes
 // as they are too (their offset of 8 s makes that rounding three times larger,
-// far below bf16's); fp16 outputs take u - 8.  Values are carried times 2^-E,
-// E raised when a token's values need it, so that no size of value leaves
-// fp16's or, summed, fp32's range.
+// far below bf16's); fp16 outputs take u - 8.
 //
-// Softmax: running reference per column, raised only when a score passes it by
-// 4 (in powers of two), so that most blocks rescale nothing; sums are fp32.  A
-// column that sees no token keeps the sum 0.
+// Softmax: weights are 2^(score - reference) with a running reference per
+// column, raised only when a score passes it by 4, so that most blocks rescale
+// nothing; sums are fp32.  O is carried times 2^-E, E raised when a token's
+// values need it: weights times values of any size stay inside fp16's and,
+// summed, fp32's range.  A column that sees no token keeps the sum 0.
+//
+// One warp's chain score -> weight -> product is long and four warps per
+// scheduler do not hide it: the next block's scores are computed between this
+// block's weights and its product.
 //
 // Work split: all rounds (8 blocks of 16 tokens of one kv head and column tile)
 // of the batch in one line, cut into equal shares, one per CTA; a share covers
@@ -46,8 +50,6 @@ namespace {
 constexpr int kDecWarps = 8;
 constexpr float kDecSlack = 4.0f;      // weights reach 2^4
 constexpr float kDecValues = 8192.0f;  // bound of |c| + 8 s times 2^-E
-// O leaves a warp times 2^-32: sums of 2^28 weights times bf16's largest value stay finite
-constexpr int kDecDown = 32;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -116,6 +118,29 @@ struct Cursor {
   }
 };
 
+// State that the block loop does not touch lives in shared memory, not in registers.
+struct Item {  // the item at hand
+  Cursor at;
+  int s, head, ctile, row_lo, cols;  // sequence, kv head, column tile, first row, columns of all tiles
+  int rows, len;                     // KvSeq
+  int64_t row0;
+  __device__ __forceinline__ KvSeq seq() const volatile { return {row0, rows, len}; }
+};
+struct Fetch {  // a warp's next fetch
+  Cursor at;
+  int round, head, seen;  // its round; positions from `seen` on are not read
+  const int32_t* table;   // the sequence's table
+  const int32_t* list;    // the chosen pages
+  int pos[kDecWarps], pid[kDecWarps];  // the blocks' positions, and their pages once they have arrived
+};
+__device__ __forceinline__ Cursor load(const volatile Cursor& c) {
+  return {c.group, c.end, c.rounds, c.item, c.item0, c.item_end};
+}
+__device__ __forceinline__ void store(volatile Cursor& c, const Cursor& v) {
+  c.group = v.group, c.end = v.end, c.rounds = v.rounds;
+  c.item = v.item, c.item0 = v.item0, c.item_end = v.item_end;
+}
+
 template <typename T, int D, int G, int NT>
 __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
     kv_decode_kernel(const __grid_constant__ KvAttnArgs a, const __grid_constant__ DecPlan p, float* __restrict__ ws,
@@ -134,6 +159,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
   int* spos = reinterpret_cast<int*>(empty + kStages);                          // [stage][block] its position, -1: not there
   __shared__ int sh_sum[kDecWarps];
   __shared__ int sh_base, sh_group;
+  __shared__ Item sh_item;
+  __shared__ Fetch sh_fetch[kDecWarps];
   __shared__ unsigned sh_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
@@ -194,55 +221,66 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
       }
     }
     __syncthreads();
-    Cursor seed;
-    seed.group = sh_group - 1;
-    seed.end = sh_base;
-    seed.rounds = 0;
+    const Cursor seed{sh_group - 1, sh_base, 0, 0, 0, 0};
 
     // ---- fetching: this warp's rounds are first + warp, + 8, ...; lane b < 8 looks after block b
-    Cursor pc = seed;
-    pc.item_end = 0;
-    const int per_page = a.c.page_shift - 4;
-    const int run = min(1 << per_page, kDecWarps);  // blocks per copy
-    int pu = first + warp;
-    int ppos = 0, pid = -1;           // position and page of the block
-    int pseen = 0;                    // positions from here on are not read
-    const int32_t* ptable = nullptr;  // the sequence's table
-    const int32_t* plist = nullptr;   // the chosen pages
-    int phead = 0;
-    auto look = [&]() {  // asks for the pages of round pu
-      if (pu >= last) return;
-      if (pu >= pc.item_end) {
-        pc.enter(a, p, pu);
-        phead = pc.item / p.ctiles;
-        int s = pc.group;
-        if (a.sel) {
-          s = pc.group / a.b.max_new;
-          const KvSeq q = kv_seq(a.b, s);
-          const int i = pc.group % a.b.max_new;
-          plist = a.sel + (kv_row_index(a.b, s, q.row0, i) * a.c.heads + phead) * a.budget;
-          pseen = (int)min(a.causal ? (int64_t)q.len - q.rows + i + 1 : (int64_t)q.len, (int64_t)kv_capacity(a.c, a.b));
-        } else {
-          pseen = min(kv_seq(a.b, s).len, kv_capacity(a.c, a.b));
+    volatile Fetch& ft = sh_fetch[warp];
+    if (lane == 0) {
+      store(ft.at, seed);
+      ft.round = first + warp;
+    }
+    __syncwarp();
+    auto look = [&]() {  // asks for the pages of the next fetch's round
+      const int u = ft.round;
+      if (u >= last) return;
+      if (u >= ft.at.item_end) {
+        Cursor pc = load(ft.at);
+        pc.enter(a, p, u);
+        const int head = pc.item / p.ctiles, s = a.sel ? pc.group / a.b.max_new : pc.group;
+        const KvSeq q = kv_seq(a.b, s);
+        int64_t seen = q.len;
+        __syncwarp();
+        if (lane == 0) {
+          if (a.sel) {
+            const int i = pc.group % a.b.max_new;
+            ft.list = a.sel + (kv_row_index(a.b, s, q.row0, i) * a.c.heads + head) * a.budget;
+            if (a.causal) seen = (int64_t)q.len - q.rows + i + 1;
+          }
+          store(ft.at, pc);
+          ft.head = head;
+          ft.seen = (int)min(seen, (int64_t)kv_capacity(a.c, a.b));
+          ft.table = a.b.table + (int64_t)s * a.b.table_stride;
         }
-        ptable = a.b.table + (int64_t)s * a.b.table_stride;
+        __syncwarp();
       }
-      const int ub = (pu - pc.item0) * kDecWarps + lane;
-      int j = ub >> per_page;
-      ppos = ub * 16;
-      if (a.sel) {
-        j = j < a.budget ? plist[j] : -1;
-        // pages beyond the row's are skipped (compared as pages: positions could wrap)
-        const bool in = j >= 0 && j <= (pseen - 1) >> a.c.page_shift;
-        ppos = in ? (j << a.c.page_shift) + 16 * (ub & ((1 << per_page) - 1)) : 0x7fffffff;
+      if (lane < kDecWarps) {
+        const int per_page = a.c.page_shift - 4, seen = ft.seen;
+        const int ub = (u - ft.at.item0) * kDecWarps + lane;
+        int j = ub >> per_page, pos = ub * 16;
+        if (a.sel) {
+          j = j < a.budget ? ft.list[j] : -1;
+          // pages beyond the row's are skipped (compared as pages: positions could wrap)
+          const bool in = j >= 0 && j <= (seen - 1) >> a.c.page_shift;
+          pos = in ? (j << a.c.page_shift) + 16 * (ub & ((1 << per_page) - 1)) : 0x7fffffff;
+        }
+        ft.pos[lane] = pos;
+        if (pos < seen)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(const_cast<int*>(&ft.pid[lane]))),
+                       "l"(ft.table + j)
+                       : "memory");
+        else
+          ft.pid[lane] = -1;
       }
-      pid = lane < kDecWarps && ppos < pseen ? ptable[j] : -1;
     };
-    auto fetch = [&](int stage) {  // copies round pu into a free stage
-      if (pu >= last) return;
-      const bool ok = lane < kDecWarps && ppos < pseen && (uint32_t)pid < (uint32_t)a.c.num_pages;
+    auto fetch = [&](int stage) {  // copies that round into a free stage
+      const int u = ft.round;
+      if (u >= last) return;
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      const int run = min(a.c.page_size >> 4, kDecWarps);  // blocks per copy
+      const int pos = lane < kDecWarps ? ft.pos[lane] : 0, pid = lane < kDecWarps ? ft.pid[lane] : -1;
+      const bool ok = (uint32_t)pid < (uint32_t)a.c.num_pages;
       const uint32_t there = __ballot_sync(0xffffffffu, ok);
-      if (lane < kDecWarps) spos[stage * kDecWarps + lane] = ok ? ppos : -1;
+      if (lane < kDecWarps) spos[stage * kDecWarps + lane] = ok ? pos : -1;
       __syncwarp();
       const uint32_t bar = smem_addr(&full[stage]);
       if (lane == 0) mbar_arrive_expect_tx(bar, __popc(there) * Geo::kBytes);
@@ -251,34 +289,44 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
       const int count = __popc(there >> lane & ((1u << run) - 1u));
       if (ok && lane % run == 0)
         bulk_g2s(smem_addr(smem) + (stage * kDecWarps + lane) * Geo::kBytes,
-                 a.c.pages + (int64_t)pid * a.c.page_stride + phead * a.c.head_stride +
-                     (int64_t)((ppos & (a.c.page_size - 1)) >> 4) * Geo::kBytes,
+                 a.c.pages + (int64_t)pid * a.c.page_stride + ft.head * a.c.head_stride +
+                     (int64_t)((pos & (a.c.page_size - 1)) >> 4) * Geo::kBytes,
                  count * Geo::kBytes, bar);
-      pu += kDecWarps;
+      __syncwarp();
+      if (lane == 0) ft.round = u + kDecWarps;
+      __syncwarp();
       look();
     };
     look();
     if (warp < kStages - 1) fetch(warp);
+    int turn = (warp - (kStages - 1) + kDecWarps) % kDecWarps + 1;  // rounds to this warp's next fetch
     int stage = 0;         // of the round at hand
     uint32_t parity = 0;   // of its fill
 
     // where this lane's words lie in a block
     const int at_k = r * Geo::kRow + c * (D / 8), at_p = Geo::kKPar + r * Geo::kParRow;
     const int at_v = Geo::kVOff + c * Geo::kRow + (r ^ ((c >> 1) << 2)) * (D / 16);
-    Cursor cc = seed;
+    volatile Item& it = sh_item;
+    if (tid == 0) store(it.at, seed);
     for (int seg = first; seg < last;) {
-      cc.enter(a, p, seg);
-      const int seg_end = min(cc.item_end, last);
-      // ---- the item's columns
-      int s = cc.group, row_lo = 0, ncols;
-      const int h = cc.item / p.ctiles, ct = cc.item % p.ctiles;
-      if (a.sel) {
-        s = cc.group / a.b.max_new;
-        row_lo = cc.group % a.b.max_new;
+      if (tid == 0) {
+        Cursor cc = load(it.at);
+        cc.enter(a, p, seg);
+        const int s = a.sel ? cc.group / a.b.max_new : cc.group;
+        const KvSeq q = kv_seq(a.b, s);
+        store(it.at, cc);
+        it.s = s;
+        it.head = cc.item / p.ctiles;
+        it.ctile = cc.item % p.ctiles;
+        it.row_lo = a.sel ? cc.group % a.b.max_new : 0;
+        it.cols = (a.sel ? 1 : q.rows) * p.per;
+        it.rows = q.rows;
+        it.len = q.len;
+        it.row0 = q.row0;
       }
-      const KvSeq q = kv_seq(a.b, s);
-      ncols = (a.sel ? 1 : q.rows) * p.per;
-      const int cap = kv_capacity(a.c, a.b);
+      __syncthreads();
+      const int seg_end = min(it.at.item_end, last);
+      // ---- the item's columns
       uint32_t qf[NT][D / 8];    // this lane's query operand: column 8 nt + r, its quarter of every group
       float qsum[NT][NG][2];     // 2^-24 sums over a group's channels, columns 8 nt + 2c, + 1
       float factor[NT][2];       // what makes the columns' sums scores (log2)
@@ -286,7 +334,10 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
       int least = 0x7fffffff, most = 0;  // over the columns
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const int x = ct * C + nt * 8 + r;  // column 8 nt + r; a column of nobody is zeros, never written
+        const int s = it.s, h = it.head, row_lo = it.row_lo, ncols = it.cols;
+        const KvSeq q = it.seq();
+        const int cap = kv_capacity(a.c, a.b);
+        const int x = it.ctile * C + nt * 8 + r;  // column 8 nt + r; a column of nobody is zeros, never written
         const bool real = x < ncols;
         const int i = row_lo + (real ? x / p.per : 0);
         const uint16_t* src = a.q + kv_row_offset(a.b, a.qs, s, q.row0, i) + (int64_t)(h * p.per + x % p.per) * a.qs.head;
@@ -341,9 +392,9 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
       float acc[D / 16][NT][4];  // O^T: channel tiles by columns
       float oc[NT][NG][2];       // this lane's tokens' part of sum P (c - 8 s), or of sum P c
       float m[NT][2], l[NT][2];
-      int vexp = 0;              // E
-      float vdown = 0.0f;        // 2^-E
-      float vlimit = -1.0f;      // the values' bound for this E; negative before the first block
+      int vexp = 0;                    // E
+      float vlimit = -1.0f;            // the values' bound for this E; negative before the first block
+      float vdown = 0.0f;              // 2^-E
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -359,33 +410,14 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
         }
       }
 
-      // One block; part: some column does not see some of its tokens.
-      auto block = [&](const uint8_t* blk, int pos, auto part_) {
-        constexpr bool part = decltype(part_)::value;
-        // codes and params of tokens r and r + 8 (keys, params) and 2c, 2c + 1, 2c + 8, 2c + 9 (values)
-        uint32_t kw[2][D / 32], kp[2][NG], vp[2][NG], vw[4][D / 64];
+      // Scores of a block's tokens r and r + 8, columns 2c and 2c + 1 (what is masked may be anything).
+      auto scores = [&](const uint8_t* blk, float (&sc)[NT][4]) {
+        uint32_t kw[2][D / 32], kp[2][NG];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           load_words(kw[e], blk + at_k + 8 * e * Geo::kRow);
           load_words(kp[e], blk + at_p + 8 * e * Geo::kParRow);
-          load_words(vp[e], blk + at_p + Geo::kVPar - Geo::kKPar + 8 * e * Geo::kParRow);
         }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) load_words(vw[t], blk + at_v + t * 4 * Geo::kRow);
-        bool hidden[NT][4];  // scores that their column does not see
-        if constexpr (part) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (pos + r + 8 * e >= most)  // what no column sees may be anything
-#pragma unroll
-              for (int g = 0; g < NG; ++g) kp[e][g] = vp[e][g] = 0;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) hidden[nt][e] = pos + r + 8 * (e >> 1) >= seen[nt][e & 1];
-        }
-        // ---- scores of tokens r and r + 8, columns 2c and 2c + 1
-        float sc[NT][4];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           float d[NT][4];
@@ -414,6 +446,29 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
                 sc[nt][2 * e + x] = fmaf(ks, d[nt][2 * e + x], z);
               }
           }
+        }
+      };
+      // One block from its scores sc, which the next block's then replace (ahead).  part: some
+      // column does not see some of its tokens.
+      auto block = [&](const uint8_t* blk, int pos, float (&sc)[NT][4], const uint8_t* next, auto part_, auto ahead_) {
+        constexpr bool part = decltype(part_)::value, ahead = decltype(ahead_)::value;
+        // params of tokens r and r + 8, values' codes of tokens 2c, 2c + 1, 2c + 8, 2c + 9
+        uint32_t vp[2][NG], vw[4][D / 64];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) load_words(vp[e], blk + at_p + Geo::kVPar - Geo::kKPar + 8 * e * Geo::kParRow);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) load_words(vw[t], blk + at_v + t * 4 * Geo::kRow);
+        bool hidden[NT][4];  // scores that their column does not see
+        if constexpr (part) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (pos + r + 8 * e >= most)  // what no column sees may be anything
+#pragma unroll
+              for (int g = 0; g < NG; ++g) vp[e][g] = 0;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) hidden[nt][e] = pos + r + 8 * (e >> 1) >= seen[nt][e & 1];
         }
         // exponents against the reference; it and E are raised where one passes it
         float ex[NT][4];
@@ -444,10 +499,10 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) top = fmaxf(top, ex[nt][e]);
         if (__any_sync(0xffffffffu, top > kDecSlack || big > vlimit)) {
-          const uint32_t vtop = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
-          float fv = 1.0f;
-          if (__uint_as_float(vtop) > vlimit) {  // to about 2^5, room for 2^13
-            const int to = min(max((int)(vtop >> 23) - 127 - 5, -90), 120);
+          const float vtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+          float fv = 1.0f;      // for what was summed with the E before
+          if (vtop > vlimit) {  // values to about 2^5, room for 2^13
+            const int to = min(max((int)(__float_as_uint(vtop) >> 23) - 127 - 5, -90), 120);
             fv = vlimit < 0.0f ? 0.0f : pow2(max(vexp - to, -126));
             vexp = to;
             vdown = pow2(-to);
@@ -468,28 +523,22 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
               t = fmaxf(t, m[nt][x]);
-              const float f = exp2_fast(m[nt][x] - t), g2 = f * fv;
+              const float f = exp2_fast(m[nt][x] - t), fo = f * fv;
               m[nt][x] = t;
               l[nt][x] *= f;
 #pragma unroll
-              for (int g = 0; g < NG; ++g) oc[nt][g][x] *= g2;
+              for (int g = 0; g < NG; ++g) oc[nt][g][x] *= fo;
 #pragma unroll
               for (int j = 0; j < D / 16; ++j) {
-                acc[j][nt][x] *= g2;
-                acc[j][nt][2 + x] *= g2;
+                acc[j][nt][x] *= fo;
+                acc[j][nt][2 + x] *= fo;
               }
             }
           exponents();
         }
+        if constexpr (ahead) scores(next, sc);
         // ---- weights, their sums, and P s as the second product's operand
         uint32_t pf[NT][NG][2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            vs[e][g] *= vdown;
-            vc[e][g] *= vdown;
-          }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float pr[4];
@@ -497,6 +546,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
           for (int e = 0; e < 4; ++e) pr[e] = exp2_fast(ex[nt][e]);
           l[nt][0] += pr[0] + pr[2];
           l[nt][1] += pr[1] + pr[3];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) pr[e] *= vdown;
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
             float y[4];
@@ -540,22 +591,29 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
         }
       };
 
+      // a round's stage, once it is there: this warp's block and its position
+      auto arrive = [&](int st, uint32_t par, int& pos) {
+        const uint32_t bar = smem_addr(&full[st]);
+        if (!mbar_wait<false>(bar, par, err)) mbar_drain(bar, par);
+        pos = spos[st * kDecWarps + warp];
+        return smem + (st * kDecWarps + warp) * Geo::kBytes;
+      };
       for (int cu = seg; cu < seg_end; ++cu) {
-        const uint32_t bar = smem_addr(&full[stage]);
-        if (!mbar_wait<false>(bar, parity, err)) mbar_drain(bar, parity);
-        const int pos = spos[stage * kDecWarps + warp];
+        int pos;
+        const uint8_t* blk = arrive(stage, parity, pos);
         if (pos >= 0) {
-          const uint8_t* blk = smem + (stage * kDecWarps + warp) * Geo::kBytes;
-          if (pos + 16 <= least) block(blk, pos, std::false_type());
-          else block(blk, pos, std::true_type());
+          float sc[NT][4];
+          scores(blk, sc);
+          if (pos + 16 > least) block(blk, pos, sc, blk, std::true_type(), std::false_type());
+          else block(blk, pos, sc, blk, std::false_type(), std::false_type());
         }
         __syncwarp();  // every lane is done with the stage
         if (lane == 0) mbar_arrive(smem_addr(&empty[stage]));
         // the round kStages - 1 on goes where the last one was, once every warp is done with that
-        const int next = cu + kStages - 1;
-        if (next < last && (next - first) % kDecWarps == warp) {
+        if (--turn == 0) {
+          turn = kDecWarps;
           const int to = stage == 0 ? kStages - 1 : stage - 1;
-          if (cu > first) mbar_wait<false>(smem_addr(&empty[to]), parity ^ (stage == 0 ? 1u : 0u), err);
+          if (cu > first && ft.round < last) mbar_wait<false>(smem_addr(&empty[to]), parity ^ (stage == 0 ? 1u : 0u), err);
           fetch(to);
         }
         if (++stage == kStages) {
@@ -565,7 +623,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
       }
 
       // ---- join the warps: O of this warp with its centres' part, then all of them
-      const float mid = pow2(vexp - kDecDown), even = mid * (kCentred ? 1.0f : 0x1p24f), odd = even * (kCentred ? 1.0f : 0.0625f);
+      constexpr float even = kCentred ? 1.0f : 0x1p24f, odd = kCentred ? 1.0f : 0x1p20f;  // of the codes as subnormals
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -574,14 +632,12 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], o);
 #pragma unroll
-          for (int g = 0; g < NG; ++g) {
+          for (int g = 0; g < NG; ++g)
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) oc[nt][g][x] += __shfl_xor_sync(0xffffffffu, oc[nt][g][x], o);
-            oc[nt][g][x] *= mid;
-          }
-          if (r == 0) {
-            mm[warp * C + col] = m[nt][x];
-            ml[warp * C + col] = l[nt][x];
+          if (r == 0) {  // from here on E is part of the reference: the sum is scaled as O is
+            mm[warp * C + col] = m[nt][x] + (float)vexp;
+            ml[warp * C + col] = l[nt][x] * pow2(-vexp);
           }
           float* dst = mo + (warp * C + col) * (D + 4);
 #pragma unroll
@@ -593,14 +649,16 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
           }
         }
       __syncthreads();
-      const bool whole = seg == cc.item0 && seg_end == cc.item_end;
+      const int item0 = it.at.item0, item_end = it.at.item_end;
+      const bool whole = seg == item0 && seg_end == item_end;
       // partial results: a CTA's first stretch in slot 0, its last in slot 1
       float* part = ws + (int64_t)(2 * me + (seg == first ? 0 : 1)) * kSlot;
       auto finish = [&](int col, int d4, float4 o, float M, float L) {  // four channels of a column
-        const int x = ct * C + col;
-        if (x >= ncols) return;
-        const int i = row_lo + x / p.per, hq = h * p.per + x % p.per;
-        const float inv = L == 0.0f ? 0.0f : pow2(kDecDown) / L;  // a row that sees nothing is zero
+        const int x = it.ctile * C + col, s = it.s;
+        if (x >= it.cols) return;
+        const int i = it.row_lo + x / p.per, hq = it.head * p.per + x % p.per;
+        const KvSeq q = it.seq();
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;  // a row that sees nothing is zero
         *reinterpret_cast<uint2*>(a.out + kv_row_offset(a.b, a.os, s, q.row0, i) + (int64_t)hq * a.os.head + 4 * d4) =
             make_uint2(KvType<T>::pack(o.x * inv, o.y * inv), KvType<T>::pack(o.z * inv, o.w * inv));
         if (a.lse && d4 == 0)
@@ -635,7 +693,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
         }
       }
       if (!whole) {  // the CTA that finishes the item last joins its parts
-        const int c0 = owner(cc.item0, total, n), c1 = owner(cc.item_end - 1, total, n);
+        const int c0 = owner(item0, total, n), c1 = owner(item_end - 1, total, n);
         __threadfence();
         __syncthreads();
         if (tid == 0) sh_last = atomicAdd(&counters[c0], 1u);
@@ -643,7 +701,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
         if (sh_last == (unsigned)(c1 - c0)) {
           __threadfence();
           // the item began c0's last stretch: its only one if the item begins c0's share
-          const int head = 2 * c0 + (cc.item0 == share(total, c0, n) ? 0 : 1);
+          const int head = 2 * c0 + (item0 == share(total, c0, n) ? 0 : 1);
           for (int x = tid; x < C * (D / 4); x += kDecWarps * 32) {
             const int col = x / (D / 4), d4 = x % (D / 4);
             float M = kNone, L = 0.0f;
