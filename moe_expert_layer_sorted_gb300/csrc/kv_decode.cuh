@@ -23,17 +23,12 @@
 // values need it: weights times values of any size stay inside fp16's and,
 // summed, fp32's range.  A column that sees no token keeps the sum 0.
 //
-// One warp's chain score -> weight -> product is long and four warps per
-// scheduler do not hide it: the next block's scores are computed between this
-// block's weights and its product.
-//
 // Work split: all rounds (8 blocks of 16 tokens of one kv head and column tile)
 // of the batch in one line, cut into equal shares, one per CTA; a share covers
 // any number of items (sequence, head, column tile) or part of one.  Rounds come
-// through a ring in shared memory, one bulk copy per page (or its 128 tokens);
-// each of the 8 warps takes one block of a round.  The warps fetch in turn, warp
-// w every eighth round, its page numbers asked for eight rounds ahead: what a
-// fetch costs is paid once per 8 blocks, and no warp is set aside for it.  At the end of an item's stretch the warps' (max, sum, O) are
+// through a ring in shared memory, one bulk copy per page (or its 128 tokens),
+// fetched by a ninth warp, its page numbers asked for a round ahead; each of the
+// 8 others takes one block of a round.  At the end of an item's stretch the warps' (max, sum, O) are
 // joined in shared memory; an item cut between CTAs is joined by the CTA that
 // finishes last, in the order of the CTAs, so results do not depend on timing.
 #pragma once
@@ -47,10 +42,13 @@ namespace {
 #include "device_common.cuh"
 #include "kv_operand.cuh"
 
-constexpr int kDecWarps = 8;
+constexpr int kDecWarps = 8;                         // that compute
+constexpr int kDecThreads = (kDecWarps + 1) * 32;  // and one that fetches
+constexpr int kDecMaxParts = kDecWarps * (64 + 4);  // CTAs, so parts of an item, whose references fit the merge buffer
 constexpr float kDecSlack = 4.0f;      // weights reach 2^4
 constexpr float kDecValues = 8192.0f;  // bound of |c| + 8 s times 2^-E
 
+__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kDecWarps * 32) : "memory"); }
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -126,13 +124,6 @@ struct Item {  // the item at hand
   int64_t row0;
   __device__ __forceinline__ KvSeq seq() const volatile { return {row0, rows, len}; }
 };
-struct Fetch {  // a warp's next fetch
-  Cursor at;
-  int round, head, seen;  // its round; positions from `seen` on are not read
-  const int32_t* table;   // the sequence's table
-  const int32_t* list;    // the chosen pages
-  int pos[kDecWarps], pid[kDecWarps];  // the blocks' positions, and their pages once they have arrived
-};
 __device__ __forceinline__ Cursor load(const volatile Cursor& c) {
   return {c.group, c.end, c.rounds, c.item, c.item0, c.item_end};
 }
@@ -142,7 +133,7 @@ __device__ __forceinline__ void store(volatile Cursor& c, const Cursor& v) {
 }
 
 template <typename T, int D, int G, int NT>
-__global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
     kv_decode_kernel(const __grid_constant__ KvAttnArgs a, const __grid_constant__ DecPlan p, float* __restrict__ ws,
                      unsigned* __restrict__ counters, uint32_t* err) {
   using Geo = KvGeom<D, G>;
@@ -157,10 +148,9 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(ml + kDecWarps * C);             // [stage]
   uint64_t* empty = full + kStages;                                             // [stage]
   int* spos = reinterpret_cast<int*>(empty + kStages);                          // [stage][block] its position, -1: not there
-  __shared__ int sh_sum[kDecWarps];
+  __shared__ int sh_sum[kDecWarps + 1];
   __shared__ int sh_base, sh_group;
   __shared__ Item sh_item;
-  __shared__ Fetch sh_fetch[kDecWarps];
   __shared__ unsigned sh_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
@@ -183,14 +173,14 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
     __syncthreads();
     all = 0;
 #pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) {
+    for (int w = 0; w < kDecThreads / 32; ++w) {
       if (w < warp) v += sh_sum[w];
       all += sh_sum[w];
     }
     return v;
   };
-  int total = 0, mine = 0, upto = 0;  // the last 256 groups' (for up to 256 groups: the only) prefix
-  for (int g0 = 0; g0 < p.groups; g0 += kDecWarps * 32) {
+  int total = 0, mine = 0, upto = 0;  // the last groups' (for up to kDecThreads groups: the only) prefix
+  for (int g0 = 0; g0 < p.groups; g0 += kDecThreads) {
     const int gi = g0 + tid;
     int all;
     mine = gi < p.groups ? group_rounds(a, gi) * p.items : 0;
@@ -201,14 +191,14 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
   const int me = blockIdx.x;
   const int first = me < n ? share(total, me, n) : total, last = me < n ? share(total, me + 1, n) : total;
   if (first < last) {
-    if (p.groups <= kDecWarps * 32) {
+    if (p.groups <= kDecThreads) {
       if (upto - mine <= first && first < upto) {
         sh_group = tid;
         sh_base = upto - mine;
       }
     } else {
       int before = 0;
-      for (int g0 = 0; g0 < p.groups && before <= first; g0 += kDecWarps * 32) {
+      for (int g0 = 0; g0 < p.groups && before <= first; g0 += kDecThreads) {
         const int gi = g0 + tid;
         int all;
         mine = gi < p.groups ? group_rounds(a, gi) * p.items : 0;
@@ -223,86 +213,70 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
     __syncthreads();
     const Cursor seed{sh_group - 1, sh_base, 0, 0, 0, 0};
 
-    // ---- fetching: this warp's rounds are first + warp, + 8, ...; lane b < 8 looks after block b
-    volatile Fetch& ft = sh_fetch[warp];
-    if (lane == 0) {
-      store(ft.at, seed);
-      ft.round = first + warp;
-    }
-    __syncwarp();
-    auto look = [&]() {  // asks for the pages of the next fetch's round
-      const int u = ft.round;
-      if (u >= last) return;
-      if (u >= ft.at.item_end) {
-        Cursor pc = load(ft.at);
-        pc.enter(a, p, u);
-        const int head = pc.item / p.ctiles, s = a.sel ? pc.group / a.b.max_new : pc.group;
-        const KvSeq q = kv_seq(a.b, s);
-        int64_t seen = q.len;
-        __syncwarp();
-        if (lane == 0) {
+    if (warp == kDecWarps) {
+      // ---- fetching: lane b < 8 looks after block b of each round
+      Cursor pc = seed;
+      const int per_page = a.c.page_shift - 4;
+      const int run = min(1 << per_page, kDecWarps);  // blocks per copy
+      int head = 0, seen = 0;                         // kv head; positions from `seen` on are not read
+      const int32_t *table = nullptr, *list = nullptr;  // of the sequence's pages, of the chosen ones
+      int pos = 0, pid = -1;                          // of the block
+      const uint8_t* src = nullptr;
+      auto look = [&](int u) {  // asks for the pages of round u
+        if (u >= last) return;
+        if (u >= pc.item_end) {
+          pc.enter(a, p, u);
+          head = pc.item / p.ctiles;
+          const int s = a.sel ? pc.group / a.b.max_new : pc.group;
+          const KvSeq q = kv_seq(a.b, s);
+          int64_t n = q.len;
           if (a.sel) {
             const int i = pc.group % a.b.max_new;
-            ft.list = a.sel + (kv_row_index(a.b, s, q.row0, i) * a.c.heads + head) * a.budget;
-            if (a.causal) seen = (int64_t)q.len - q.rows + i + 1;
+            list = a.sel + (kv_row_index(a.b, s, q.row0, i) * a.c.heads + head) * a.budget;
+            if (a.causal) n = (int64_t)q.len - q.rows + i + 1;
           }
-          store(ft.at, pc);
-          ft.head = head;
-          ft.seen = (int)min(seen, (int64_t)kv_capacity(a.c, a.b));
-          ft.table = a.b.table + (int64_t)s * a.b.table_stride;
+          seen = (int)min(n, (int64_t)kv_capacity(a.c, a.b));
+          table = a.b.table + (int64_t)s * a.b.table_stride;
+          src = a.c.pages + head * a.c.head_stride;
         }
-        __syncwarp();
-      }
-      if (lane < kDecWarps) {
-        const int per_page = a.c.page_shift - 4, seen = ft.seen;
-        const int ub = (u - ft.at.item0) * kDecWarps + lane;
-        int j = ub >> per_page, pos = ub * 16;
+        const int ub = (u - pc.item0) * kDecWarps + lane;
+        int j = ub >> per_page;
+        pos = ub * 16;
         if (a.sel) {
-          j = j < a.budget ? ft.list[j] : -1;
+          j = j < a.budget ? list[j] : -1;
           // pages beyond the row's are skipped (compared as pages: positions could wrap)
           const bool in = j >= 0 && j <= (seen - 1) >> a.c.page_shift;
           pos = in ? (j << a.c.page_shift) + 16 * (ub & ((1 << per_page) - 1)) : 0x7fffffff;
         }
-        ft.pos[lane] = pos;
-        if (pos < seen)
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(const_cast<int*>(&ft.pid[lane]))),
-                       "l"(ft.table + j)
-                       : "memory");
-        else
-          ft.pid[lane] = -1;
+        pid = lane < kDecWarps && pos < seen ? table[j] : -1;
+      };
+      int stage = 0;
+      uint32_t parity = 1;  // of the stage's last release; a fresh barrier reports it as done
+      look(first);
+      for (int u = first; u < last; ++u) {
+        const uint8_t* from = src + (int64_t)pid * a.c.page_stride + (int64_t)((pos & (a.c.page_size - 1)) >> 4) * Geo::kBytes;
+        const bool ok = (uint32_t)pid < (uint32_t)a.c.num_pages;
+        const int at = ok ? pos : -1;
+        look(u + 1);
+        const uint32_t there = __ballot_sync(0xffffffffu, ok);
+        mbar_wait<false>(smem_addr(&empty[stage]), parity, err);
+        if (lane < kDecWarps) spos[stage * kDecWarps + lane] = at;
+        __syncwarp();
+        const uint32_t bar = smem_addr(&full[stage]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(there) * Geo::kBytes);
+        __syncwarp();
+        // the blocks of a page that are there are its first ones: one copy
+        const int count = __popc(there >> lane & ((1u << run) - 1u));
+        if (ok && lane % run == 0)
+          bulk_g2s(smem_addr(smem) + (stage * kDecWarps + lane) * Geo::kBytes, from, count * Geo::kBytes, bar);
+        if (++stage == kStages) {
+          stage = 0;
+          parity ^= 1u;
+        }
       }
-    };
-    auto fetch = [&](int stage) {  // copies that round into a free stage
-      const int u = ft.round;
-      if (u >= last) return;
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      const int run = min(a.c.page_size >> 4, kDecWarps);  // blocks per copy
-      const int pos = lane < kDecWarps ? ft.pos[lane] : 0, pid = lane < kDecWarps ? ft.pid[lane] : -1;
-      const bool ok = (uint32_t)pid < (uint32_t)a.c.num_pages;
-      const uint32_t there = __ballot_sync(0xffffffffu, ok);
-      if (lane < kDecWarps) spos[stage * kDecWarps + lane] = ok ? pos : -1;
-      __syncwarp();
-      const uint32_t bar = smem_addr(&full[stage]);
-      if (lane == 0) mbar_arrive_expect_tx(bar, __popc(there) * Geo::kBytes);
-      __syncwarp();
-      // the blocks of a page that are there are its first ones: one copy
-      const int count = __popc(there >> lane & ((1u << run) - 1u));
-      if (ok && lane % run == 0)
-        bulk_g2s(smem_addr(smem) + (stage * kDecWarps + lane) * Geo::kBytes,
-                 a.c.pages + (int64_t)pid * a.c.page_stride + ft.head * a.c.head_stride +
-                     (int64_t)((pos & (a.c.page_size - 1)) >> 4) * Geo::kBytes,
-                 count * Geo::kBytes, bar);
-      __syncwarp();
-      if (lane == 0) ft.round = u + kDecWarps;
-      __syncwarp();
-      look();
-    };
-    look();
-    if (warp < kStages - 1) fetch(warp);
-    int turn = (warp - (kStages - 1) + kDecWarps) % kDecWarps + 1;  // rounds to this warp's next fetch
+    } else {
     int stage = 0;         // of the round at hand
     uint32_t parity = 0;   // of its fill
-
     // where this lane's words lie in a block
     const int at_k = r * Geo::kRow + c * (D / 8), at_p = Geo::kKPar + r * Geo::kParRow;
     const int at_v = Geo::kVOff + c * Geo::kRow + (r ^ ((c >> 1) << 2)) * (D / 16);
@@ -324,7 +298,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
         it.len = q.len;
         it.row0 = q.row0;
       }
-      __syncthreads();
+      compute_sync();
       const int seg_end = min(it.at.item_end, last);
       // ---- the item's columns
       uint32_t qf[NT][D / 8];    // this lane's query operand: column 8 nt + r, its quarter of every group
@@ -448,10 +422,9 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
           }
         }
       };
-      // One block from its scores sc, which the next block's then replace (ahead).  part: some
-      // column does not see some of its tokens.
-      auto block = [&](const uint8_t* blk, int pos, float (&sc)[NT][4], const uint8_t* next, auto part_, auto ahead_) {
-        constexpr bool part = decltype(part_)::value, ahead = decltype(ahead_)::value;
+      // One block from its scores.  part: some column does not see some of its tokens.
+      auto block = [&](const uint8_t* blk, int pos, const float (&sc)[NT][4], auto part_) {
+        constexpr bool part = decltype(part_)::value;
         // params of tokens r and r + 8, values' codes of tokens 2c, 2c + 1, 2c + 8, 2c + 9
         uint32_t vp[2][NG], vw[4][D / 64];
 #pragma unroll
@@ -536,7 +509,6 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
             }
           exponents();
         }
-        if constexpr (ahead) scores(next, sc);
         // ---- weights, their sums, and P s as the second product's operand
         uint32_t pf[NT][NG][2];
 #pragma unroll
@@ -604,18 +576,11 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
         if (pos >= 0) {
           float sc[NT][4];
           scores(blk, sc);
-          if (pos + 16 > least) block(blk, pos, sc, blk, std::true_type(), std::false_type());
-          else block(blk, pos, sc, blk, std::false_type(), std::false_type());
+          if (pos + 16 > least) block(blk, pos, sc, std::true_type());
+          else block(blk, pos, sc, std::false_type());
         }
         __syncwarp();  // every lane is done with the stage
         if (lane == 0) mbar_arrive(smem_addr(&empty[stage]));
-        // the round kStages - 1 on goes where the last one was, once every warp is done with that
-        if (--turn == 0) {
-          turn = kDecWarps;
-          const int to = stage == 0 ? kStages - 1 : stage - 1;
-          if (cu > first && ft.round < last) mbar_wait<false>(smem_addr(&empty[to]), parity ^ (stage == 0 ? 1u : 0u), err);
-          fetch(to);
-        }
         if (++stage == kStages) {
           stage = 0;
           parity ^= 1u;
@@ -648,7 +613,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
                 make_float2(fmaf(acc[j][nt][x], f, oc[nt][g][x]), fmaf(acc[j][nt][2 + x], f, oc[nt][g][x]));
           }
         }
-      __syncthreads();
+      compute_sync();
       const int item0 = it.at.item0, item_end = it.at.item_end;
       const bool whole = seg == item0 && seg_end == item_end;
       // partial results: a CTA's first stretch in slot 0, its last in slot 1
@@ -695,37 +660,42 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
       if (!whole) {  // the CTA that finishes the item last joins its parts
         const int c0 = owner(item0, total, n), c1 = owner(item_end - 1, total, n);
         __threadfence();
-        __syncthreads();
+        compute_sync();
         if (tid == 0) sh_last = atomicAdd(&counters[c0], 1u);
-        __syncthreads();
+        compute_sync();
         if (sh_last == (unsigned)(c1 - c0)) {
           __threadfence();
           // the item began c0's last stretch: its only one if the item begins c0's share
           const int head = 2 * c0 + (item0 == share(total, c0, n) ? 0 : 1);
+          auto slot_of = [&](int y) { return ws + (int64_t)(y == c0 ? head : 2 * y) * kSlot; };
+          // the parts' references first, all at once, into the merge buffer (at most kDecMaxParts of them)
+          for (int x = tid; x < (c1 - c0 + 1) * C; x += kDecWarps * 32) mo[x] = __ldcg(slot_of(c0 + x / C) + C * D + x % C);
+          compute_sync();
           for (int x = tid; x < C * (D / 4); x += kDecWarps * 32) {
             const int col = x / (D / 4), d4 = x % (D / 4);
             float M = kNone, L = 0.0f;
             float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-            for (int y = c0; y <= c1; ++y) M = fmaxf(M, __ldcg(ws + (int64_t)(y == c0 ? head : 2 * y) * kSlot + C * D + col));
-#pragma unroll 4
+            for (int y = 0; y <= c1 - c0; ++y) M = fmaxf(M, mo[y * C + col]);
+#pragma unroll 8
             for (int y = c0; y <= c1; ++y) {
-              const float* src = ws + (int64_t)(y == c0 ? head : 2 * y) * kSlot;
-              const float f = exp2_fast(__ldcg(src + C * D + col) - M);
+              const float* src = slot_of(y);
               const float4 v = __ldcg(reinterpret_cast<const float4*>(src) + x);
+              const float w = __ldcg(src + C * D + C + col), f = exp2_fast(mo[(y - c0) * C + col] - M);
               o.x = fmaf(f, v.x, o.x);
               o.y = fmaf(f, v.y, o.y);
               o.z = fmaf(f, v.z, o.z);
               o.w = fmaf(f, v.w, o.w);
-              L = fmaf(f, __ldcg(src + C * D + C + col), L);
+              L = fmaf(f, w, L);
             }
             finish(col, d4, o, M, L);
           }
           if (tid == 0) counters[c0] = 0;  // for the next call
         }
       }
-      __syncthreads();  // the merge buffer is free
+      compute_sync();  // the merge buffer is free
       seg = seg_end;
+    }
     }
   }
 
@@ -736,7 +706,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, NT == 1 ? 2 : 1)
     const KvSeq q = kv_seq(a.b, s);
     const int lo = a.sel ? gi % a.b.max_new : 0, hi = a.sel ? min(lo + 1, q.rows) : q.rows;
     for (int i = lo; i < hi; ++i)
-      for (int x = tid; x < a.q_heads * (D / 8); x += kDecWarps * 32) {
+      for (int x = tid; x < a.q_heads * (D / 8); x += kDecThreads) {
         const int hq = x / (D / 8);
         *reinterpret_cast<uint4*>(a.out + kv_row_offset(a.b, a.os, s, q.row0, i) + (int64_t)hq * a.os.head + 8 * (x % (D / 8))) =
             make_uint4(0, 0, 0, 0);
@@ -753,9 +723,10 @@ cudaError_t launch_decode(Kv& kv, const KvAttnArgs& a, const DecPlan& p, cudaStr
   const auto kernel = kv_decode_kernel<T, D, G, NT>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
-  const int grid = std::min(kv.sms * (NT == 1 ? 2 : 1), Kv::kMaxParts);
+  const int grid = std::min(kv.sms * (NT == 1 ? 2 : 1), kDecMaxParts);
+  static_assert(kDecMaxParts <= Kv::kMaxParts, "two partial results per CTA");
   static_assert((size_t)C * (D + 2) * sizeof(float) <= Kv::kPartBytes, "partial results fit their slots");
-  kernel<<<grid, kDecWarps * 32, smem, s>>>(a, p, kv.parts(), kv.counters(), kv.err_dev);
+  kernel<<<grid, kDecThreads, smem, s>>>(a, p, kv.parts(), kv.counters(), kv.err_dev);
   return cudaGetLastError();
 }
 
