@@ -43,7 +43,14 @@ namespace {
 #include "kv_operand.cuh"
 
 constexpr int kDecWarps = 8;                         // that compute
-constexpr int kDecThreads = (kDecWarps + 1) * 32;  // and one that fetches
+constexpr int kDecThreads = (kDecWarps + 4) * 32;  // and one that fetches; three only fill its warpgroup
+// Registers, two CTAs per SM for 8 columns and one for 16: the launch's are dealt out
+// again between the warpgroups.
+template <int NT>
+struct DecRegs {
+  static constexpr int kLaunch = NT == 1 ? 80 : 168, kCompute = NT == 1 ? 104 : 232, kFetch = NT == 1 ? 32 : 40;
+  static_assert(2 * kCompute + kFetch <= 3 * kLaunch, "a split above the launch's registers never ends");
+};
 constexpr int kDecMaxParts = kDecWarps * (64 + 4);  // CTAs, so parts of an item, whose references fit the merge buffer
 constexpr float kDecSlack = 4.0f;      // weights reach 2^4
 constexpr float kDecValues = 8192.0f;  // bound of |c| + 8 s times 2^-E
@@ -148,7 +155,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(ml + kDecWarps * C);             // [stage]
   uint64_t* empty = full + kStages;                                             // [stage]
   int* spos = reinterpret_cast<int*>(empty + kStages);                          // [stage][block] its position, -1: not there
-  __shared__ int sh_sum[kDecWarps + 1];
+  __shared__ int sh_sum[kDecThreads / 32];
   __shared__ int sh_base, sh_group;
   __shared__ Item sh_item;
   __shared__ unsigned sh_last;
@@ -213,7 +220,9 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
     __syncthreads();
     const Cursor seed{sh_group - 1, sh_base, 0, 0, 0, 0};
 
-    if (warp == kDecWarps) {
+    if (warp >= kDecWarps) {
+      set_registers<DecRegs<NT>::kFetch, false>();
+      if (warp == kDecWarps) {
       // ---- fetching: lane b < 8 looks after block b of each round
       Cursor pc = seed;
       const int per_page = a.c.page_shift - 4;
@@ -274,7 +283,9 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
           parity ^= 1u;
         }
       }
+      }
     } else {
+    set_registers<DecRegs<NT>::kCompute, true>();
     int stage = 0;         // of the round at hand
     uint32_t parity = 0;   // of its fill
     // where this lane's words lie in a block
@@ -721,6 +732,8 @@ cudaError_t launch_decode(Kv& kv, const KvAttnArgs& a, const DecPlan& p, cudaStr
   const size_t smem = (size_t)kDecStages<D, G> * (kDecWarps * (KvGeom<D, G>::kBytes + 4) + 16) +
                       (size_t)kDecWarps * C * (D + 6) * sizeof(float);
   const auto kernel = kv_decode_kernel<T, D, G, NT>;
+  static const bool registers_fit = brings_registers(reinterpret_cast<const void*>(kernel), DecRegs<NT>::kLaunch);
+  if (!registers_fit) return cudaErrorInvalidKernelImage;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
   const int grid = std::min(kv.sms * (NT == 1 ? 2 : 1), kDecMaxParts);

@@ -33,3 +33,15 @@ __device__ __forceinline__ uint32_t centred_pair(uint32_t x) {
   }
   return d;
 }
+
+// Registers of a warpgroup's threads from here on.
+template <int R, bool Inc>
+__device__ __forceinline__ void set_registers() {
+  if constexpr (Inc) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+// Whether a launch of `kernel` brings the registers per thread that its split deals out.
+inline bool brings_registers(const void* kernel, int regs) {
+  cudaFuncAttributes f{};
+  return cudaFuncGetAttributes(&f, kernel) == cudaSuccess && f.numRegs == regs;
+}

@@ -44,11 +44,6 @@ constexpr int kPrThreads = 512;  // four warpgroups; warps 13-15 only fill their
 // 128 threads x (176 + 176 + 112 + 48) = 512 x 128.
 constexpr int kPrRegs = 128, kPrSoftRegs = 176, kPrDequantRegs = 112, kPrMmaRegs = 48;
 static_assert(2 * kPrSoftRegs + kPrDequantRegs + kPrMmaRegs == 4 * kPrRegs, "a split above the launch's registers never ends");
-template <int R, bool Inc>
-__device__ __forceinline__ void set_registers() {
-  if constexpr (Inc) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
-  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
-}
 constexpr int kPrTile = 128;  // rows of a row tile, tokens of a token tile
 // weights are 2^(score - reference): the reference is set kPrDrop below the largest score and
 // raised when a tile's weights sum to kPrLimit; so no weight passes 2^15 and fp16 holds those
@@ -622,10 +617,7 @@ template <typename T, int D, int G>
 cudaError_t launch_prompt(Kv& kv, const PromptArgs& p, unsigned ctas, cudaStream_t s) {
   const size_t smem = 1024 + (size_t)6 * kPrTile * D * 2;
   const auto kernel = kv_prompt_kernel<T, D, G>;
-  static const bool registers_fit = [&] {  // what the split needs is what a launch brings
-    cudaFuncAttributes f{};
-    return cudaFuncGetAttributes(&f, reinterpret_cast<const void*>(kernel)) == cudaSuccess && f.numRegs == kPrRegs;
-  }();
+  static const bool registers_fit = brings_registers(reinterpret_cast<const void*>(kernel), kPrRegs);
   if (!registers_fit) return cudaErrorInvalidKernelImage;
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
