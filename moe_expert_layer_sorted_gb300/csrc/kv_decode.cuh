@@ -55,6 +55,13 @@ constexpr int kDecMaxParts = kDecWarps * (64 + 4);  // CTAs, so parts of an item
 constexpr float kDecSlack = 4.0f;      // weights reach 2^4
 constexpr float kDecValues = 8192.0f;  // bound of |c| + 8 s times 2^-E
 
+// Adds 1; what this CTA wrote before (seen by this thread through a barrier) is visible to whoever
+// reads the new count this way, and the other way round.
+__device__ __forceinline__ unsigned add_acq_rel(unsigned* p) {
+  unsigned d;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(d) : "l"(p) : "memory");
+  return d;
+}
 __device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kDecWarps * 32) : "memory"); }
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -670,12 +677,10 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
       }
       if (!whole) {  // the CTA that finishes the item last joins its parts
         const int c0 = owner(item0, total, n), c1 = owner(item_end - 1, total, n);
-        __threadfence();
-        compute_sync();
-        if (tid == 0) sh_last = atomicAdd(&counters[c0], 1u);
+        compute_sync();  // every thread's part is written: one release covers them
+        if (tid == 0) sh_last = add_acq_rel(&counters[c0]);
         compute_sync();
         if (sh_last == (unsigned)(c1 - c0)) {
-          __threadfence();
           // the item began c0's last stretch: its only one if the item begins c0's share
           const int head = 2 * c0 + (item0 == share(total, c0, n) ? 0 : 1);
           auto slot_of = [&](int y) { return ws + (int64_t)(y == c0 ? head : 2 * y) * kSlot; };

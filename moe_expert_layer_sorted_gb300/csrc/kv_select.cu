@@ -19,7 +19,7 @@ using namespace moe;
 namespace {
 
 constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
-constexpr int kSelPages = 64;     // pages per scoring CTA
+constexpr int kSelPages = 32;     // pages per scoring CTA
 constexpr int kSelHeads = 16;     // kv heads per scoring CTA
 constexpr int kSelOwn = 512;      // rows with at most this many pages are scored and picked by one CTA
 constexpr uint32_t kAlways = 0xffffffffu;  // above the key of +infinity
@@ -51,15 +51,24 @@ __device__ __forceinline__ Row row_of(const KvSelectArgs& a, int64_t r) {
   return w;
 }
 
-// qs[d] of one head.
+// qs[8 o ..] of one head, eight channels.
 template <typename T, int D>
-__device__ __forceinline__ void head_sum(const KvSelectArgs& a, const Row& w, int h, int d, float* qs) {
+__device__ __forceinline__ void head_sum(const KvSelectArgs& a, const Row& w, int h, int o, float* qs) {
   const int per = a.q_heads / a.c.heads;
-  const uint16_t* src = a.q + kv_row_offset(a.b, a.qs, w.s, w.q.row0, w.i) + (int64_t)h * per * a.qs.head + d;
-  float v = KvType<T>::to_f(src[0]);
-#pragma unroll 4
-  for (int x = 1; x < per; ++x) v = __fadd_rn(v, KvType<T>::to_f(src[x * a.qs.head]));
-  qs[d] = v;
+  const uint16_t* src = a.q + kv_row_offset(a.b, a.qs, w.s, w.q.row0, w.i) + (int64_t)h * per * a.qs.head + 8 * o;
+  float v[8];
+#pragma unroll 8
+  for (int x = 0; x < per; ++x) {
+    const uint4 r = __ldg(reinterpret_cast<const uint4*>(src + x * a.qs.head));
+    const uint32_t c[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[2 * e] = x ? __fadd_rn(v[2 * e], KvType<T>::lo(c[e])) : KvType<T>::lo(c[e]);
+      v[2 * e + 1] = x ? __fadd_rn(v[2 * e + 1], KvType<T>::hi(c[e])) : KvType<T>::hi(c[e]);
+    }
+  }
+  *reinterpret_cast<float4*>(qs + 8 * o) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(qs + 8 * o + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
 
 // Score of a page and head by D / 8 neighbouring lanes, eight channels each.
@@ -85,10 +94,11 @@ __device__ __forceinline__ float page_score(const float* qs, uint4 hi, uint4 lo)
 
 // Keys of pages [j0, j1) and heads [h0, h1) of a row: units (page, head), heads
 // fastest as the bounds lie, D / 8 lanes a unit, four units of each asked for at once.
-// qs: [head - h0][D]; keys[(head - h0) * stride + page - j0].
+// ids: [page - j0] page numbers, -1 where there is none; qs: [head - h0][D];
+// keys[(head - h0) * stride + page - j0].
 template <typename T, int D>
 __device__ __forceinline__ void score_pages(const KvSelectArgs& a, const Row& w, int j0, int j1, int h0, int h1,
-                                            const float* qs, uint32_t* keys, int64_t stride) {
+                                            const int32_t* ids, const float* qs, uint32_t* keys, int64_t stride) {
   constexpr int L = D / 8, kGroups = kSelThreads / L, kUnroll = 4;
   const int l = threadIdx.x % L, grp = threadIdx.x / L, nh = h1 - h0;
   const int units = (j1 - j0) * nh;
@@ -101,7 +111,7 @@ __device__ __forceinline__ void score_pages(const KvSelectArgs& a, const Row& w,
       ok[x] = false;
       if (u < units) {
         const int j = j0 + u / nh, h = h0 + u % nh;
-        const int64_t pid = kv_page(a.c, a.b, w.s, j);
+        const int64_t pid = ids[j - j0];
         ok[x] = pid >= 0;
         if (ok[x]) {
           const uint4* ends = reinterpret_cast<const uint4*>(a.c.bounds + (pid * a.c.heads + h) * (2 * D));
@@ -140,21 +150,37 @@ __device__ __forceinline__ int cta_scan(int v, int* sh) {
   return v;
 }
 
-// The list of a row and head from its n > budget keys.
+// The list of a row and head from its n > budget keys.  KEYS > 0: every thread holds
+// the keys tid, tid + 256, ... in registers (n <= 256 KEYS); 0: they are read each time.
+template <int KEYS>
 __device__ __forceinline__ void pick(const KvSelectArgs& a, const uint32_t* keys, int n, int32_t* out) {
   __shared__ uint32_t sh_lo[kSelWarps], sh_hi[kSelWarps];
   __shared__ int sh_cnt[2][kSelWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t held[KEYS > 0 ? KEYS : 1];  // kAlways and the places past n as 0: below every key that counts
+  if constexpr (KEYS > 0) {
+#pragma unroll
+    for (int x = 0; x < KEYS; ++x) {
+      const int j = tid + x * kSelThreads;
+      held[x] = j < n ? keys[j] : 0u;
+      if (held[x] == kAlways) held[x] = 0u;
+    }
+  }
   int need = a.budget - a.first - a.last;  // pages to take by score
   uint32_t tau = kAlways - 1;              // keys above are taken, and `need` of those equal, lowest pages first
   if (need > 0) {
     uint32_t lo = kAlways, hi = 0;  // of the keys that count
-    for (int j = tid; j < n; j += kSelThreads) {
-      const uint32_t k = keys[j];
-      if (k != kAlways) {
+    auto widen = [&](uint32_t k) {
+      if (k != 0u && k != kAlways) {
         lo = min(lo, k);
         hi = max(hi, k);
       }
+    };
+    if constexpr (KEYS > 0) {
+#pragma unroll
+      for (int x = 0; x < KEYS; ++x) widen(held[x]);
+    } else {
+      for (int j = tid; j < n; j += kSelThreads) widen(keys[j]);
     }
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
@@ -173,10 +199,15 @@ __device__ __forceinline__ void pick(const KvSelectArgs& a, const uint32_t* keys
     for (int it = 0; lo < hi; it ^= 1) {
       const uint32_t mid = lo + (hi - lo + 1) / 2;
       int c = 0;
+      if constexpr (KEYS > 0) {
+#pragma unroll
+        for (int x = 0; x < KEYS; ++x) c += held[x] >= mid;
+      } else {
 #pragma unroll 4
-      for (int j = tid; j < n; j += kSelThreads) {
-        const uint32_t k = keys[j];
-        c += k >= mid && k != kAlways;
+        for (int j = tid; j < n; j += kSelThreads) {
+          const uint32_t k = keys[j];
+          c += k >= mid && k != kAlways;
+        }
       }
       c = __reduce_add_sync(0xffffffffu, c);
       if (lane == 0) sh_cnt[it][warp] = c;  // two buffers: one barrier per step
@@ -203,8 +234,9 @@ __device__ __forceinline__ void pick(const KvSelectArgs& a, const uint32_t* keys
   const int b = min(tid * run, n), e = min(b + run, n);
   int eq = 0, gt = 0;
   for (int j = b; j < e; ++j) {
-    eq += keys[j] == tau;
-    gt += keys[j] > tau;
+    const uint32_t k = keys[j];
+    eq += k == tau;
+    gt += k > tau;
   }
   int rank = cta_scan(eq, sh_cnt[0]) - eq;
   const int taken = gt + min(eq, max(need - rank, 0));
@@ -228,16 +260,18 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_constant__ KvSelectArgs a) {
   __shared__ __align__(16) float qs[D];
   __shared__ uint32_t keys[kSelOwn];
+  __shared__ int32_t ids[kSelOwn];
   const int h = blockIdx.x % a.c.heads;
   const Row w = row_of(a, blockIdx.x / a.c.heads);
   if (w.i >= w.q.rows) return;
   int32_t* out = list_of(a, w, h);
   if (w.pages <= a.budget) return list_all(a, w, out);
-  if (threadIdx.x < D) head_sum<T, D>(a, w, h, threadIdx.x, qs);
+  for (int j = threadIdx.x; j < w.pages; j += kSelThreads) ids[j] = (int32_t)kv_page(a.c, a.b, w.s, j);
+  if (threadIdx.x < D / 8) head_sum<T, D>(a, w, h, threadIdx.x, qs);
   __syncthreads();
-  score_pages<T, D>(a, w, 0, w.pages, h, h + 1, qs, keys, 0);
+  score_pages<T, D>(a, w, 0, w.pages, h, h + 1, ids, qs, keys, 0);
   __syncthreads();
-  pick(a, keys, w.pages, out);
+  pick<kSelOwn / kSelThreads>(a, keys, w.pages, out);
 }
 
 // Scores: one CTA per (row, kSelPages pages, kSelHeads heads).
@@ -245,23 +279,28 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kSelThreads) kv_score_kernel(const __grid_constant__ KvSelectArgs a, int64_t first_row,
                                                                int chunks, uint32_t* __restrict__ keys) {
   __shared__ __align__(16) float qs[kSelHeads * D];
+  __shared__ int32_t ids[kSelPages];
+  static_assert(kSelPages <= kSelThreads, "one page number per thread");
   const int64_t r = blockIdx.x / chunks;
   const Row w = row_of(a, first_row + r);
   const int j0 = blockIdx.x % chunks * kSelPages, j1 = min(j0 + kSelPages, w.pages);
   if (w.pages <= a.budget || j0 >= j1) return;
   const int h0 = blockIdx.y * kSelHeads, h1 = min(h0 + kSelHeads, a.c.heads);
-  for (int x = threadIdx.x; x < (h1 - h0) * D; x += kSelThreads) head_sum<T, D>(a, w, h0 + x / D, x % D, qs + x / D * D);
+  if (threadIdx.x < j1 - j0) ids[threadIdx.x] = (int32_t)kv_page(a.c, a.b, w.s, j0 + threadIdx.x);
+  for (int x = threadIdx.x; x < (h1 - h0) * (D / 8); x += kSelThreads)
+    head_sum<T, D>(a, w, h0 + x / (D / 8), x % (D / 8), qs + x / (D / 8) * D);
   __syncthreads();
-  score_pages<T, D>(a, w, j0, j1, h0, h1, qs, keys + (r * a.c.heads + h0) * a.b.table_pages + j0, a.b.table_pages);
+  score_pages<T, D>(a, w, j0, j1, h0, h1, ids, qs, keys + (r * a.c.heads + h0) * a.b.table_pages + j0, a.b.table_pages);
 }
 // ... and the choice: one CTA per (row, head).
+template <int KEYS>
 __global__ void __launch_bounds__(kSelThreads) kv_pick_kernel(const __grid_constant__ KvSelectArgs a, int64_t first_row,
                                                               const uint32_t* __restrict__ keys) {
   const int h = blockIdx.x % a.c.heads;
   const Row w = row_of(a, first_row + blockIdx.x / a.c.heads);
   if (w.i >= w.q.rows) return;
   if (w.pages <= a.budget) return list_all(a, w, list_of(a, w, h));
-  pick(a, keys + (int64_t)blockIdx.x * a.b.table_pages, w.pages, list_of(a, w, h));
+  pick<KEYS>(a, keys + (int64_t)blockIdx.x * a.b.table_pages, w.pages, list_of(a, w, h));
 }
 
 template <typename T, int D>
@@ -280,7 +319,8 @@ cudaError_t select(Kv& kv, const KvSelectArgs& a, cudaStream_t s) {
   for (int64_t r = 0; r < rows; r += step) {  // as many rows at a time as the workspace holds scores for
     const int64_t n = std::min(step, rows - r);
     kv_score_kernel<T, D><<<dim3((unsigned)(n * chunks), head_tiles), kSelThreads, 0, s>>>(a, r, chunks, keys);
-    kv_pick_kernel<<<(unsigned)(n * a.c.heads), kSelThreads, 0, s>>>(a, r, keys);
+    const auto pick_kernel = a.b.table_pages <= 16 * kSelThreads ? kv_pick_kernel<16> : kv_pick_kernel<0>;
+    pick_kernel<<<(unsigned)(n * a.c.heads), kSelThreads, 0, s>>>(a, r, keys);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
