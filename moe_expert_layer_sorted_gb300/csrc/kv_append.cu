@@ -17,16 +17,17 @@ using namespace moe;
 
 namespace {
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+// Larger halves of two pairs of the cache's type, NaN where either is.
+template <typename T>
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float d;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
+constexpr uint32_t kNegate = 0x80008000u;
 
 // One CTA per (sequence, page it writes to, head), the first half of its warps
 // on the keys and the second on the values; D / 8 lanes hold a row, eight
@@ -37,7 +38,7 @@ __global__ void kv_append_kernel(KvView c, KvBatch b, const uint16_t* __restrict
                                  const uint16_t* __restrict__ v, KvRows vs, int pages_per_seq) {
   using Geo = KvGeom<D, G>;
   constexpr int kLanes = D / 8, kTok = 32 / kLanes;  // lanes per row, rows per warp
-  extern __shared__ float red[];                     // [key warps][max, min][D]
+  extern __shared__ uint32_t red[];                  // [key warps][max, -min][D / 2] pairs
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = blockDim.x >> 6;
   const int h = blockIdx.x % c.heads;
   const int u = blockIdx.x / c.heads, s = u / pages_per_seq;
@@ -55,17 +56,22 @@ __global__ void kv_append_kernel(KvView c, KvBatch b, const uint16_t* __restrict
   const uint16_t* src = (keys ? k : v) + kv_row_offset(b, keys ? ks : vs, s, q.row0, 0) + h * (keys ? ks.head : vs.head);
   const int64_t stride = keys ? ks.row : vs.row;
   const int w = lane % kLanes, g = 8 * w / G;
-  float top[8], bot[8];
+  // largest stored keys, and largest of the negated ones, as pairs of the cache's type: what is
+  // rounded after the maximum is the maximum of the rounded
+  const uint32_t least = (uint32_t)KvType<T>::from_f(-__int_as_float(0x7f800000)) * 0x10001u;
+  uint32_t top[4], bot[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    top[e] = -__int_as_float(0x7f800000);
-    bot[e] = __int_as_float(0x7f800000);
-  }
-  for (int64_t p = begin + (warp % half) * kTok; p < end; p += half * kTok) {
-    const int64_t pos = p + lane / kLanes;
+  for (int e = 0; e < 4; ++e) top[e] = bot[e] = least;
+  const int step = half * kTok;
+  uint4 next = make_uint4(0, 0, 0, 0);
+  const uint16_t* row = src + (begin + (warp % half) * kTok + lane / kLanes - first) * stride + 8 * w;
+  int64_t pos = begin + (warp % half) * kTok + lane / kLanes;
+  if (pos < end) next = *reinterpret_cast<const uint4*>(row);
+  for (; __any_sync(0xffffffffu, pos < end); pos += step) {  // the next row arrives while this one is turned
     const bool live = pos < end;
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (live) raw = *reinterpret_cast<const uint4*>(src + (pos - first) * stride + 8 * w);
+    const uint4 raw = next;
+    row += step * stride;
+    if (pos + step < end) next = *reinterpret_cast<const uint4*>(row);
     const uint32_t r4[4] = {raw.x, raw.y, raw.z, raw.w};
     float x[8];
 #pragma unroll
@@ -73,37 +79,57 @@ __global__ void kv_append_kernel(KvView c, KvBatch b, const uint16_t* __restrict
       x[2 * i] = KvType<T>::lo(r4[i]);
       x[2 * i + 1] = KvType<T>::hi(r4[i]);
     }
-    float lo = x[0], hi = x[0], zero = 0.0f;
+    // the group's largest element and the largest of its negated ones, exact in 16 bits
+    uint32_t hl = max_pair<T>(max_pair<T>(r4[0], r4[1]), max_pair<T>(r4[2], r4[3]));
+    const uint32_t neg = max_pair<T>(max_pair<T>(r4[0] ^ kNegate, r4[1] ^ kNegate), max_pair<T>(r4[2] ^ kNegate, r4[3] ^ kNegate));
+    hl = max_pair<T>(__byte_perm(hl, neg, 0x5410), __byte_perm(hl, neg, 0x7632));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      lo = fminf(lo, x[e]);
-      hi = fmaxf(hi, x[e]);
-      zero = fmaf(x[e], 0.0f, zero);  // NaN where an element is not finite
-    }
-    bool bad = !(zero == 0.0f);
-#pragma unroll
-    for (int o = 1; o < G / 8; o <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-      bad |= __shfl_xor_sync(0xffffffffu, (int)bad, o) != 0;
-    }
+    for (int o = 1; o < G / 8; o <<= 1) hl = max_pair<T>(hl, __shfl_xor_sync(0xffffffffu, hl, o));
+    const float hi = KvType<T>::lo(hl), lo = -KvType<T>::hi(hl);
+    const bool bad = !(fabsf(hi) < __int_as_float(0x7f800000) && fabsf(lo) < __int_as_float(0x7f800000));
     uint16_t sb = KvType<T>::from_f(__fsub_rn(__fdiv_rn(hi, 15.0f), __fdiv_rn(lo, 15.0f)));
     uint16_t cb = KvType<T>::from_f(fmaf(8.0f, KvType<T>::to_f(sb), lo));  // 8 s is exact
     if (bad) {
       sb = 0;
       cb = 0x7fff;  // NaN in both types
     }
-    const float sf = KvType<T>::to_f(sb), cf = KvType<T>::to_f(cb);
-    uint32_t word = 0;
+    const float sf = KvType<T>::to_f(sb), cf = KvType<T>::to_f(cb), inv = __frcp_rn(sf);
+    // rint of the quotients: (x - c) / s as a product with the reciprocal, rounded to a whole
+    // number by an addition of 1.5 2^23, is right for all but quotients that near a half (the
+    // product is within 2^-20 of one that is not cut to -8 or 7); those rows are divided.  s = 0
+    // gives NaN, then 0.
+    constexpr float kWhole = 12582912.0f;
+    float q[8], worst = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      float q8 = sf > 0.0f ? rintf(__fdiv_rn(__fsub_rn(x[e], cf), sf)) : 0.0f;
-      q8 = fminf(fmaxf(q8, -8.0f), 7.0f);
-      word |= (uint32_t)((int)q8 + 8) << (4 * ((e >> 1) + 4 * (e & 1)));
-      if (live && keys) {
-        const float y = fmaf(sf, q8, cf);  // s q8 is exact
-        top[e] = max_nan(top[e], y);
-        bot[e] = min_nan(bot[e], y);
+      const float num = __fsub_rn(x[e], cf);
+      q[e] = __fsub_rn(fmaf(num, inv, kWhole), kWhole);
+      const float off = fabsf(fmaf(num, inv, -q[e]));
+      worst = off < 0.49999f ? worst : 1.0f;
+    }
+    if (worst != 0.0f) {
+#pragma unroll 1
+      for (int e = 0; e < 8; ++e) {
+        const float num = __fsub_rn(e < 4 ? (e < 2 ? (e ? x[1] : x[0]) : (e == 2 ? x[2] : x[3]))
+                                          : (e < 6 ? (e == 4 ? x[4] : x[5]) : (e == 6 ? x[6] : x[7])), cf);
+        const float y = sf > 0.0f ? rintf(__fdiv_rn(num, sf)) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = i == e ? y : q[i];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = fminf(fmaxf(q[e], -8.0f), 7.0f);
+    // the word's half-words, each a whole number below 2^16 in fp32's low bits
+    auto half_word = [&](int e) {
+      return __float_as_uint(fmaf(q[e + 6], 4096.0f, fmaf(q[e + 4], 256.0f, fmaf(q[e + 2], 16.0f, q[e]))) + (kWhole + 34952.0f));
+    };
+    uint32_t word = __byte_perm(half_word(0), half_word(1), 0x5410);
+    if (live && keys) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t y = KvType<T>::pack(fmaf(sf, q[2 * e], cf), fmaf(sf, q[2 * e + 1], cf));  // s q is exact
+        top[e] = max_pair<T>(top[e], y);
+        bot[e] = max_pair<T>(bot[e], y ^ kNegate);
       }
     }
     uint32_t other = 0;  // groups of 32: the values' words join half a word of two neighbouring groups
@@ -131,28 +157,26 @@ __global__ void kv_append_kernel(KvView c, KvBatch b, const uint16_t* __restrict
   if (!c.bounds) return;
   if (keys) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < 4; ++e) {
 #pragma unroll
       for (int o = kLanes; o < 32; o <<= 1) {
-        top[e] = max_nan(top[e], __shfl_xor_sync(0xffffffffu, top[e], o));
-        bot[e] = min_nan(bot[e], __shfl_xor_sync(0xffffffffu, bot[e], o));
+        top[e] = max_pair<T>(top[e], __shfl_xor_sync(0xffffffffu, top[e], o));
+        bot[e] = max_pair<T>(bot[e], __shfl_xor_sync(0xffffffffu, bot[e], o));
       }
       if (lane < kLanes) {
-        red[(warp * 2) * D + 8 * w + e] = top[e];
-        red[(warp * 2 + 1) * D + 8 * w + e] = bot[e];
+        red[warp * D + 4 * w + e] = top[e];
+        red[warp * D + D / 2 + 4 * w + e] = bot[e];
       }
     }
   }
   __syncthreads();
-  uint16_t* ends = c.bounds + (pid * c.heads + h) * (2 * D);
-  for (int i = threadIdx.x; i < 2 * D; i += blockDim.x) {
-    float y = red[i];
-    for (int ww = 1; ww < half; ++ww) y = i < D ? max_nan(y, red[ww * 2 * D + i]) : min_nan(y, red[ww * 2 * D + i]);
-    if (begin > (j << c.page_shift)) {  // the page held tokens before
-      const float z = KvType<T>::to_f(ends[i]);
-      y = i < D ? max_nan(y, z) : min_nan(y, z);
-    }
-    ends[i] = KvType<T>::from_f(y);
+  uint32_t* ends = reinterpret_cast<uint32_t*>(c.bounds + (pid * c.heads + h) * (2 * D));  // [max, min][D / 2] pairs
+  for (int i = threadIdx.x; i < D; i += blockDim.x) {
+    const uint32_t flip = i < D / 2 ? 0u : kNegate;  // minima as negated maxima
+    uint32_t y = red[i];
+    for (int ww = 1; ww < half; ++ww) y = max_pair<T>(y, red[ww * D + i]);
+    if (begin > (j << c.page_shift)) y = max_pair<T>(y, ends[i] ^ flip);  // the page held tokens before
+    ends[i] = y ^ flip;
   }
 }
 
@@ -223,7 +247,7 @@ cudaError_t moe::kv_append(const Kv& kv, const KvView& c, const KvBatch& b, cons
   const int half = b.max_new == 1 ? 1 : 4;  // key warps
   cudaError_t e = cudaSuccess;
   KV_DISPATCH(kv.d, {
-    kv_append_kernel<T, D, G><<<(unsigned)ctas, half * 64, half * 2 * D * sizeof(float), s>>>(c, b, k, ks, v, vs, per_seq);
+    kv_append_kernel<T, D, G><<<(unsigned)ctas, half * 64, half * D * sizeof(uint32_t), s>>>(c, b, k, ks, v, vs, per_seq);
     e = cudaGetLastError();
   });
   return e;

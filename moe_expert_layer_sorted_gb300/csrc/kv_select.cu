@@ -92,43 +92,39 @@ __device__ __forceinline__ float page_score(const float* qs, uint4 hi, uint4 lo)
   return s;
 }
 
-// Keys of pages [j0, j1) and heads [h0, h1) of a row: units (page, head), heads
-// fastest as the bounds lie, D / 8 lanes a unit, four units of each asked for at once.
-// ids: [page - j0] page numbers, -1 where there is none; qs: [head - h0][D];
-// keys[(head - h0) * stride + page - j0].
-template <typename T, int D>
+// Keys of pages [j0, j1) and heads [h0, h1) of a row: D / 8 lanes take a page of every
+// kSelThreads / (D / 8), and of it four heads at once (HEADS), or they take one head (h0)
+// of four pages at once.  ids: [page - j0] page numbers, -1 where there is none; qs:
+// [head - h0][D]; keys[(head - h0) * stride + page - j0].
+template <typename T, int D, bool HEADS>
 __device__ __forceinline__ void score_pages(const KvSelectArgs& a, const Row& w, int j0, int j1, int h0, int h1,
                                             const int32_t* ids, const float* qs, uint32_t* keys, int64_t stride) {
-  constexpr int L = D / 8, kGroups = kSelThreads / L, kUnroll = 4;
-  const int l = threadIdx.x % L, grp = threadIdx.x / L, nh = h1 - h0;
-  const int units = (j1 - j0) * nh;
-  for (int u0 = 0; u0 < units; u0 += kGroups * kUnroll) {
-    uint4 hi[kUnroll], lo[kUnroll];
-    bool ok[kUnroll];
+  constexpr int L = D / 8, kGroups = kSelThreads / L, kAtOnce = 4;
+  const int l = threadIdx.x % L, grp = threadIdx.x / L, nh = HEADS ? h1 - h0 : 1, np = j1 - j0;
+  for (int p0 = 0; p0 < np; p0 += kGroups * (HEADS ? 1 : kAtOnce)) {  // every lane goes round: lanes of a group shuffle
+    for (int x0 = 0; x0 < nh; x0 += kAtOnce) {
+      uint4 hi[kAtOnce], lo[kAtOnce];
+      bool ok[kAtOnce];
 #pragma unroll
-    for (int x = 0; x < kUnroll; ++x) {
-      const int u = u0 + x * kGroups + grp;
-      ok[x] = false;
-      if (u < units) {
-        const int j = j0 + u / nh, h = h0 + u % nh;
-        const int64_t pid = ids[j - j0];
+      for (int x = 0; x < kAtOnce; ++x) {
+        const int p = p0 + grp + (HEADS ? 0 : x * kGroups), h = HEADS ? x0 + x : 0;
+        const int32_t pid = p < np && h < nh ? ids[p] : -1;
         ok[x] = pid >= 0;
+        hi[x] = lo[x] = make_uint4(0, 0, 0, 0);
         if (ok[x]) {
-          const uint4* ends = reinterpret_cast<const uint4*>(a.c.bounds + (pid * a.c.heads + h) * (2 * D));
+          const uint4* ends = reinterpret_cast<const uint4*>(a.c.bounds + ((int64_t)pid * a.c.heads + h0 + h) * (2 * D));
           hi[x] = __ldg(ends + l);
           lo[x] = __ldg(ends + L + l);
         }
       }
-      if (!ok[x]) hi[x] = lo[x] = make_uint4(0, 0, 0, 0);
-    }
 #pragma unroll
-    for (int x = 0; x < kUnroll; ++x) {
-      const int u = u0 + x * kGroups + grp;
-      const int j = j0 + u / nh, h = u % nh;
-      const float s = page_score<T, D>(qs + h * D, hi[x], lo[x]);
-      if (l == 0 && u < units)
-        keys[h * stride + j - j0] =
-            j < a.first || j >= w.pages - a.last ? kAlways : score_key(ok[x] ? s : -__int_as_float(0x7f800000));
+      for (int x = 0; x < kAtOnce; ++x) {
+        const int p = p0 + grp + (HEADS ? 0 : x * kGroups), h = HEADS ? x0 + x : 0, j = j0 + p;
+        const float s = page_score<T, D>(qs + (HEADS ? min(h, nh - 1) : 0) * D, hi[x], lo[x]);
+        if (l == 0 && p < np && h < nh)
+          keys[h * stride + p] =
+              j < a.first || j >= w.pages - a.last ? kAlways : score_key(ok[x] ? s : -__int_as_float(0x7f800000));
+      }
     }
   }
 }
@@ -269,7 +265,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
   for (int j = threadIdx.x; j < w.pages; j += kSelThreads) ids[j] = (int32_t)kv_page(a.c, a.b, w.s, j);
   if (threadIdx.x < D / 8) head_sum<T, D>(a, w, h, threadIdx.x, qs);
   __syncthreads();
-  score_pages<T, D>(a, w, 0, w.pages, h, h + 1, ids, qs, keys, 0);
+  score_pages<T, D, false>(a, w, 0, w.pages, h, h + 1, ids, qs, keys, 0);
   __syncthreads();
   pick<kSelOwn / kSelThreads>(a, keys, w.pages, out);
 }
@@ -290,7 +286,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_score_kernel(const __grid_cons
   for (int x = threadIdx.x; x < (h1 - h0) * (D / 8); x += kSelThreads)
     head_sum<T, D>(a, w, h0 + x / (D / 8), x % (D / 8), qs + x / (D / 8) * D);
   __syncthreads();
-  score_pages<T, D>(a, w, j0, j1, h0, h1, ids, qs, keys + (r * a.c.heads + h0) * a.b.table_pages + j0, a.b.table_pages);
+  score_pages<T, D, true>(a, w, j0, j1, h0, h1, ids, qs, keys + (r * a.c.heads + h0) * a.b.table_pages + j0, a.b.table_pages);
 }
 // ... and the choice: one CTA per (row, head).
 template <int KEYS>
