@@ -29,6 +29,24 @@ __device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
 }
 constexpr uint32_t kNegate = 0x80008000u;
 
+// x / 15 rounded to nearest: the product with the reciprocal, corrected once, is the division's
+// result for every finite 16-bit x (compared for all of them).
+__device__ __forceinline__ float over15(float x) {
+  constexpr float kInv = 1.0f / 15.0f;
+  const float q = __fmul_rn(x, kInv);
+  return fmaf(fmaf(-15.0f, q, x), kInv, q);
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float reciprocal(float x) {  // within an ulp; infinite for a subnormal
+  float d;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
+  return d;
+}
+
 // One CTA per (sequence, page it writes to, head), the first half of its warps
 // on the keys and the second on the values; D / 8 lanes hold a row, eight
 // channels each, so that a lane makes one code word.  The page is the CTA's
@@ -63,15 +81,17 @@ __global__ void kv_append_kernel(KvView c, KvBatch b, const uint16_t* __restrict
 #pragma unroll
   for (int e = 0; e < 4; ++e) top[e] = bot[e] = least;
   const int step = half * kTok;
+  // offsets in the page
+  const int p_end = (int)(end - (j << c.page_shift));
+  int off = (int)(begin - (j << c.page_shift)) + (warp % half) * kTok + lane / kLanes;
+  const uint16_t* row = src + ((j << c.page_shift) + off - first) * stride + 8 * w;
   uint4 next = make_uint4(0, 0, 0, 0);
-  const uint16_t* row = src + (begin + (warp % half) * kTok + lane / kLanes - first) * stride + 8 * w;
-  int64_t pos = begin + (warp % half) * kTok + lane / kLanes;
-  if (pos < end) next = *reinterpret_cast<const uint4*>(row);
-  for (; __any_sync(0xffffffffu, pos < end); pos += step) {  // the next row arrives while this one is turned
-    const bool live = pos < end;
+  if (off < p_end) next = *reinterpret_cast<const uint4*>(row);
+  for (; __any_sync(0xffffffffu, off < p_end); off += step) {  // the next row arrives while this one is turned
+    const bool live = off < p_end;
     const uint4 raw = next;
     row += step * stride;
-    if (pos + step < end) next = *reinterpret_cast<const uint4*>(row);
+    if (off + step < p_end) next = *reinterpret_cast<const uint4*>(row);
     const uint32_t r4[4] = {raw.x, raw.y, raw.z, raw.w};
     float x[8];
 #pragma unroll
@@ -87,32 +107,31 @@ __global__ void kv_append_kernel(KvView c, KvBatch b, const uint16_t* __restrict
     for (int o = 1; o < G / 8; o <<= 1) hl = max_pair<T>(hl, __shfl_xor_sync(0xffffffffu, hl, o));
     const float hi = KvType<T>::lo(hl), lo = -KvType<T>::hi(hl);
     const bool bad = !(fabsf(hi) < __int_as_float(0x7f800000) && fabsf(lo) < __int_as_float(0x7f800000));
-    uint16_t sb = KvType<T>::from_f(__fsub_rn(__fdiv_rn(hi, 15.0f), __fdiv_rn(lo, 15.0f)));
+    uint16_t sb = KvType<T>::from_f(__fsub_rn(over15(hi), over15(lo)));
     uint16_t cb = KvType<T>::from_f(fmaf(8.0f, KvType<T>::to_f(sb), lo));  // 8 s is exact
     if (bad) {
       sb = 0;
       cb = 0x7fff;  // NaN in both types
     }
-    const float sf = KvType<T>::to_f(sb), cf = KvType<T>::to_f(cb), inv = __frcp_rn(sf);
+    const float sf = KvType<T>::to_f(sb), cf = KvType<T>::to_f(cb);
+    const float inv = sf > 0.0f ? reciprocal(sf) : 0.0f;
     // rint of the quotients: (x - c) / s as a product with the reciprocal, rounded to a whole
     // number by an addition of 1.5 2^23, is right for all but quotients that near a half (the
-    // product is within 2^-20 of one that is not cut to -8 or 7); those rows are divided.  s = 0
-    // gives NaN, then 0.
+    // product is within 2^-18 of one that is not cut to -8 or 7); those rows are divided.
     constexpr float kWhole = 12582912.0f;
     float q[8], worst = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float num = __fsub_rn(x[e], cf);
       q[e] = __fsub_rn(fmaf(num, inv, kWhole), kWhole);
-      const float off = fabsf(fmaf(num, inv, -q[e]));
-      worst = off < 0.49999f ? worst : 1.0f;
+      worst = max_nan(worst, fabsf(fmaf(num, inv, -q[e])));
     }
-    if (worst != 0.0f) {
+    if (!(worst < 0.4999f) && sf > 0.0f) {
 #pragma unroll 1
       for (int e = 0; e < 8; ++e) {
         const float num = __fsub_rn(e < 4 ? (e < 2 ? (e ? x[1] : x[0]) : (e == 2 ? x[2] : x[3]))
                                           : (e < 6 ? (e == 4 ? x[4] : x[5]) : (e == 6 ? x[6] : x[7])), cf);
-        const float y = sf > 0.0f ? rintf(__fdiv_rn(num, sf)) : 0.0f;
+        const float y = rintf(__fdiv_rn(num, sf));
 #pragma unroll
         for (int i = 0; i < 8; ++i) q[i] = i == e ? y : q[i];
       }
@@ -124,6 +143,7 @@ __global__ void kv_append_kernel(KvView c, KvBatch b, const uint16_t* __restrict
       return __float_as_uint(fmaf(q[e + 6], 4096.0f, fmaf(q[e + 4], 256.0f, fmaf(q[e + 2], 16.0f, q[e]))) + (kWhole + 34952.0f));
     };
     uint32_t word = __byte_perm(half_word(0), half_word(1), 0x5410);
+    if (bad) word = 0x88888888u;
     if (live && keys) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -136,8 +156,8 @@ __global__ void kv_append_kernel(KvView c, KvBatch b, const uint16_t* __restrict
     if constexpr (G == 32)
       other = __shfl_xor_sync(0xffffffffu, (g & 1) ? (word & 0x00ff00ffu) << 8 : (word & 0xff00ff00u) >> 8, 4);
     if (!live) continue;
-    const int off = (int)(pos & (c.page_size - 1)), t = off & 15;
-    uint8_t* blk = base + (int64_t)(off >> 4) * Geo::kBytes;
+    const int t = off & 15;
+    uint8_t* blk = base + (off >> 4) * Geo::kBytes;
     if (keys) {
       reinterpret_cast<uint32_t*>(blk + t * Geo::kRow)[Geo::k_word(w)] = word;
     } else {

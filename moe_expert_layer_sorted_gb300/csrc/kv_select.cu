@@ -71,11 +71,10 @@ __device__ __forceinline__ void head_sum(const KvSelectArgs& a, const Row& w, in
   *reinterpret_cast<float4*>(qs + 8 * o + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-// Score of a page and head by D / 8 neighbouring lanes, eight channels each.
+// A lane's part (eight channels) of a page's score: three levels of the sum's tree.
 template <typename T, int D>
-__device__ __forceinline__ float page_score(const float* qs, uint4 hi, uint4 lo) {
-  constexpr int L = D / 8;
-  const int l = threadIdx.x % L;
+__device__ __forceinline__ float score_part(const float* qs, uint4 hi, uint4 lo) {
+  const int l = threadIdx.x % (D / 8);
   const float4 q0 = *reinterpret_cast<const float4*>(qs + 8 * l), q1 = *reinterpret_cast<const float4*>(qs + 8 * l + 4);
   const float q[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
   const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, o[4] = {lo.x, lo.y, lo.z, lo.w};
@@ -85,11 +84,8 @@ __device__ __forceinline__ float page_score(const float* qs, uint4 hi, uint4 lo)
     v[2 * e] = max_nan(__fmul_rn(q[2 * e], KvType<T>::lo(h[e])), __fmul_rn(q[2 * e], KvType<T>::lo(o[e])));
     v[2 * e + 1] = max_nan(__fmul_rn(q[2 * e + 1], KvType<T>::hi(h[e])), __fmul_rn(q[2 * e + 1], KvType<T>::hi(o[e])));
   }
-  float s = __fadd_rn(__fadd_rn(__fadd_rn(v[0], v[1]), __fadd_rn(v[2], v[3])),
-                      __fadd_rn(__fadd_rn(v[4], v[5]), __fadd_rn(v[6], v[7])));
-#pragma unroll
-  for (int x = 1; x < L; x <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, x));
-  return s;
+  return __fadd_rn(__fadd_rn(__fadd_rn(v[0], v[1]), __fadd_rn(v[2], v[3])),
+                   __fadd_rn(__fadd_rn(v[4], v[5]), __fadd_rn(v[6], v[7])));
 }
 
 // Keys of pages [j0, j1) and heads [h0, h1) of a row: D / 8 lanes take a page of every
@@ -104,27 +100,31 @@ __device__ __forceinline__ void score_pages(const KvSelectArgs& a, const Row& w,
   for (int p0 = 0; p0 < np; p0 += kGroups * (HEADS ? 1 : kAtOnce)) {  // every lane goes round: lanes of a group shuffle
     for (int x0 = 0; x0 < nh; x0 += kAtOnce) {
       uint4 hi[kAtOnce], lo[kAtOnce];
-      bool ok[kAtOnce];
 #pragma unroll
-      for (int x = 0; x < kAtOnce; ++x) {
-        const int p = p0 + grp + (HEADS ? 0 : x * kGroups), h = HEADS ? x0 + x : 0;
-        const int32_t pid = p < np && h < nh ? ids[p] : -1;
-        ok[x] = pid >= 0;
-        hi[x] = lo[x] = make_uint4(0, 0, 0, 0);
-        if (ok[x]) {
-          const uint4* ends = reinterpret_cast<const uint4*>(a.c.bounds + ((int64_t)pid * a.c.heads + h0 + h) * (2 * D));
-          hi[x] = __ldg(ends + l);
-          lo[x] = __ldg(ends + L + l);
-        }
+      for (int x = 0; x < kAtOnce; ++x) {  // what is out of range or in no page reads something, and is not used
+        const int p = min(p0 + grp + (HEADS ? 0 : x * kGroups), np - 1), h = HEADS ? min(x0 + x, nh - 1) : 0;
+        const uint4* ends = reinterpret_cast<const uint4*>(a.c.bounds + ((int64_t)max(ids[p], 0) * a.c.heads + h0 + h) * (2 * D));
+        hi[x] = __ldg(ends + l);
+        lo[x] = __ldg(ends + L + l);
       }
+      float s[kAtOnce];
 #pragma unroll
-      for (int x = 0; x < kAtOnce; ++x) {
-        const int p = p0 + grp + (HEADS ? 0 : x * kGroups), h = HEADS ? x0 + x : 0, j = j0 + p;
-        const float s = page_score<T, D>(qs + (HEADS ? min(h, nh - 1) : 0) * D, hi[x], lo[x]);
-        if (l == 0 && p < np && h < nh)
-          keys[h * stride + p] =
-              j < a.first || j >= w.pages - a.last ? kAlways : score_key(ok[x] ? s : -__int_as_float(0x7f800000));
-      }
+      for (int x = 0; x < kAtOnce; ++x) s[x] = score_part<T, D>(qs + (HEADS ? min(x0 + x, nh - 1) : 0) * D, hi[x], lo[x]);
+      // the tree's next levels pair neighbouring lanes; in the first two every lane keeps one of
+      // two units and gives the other away, so that lane l ends with unit l % 4
+      const bool odd = l & 1, upper = l & 2;
+      float s0 = odd ? s[1] : s[0], s1 = odd ? s[3] : s[2];
+      s0 = __fadd_rn(s0, __shfl_xor_sync(0xffffffffu, odd ? s[0] : s[1], 1));
+      s1 = __fadd_rn(s1, __shfl_xor_sync(0xffffffffu, odd ? s[2] : s[3], 1));
+      float sum = upper ? s1 : s0;
+      sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, upper ? s0 : s1, 2));
+#pragma unroll
+      for (int x = 4; x < L; x <<= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, x));
+      const int p = p0 + grp + (HEADS ? 0 : l * kGroups), h = HEADS ? x0 + l : 0, j = j0 + p;
+      if (l < kAtOnce && p < np && h < nh)
+        keys[h * stride + p] = j < a.first || j >= w.pages - a.last
+                                   ? kAlways
+                                   : score_key(ids[p] >= 0 ? sum : -__int_as_float(0x7f800000));
     }
   }
 }
