@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
     const Cursor seed{sh_group - 1, sh_base, 0, 0, 0, 0};
 
     if (warp >= kDecWarps) {
-      set_registers<DecRegs<NT>::kFetch, false>();
+      set_registers<DecRegs<NT>::kLaunch, DecRegs<NT>::kFetch>();
       if (warp == kDecWarps) {
       // ---- fetching: lane b < 8 looks after block b of each round
       Cursor pc = seed;
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
       }
       }
     } else {
-    set_registers<DecRegs<NT>::kCompute, true>();
+    set_registers<DecRegs<NT>::kLaunch, DecRegs<NT>::kCompute>();
     int stage = 0;         // of the round at hand
     uint32_t parity = 0;   // of its fill
     // where this lane's words lie in a block

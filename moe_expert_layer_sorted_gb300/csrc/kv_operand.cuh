@@ -35,9 +35,11 @@ __device__ __forceinline__ uint32_t centred_pair(uint32_t x) {
 }
 
 // Registers of a warpgroup's threads from here on.
-template <int R, bool Inc>
+// `Launch`: what the block was launched with; the direction of the change has to match it.
+template <int Launch, int R>
 __device__ __forceinline__ void set_registers() {
-  if constexpr (Inc) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+  static_assert(R % 8 == 0 && R >= 24 && R <= 256 && R != Launch, "a multiple of 8 within the range");
+  if constexpr (R > Launch) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 // Whether a launch of `kernel` brings the registers per thread that its split deals out.

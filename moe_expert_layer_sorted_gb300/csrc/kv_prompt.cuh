@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
 
   if (warp < kPrSoft) {
     // ------------------------------------------------------------------ softmax
-    set_registers<kPrSoftRegs, true>();
+    set_registers<kPrRegs, kPrSoftRegs>();
     const int t = warp >> 2, quad = warp & 3;
     const int64_t x = x0 + t * kPrTile + quad * 32 + lane;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
@@ -292,20 +292,20 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
       };
       uint64_t sum = 0;
       auto weights = [&](const uint32_t (&v)[32], int k, uint64_t factor, uint64_t neg) {
-        uint64_t more = 0;
+        float e[32];  // step by step over all 32: independent instructions side by side
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          float e[4];
-          split2(fma2(pair2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), factor, neg), e[0], e[1]);
-          split2(fma2(pair2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), factor, neg), e[2], e[3]);
+        for (int i = 0; i < 32; i += 2)
+          split2(fma2(pair2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), factor, neg), e[i], e[i + 1]);
 #pragma unroll
-          for (int y = 0; y < 4; ++y) e[y] = exp2_fast(e[y]);
-          sum = add2(sum, pair2(e[0], e[1]));
-          more = add2(more, pair2(e[2], e[3]));
-          pr[16 * k + i / 2] = KvType<__half>::pack(e[0], e[1]);
-          pr[16 * k + i / 2 + 1] = KvType<__half>::pack(e[2], e[3]);
-        }
-        sum = add2(sum, more);
+        for (int i = 0; i < 32; ++i) e[i] = exp2_fast(e[i]);
+        uint64_t part[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[i] = pair2(e[2 * i], e[2 * i + 1]);
+#pragma unroll
+        for (int i = 8; i < 32; i += 2) part[i / 2 % 4] = add2(part[i / 2 % 4], pair2(e[i], e[i + 1]));
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) pr[16 * k + i / 2] = KvType<__half>::pack(e[i], e[i + 1]);
+        sum = add2(sum, add2(add2(part[0], part[1]), add2(part[2], part[3])));
       };
       auto masked_pass = [&]() {
         const uint64_t neg = pair2(-m, -m), one = pair2(1.0f, 1.0f);
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
     }
   } else if (warp < kPrMma) {
     // ------------------------------------------------------------------ codes to K and V tiles
-    set_registers<kPrDequantRegs, false>();
+    set_registers<kPrRegs, kPrDequantRegs>();
     const int t = tid - kPrSoft * 32;  // token of the tile
     const int dw = warp - kPrSoft;
     uint4 kq[D / 32], vq[D / 32];
@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
       if (lane == 0) mbar_arrive(smem_addr(&vFull[st]));
     }
   } else {
-    set_registers<kPrMmaRegs, false>();
+    set_registers<kPrRegs, kPrMmaRegs>();
     // ------------------------------------------------------------------ MMA issue
     const uint32_t ids = idesc(kPrTile, false), ido = idesc(D, true);
     const int nt = two ? 2 : 1;
