@@ -55,13 +55,6 @@ constexpr int kDecMaxParts = kDecWarps * (64 + 4);  // CTAs, so parts of an item
 constexpr float kDecSlack = 4.0f;      // weights reach 2^4
 constexpr float kDecValues = 8192.0f;  // bound of |c| + 8 s times 2^-E
 
-// Adds 1; what this CTA wrote before (seen by this thread through a barrier) is visible to whoever
-// reads the new count this way, and the other way round.
-__device__ __forceinline__ unsigned add_acq_rel(unsigned* p) {
-  unsigned d;
-  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(d) : "l"(p) : "memory");
-  return d;
-}
 __device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kDecWarps * 32) : "memory"); }
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -742,8 +735,8 @@ cudaError_t launch_decode(Kv& kv, const KvAttnArgs& a, const DecPlan& p, cudaStr
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
   const int grid = std::min(kv.sms * (NT == 1 ? 2 : 1), kDecMaxParts);
-  static_assert(kDecMaxParts <= Kv::kMaxParts, "two partial results per CTA");
-  static_assert((size_t)C * (D + 2) * sizeof(float) <= Kv::kPartBytes, "partial results fit their slots");
+  static_assert(kDecMaxParts <= Kv::kCounters, "a counter per CTA");
+  static_assert(2 * (size_t)kDecMaxParts * C * (D + 2) * sizeof(float) <= Kv::kPartsBytes, "two partial results per CTA");
   kernel<<<grid, kDecThreads, smem, s>>>(a, p, kv.parts(), kv.counters(), kv.err_dev);
   return cudaGetLastError();
 }

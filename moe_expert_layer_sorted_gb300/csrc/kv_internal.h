@@ -1,6 +1,7 @@
 // The 4-bit key/value cache's handle and the launchers of its kernels.
 #pragma once
 
+#include <algorithm>
 #include <atomic>
 #include <string>
 
@@ -14,13 +15,12 @@ struct Kv {
   int sms = 0;
   int64_t block_bytes = 0, head_bytes = 0, page_bytes = 0, layer_bytes = 0, bounds_layer = 0;  // bounds_layer: elements
   // workspace: the selection's scores; partial results of attention items that are cut
-  // between CTAs (two per CTA); their counters, zero between calls
+  // between CTAs; their counters, zero between calls
   uint8_t* ws = nullptr;
   static constexpr size_t kScoreBytes = size_t(16) << 20;
-  static constexpr int kMaxParts = 1024;                                // CTAs
-  static constexpr size_t kPartBytes = size_t(16) * (128 + 2) * 4;      // 16 columns of (O, max, sum)
-  static constexpr size_t kPartsBytes = 2 * kMaxParts * kPartBytes;
-  static constexpr size_t kCounterBytes = kMaxParts * sizeof(unsigned);
+  static constexpr size_t kPartsBytes = size_t(24) << 20;
+  static constexpr int kCounters = 1024;
+  static constexpr size_t kCounterBytes = kCounters * sizeof(unsigned);
   static constexpr size_t kWorkspace = kScoreBytes + kPartsBytes + kCounterBytes;
   float* parts() const { return reinterpret_cast<float*>(ws + kScoreBytes); }
   unsigned* counters() const { return reinterpret_cast<unsigned*>(ws + kScoreBytes + kPartsBytes); }

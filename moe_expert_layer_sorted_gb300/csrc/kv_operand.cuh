@@ -42,6 +42,13 @@ __device__ __forceinline__ void set_registers() {
   if constexpr (R > Launch) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
+// Adds 1; what this CTA wrote before (seen by this thread through a barrier) is visible to whoever
+// reads the new count this way, and the other way round.
+__device__ __forceinline__ unsigned add_acq_rel(unsigned* p) {
+  unsigned d;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(d) : "l"(p) : "memory");
+  return d;
+}
 // Whether a launch of `kernel` brings the registers per thread that its split deals out.
 inline bool brings_registers(const void* kernel, int regs) {
   cudaFuncAttributes f{};

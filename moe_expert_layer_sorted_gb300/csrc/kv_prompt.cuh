@@ -23,6 +23,10 @@
 // whose keys are all tiny or huge (back on its column, in tiles that hold one); of
 // all values, 2^E with E raised when a token needs it (O is rescaled as for m).
 //
+// Where there are fewer tiles of rows than half the SMs, the tokens are cut into as
+// many stretches as fill them; the CTA that finishes last joins a tile's parts, in
+// the order of the stretches.
+//
 // Masks: a score that its row may not see becomes -infinity.  A masked weight
 // is an exact zero, but zero times a NaN value is not: values of a poisoned
 // group enter the tile as zeros and its groups are remembered per row that sees
@@ -157,6 +161,9 @@ struct PromptArgs {
   KvAttnArgs a;
   int per;        // query heads per kv head
   int tiles;      // row-tile pairs per sequence and head, at most
+  int splits;     // stretches of tokens per row-tile pair, at most
+  float* ws;      // [pair][split] partial results
+  unsigned* counters;
   uint32_t* err;
 };
 
@@ -169,6 +176,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t kFull[2], kEmpty[2], vFull[2], vEmpty[2], sFull[2], pFull[2], oFull;
   __shared__ uint32_t tmem_base;
+  __shared__ unsigned sh_last;
   // per token tile (ring of 4): tokens that exist, tokens with a poisoned value, tokens with scaled keys
   __shared__ uint4 sh_valid[4], sh_poison[4], sh_scaled[4];
   __shared__ float sh_kscale[4][kPrTile];      // what the scaled keys' scores are multiplied by
@@ -193,7 +201,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
     return (int)min(max(a.causal ? first + x / p.per + 1 : (int64_t)q.len, (int64_t)0), (int64_t)cap);
   };
   const int most = seen_of(min(x0 + 2 * kPrTile, nx) - 1);
-  const int ntiles = (most + kPrTile - 1) / kPrTile;
+  const int all = (most + kPrTile - 1) / kPrTile;  // token tiles
+  const int splits = min(p.splits, max(all / 2, 1)), z = blockIdx.y;
+  if (z >= splits) return;
+  const int base = (int)((int64_t)all * z / splits) * kPrTile;  // this CTA's first token
+  const int ntiles = (int)((int64_t)all * (z + 1) / splits) - base / kPrTile;
   const bool two = nx > x0 + kPrTile;  // the second row tile has rows
   const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t sq = smem, sk = smem + 2 * kTileBytes, sv = sk + 2 * kTileBytes;
@@ -255,7 +267,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
     const int64_t x = x0 + t * kPrTile + quad * 32 + lane;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const uint32_t ts = tm + t * kPrTile + lanes, to = tm + 2 * kPrTile + t * D + lanes;
-    const int seen = x < nx ? seen_of(x) : most;  // rows past the last (zeros, not written) ask for no masks
+    // tokens from `base` on that the row sees; rows past the last (zeros, not written) ask for no masks
+    const int seen = (x < nx ? seen_of(x) : most) - base;
     const float kappa = a.scale * 1.4426950408889634f * sh_qscale[t * kPrTile + quad * 32 + lane];
     const uint64_t kappa2 = pair2(kappa, kappa);
     float m = kNone;
@@ -386,38 +399,107 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
     }
     float s0, s1;
     split2(l2, s0, s1);
-    const float l = s0 + s1, inv = l == 0.0f ? 0.0f : 1.0f / l;
+    float l = s0 + s1;
+    const int row = t * kPrTile + quad * 32 + lane;
+    const bool has = t == 0 || two;
+    auto sums = [&](int k, uint32_t (&v)[32]) {  // 32 channels of the row's O
+      if (ntiles > 0) {
+        tmem_ld32(to + 32 * k, v);
+        tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = 0;
+      }
+    };
     const int i = (int)(x / p.per), hq = h * p.per + (int)(x % p.per);
-    const float back = pow2(vexp);
-    uint16_t* dst = x < nx ? a.out + kv_row_offset(a.b, a.os, s, q.row0, i) + (int64_t)hq * a.os.head : nullptr;
-    if (t == 0 || two) {
+    uint16_t* dst = has && x < nx ? a.out + kv_row_offset(a.b, a.os, s, q.row0, i) + (int64_t)hq * a.os.head : nullptr;
+    auto write = [&](int k, const uint32_t (&v)[32], float f0, float f1) {  // 32 channels, times both factors
+      // the groups of a poisoned value are NaN
+      if ((poisoned >> (32 * k / G)) & 1u) f0 = __int_as_float(0x7fffffff);
+#pragma unroll
+      for (int e = 0; e < 32; e += 8) {
+        uint32_t o[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          o[y] = KvType<T>::pack(__uint_as_float(v[e + 2 * y]) * f0 * f1, __uint_as_float(v[e + 2 * y + 1]) * f0 * f1);
+        *reinterpret_cast<uint4*>(dst + 32 * k + e) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    };
+    bool done = true;  // the row is this thread's to write
+    if (splits == 1) {
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row that sees nothing is zero
+      if (has) {
 #pragma unroll 1
-      for (int k = 0; k < D / 32; ++k) {
-        uint32_t v[32];
-        if (ntiles > 0) {
-          tmem_ld32(to + 32 * k, v);
-          tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = 0;
-        }
-        // a row that sees nothing is zero; the groups of a poisoned value are NaN
-        const float f = (poisoned >> (32 * k / G)) & 1u ? __int_as_float(0x7fffffff) : inv;
-        if (dst) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint32_t o[4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-              o[y] = KvType<T>::pack(__uint_as_float(v[e + 2 * y]) * f * back, __uint_as_float(v[e + 2 * y + 1]) * f * back);
-            *reinterpret_cast<uint4*>(dst + 32 * k + e) = make_uint4(o[0], o[1], o[2], o[3]);
-          }
+        for (int k = 0; k < D / 32; ++k) {
+          uint32_t v[32];
+          sums(k, v);
+          if (dst) write(k, v, inv, pow2(vexp));
         }
       }
-      if (dst && a.lse)
-        a.lse[kv_row_index(a.b, s, q.row0, i) * a.q_heads + hq] =
-            l == 0.0f ? -__int_as_float(0x7f800000) : (m + log2f(l)) * 0.6931471805599453f;
+    } else {
+      // a stretch's part: O [D / 4][row] of four channels, then reference, sum and poisoned groups;
+      // from here on E is part of the reference
+      constexpr int64_t kSlot = 2 * kPrTile * (D + 3);
+      float* slots = p.ws + (int64_t)blockIdx.x * p.splits * kSlot;
+      auto soft_sync = [&]() { asm volatile("bar.sync 2, %0;" ::"n"(kPrSoft * 32) : "memory"); };
+      float* slot = slots + z * kSlot;
+      if (has) {
+#pragma unroll 1
+        for (int k = 0; k < D / 32; ++k) {
+          uint32_t v[32];
+          sums(k, v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            reinterpret_cast<uint4*>(slot)[(8 * k + e) * (2 * kPrTile) + row] =
+                make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        }
+        float* ends = slot + 2 * kPrTile * D + row;
+        ends[0] = m + (float)vexp;
+        ends[2 * kPrTile] = l * pow2(-vexp);
+        ends[4 * kPrTile] = __uint_as_float(poisoned);
+      }
+      soft_sync();  // every thread's part is written: one release covers them
+      if (tid == 0) sh_last = add_acq_rel(&p.counters[blockIdx.x]);
+      soft_sync();
+      done = sh_last == (unsigned)(splits - 1);
+      if (done && has) {
+        m = kNone;
+        for (int y = 0; y < splits; ++y) m = fmaxf(m, __ldcg(slots + y * kSlot + 2 * kPrTile * D + row));
+        l = 0.0f;
+        poisoned = 0;
+        for (int y = 0; y < splits; ++y) {
+          const float* ends = slots + y * kSlot + 2 * kPrTile * D + row;
+          l = fmaf(exp2_fast(__ldcg(ends) - m), __ldcg(ends + 2 * kPrTile), l);
+          poisoned |= __float_as_uint(__ldcg(ends + 4 * kPrTile));
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+        for (int k = 0; k < D / 32; ++k) {
+          float o[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+          for (int y = 0; y < splits; ++y) {
+            const float f = exp2_fast(__ldcg(slots + y * kSlot + 2 * kPrTile * D + row) - m);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(slots + y * kSlot) + (8 * k + e) * (2 * kPrTile) + row);
+              o[4 * e] = fmaf(f, v.x, o[4 * e]);
+              o[4 * e + 1] = fmaf(f, v.y, o[4 * e + 1]);
+              o[4 * e + 2] = fmaf(f, v.z, o[4 * e + 2]);
+              o[4 * e + 3] = fmaf(f, v.w, o[4 * e + 3]);
+            }
+          }
+          uint32_t v[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(o[e]);
+          if (dst) write(k, v, inv, 1.0f);
+        }
+      }
+      if (done && tid == 0) p.counters[blockIdx.x] = 0;  // for the next call
     }
+    if (done && dst && a.lse)
+      a.lse[kv_row_index(a.b, s, q.row0, i) * a.q_heads + hq] =
+          l == 0.0f ? -__int_as_float(0x7f800000) : (m + log2f(l)) * 0.6931471805599453f;
   } else if (warp < kPrMma) {
     // ------------------------------------------------------------------ codes to K and V tiles
     set_registers<kPrRegs, kPrDequantRegs>();
@@ -432,13 +514,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
     int vexp = kNoExp;            // E
     int64_t pid = -1;             // page of the token one tile on
     auto page_of = [&](int j) {
-      const int pos = j * kPrTile + t;
+      const int pos = base + j * kPrTile + t;
       pid = j < ntiles && pos < most ? kv_page(a.c, a.b, s, pos >> a.c.page_shift) : -1;
     };
     const int row = t & 15;
     const uint32_t flip = (uint32_t)((t >> 2) & 1) * (D / 4);
     auto load_k = [&](int j) {
-      const int pos = j * kPrTile + t;
+      const int pos = base + j * kPrTile + t;
       ok = pid >= 0;
       at = a.c.pages + pid * a.c.page_stride + h * a.c.head_stride +
            ((pos & (a.c.page_size - 1)) >> 4) * (int64_t)Geo::kBytes;
@@ -614,28 +696,31 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
 }
 
 template <typename T, int D, int G>
-cudaError_t launch_prompt(Kv& kv, const PromptArgs& p, unsigned ctas, cudaStream_t s) {
+cudaError_t launch_prompt(const PromptArgs& p, unsigned ctas, cudaStream_t s) {
   const size_t smem = 1024 + (size_t)6 * kPrTile * D * 2;
   const auto kernel = kv_prompt_kernel<T, D, G>;
   static const bool registers_fit = brings_registers(reinterpret_cast<const void*>(kernel), kPrRegs);
   if (!registers_fit) return cudaErrorInvalidKernelImage;
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
-  kernel<<<ctas, kPrThreads, smem, s>>>(p);
+  kernel<<<dim3(ctas, (unsigned)p.splits), kPrThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t prompt(Kv& kv, const KvAttnArgs& a, cudaStream_t s) {
-  PromptArgs p{a, a.q_heads / a.c.heads, 0, kv.err_dev};
+  PromptArgs p{a, a.q_heads / a.c.heads, 0, 1, kv.parts(), kv.counters(), kv.err_dev};
   const int64_t tiles = ((int64_t)a.b.max_new * p.per + 2 * kPrTile - 1) / (2 * kPrTile);
   const int64_t ctas = tiles * a.c.heads * a.b.batch;
   if (ctas > 0x7fffffff || (int64_t)a.c.heads * a.b.batch > 0x7fffffff) return cudaErrorInvalidConfiguration;
   p.tiles = (int)tiles;
+  // the SMs hold one CTA each; the parts have to fit the workspace
+  const int64_t slots = Kv::kPartsBytes / (2 * kPrTile * (kv.d.head_dim + 3) * sizeof(float));
+  p.splits = (int)std::max<int64_t>(std::min<int64_t>(kv.sms, slots) / ctas, 1);
   cudaError_t e = cudaErrorInvalidValue;
   const int dg = kv.d.head_dim * 1000 + kv.d.group_size;
 #define KV_CASE(DD, GG) \
-  if (dg == DD * 1000 + GG) e = launch_prompt<T, DD, GG>(kv, p, (unsigned)ctas, s);
+  if (dg == DD * 1000 + GG) e = launch_prompt<T, DD, GG>(p, (unsigned)ctas, s);
   KV_CASE(64, 32)
   KV_CASE(64, 64)
   KV_CASE(128, 32)

@@ -306,6 +306,20 @@ def test_long_sequences_are_split_and_joined():
     run_attention(World(128, 128, 128, FP, 1, [20011, 3], seed=7).fill(), [2, 3], 2)
 
 
+@pytest.mark.parametrize("D,G,P,dtype,per", [(128, 64, 64, BF, 4), (64, 32, 16, FP, 1), (128, 128, 128, FP, 8)])
+def test_prompts_over_long_contexts(D, G, P, dtype, per):
+    """Few rows and many tokens: the tokens are cut into stretches, some rows see none of the last."""
+    run_attention(World(D, G, P, dtype, 1, [9001, 700, 20], seed=per).fill(), [50, 300, 40], per)
+    w = World(D, G, P, dtype, 2, [4003], seed=per + 1)
+    w.v[0][17, 1, 5] = math.inf
+    w.fill()
+    q = w.rand(1, 60, 2 * per, D)
+    out = torch.empty_like(q)
+    w.cache.attention(q, out, **w.batch)
+    assert torch.isnan(out[0, :, per:, :G]).all() and torch.isfinite(out[0, :, :per]).all()
+    assert torch.isfinite(out[0, :, per:, G:]).all()
+
+
 def test_many_short_sequences():
     rng = np.random.default_rng(0)
     lens = rng.integers(0, 90, 300).tolist()
