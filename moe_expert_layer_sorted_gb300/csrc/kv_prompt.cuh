@@ -24,8 +24,8 @@
 // all values, 2^E with E raised when a token needs it (O is rescaled as for m).
 //
 // Where there are fewer tiles of rows than half the SMs, the tokens are cut into as
-// many stretches as fill them; the CTA that finishes last joins a tile's parts, in
-// the order of the stretches.
+// many stretches as fill them, and a second kernel joins a tile's parts, in the order
+// of the stretches (one CTA would take longer over them than over its tokens).
 //
 // Masks: a score that its row may not see becomes -infinity.  A masked weight
 // is an exact zero, but zero times a NaN value is not: values of a poisoned
@@ -163,9 +163,40 @@ struct PromptArgs {
   int tiles;      // row-tile pairs per sequence and head, at most
   int splits;     // stretches of tokens per row-tile pair, at most
   float* ws;      // [pair][split] partial results
-  unsigned* counters;
   uint32_t* err;
 };
+
+// A pair of row tiles: its rows x0 .. of the nx of sequence s and kv head h, and its tokens.
+struct PromptTile {
+  int s, h;
+  KvSeq q;
+  int nx, x0;     // numbered in 32 bits
+  int64_t first;  // position of row 0
+  int cap, most;          // tokens that its last row sees
+  int all, splits;        // token tiles, stretches they are cut into
+
+  __device__ __forceinline__ PromptTile(const PromptArgs& p) {
+    // heavy tiles first: the last rows of every sequence see the most
+    const int hs = blockIdx.x % (p.a.c.heads * p.a.b.batch);
+    const int rt = p.tiles - 1 - blockIdx.x / (p.a.c.heads * p.a.b.batch);
+    h = hs % p.a.c.heads;
+    s = hs / p.a.c.heads;
+    q = kv_seq(p.a.b, s);
+    nx = q.rows * p.per;
+    x0 = rt * 2 * kPrTile;
+    cap = kv_capacity(p.a.c, p.a.b);
+    first = (int64_t)q.len - q.rows;
+    most = x0 < nx ? seen(p, min(x0 + 2 * kPrTile, nx) - 1) : 0;
+    all = (most + kPrTile - 1) / kPrTile;
+    splits = min(p.splits, max(all / 2, 1));
+  }
+  __device__ __forceinline__ int seen(const PromptArgs& p, int x) const {  // tokens that row x sees
+    return (int)min(max(p.a.causal ? first + x / p.per + 1 : (int64_t)q.len, (int64_t)0), (int64_t)cap);
+  }
+};
+// Floats of a stretch's part: O [D / 4][row] of four channels, then references, sums, poisoned groups.
+template <int D>
+constexpr int64_t kPrPart = 2 * kPrTile * (D + 3);
 
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_constant__ PromptArgs p) {
@@ -174,9 +205,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
   constexpr uint32_t kSlab = kPrTile * 128;          // 128 rows of 64 channels
   constexpr uint32_t kTileBytes = kSlab * (D / 64);  // a Q, K or V tile
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t kFull[2], kEmpty[2], vFull[2], vEmpty[2], sFull[2], pFull[2], oFull;
+  __shared__ uint64_t kFull[2], kEmpty[2], vFull[2], vEmpty[2], sFull[2], pFull[2], qFull, oFull;
   __shared__ uint32_t tmem_base;
-  __shared__ unsigned sh_last;
   // per token tile (ring of 4): tokens that exist, tokens with a poisoned value, tokens with scaled keys
   __shared__ uint4 sh_valid[4], sh_poison[4], sh_scaled[4];
   __shared__ float sh_kscale[4][kPrTile];      // what the scaled keys' scores are multiplied by
@@ -187,25 +217,14 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
   const KvAttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  // heavy tiles first: the last rows of every sequence see the most
-  const int hs = blockIdx.x % (a.c.heads * a.b.batch);
-  const int rt = p.tiles - 1 - blockIdx.x / (a.c.heads * a.b.batch);
-  const int h = hs % a.c.heads, s = hs / a.c.heads;
-  const KvSeq q = kv_seq(a.b, s);
-  const int64_t nx = (int64_t)q.rows * p.per;  // rows x of this sequence and head
-  const int64_t x0 = (int64_t)rt * 2 * kPrTile;
+  const PromptTile tile(p);
+  const int nx = tile.nx, x0 = tile.x0;
   if (x0 >= nx) return;
-  const int cap = kv_capacity(a.c, a.b);
-  const int64_t first = (int64_t)q.len - q.rows;  // position of row 0
-  auto seen_of = [&](int64_t x) {  // tokens that row x sees
-    return (int)min(max(a.causal ? first + x / p.per + 1 : (int64_t)q.len, (int64_t)0), (int64_t)cap);
-  };
-  const int most = seen_of(min(x0 + 2 * kPrTile, nx) - 1);
-  const int all = (most + kPrTile - 1) / kPrTile;  // token tiles
-  const int splits = min(p.splits, max(all / 2, 1)), z = blockIdx.y;
+  const int s = tile.s, h = tile.h, most = tile.most, splits = tile.splits, z = blockIdx.y;
+  const KvSeq q = tile.q;
   if (z >= splits) return;
-  const int base = (int)((int64_t)all * z / splits) * kPrTile;  // this CTA's first token
-  const int ntiles = (int)((int64_t)all * (z + 1) / splits) - base / kPrTile;
+  const int base = (int)((int64_t)tile.all * z / splits) * kPrTile;  // this CTA's first token
+  const int ntiles = (int)((int64_t)tile.all * (z + 1) / splits) - base / kPrTile;
   const bool two = nx > x0 + kPrTile;  // the second row tile has rows
   const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t sq = smem, sk = smem + 2 * kTileBytes, sv = sk + 2 * kTileBytes;
@@ -220,6 +239,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
       mbar_init(smem_addr(&sFull[i]), 1);
       mbar_init(smem_addr(&pFull[i]), 4);
     }
+    mbar_init(smem_addr(&qFull), 1);
     mbar_init(smem_addr(&oFull), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -227,34 +247,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_base)), "n"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  // Q: both tiles, rows past the last as zeros; D / 8 neighbouring lanes hold a row
-  for (int i = tid; i < 2 * kPrTile * (D / 8); i += kPrThreads) {
-    const int row = i / (D / 8), ch = i % (D / 8);
-    const int64_t x = x0 + row;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (x < nx)
-      v = *reinterpret_cast<const uint4*>(a.q + kv_row_offset(a.b, a.qs, s, q.row0, (int)(x / p.per)) +
-                                          (int64_t)(h * p.per + (int)(x % p.per)) * a.qs.head + 8 * ch);
-    float back = 1.0f;
-    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-      uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      uint32_t top = 0;  // largest magnitude's bits
-#pragma unroll
-      for (int e = 0; e < 4; ++e) top = max(top, max(w[e] << 16 & 0x7fff0000u, w[e] & 0x7fff0000u));
-#pragma unroll
-      for (int o = 1; o < D / 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int ex = (int)(top >> 23) - 127;  // to 2^14; an infinity or a NaN stays what it is
-      const int by = top == 0u || ex > 127 ? 0 : min(max(14 - ex, -113), 113);
-      back = pow2(-by);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = KvType<__half>::pack(KvType<T>::lo(w[e]) * pow2(by), KvType<T>::hi(w[e]) * pow2(by));
-      v = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    if (ch == 0) sh_qscale[row] = back;
-    *reinterpret_cast<uint4*>(gen + (row / kPrTile) * kTileBytes + (ch / 8) * kSlab + (row % kPrTile) * 128 +
-                              ((ch % 8) ^ (row & 7)) * 16) = v;
-  }
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   fence_before();
   __syncthreads();
   fence_after();
@@ -264,11 +256,53 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
     // ------------------------------------------------------------------ softmax
     set_registers<kPrRegs, kPrSoftRegs>();
     const int t = warp >> 2, quad = warp & 3;
-    const int64_t x = x0 + t * kPrTile + quad * 32 + lane;
+    const int x = x0 + t * kPrTile + quad * 32 + lane;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const uint32_t ts = tm + t * kPrTile + lanes, to = tm + 2 * kPrTile + t * D + lanes;
     // tokens from `base` on that the row sees; rows past the last (zeros, not written) ask for no masks
-    const int seen = (x < nx ? seen_of(x) : most) - base;
+    const int seen = (x < nx ? tile.seen(p, x) : most) - base;
+    auto soft_sync = [&]() { asm volatile("bar.sync 2, %0;" ::"n"(kPrSoft * 32) : "memory"); };
+    // Q: both tiles, rows past the last as zeros; D / 8 neighbouring lanes hold a row, and a thread
+    // asks for eight pieces at once
+    constexpr int kPieces = 2 * kPrTile * (D / 8) / (kPrSoft * 32), kAtOnce = 8;
+#pragma unroll 1
+    for (int n0 = 0; n0 < kPieces; n0 += kAtOnce) {
+      uint4 raw[kAtOnce];
+#pragma unroll
+      for (int n = 0; n < kAtOnce; ++n) {
+        const int i = tid + (n0 + n) * kPrSoft * 32, r = i / (D / 8), ch = i % (D / 8);
+        const int xr = x0 + r;
+        raw[n] = make_uint4(0, 0, 0, 0);
+        if (xr < nx)
+          raw[n] = *reinterpret_cast<const uint4*>(a.q + kv_row_offset(a.b, a.qs, s, q.row0, xr / p.per) +
+                                                   (int64_t)(h * p.per + xr % p.per) * a.qs.head + 8 * ch);
+      }
+#pragma unroll
+      for (int n = 0; n < kAtOnce; ++n) {
+        const int i = tid + (n0 + n) * kPrSoft * 32, r = i / (D / 8), ch = i % (D / 8);
+        float back = 1.0f;
+        uint32_t w[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+          uint32_t top = 0;  // largest magnitude's bits
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, max(w[e] << 16 & 0x7fff0000u, w[e] & 0x7fff0000u));
+#pragma unroll
+          for (int o = 1; o < D / 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const int ex = (int)(top >> 23) - 127;  // to 2^14; an infinity or a NaN stays what it is
+          const int by = top == 0u || ex > 127 ? 0 : min(max(14 - ex, -113), 113);
+          back = pow2(-by);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = KvType<__half>::pack(KvType<T>::lo(w[e]) * pow2(by), KvType<T>::hi(w[e]) * pow2(by));
+        }
+        if (ch == 0) sh_qscale[r] = back;
+        *reinterpret_cast<uint4*>(gen + (r / kPrTile) * kTileBytes + (ch / 8) * kSlab + (r % kPrTile) * 128 +
+                                  ((ch % 8) ^ (r & 7)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    soft_sync();
+    if (tid == 0) mbar_arrive(smem_addr(&qFull));
     const float kappa = a.scale * 1.4426950408889634f * sh_qscale[t * kPrTile + quad * 32 + lane];
     const uint64_t kappa2 = pair2(kappa, kappa);
     float m = kNone;
@@ -320,20 +354,44 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
         for (int i = 0; i < 32; i += 2) pr[16 * k + i / 2] = KvType<__half>::pack(e[i], e[i + 1]);
         sum = add2(sum, add2(add2(part[0], part[1]), add2(part[2], part[3])));
       };
-      auto masked_pass = [&]() {
-        const uint64_t neg = pair2(-m, -m), one = pair2(1.0f, 1.0f);
-        sum = 0;
+      // weights against the reference as it stands, and once more where it has to rise: for the
+      // first tile, with E, or where a weight is above the limit, which shows in the sum (that may
+      // reach the limit without one: no harm)
+      bool raise = j == 0 || sh_vexp[j & 3] != vexp, asked = true;
+      while (true) {
+        if (raise) {
+          // the row's largest score of this tile becomes its reference; what was summed so far shrinks
+          float best = kNone;
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            load(k, v[0]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t v[32];
-          load(k, v);
-          weights(v, k, one, neg);
+            for (int i = 0; i < 32; ++i) best = fmaxf(best, __uint_as_float(v[0][i]));
+          }
+          asked = false;
+          best = fmaxf(best - kPrDrop, m);
+          const float f = exp2_fast(m - best), fo = f * pow2(max(vexp - sh_vexp[j & 3], -126));
+          m = best;
+          vexp = sh_vexp[j & 3];
+          float s0, s1;
+          split2(l2, s0, s1);
+          l2 = pair2(s0 * f, s1 * f);
+          if (j > 0) {
+#pragma unroll 1
+            for (int k = 0; k < D / 32; ++k) {
+              tmem_ld32(to + 32 * k, v[0]);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[0][i] = __float_as_uint(__uint_as_float(v[0][i]) * fo);
+              tmem_st32(to + 32 * k, v[0]);
+            }
+            tmem_wait_st();
+          }
         }
-      };
-      bool raise = j == 0 || sh_vexp[j & 3] != vexp;
-      if (!raise) {  // weights against the reference as it stands
+        const uint64_t neg = pair2(-m, -m);
+        sum = 0;
         if (plain) {
-          const uint64_t neg = pair2(-m, -m);
+          if (!asked) tmem_ld32(ts, v[0]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {  // the next 32 scores arrive while these are worked on
             tmem_wait_ld();
@@ -341,43 +399,18 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
             weights(v[k & 1], k, kappa2, neg);
           }
         } else {
-          masked_pass();
+          const uint64_t one = pair2(1.0f, 1.0f);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            load(k, v[0]);
+            weights(v[0], k, one, neg);
+          }
         }
-        // a weight above the limit shows in the sum (which may reach it without one: no harm)
+        if (raise) break;
         float s0, s1;
         split2(sum, s0, s1);
         raise = __any_sync(0xffffffffu, fmaxf(s0, s1) > kPrLimit);
-      }
-      if (raise) {
-        // the row's largest score of this tile becomes its reference; what was summed so far shrinks
-        float best = kNone;
-#pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          uint32_t v[32];
-          load(k, v);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) best = fmaxf(best, __uint_as_float(v[i]));
-        }
-        best = fmaxf(best - kPrDrop, m);
-        const float f = exp2_fast(m - best), fo = f * pow2(max(vexp - sh_vexp[j & 3], -126));
-        m = best;
-        vexp = sh_vexp[j & 3];
-        float s0, s1;
-        split2(l2, s0, s1);
-        l2 = pair2(s0 * f, s1 * f);
-        if (j > 0) {
-#pragma unroll 1
-          for (int k = 0; k < D / 32; ++k) {
-            uint32_t v[32];
-            tmem_ld32(to + 32 * k, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * fo);
-            tmem_st32(to + 32 * k, v);
-          }
-          tmem_wait_st();
-        }
-        masked_pass();
+        if (!raise) break;
       }
       l2 = add2(l2, sum);
       tmem_st32(ts, pr);
@@ -399,7 +432,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
     }
     float s0, s1;
     split2(l2, s0, s1);
-    float l = s0 + s1;
+    const float l = s0 + s1;
     const int row = t * kPrTile + quad * 32 + lane;
     const bool has = t == 0 || two;
     auto sums = [&](int k, uint32_t (&v)[32]) {  // 32 channels of the row's O
@@ -411,7 +444,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
         for (int e = 0; e < 32; ++e) v[e] = 0;
       }
     };
-    const int i = (int)(x / p.per), hq = h * p.per + (int)(x % p.per);
+    const int i = x / p.per, hq = h * p.per + x % p.per;
     uint16_t* dst = has && x < nx ? a.out + kv_row_offset(a.b, a.os, s, q.row0, i) + (int64_t)hq * a.os.head : nullptr;
     auto write = [&](int k, const uint32_t (&v)[32], float f0, float f1) {  // 32 channels, times both factors
       // the groups of a poisoned value are NaN
@@ -425,7 +458,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
         *reinterpret_cast<uint4*>(dst + 32 * k + e) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     };
-    bool done = true;  // the row is this thread's to write
     if (splits == 1) {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row that sees nothing is zero
       if (has) {
@@ -436,70 +468,25 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
           if (dst) write(k, v, inv, pow2(vexp));
         }
       }
-    } else {
-      // a stretch's part: O [D / 4][row] of four channels, then reference, sum and poisoned groups;
-      // from here on E is part of the reference
-      constexpr int64_t kSlot = 2 * kPrTile * (D + 3);
-      float* slots = p.ws + (int64_t)blockIdx.x * p.splits * kSlot;
-      auto soft_sync = [&]() { asm volatile("bar.sync 2, %0;" ::"n"(kPrSoft * 32) : "memory"); };
-      float* slot = slots + z * kSlot;
-      if (has) {
+      if (dst && a.lse)
+        a.lse[kv_row_index(a.b, s, q.row0, i) * a.q_heads + hq] =
+            l == 0.0f ? -__int_as_float(0x7f800000) : (m + log2f(l)) * 0.6931471805599453f;
+    } else if (has) {  // a stretch's part; from here on E is part of the reference
+      float* part = p.ws + ((int64_t)blockIdx.x * p.splits + z) * kPrPart<D>;
 #pragma unroll 1
-        for (int k = 0; k < D / 32; ++k) {
-          uint32_t v[32];
-          sums(k, v);
+      for (int k = 0; k < D / 32; ++k) {
+        uint32_t v[32];
+        sums(k, v);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            reinterpret_cast<uint4*>(slot)[(8 * k + e) * (2 * kPrTile) + row] =
-                make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-        }
-        float* ends = slot + 2 * kPrTile * D + row;
-        ends[0] = m + (float)vexp;
-        ends[2 * kPrTile] = l * pow2(-vexp);
-        ends[4 * kPrTile] = __uint_as_float(poisoned);
+        for (int e = 0; e < 8; ++e)
+          reinterpret_cast<uint4*>(part)[(8 * k + e) * (2 * kPrTile) + row] =
+              make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
       }
-      soft_sync();  // every thread's part is written: one release covers them
-      if (tid == 0) sh_last = add_acq_rel(&p.counters[blockIdx.x]);
-      soft_sync();
-      done = sh_last == (unsigned)(splits - 1);
-      if (done && has) {
-        m = kNone;
-        for (int y = 0; y < splits; ++y) m = fmaxf(m, __ldcg(slots + y * kSlot + 2 * kPrTile * D + row));
-        l = 0.0f;
-        poisoned = 0;
-        for (int y = 0; y < splits; ++y) {
-          const float* ends = slots + y * kSlot + 2 * kPrTile * D + row;
-          l = fmaf(exp2_fast(__ldcg(ends) - m), __ldcg(ends + 2 * kPrTile), l);
-          poisoned |= __float_as_uint(__ldcg(ends + 4 * kPrTile));
-        }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll 1
-        for (int k = 0; k < D / 32; ++k) {
-          float o[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0.0f;
-          for (int y = 0; y < splits; ++y) {
-            const float f = exp2_fast(__ldcg(slots + y * kSlot + 2 * kPrTile * D + row) - m);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(slots + y * kSlot) + (8 * k + e) * (2 * kPrTile) + row);
-              o[4 * e] = fmaf(f, v.x, o[4 * e]);
-              o[4 * e + 1] = fmaf(f, v.y, o[4 * e + 1]);
-              o[4 * e + 2] = fmaf(f, v.z, o[4 * e + 2]);
-              o[4 * e + 3] = fmaf(f, v.w, o[4 * e + 3]);
-            }
-          }
-          uint32_t v[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(o[e]);
-          if (dst) write(k, v, inv, 1.0f);
-        }
-      }
-      if (done && tid == 0) p.counters[blockIdx.x] = 0;  // for the next call
+      float* ends = part + 2 * kPrTile * D + row;
+      ends[0] = m + (float)vexp;
+      ends[2 * kPrTile] = l * pow2(-vexp);
+      ends[4 * kPrTile] = __uint_as_float(poisoned);
     }
-    if (done && dst && a.lse)
-      a.lse[kv_row_index(a.b, s, q.row0, i) * a.q_heads + hq] =
-          l == 0.0f ? -__int_as_float(0x7f800000) : (m + log2f(l)) * 0.6931471805599453f;
   } else if (warp < kPrMma) {
     // ------------------------------------------------------------------ codes to K and V tiles
     set_registers<kPrRegs, kPrDequantRegs>();
@@ -665,6 +652,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
       if (t == nt - 1) commit(leader, &kEmpty[j & 1]);
     };
     if (warp == kPrMma && ntiles > 0) {
+      mbar_wait<false>(smem_addr(&qFull), 0, p.err);
       mbar_wait<false>(smem_addr(&kFull[0]), 0, p.err);
       fence_after();
       for (int t = 0; t < nt; ++t) scores(t, 0);
@@ -695,6 +683,58 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
   }
 }
 
+// Joins the stretches' parts of a pair of row tiles: a CTA takes 32 rows, lane by lane, a warp
+// every eighth four channels.
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ PromptArgs p) {
+  const KvAttnArgs& a = p.a;
+  const PromptTile tile(p);
+  const int row = blockIdx.y * 32 + (threadIdx.x & 31);
+  const int x = tile.x0 + row;
+  if (x >= tile.nx || tile.splits == 1) return;
+  const float* parts = p.ws + (int64_t)blockIdx.x * p.splits * kPrPart<D>;
+  const float* ends = parts + 2 * kPrTile * D + row;
+  float m = kNone, l = 0.0f;
+  uint32_t poisoned = 0;
+#pragma unroll 4
+  for (int y = 0; y < tile.splits; ++y) m = fmaxf(m, __ldcg(ends + y * kPrPart<D>));
+#pragma unroll 4
+  for (int y = 0; y < tile.splits; ++y) {
+    l = fmaf(exp2_fast(__ldcg(ends + y * kPrPart<D>) - m), __ldcg(ends + y * kPrPart<D> + 2 * kPrTile), l);
+    poisoned |= __float_as_uint(__ldcg(ends + y * kPrPart<D> + 4 * kPrTile));
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row that sees nothing is zero
+  const int i = x / p.per, hq = tile.h * p.per + x % p.per;
+  uint16_t* dst = a.out + kv_row_offset(a.b, a.os, tile.s, tile.q.row0, i) + (int64_t)hq * a.os.head;
+  constexpr int kQuads = D / 4 / 8;  // of four channels, per thread
+  float4 o[kQuads];
+#pragma unroll
+  for (int k = 0; k < kQuads; ++k) o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int y = 0; y < tile.splits; ++y) {
+    const float f = exp2_fast(__ldcg(ends + y * kPrPart<D>) - m);
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k) {
+      const int d4 = (threadIdx.x >> 5) * kQuads + k;
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(parts + y * kPrPart<D>) + d4 * (2 * kPrTile) + row);
+      o[k].x = fmaf(f, v.x, o[k].x);
+      o[k].y = fmaf(f, v.y, o[k].y);
+      o[k].z = fmaf(f, v.z, o[k].z);
+      o[k].w = fmaf(f, v.w, o[k].w);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kQuads; ++k) {
+    const int d4 = (threadIdx.x >> 5) * kQuads + k;
+    const float f = (poisoned >> (4 * d4 / G)) & 1u ? __int_as_float(0x7fffffff) : inv;
+    *reinterpret_cast<uint2*>(dst + 4 * d4) =
+        make_uint2(KvType<T>::pack(o[k].x * f, o[k].y * f), KvType<T>::pack(o[k].z * f, o[k].w * f));
+  }
+  if (a.lse && threadIdx.x < 32)
+    a.lse[kv_row_index(a.b, tile.s, tile.q.row0, i) * a.q_heads + hq] =
+        l == 0.0f ? -__int_as_float(0x7f800000) : (m + log2f(l)) * 0.6931471805599453f;
+}
+
 template <typename T, int D, int G>
 cudaError_t launch_prompt(const PromptArgs& p, unsigned ctas, cudaStream_t s) {
   const size_t smem = 1024 + (size_t)6 * kPrTile * D * 2;
@@ -704,15 +744,17 @@ cudaError_t launch_prompt(const PromptArgs& p, unsigned ctas, cudaStream_t s) {
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
   kernel<<<dim3(ctas, (unsigned)p.splits), kPrThreads, smem, s>>>(p);
+  if (p.splits > 1) kv_join_kernel<T, D, G><<<dim3(ctas, 2 * kPrTile / 32), 256, 0, s>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t prompt(Kv& kv, const KvAttnArgs& a, cudaStream_t s) {
-  PromptArgs p{a, a.q_heads / a.c.heads, 0, 1, kv.parts(), kv.counters(), kv.err_dev};
+  PromptArgs p{a, a.q_heads / a.c.heads, 0, 1, kv.parts(), kv.err_dev};
   const int64_t tiles = ((int64_t)a.b.max_new * p.per + 2 * kPrTile - 1) / (2 * kPrTile);
   const int64_t ctas = tiles * a.c.heads * a.b.batch;
-  if (ctas > 0x7fffffff || (int64_t)a.c.heads * a.b.batch > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  if (ctas > 0x7fffffff || (int64_t)a.c.heads * a.b.batch > 0x7fffffff || tiles * 2 * kPrTile > 0x7fffffff)
+    return cudaErrorInvalidConfiguration;
   p.tiles = (int)tiles;
   // the SMs hold one CTA each; the parts have to fit the workspace
   const int64_t slots = Kv::kPartsBytes / (2 * kPrTile * (kv.d.head_dim + 3) * sizeof(float));
