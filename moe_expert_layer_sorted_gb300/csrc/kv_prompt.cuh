@@ -262,42 +262,48 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
     // tokens from `base` on that the row sees; rows past the last (zeros, not written) ask for no masks
     const int seen = (x < nx ? tile.seen(p, x) : most) - base;
     auto soft_sync = [&]() { asm volatile("bar.sync 2, %0;" ::"n"(kPrSoft * 32) : "memory"); };
-    // Q: both tiles, rows past the last as zeros; D / 8 neighbouring lanes hold a row, and a thread
-    // asks for eight pieces at once
-    constexpr int kPieces = 2 * kPrTile * (D / 8) / (kPrSoft * 32), kAtOnce = 8;
+    // Q: both tiles, rows past the last as zeros; two threads take a row, half of its channels each
+    static_assert(kPrSoft * 32 == 2 * kPrTile, "two threads per row of a tile");
 #pragma unroll 1
-    for (int n0 = 0; n0 < kPieces; n0 += kAtOnce) {
-      uint4 raw[kAtOnce];
+    for (int y = 0; y < 2; ++y) {
+      const int r = tid >> 1, side = tid & 1, xr = x0 + y * kPrTile + r;
+      uint4 raw[D / 16];
 #pragma unroll
-      for (int n = 0; n < kAtOnce; ++n) {
-        const int i = tid + (n0 + n) * kPrSoft * 32, r = i / (D / 8), ch = i % (D / 8);
-        const int xr = x0 + r;
-        raw[n] = make_uint4(0, 0, 0, 0);
-        if (xr < nx)
-          raw[n] = *reinterpret_cast<const uint4*>(a.q + kv_row_offset(a.b, a.qs, s, q.row0, xr / p.per) +
-                                                   (int64_t)(h * p.per + xr % p.per) * a.qs.head + 8 * ch);
+      for (int n = 0; n < D / 16; ++n) raw[n] = make_uint4(0, 0, 0, 0);
+      if (xr < nx) {
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + kv_row_offset(a.b, a.qs, s, q.row0, xr / p.per) +
+                                                          (int64_t)(h * p.per + xr % p.per) * a.qs.head + side * (D / 2));
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) raw[n] = src[n];
       }
+      float back = 1.0f;
+      if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        uint32_t top = 0;  // largest magnitudes of the even and the odd channels (NaN above all)
 #pragma unroll
-      for (int n = 0; n < kAtOnce; ++n) {
-        const int i = tid + (n0 + n) * kPrSoft * 32, r = i / (D / 8), ch = i % (D / 8);
-        float back = 1.0f;
-        uint32_t w[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
-        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-          uint32_t top = 0;  // largest magnitude's bits
+        for (int n = 0; n < D / 16; ++n) {
+          const uint32_t w[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) top = max(top, max(w[e] << 16 & 0x7fff0000u, w[e] & 0x7fff0000u));
-#pragma unroll
-          for (int o = 1; o < D / 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const int ex = (int)(top >> 23) - 127;  // to 2^14; an infinity or a NaN stays what it is
-          const int by = top == 0u || ex > 127 ? 0 : min(max(14 - ex, -113), 113);
-          back = pow2(-by);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = KvType<__half>::pack(KvType<T>::lo(w[e]) * pow2(by), KvType<T>::hi(w[e]) * pow2(by));
+          for (int e = 0; e < 4; ++e) top = __vmaxu2(top, w[e] & 0x7fff7fffu);
         }
-        if (ch == 0) sh_qscale[r] = back;
-        *reinterpret_cast<uint4*>(gen + (r / kPrTile) * kTileBytes + (ch / 8) * kSlab + (r % kPrTile) * 128 +
-                                  ((ch % 8) ^ (r & 7)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top >> 16, top & 0xffffu);
+        const int ex = (int)(top >> 7) - 127;  // to 2^14; an infinity or a NaN stays what it is
+        const int by = top == 0u || ex > 127 ? 0 : min(max(14 - ex, -113), 113);
+        const float up = pow2(by);
+        back = pow2(-by);
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+          uint32_t w[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = KvType<__half>::pack(KvType<T>::lo(w[e]) * up, KvType<T>::hi(w[e]) * up);
+          raw[n] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      if (side == 0) sh_qscale[y * kPrTile + r] = back;
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n) {
+        const int ch = side * (D / 16) + n;
+        *reinterpret_cast<uint4*>(gen + y * kTileBytes + (ch / 8) * kSlab + r * 128 + ((ch % 8) ^ (r & 7)) * 16) = raw[n];
       }
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -449,13 +455,19 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
     auto write = [&](int k, const uint32_t (&v)[32], float f0, float f1) {  // 32 channels, times both factors
       // the groups of a poisoned value are NaN
       if ((poisoned >> (32 * k / G)) & 1u) f0 = __int_as_float(0x7fffffff);
+      f0 *= f1;
+      uint32_t o[16];
 #pragma unroll
-      for (int e = 0; e < 32; e += 8) {
-        uint32_t o[4];
+      for (int e = 0; e < 16; ++e) o[e] = KvType<T>::pack(__uint_as_float(v[2 * e]) * f0, __uint_as_float(v[2 * e + 1]) * f0);
+      if (reinterpret_cast<uintptr_t>(dst) & 31) {
 #pragma unroll
-        for (int y = 0; y < 4; ++y)
-          o[y] = KvType<T>::pack(__uint_as_float(v[e + 2 * y]) * f0 * f1, __uint_as_float(v[e + 2 * y + 1]) * f0 * f1);
-        *reinterpret_cast<uint4*>(dst + 32 * k + e) = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(dst + 32 * k + 2 * e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      } else {  // whole sectors
+#pragma unroll
+        for (int e = 0; e < 16; e += 8)
+          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 32 * k + 2 * e), "r"(o[e]),
+                       "r"(o[e + 1]), "r"(o[e + 2]), "r"(o[e + 3]), "r"(o[e + 4]), "r"(o[e + 5]), "r"(o[e + 6]), "r"(o[e + 7])
+                       : "memory");
       }
     };
     if (splits == 1) {
