@@ -13,6 +13,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
+BINDING = os.path.join(PKG, "_kv_binding.so")
 SOURCES = ["plan.cu", "decode.cu", "prefill.cu", "cache.cu", "noalloc.cu", "kv.cu", "kv_append.cu",
            "kv_attention.cu", "kv_select.cu", "kv_decode_bf16.cu", "kv_decode_f16.cu",
            "kv_prompt_bf16.cu", "kv_prompt_f16.cu"]
@@ -29,6 +30,23 @@ def _deps():
     hdrs = [os.path.join(INCLUDE, "moe.h")] + [os.path.join(CSRC, f) for f in os.listdir(CSRC)
                                                 if f.endswith((".h", ".cuh"))]
     return max(os.path.getmtime(h) for h in hdrs)
+
+
+def _binding_cmd(header_time: float) -> list | None:
+    """g++ command of the key/value cache's Python binding, or None where it is up to date."""
+    src = os.path.join(CSRC, "kv_binding.cpp")
+    if os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(src), header_time):
+        return None
+    import sysconfig
+
+    import torch
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    inc = [INCLUDE, os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[f"-I{i}" for i in inc], src, "-o", BINDING + ".tmp", f"-L{PKG}", f"-L{os.path.join(t, 'lib')}", "-l:libmoe_gb300.so",
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
@@ -63,6 +81,14 @@ def build(verbose: bool = False, force: bool = False) -> str:
             print(r.stdout + r.stderr)
             raise RuntimeError("link failed")
         os.replace(LIB + ".tmp", LIB)
+    cmd = _binding_cmd(os.path.getmtime(os.path.join(INCLUDE, "moe.h")))
+    if cmd:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode:
+            print(" ".join(cmd))
+            print(r.stdout + r.stderr)
+            raise RuntimeError("the Python binding did not build")
+        os.replace(BINDING + ".tmp", BINDING)
     return LIB
 
 

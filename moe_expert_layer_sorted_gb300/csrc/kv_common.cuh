@@ -7,7 +7,7 @@
 // (params: step s and centre c in the cache's type, a stored value being
 // c + s (u - 8)), so that any run of blocks of a page and head is one bulk
 // copy.  The order of the codes inside a row is the order in which the
-// attention over single tokens wants its matrix operands (kv_decode.cu):
+// attention over single tokens wants its matrix operands (kv_decode.cuh):
 //   - K: a row is four quarters, one per lane of a quad, and a quarter holds
 //     the matching quarter of every group, so that 16 bytes of a lane feed
 //     whole k-steps of one group after the other;

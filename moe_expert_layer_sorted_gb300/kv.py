@@ -1,10 +1,8 @@
-"""The 4-bit key/value cache (see moe_kv_* in include/moe.h): argument checks and
-marshalling; the work is done in the CUDA library."""
+"""The 4-bit key/value cache (see moe_kv_* in include/moe.h): the handle and its
+tensors; the work is done in the CUDA library."""
 from __future__ import annotations
 
 import ctypes
-import math
-import struct
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -18,22 +16,16 @@ class KVDesc(ctypes.Structure):
                 ("pages", _P), ("bounds", _P), ("reserved", _I64 * 2)]
 
 
-# moe_kv_batch and moe_kv_tensor, packed
-_BATCH = struct.Struct("=I3i2q3Q")
-_BATCH_SIZE = _BATCH.size
-_TENSOR = struct.Struct("=Q3q")
-
-
 def declare(L):
     """Argument types of the library's moe_kv_* functions."""
-    i32, B, X = ctypes.c_int, ctypes.c_char_p, ctypes.c_char_p  # packed structures
+    i32 = ctypes.c_int
     L.moe_kv_sizes.argtypes = [ctypes.POINTER(KVDesc), ctypes.POINTER(_I64), ctypes.POINTER(_I64)]
     L.moe_kv_create.argtypes = [ctypes.POINTER(KVDesc), ctypes.POINTER(_P)]
     L.moe_kv_destroy.argtypes = [_P]
-    L.moe_kv_append.argtypes = [_P, i32, B, X, X, _P]
-    L.moe_kv_read.argtypes = [_P, i32, B, X, X, _P]
-    L.moe_kv_attention.argtypes = [_P, i32, B, X, i32, ctypes.c_float, i32, X, _P, _P, i32, _P]
-    L.moe_kv_select.argtypes = [_P, i32, B, X, i32, i32, i32, i32, _P, _P]
+    L.moe_kv_append.argtypes = [_P, i32, _P, _P, _P, _P]
+    L.moe_kv_read.argtypes = [_P, i32, _P, _P, _P, _P]
+    L.moe_kv_attention.argtypes = [_P, i32, _P, _P, i32, ctypes.c_float, i32, _P, _P, _P, i32, _P]
+    L.moe_kv_select.argtypes = [_P, i32, _P, _P, i32, i32, i32, i32, _P, _P]
     L.moe_kv_last_error.argtypes = [_P]
     L.moe_kv_last_error.restype = ctypes.c_char_p
 
@@ -110,9 +102,8 @@ class KVCache:
         self.dtype, self.device = dtype, pages.device
         self.layers, self.kv_heads, self.head_dim = layers, kv_heads, head_dim
         self.page_size, self.group_size = page_size, group_size
-        self._scale = 1.0 / math.sqrt(head_dim)
-        self._index, self._i32 = pages.device.index, torch.int32
-        self._current_stream = torch._C._cuda_getCurrentRawStream
+        from . import _kv_binding
+        self._c = _kv_binding.Cache(MoeError, h.value, d.device, dtype == torch.bfloat16, kv_heads, head_dim)
 
     @staticmethod
     def _block_shape(head_dim, group_size, page_size):
@@ -133,6 +124,8 @@ class KVCache:
 
     def close(self):
         if getattr(self, "_h", None):
+            if getattr(self, "_c", None):
+                self._c.closed()
             self._lib.moe_kv_destroy(self._h)
             self._h = None
 
@@ -142,142 +135,30 @@ class KVCache:
         except Exception:
             pass
 
-    # ------------------------------------------------------------------ marshalling
-    # A decode step's calls are a few microseconds of GPU work each, so the host's share
-    # counts: the C structures are packed in one step each, and tensors are asked for
-    # nothing twice.
+    # The tensors are checked and unpacked in csrc/kv_binding.cpp.
 
-    def _int(self, t, name, dim):
-        if not (t.dtype is self._i32 and t.is_cuda and t.get_device() == self._index and t.dim() == dim):
-            _bad(f"{name}: int32 tensor of {dim} axes on {self.device}")
-        return t.data_ptr()
-
-    def _batch(self, shape, table, lens, starts, max_new):
-        tp, lp, sp = self._int(table, "table", 2), self._int(lens, "lens", 1), 0
-        n, (sequences, cols) = len(shape), table.shape
-        batch = lens.shape[0]
-        if sequences != batch:
-            _bad("table and lens name different numbers of sequences")
-        stride, step = table.stride()
-        if (step != 1 and cols > 1) or (batch > 1 and lens.stride(0) != 1):
-            _bad("table's rows and lens must be contiguous")
-        if batch <= 1:
-            stride = cols
-        if starts is None:
-            if n != 4 or shape[0] != batch:
-                _bad("row tensors without starts: [sequences, rows, heads, head_dim]")
-            if max_new is not None and max_new != shape[1]:
-                _bad("max_new belongs to starts")
-            max_new = shape[1]
-            rows = batch * max_new
-        else:
-            if n != 3:
-                _bad("row tensors with starts: [rows, heads, head_dim]")
-            sp = self._int(starts, "starts", 1)
-            if starts.shape[0] != batch + 1 or starts.stride(0) != 1:
-                _bad("starts: contiguous, one entry more than sequences")
-            rows = shape[0]
-            if max_new is None:
-                max_new = rows
-        if not (0 <= max_new < 1 << 31 and rows < 1 << 62 and batch < 1 << 31 and cols < 1 << 31):
-            _bad("max_new, the sequences or the table's pages are out of range")
-        return rows, _BATCH.pack(_BATCH_SIZE, batch, max_new, cols, stride, rows, tp, lp, sp)
-
-    def _rows(self, t, name, shape, written=False):
-        if not (t.dtype is self.dtype and t.is_cuda and t.get_device() == self._index and t.shape == shape):
-            _bad(f"{name}: {self.dtype} on {self.device}, expected shape {tuple(shape)}")
-        st = t.stride()
-        if written and 0 in st and any(n > 1 and d == 0 for n, d in zip(shape, st)):
-            _bad(f"{name}: an expanded tensor cannot be written to")
-        if st[-1] != 1:
-            _bad(f"{name}: the channels must be contiguous")
-        if len(shape) == 4:
-            b, r, h, _ = st
-            nb, nr, nh, _ = shape
-            # axes of length 1 have no stride that matters
-            return _TENSOR.pack(t.data_ptr(), b if nb > 1 else 0, r if nr > 1 else 0, h if nh > 1 else 0)
-        r, h, _ = st
-        return _TENSOR.pack(t.data_ptr(), 0, r if shape[0] > 1 else 0, h if shape[1] > 1 else 0)
-
-    def _heads(self, shape, name, kv):
-        if not (3 <= len(shape) <= 4 and shape[-1] == self.head_dim and (not kv or shape[-2] == self.kv_heads)):
-            _bad(f"{name}: [..., {self.kv_heads if kv else 'heads'}, {self.head_dim}] with 3 or 4 axes, got {tuple(shape)}")
-        return shape[-2]
-
-    def _failed(self, rc):
-        from . import MoeError
-        # a busy handle's text is the running call's
-        raise MoeError(rc, "the cache is in use by another thread" if rc == 5 else
-                       self._lib.moe_kv_last_error(self._h).decode())
-
-    def _stream(self, stream):
-        if stream is None:
-            return self._current_stream(self._index)
-        return stream if isinstance(stream, int) else stream.cuda_stream
-
-    # ------------------------------------------------------------------------- calls
+    @staticmethod
+    def _raw(stream):
+        return stream if stream is None or type(stream) is int else stream.cuda_stream
 
     def append(self, k, v, *, table, lens, starts=None, max_new=None, layer=0, stream=None):
         """Quantise the rows k, v into the sequences' pages and update the pages' bounds."""
-        shape = k.shape
-        self._heads(shape, "k", True)
-        _, b = self._batch(shape, table, lens, starts, max_new)
-        rc = self._lib.moe_kv_append(self._h, layer, b, self._rows(k, "k", shape), self._rows(v, "v", shape),
-                                     self._stream(stream))
-        if rc:
-            self._failed(rc)
+        self._c.append(k, v, table, lens, starts, max_new, layer, self._raw(stream))
 
     def read(self, k, v, *, table, lens, starts=None, max_new=None, layer=0, stream=None):
         """The stored keys and values of the rows, into k and v."""
-        shape = k.shape
-        self._heads(shape, "k", True)
-        _, b = self._batch(shape, table, lens, starts, max_new)
-        rc = self._lib.moe_kv_read(self._h, layer, b, self._rows(k, "k", shape, True), self._rows(v, "v", shape, True),
-                                   self._stream(stream))
-        if rc:
-            self._failed(rc)
+        self._c.read(k, v, table, lens, starts, max_new, layer, self._raw(stream))
 
     def attention(self, q, out, *, table, lens, starts=None, max_new=None, scale=None, causal=True, lse=None,
                   pages=None, layer=0, stream=None):
         """out = softmax(scale q k^T) v of the rows q (scale None: 1 / sqrt(head_dim)).
         pages: None, or `select`'s choice, the only pages then attended to.  lse: None, or
         float32 [rows, heads] for the logarithm of each row's sum of exponentials."""
-        shape = q.shape
-        heads = self._heads(shape, "q", False)
-        rows, b = self._batch(shape, table, lens, starts, max_new)
-        lp = pp = None
-        budget = 0
-        if lse is not None:
-            import torch
-            if not (lse.device == self.device and lse.dtype == torch.float32 and lse.is_contiguous()
-                    and lse.numel() == rows * heads):
-                _bad("lse: contiguous float32, one value per row and query head")
-            lp = lse.data_ptr()
-        if pages is not None:
-            budget = self._choice(pages, rows)
-            pp = pages.data_ptr()
-        rc = self._lib.moe_kv_attention(self._h, layer, b, self._rows(q, "q", shape), heads,
-                                        self._scale if scale is None else scale, 1 if causal else 0,
-                                        self._rows(out, "out", shape, True), lp, pp, budget, self._stream(stream))
-        if rc:
-            self._failed(rc)
-
-    def _choice(self, pages, rows):
-        if not (pages.dtype is self._i32 and pages.is_cuda and pages.get_device() == self._index and pages.is_contiguous()
-                and pages.dim() >= 3 and pages.shape[-2] == self.kv_heads
-                and pages.numel() == rows * self.kv_heads * pages.shape[-1]):
-            _bad("pages: contiguous int32 [rows, kv_heads, budget]")
-        return pages.shape[-1]
+        self._c.attention(q, out, table, lens, starts, max_new, layer, self._raw(stream), scale, causal, lse, pages)
 
     def select(self, q, pages, *, table, lens, starts=None, max_new=None, keep_first=1, keep_last=1, layer=0,
                stream=None):
         """Choose pages.shape[-1] pages for each row and kv head into pages (int32 [rows,
         kv_heads, budget], ascending, -1 where a row sees fewer): the first keep_first, the
         last keep_last, then those whose bounds promise the largest q . k."""
-        shape = q.shape
-        heads = self._heads(shape, "q", False)
-        rows, b = self._batch(shape, table, lens, starts, max_new)
-        rc = self._lib.moe_kv_select(self._h, layer, b, self._rows(q, "q", shape), heads, self._choice(pages, rows),
-                                     keep_first, keep_last, pages.data_ptr(), self._stream(stream))
-        if rc:
-            self._failed(rc)
+        self._c.select(q, pages, table, lens, starts, max_new, layer, self._raw(stream), keep_first, keep_last)
