@@ -404,11 +404,12 @@ typedef struct moe_kv_tensor {
 moe_status moe_kv_sizes(const moe_kv_desc* desc, int64_t* page_bytes_per_layer, int64_t* bounds_bytes_per_layer);
 
 /* Create a handle on caller-owned pages: validates the shapes and allocates
- * the workspace of attention and selection (nothing is allocated later).  The
- * pages need no initialisation.  A handle is used by one host thread at a
- * time; a call that uses the workspace on another stream than the last such
- * call first waits for it (calls inside a stream capture take no part in
- * that).  Ordering writes to the pages before reads of them is the caller's,
+ * the workspace of attention and selection (40 MB; nothing is allocated
+ * later).  The pages need no initialisation.  A handle is used by one host
+ * thread at a time; a call that uses the workspace on another stream than the
+ * last such call first waits for it.  Calls inside a stream capture take no
+ * part in that: a graph that holds them must not run beside another use of the
+ * handle.  Ordering writes to the pages before reads of them is the caller's,
  * as for any device memory. */
 moe_status moe_kv_create(const moe_kv_desc* desc, moe_kv_cache** out);
 /* Waits for the last call that used the workspace and frees it. */

@@ -274,9 +274,11 @@ extern "C" moe_status moe_kv_attention(moe_kv_cache* h, int layer, const moe_kv_
     bool capturing = false;
     cudaError_t e = order_before(kv, s, capturing);
     if (e == cudaSuccess && *kv->err_host) {  // reported once; the counters start afresh behind the failed call
-      *kv->err_host = 0;
-      e = cudaMemsetAsync(kv->counters(), 0, Kv::kCounterBytes, s);
-      if (e == cudaSuccess) e = order_after(kv, s, capturing);
+      if (!capturing) {  // (a capture would only record it: the next call outside reports again and does it)
+        *kv->err_host = 0;
+        e = cudaMemsetAsync(kv->counters(), 0, Kv::kCounterBytes, s);
+        if (e == cudaSuccess) e = order_after(kv, s, capturing);
+      }
       if (e == cudaSuccess) return fail(kv, MOE_ERR_TIMEOUT, "a bounded wait of an earlier moe_kv_attention gave up: its results are wrong");
     }
     if (e == cudaSuccess) e = kv_attention(*kv, a, s);
@@ -304,9 +306,10 @@ extern "C" moe_status moe_kv_select(moe_kv_cache* h, int layer, const moe_kv_bat
     KvSelectArgs a{view(kv, layer), batch_of(batch), static_cast<const uint16_t*>(q->data), rows_of(q), q_heads,
                    budget, keep_first, keep_last, pages_out};
     bool capturing = false;
-    cudaError_t e = order_before(kv, s, capturing);
+    const bool shares = batch->table_pages > kKvSelOwn;  // otherwise the workspace is not used
+    cudaError_t e = shares ? order_before(kv, s, capturing) : cudaSuccess;
     if (e == cudaSuccess) e = kv_select(*kv, a, s);
-    if (e == cudaSuccess) e = order_after(kv, s, capturing);
+    if (e == cudaSuccess && shares) e = order_after(kv, s, capturing);
     return e == cudaSuccess ? MOE_OK : cuda_fail(kv, e, "moe_kv_select");
   });
 }

@@ -29,8 +29,8 @@ __device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
 }
 constexpr uint32_t kNegate = 0x80008000u;
 
-// x / 15 rounded to nearest: the product with the reciprocal, corrected once, is the division's
-// result for every finite 16-bit x (compared for all of them).
+// x / 15 rounded to nearest: the product with the reciprocal and Markstein's correction of it by
+// its remainder.  Equal to the division for every finite 16-bit x (compared for all of them).
 __device__ __forceinline__ float over15(float x) {
   constexpr float kInv = 1.0f / 15.0f;
   const float q = __fmul_rn(x, kInv);

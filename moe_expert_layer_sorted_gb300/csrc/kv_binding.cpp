@@ -57,9 +57,13 @@ int small(PyObject* o, const char* name) {
   if (v < INT32_MIN || v > INT32_MAX) throw Bad{std::string(name) + " is out of range"};
   return (int)v;
 }
+// None (the current stream), an address, or a stream object.
 void* stream_of(const Cache* c, PyObject* o) {
   if (o == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)c->device).stream();
-  void* p = PyLong_AsVoidPtr(o);
+  PyObject* address = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
+  if (!address) throw Failed();
+  void* p = PyLong_AsVoidPtr(address);
+  Py_DECREF(address);
   if (!p && PyErr_Occurred()) throw Failed();
   return p;
 }

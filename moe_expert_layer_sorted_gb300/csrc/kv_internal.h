@@ -69,6 +69,9 @@ cudaError_t kv_prompt_f16(Kv& kv, const KvAttnArgs& a, cudaStream_t s);
 cudaError_t kv_attention(Kv& kv, const KvAttnArgs& a, cudaStream_t s);
 cudaError_t kv_select(Kv& kv, const KvSelectArgs& a, cudaStream_t s);
 
+// Rows of at most this many pages are scored and picked by one CTA, without the workspace.
+constexpr int kKvSelOwn = 512;
+
 // Rounds in shared memory of the decode kernel: 3 to 8, so that two CTAs of eight warps share an SM.
 template <int D, int G>
 constexpr int kDecStages = 9216 / KvGeom<D, G>::kBytes;

@@ -21,7 +21,6 @@ namespace {
 constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
 constexpr int kSelPages = 32;     // pages per scoring CTA
 constexpr int kSelHeads = 16;     // kv heads per scoring CTA
-constexpr int kSelOwn = 512;      // rows with at most this many pages are scored and picked by one CTA
 constexpr uint32_t kAlways = 0xffffffffu;  // above the key of +infinity
 
 // Order-preserving key of a score (-0 and +0 equal), NaN as -infinity.
@@ -255,8 +254,8 @@ __device__ __forceinline__ void list_all(const KvSelectArgs& a, const Row& w, in
 template <typename T, int D>
 __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_constant__ KvSelectArgs a) {
   __shared__ __align__(16) float qs[D];
-  __shared__ uint32_t keys[kSelOwn];
-  __shared__ int32_t ids[kSelOwn];
+  __shared__ uint32_t keys[kKvSelOwn];
+  __shared__ int32_t ids[kKvSelOwn];
   const int h = blockIdx.x % a.c.heads;
   const Row w = row_of(a, blockIdx.x / a.c.heads);
   if (w.i >= w.q.rows) return;
@@ -267,7 +266,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
   __syncthreads();
   score_pages<T, D, false>(a, w, 0, w.pages, h, h + 1, ids, qs, keys, 0);
   __syncthreads();
-  pick<kSelOwn / kSelThreads>(a, keys, w.pages, out);
+  pick<kKvSelOwn / kSelThreads>(a, keys, w.pages, out);
 }
 
 // Scores: one CTA per (row, kSelPages pages, kSelHeads heads).
@@ -302,7 +301,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_pick_kernel(const __grid_const
 template <typename T, int D>
 cudaError_t select(Kv& kv, const KvSelectArgs& a, cudaStream_t s) {
   const int64_t rows = (int64_t)a.b.batch * a.b.max_new;
-  if (a.b.table_pages <= kSelOwn) {
+  if (a.b.table_pages <= kKvSelOwn) {
     if (rows * a.c.heads > 0x7fffffff) return cudaErrorInvalidConfiguration;
     kv_select_kernel<T, D><<<(unsigned)(rows * a.c.heads), kSelThreads, 0, s>>>(a);
     return cudaGetLastError();

@@ -137,28 +137,24 @@ class KVCache:
 
     # The tensors are checked and unpacked in csrc/kv_binding.cpp.
 
-    @staticmethod
-    def _raw(stream):
-        return stream if stream is None or type(stream) is int else stream.cuda_stream
-
     def append(self, k, v, *, table, lens, starts=None, max_new=None, layer=0, stream=None):
         """Quantise the rows k, v into the sequences' pages and update the pages' bounds."""
-        self._c.append(k, v, table, lens, starts, max_new, layer, self._raw(stream))
+        self._c.append(k, v, table, lens, starts, max_new, layer, stream)
 
     def read(self, k, v, *, table, lens, starts=None, max_new=None, layer=0, stream=None):
         """The stored keys and values of the rows, into k and v."""
-        self._c.read(k, v, table, lens, starts, max_new, layer, self._raw(stream))
+        self._c.read(k, v, table, lens, starts, max_new, layer, stream)
 
     def attention(self, q, out, *, table, lens, starts=None, max_new=None, scale=None, causal=True, lse=None,
                   pages=None, layer=0, stream=None):
         """out = softmax(scale q k^T) v of the rows q (scale None: 1 / sqrt(head_dim)).
         pages: None, or `select`'s choice, the only pages then attended to.  lse: None, or
         float32 [rows, heads] for the logarithm of each row's sum of exponentials."""
-        self._c.attention(q, out, table, lens, starts, max_new, layer, self._raw(stream), scale, causal, lse, pages)
+        self._c.attention(q, out, table, lens, starts, max_new, layer, stream, scale, causal, lse, pages)
 
     def select(self, q, pages, *, table, lens, starts=None, max_new=None, keep_first=1, keep_last=1, layer=0,
                stream=None):
         """Choose pages.shape[-1] pages for each row and kv head into pages (int32 [rows,
         kv_heads, budget], ascending, -1 where a row sees fewer): the first keep_first, the
         last keep_last, then those whose bounds promise the largest q . k."""
-        self._c.select(q, pages, table, lens, starts, max_new, layer, self._raw(stream), keep_first, keep_last)
+        self._c.select(q, pages, table, lens, starts, max_new, layer, stream, keep_first, keep_last)
