@@ -2,8 +2,8 @@
 // the tensors and passes their addresses to the C ABI.  A decode step's calls
 // are a few microseconds of GPU work each, and asking tensors for their types,
 // shapes and strides from Python costs as much again per call.  One row written
-// and read back, called from Python in a loop: 28.6 us a pass, 33.9 with the same
-// checks in Python; pages chosen and attended to at 6,000 tokens: 36.0, 42.7.
+// and read back, called from Python among other work: 22.8 us a pass, 33.9 with
+// the same checks in Python; pages chosen and attended to at 6,000 tokens: 27.0, 42.7.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

@@ -11,13 +11,15 @@
 // warps work for the other.  Roles:
 //   warps 0-3, 4-7  softmax of tile 0, 1: a thread owns a row (a TMEM lane);
 //                   the running reference m is raised, and O rescaled in TMEM,
-//                   only where a score passes it by 2^8;
+//                   only where a tile's weights would outgrow fp16;
 //   warps 8-11      stored codes -> 16-bit K and V tiles: a thread owns a
 //                   token, its code words and params loaded a tile ahead;
 //   warp 12         tcgen05.mma issue, TMEM allocation.
 // Rounding: k, v and P to fp16, in caches of both types, k and v from c + s (u - 8)
 // by one fma on exact operands; the sums are fp32.  (bf16's 2^-9 would be seen: in a
-// score of several hundred, and in P and v as much as in a bf16 output.)  So that
+// score of several hundred, and in P and v as much as in a bf16 output.  What is
+// left shows in an fp16 output only: 5.1e-4 of its norm at scores of a standard
+// deviation of 1.5, 4.5e-4 by the keys, where its own rounding is 2.1e-4.)  So that
 // nothing leaves fp16's range, powers of two are taken out and put back: of a query
 // row, to its largest element (back in the row's factor scale log2 e); of a token
 // whose keys are all tiny or huge (back on its column, in tiles that hold one); of
@@ -31,6 +33,15 @@
 // is an exact zero, but zero times a NaN value is not: values of a poisoned
 // group enter the tile as zeros and its groups are remembered per row that sees
 // the token.
+//
+// Measured (bf16, 32 query and 8 kv heads of 128 channels, groups of 64): 8,192
+// rows at the end of 16,384 tokens 1,160 us, 1,421 TFLOP/s, the tensor pipe busy
+// 61 % of the time.  Bound by the chain of one token tile, scores -> weights ->
+// product, of which two row tiles alternate: 1.8 us a token tile where the products
+// alone take 1.1; issue slots 54 %, exponents 31 %.  16 softmax warps, two threads a row,
+// have too few registers (1,780 us against 1,400 before other steps).  Three ragged prompts of up
+// to 333 rows over up to 2,500 tokens (fp16, 12 heads of 64): 31.6 us with the
+// join, some ten token tiles one after the other, launch and join.
 #pragma once
 
 #include "kv_internal.h"
