@@ -106,18 +106,27 @@ KvBatch batch_of(const moe_kv_batch* b) {
 KvRows rows_of(const moe_kv_tensor* t) { return {t->batch_stride, t->row_stride, t->head_stride}; }
 
 // Calls that share the workspace follow one another across streams; inside a
-// capture the graph's own edges order its nodes.
+// capture the graph's own edges order its nodes.  A stream may be gone by the
+// next call, so its work is recorded at once, but for the default stream, which
+// stays and is never captured: that one is recorded when another stream follows.
 cudaError_t order_before(Kv* kv, cudaStream_t s, bool& capturing) {
-  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-  const cudaError_t e = cudaStreamIsCapturing(s, &st);
-  if (e != cudaSuccess) return e;
-  capturing = st != cudaStreamCaptureStatusNone;
-  if (!capturing && kv->have_last && kv->last_stream != s) return cudaStreamWaitEvent(s, kv->ev_done, 0);
-  return cudaSuccess;
+  capturing = false;
+  if (s) {
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    const cudaError_t e = cudaStreamIsCapturing(s, &st);
+    if (e != cudaSuccess) return e;
+    capturing = st != cudaStreamCaptureStatusNone;
+  }
+  if (capturing || !kv->have_last || kv->last_stream == s) return cudaSuccess;
+  if (!kv->last_stream) {
+    const cudaError_t e = cudaEventRecord(kv->ev_done, kv->last_stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaStreamWaitEvent(s, kv->ev_done, 0);
 }
 cudaError_t order_after(Kv* kv, cudaStream_t s, bool capturing) {
   if (capturing) return cudaSuccess;
-  const cudaError_t e = cudaEventRecord(kv->ev_done, s);
+  const cudaError_t e = s ? cudaEventRecord(kv->ev_done, s) : cudaSuccess;
   if (e == cudaSuccess) {
     kv->last_stream = s;
     kv->have_last = true;
@@ -221,7 +230,8 @@ extern "C" moe_status moe_kv_destroy(moe_kv_cache* h) {
     if (!kv) return fail(nullptr, MOE_ERR_INVALID, "handle is NULL");
     if (kv->busy.exchange(1)) return MOE_ERR_STATE;  // another call is running: stays as it is
     DeviceScope ds(kv->d.device);
-    if (kv->have_last) cudaEventSynchronize(kv->ev_done);
+    if (kv->have_last && (kv->last_stream || cudaEventRecord(kv->ev_done, nullptr) == cudaSuccess))
+      cudaEventSynchronize(kv->ev_done);
     release(kv);
     return MOE_OK;
   });
