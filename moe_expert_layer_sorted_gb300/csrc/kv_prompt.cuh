@@ -38,10 +38,12 @@
 // rows at the end of 16,384 tokens 1,160 us, 1,421 TFLOP/s, the tensor pipe busy
 // 61 % of the time.  Bound by the chain of one token tile, scores -> weights ->
 // product, of which two row tiles alternate: 1.8 us a token tile where the products
-// alone take 1.1; issue slots 54 %, exponents 31 %.  16 softmax warps, two threads a row,
-// have too few registers (1,780 us against 1,400 before other steps).  Three ragged prompts of up
-// to 333 rows over up to 2,500 tokens (fp16, 12 heads of 64): 31.6 us with the
-// join, some ten token tiles one after the other, launch and join.
+// alone take 1.1; issue slots 54 %, exponents 31 %.  16 softmax warps, two threads
+// a row, have too few registers (1,780 us against 1,400 before other steps); halves
+// of 64 tokens, the next one's scores computed during the weights of one, need
+// products of N = 64 and twice the hand-overs (1,497 us).  Three ragged prompts of
+// up to 333 rows over up to 2,500 tokens (fp16, 12 heads of 64): 32 us, some ten
+// token tiles one after the other, launch and join.
 #pragma once
 
 #include "kv_internal.h"

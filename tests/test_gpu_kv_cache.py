@@ -522,3 +522,44 @@ def test_refusals():
     c.attention(q[:, :0], o[:, :0], **b)
     c.append(kv[:0], kv[:0], table=w.table[:0], lens=w.lens_t[:0])
     torch.cuda.synchronize()
+
+
+def test_calls_of_the_binding():
+    from moe_expert_layer_sorted_gb300 import MoeError
+    w = World(64, 32, 16, FP, 2, [40], seed=3).fill()
+    q = w.rand(1, 1, 4, 64)
+    out = [torch.empty_like(q) for _ in range(4)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for o, stream in zip(out, (None, torch.cuda.current_stream().cuda_stream, side, side.cuda_stream)):
+        w.cache.attention(q, o, stream=stream, **w.batch)  # the current one, an address, a stream
+    with torch.cuda.stream(side):
+        again = torch.empty_like(q)
+        w.cache.attention(q, again, **w.batch)
+    torch.cuda.synchronize()
+    assert all(torch.equal(out[0], o) for o in out[1:] + [again])
+    for bad in (dict(stream="0"), dict(layer="0"), dict(scale="1"), dict(layer=1 << 40)):
+        with pytest.raises((MoeError, TypeError, AttributeError, OverflowError)):
+            w.cache.attention(q, out[0], **{**w.batch, **bad})
+    for q_, o_ in ((None, out[0]), (q, None), (q.cpu().numpy(), out[0]), (q[0, 0], out[0]), (q, out[0].expand(2, 1, 4, 64))):
+        with pytest.raises(MoeError):
+            w.cache.attention(q_, o_, **w.batch)
+    with pytest.raises(MoeError):  # a destination whose rows are one row
+        w.cache.read(*(torch.empty(1, 1, 1, 64, dtype=FP, device="cuda").expand(1, 1, 2, 64) for _ in "kv"), **w.batch)
+    w.cache.close()
+    w.cache.close()
+    with pytest.raises(MoeError, match="closed"):
+        w.cache.attention(q, out[0], **w.batch)
+
+
+def test_short_rows_are_chosen_on_two_streams_at_once():
+    w = World(128, 64, 16, BF, 2, [900, 333], seed=9).fill()
+    q = w.rand(2, 1, 8, 128)
+    chosen = [torch.full((2, 2, 7), -9, dtype=torch.int32, device="cuda") for _ in range(8)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for i, pages in enumerate(chosen):
+        w.cache.select(q, pages, stream=streams[i % 2], **w.batch)
+    torch.cuda.synchronize()
+    assert (chosen[0] >= 0).all() and all(torch.equal(chosen[0], c) for c in chosen[1:])
