@@ -165,6 +165,23 @@ struct Plan {
   std::string last_error;
 };
 
+// Which stream a handle value names now (0: one that is being captured, and may not be
+// asked).  A value is given out again once its stream is destroyed, whose work may still run,
+// and the per-thread default stream's is one value for a stream in every thread.  The default
+// stream stays and is never captured.
+constexpr unsigned long long kDefaultStream = ~0ull;
+inline cudaError_t stream_identity(cudaStream_t s, bool& capturing, unsigned long long& id) {
+  capturing = false;
+  id = kDefaultStream;
+  if (!s || s == cudaStreamLegacy) return cudaSuccess;
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  const cudaError_t e = cudaStreamIsCapturing(s, &st);
+  if (e != cudaSuccess) return e;
+  capturing = st != cudaStreamCaptureStatusNone;
+  id = 0;
+  return capturing ? cudaSuccess : cudaStreamGetId(s, &id);
+}
+
 // Makes `fn` launchable with `bytes` of dynamic shared memory on the current
 // device.  The attribute belongs to the function, not to a plan, so it is only
 // ever raised (process-wide, per device): lowering it for one plan would make

@@ -109,26 +109,21 @@ KvRows rows_of(const moe_kv_tensor* t) { return {t->batch_stride, t->row_stride,
 // capture the graph's own edges order its nodes.  A stream may be gone by the
 // next call, so its work is recorded at once, but for the default stream, which
 // stays and is never captured: that one is recorded when another stream follows.
-cudaError_t order_before(Kv* kv, cudaStream_t s, bool& capturing) {
-  capturing = false;
-  if (s) {
-    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-    const cudaError_t e = cudaStreamIsCapturing(s, &st);
-    if (e != cudaSuccess) return e;
-    capturing = st != cudaStreamCaptureStatusNone;
-  }
-  if (capturing || !kv->have_last || kv->last_stream == s) return cudaSuccess;
-  if (!kv->last_stream) {
-    const cudaError_t e = cudaEventRecord(kv->ev_done, kv->last_stream);
-    if (e != cudaSuccess) return e;
-  }
+struct Order {
+  bool capturing = false;
+  unsigned long long stream = 0;
+};
+cudaError_t order_before(Kv* kv, cudaStream_t s, Order& o) {
+  cudaError_t e = stream_identity(s, o.capturing, o.stream);
+  if (e != cudaSuccess || o.capturing || !kv->have_last || kv->last_stream == o.stream) return e;
+  if (kv->last_stream == kDefaultStream && (e = cudaEventRecord(kv->ev_done, nullptr)) != cudaSuccess) return e;
   return cudaStreamWaitEvent(s, kv->ev_done, 0);
 }
-cudaError_t order_after(Kv* kv, cudaStream_t s, bool capturing) {
-  if (capturing) return cudaSuccess;
-  const cudaError_t e = s ? cudaEventRecord(kv->ev_done, s) : cudaSuccess;
+cudaError_t order_after(Kv* kv, cudaStream_t s, const Order& o) {
+  if (o.capturing) return cudaSuccess;
+  const cudaError_t e = o.stream != kDefaultStream ? cudaEventRecord(kv->ev_done, s) : cudaSuccess;
   if (e == cudaSuccess) {
-    kv->last_stream = s;
+    kv->last_stream = o.stream;
     kv->have_last = true;
   }
   return e;
@@ -230,7 +225,7 @@ extern "C" moe_status moe_kv_destroy(moe_kv_cache* h) {
     if (!kv) return fail(nullptr, MOE_ERR_INVALID, "handle is NULL");
     if (kv->busy.exchange(1)) return MOE_ERR_STATE;  // another call is running: stays as it is
     DeviceScope ds(kv->d.device);
-    if (kv->have_last && (kv->last_stream || cudaEventRecord(kv->ev_done, nullptr) == cudaSuccess))
+    if (kv->have_last && (kv->last_stream != kDefaultStream || cudaEventRecord(kv->ev_done, nullptr) == cudaSuccess))
       cudaEventSynchronize(kv->ev_done);
     release(kv);
     return MOE_OK;
@@ -281,18 +276,18 @@ extern "C" moe_status moe_kv_attention(moe_kv_cache* h, int layer, const moe_kv_
     KvAttnArgs a{view(kv, layer), batch_of(batch), static_cast<const uint16_t*>(q->data),
                  static_cast<uint16_t*>(out->data), lse, rows_of(q), rows_of(out), q_heads, scale, causal,
                  pages, pages ? budget : 0};
-    bool capturing = false;
-    cudaError_t e = order_before(kv, s, capturing);
+    Order order;
+    cudaError_t e = order_before(kv, s, order);
     if (e == cudaSuccess && *kv->err_host) {  // reported once; the counters start afresh behind the failed call
-      if (!capturing) {  // (a capture would only record it: the next call outside reports again and does it)
+      if (!order.capturing) {  // (a capture would only record it: the next call outside reports again and does it)
         *kv->err_host = 0;
         e = cudaMemsetAsync(kv->counters(), 0, Kv::kCounterBytes, s);
-        if (e == cudaSuccess) e = order_after(kv, s, capturing);
+        if (e == cudaSuccess) e = order_after(kv, s, order);
       }
       if (e == cudaSuccess) return fail(kv, MOE_ERR_TIMEOUT, "a bounded wait of an earlier moe_kv_attention gave up: its results are wrong");
     }
     if (e == cudaSuccess) e = kv_attention(*kv, a, s);
-    if (e == cudaSuccess) e = order_after(kv, s, capturing);
+    if (e == cudaSuccess) e = order_after(kv, s, order);
     return e == cudaSuccess ? MOE_OK : cuda_fail(kv, e, "moe_kv_attention");
   });
 }
@@ -315,11 +310,11 @@ extern "C" moe_status moe_kv_select(moe_kv_cache* h, int layer, const moe_kv_bat
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     KvSelectArgs a{view(kv, layer), batch_of(batch), static_cast<const uint16_t*>(q->data), rows_of(q), q_heads,
                    budget, keep_first, keep_last, pages_out};
-    bool capturing = false;
+    Order order;
     const bool shares = batch->table_pages > kKvSelOwn;  // otherwise the workspace is not used
-    cudaError_t e = shares ? order_before(kv, s, capturing) : cudaSuccess;
+    cudaError_t e = shares ? order_before(kv, s, order) : cudaSuccess;
     if (e == cudaSuccess) e = kv_select(*kv, a, s);
-    if (e == cudaSuccess && shares) e = order_after(kv, s, capturing);
+    if (e == cudaSuccess && shares) e = order_after(kv, s, order);
     return e == cudaSuccess ? MOE_OK : cuda_fail(kv, e, "moe_kv_select");
   });
 }

@@ -27,7 +27,7 @@ struct Kv {
   volatile uint32_t* err_host = nullptr;  // mapped pinned word: set by a kernel whose bounded wait gave up
   uint32_t* err_dev = nullptr;
   cudaEvent_t ev_done = nullptr;  // end of the last call that used the workspace
-  cudaStream_t last_stream = nullptr;
+  unsigned long long last_stream = 0;  // its identity
   bool have_last = false;
   std::atomic<int> busy{0};
   std::string last_error;

@@ -1,0 +1,56 @@
+// The launchers that csrc/kv.cu calls, without kernels: each call goes to the log of fake_cuda.cpp.
+#include <condition_variable>
+#include <mutex>
+
+#include "kv_internal.h"
+
+void say(const char* what, cudaStream_t s);
+
+namespace {
+
+std::mutex g_mu;
+std::condition_variable g_cv;
+bool g_blocking = false, g_inside = false;
+
+}  // namespace
+
+// 1: the next append stays inside its call until 0; 2: waits until one is inside
+extern "C" void fake_block(int what) {
+  std::unique_lock<std::mutex> l(g_mu);
+  if (what == 2) {
+    g_cv.wait(l, [] { return g_inside; });
+    return;
+  }
+  g_blocking = what;
+  g_cv.notify_all();
+}
+
+namespace moe {
+
+cudaError_t kv_append(const Kv&, const KvView&, const KvBatch&, const uint16_t*, const KvRows&, const uint16_t*,
+                      const KvRows&, cudaStream_t s) {
+  std::unique_lock<std::mutex> l(g_mu);
+  if (g_blocking) {
+    g_inside = true;
+    g_cv.notify_all();
+    g_cv.wait(l, [] { return !g_blocking; });
+    g_inside = false;
+  }
+  say("append", s);
+  return cudaSuccess;
+}
+cudaError_t kv_read(const Kv&, const KvView&, const KvBatch&, uint16_t*, const KvRows&, uint16_t*, const KvRows&,
+                    cudaStream_t s) {
+  say("read", s);
+  return cudaSuccess;
+}
+cudaError_t kv_attention(Kv&, const KvAttnArgs&, cudaStream_t s) {
+  say("attention", s);
+  return cudaSuccess;
+}
+cudaError_t kv_select(Kv&, const KvSelectArgs&, cudaStream_t s) {
+  say("select", s);
+  return cudaSuccess;
+}
+
+}  // namespace moe

@@ -1,0 +1,63 @@
+"""Order, errors and handles of the key/value cache's C entry points, on the host."""
+import pytest
+
+import kv_host
+
+
+@pytest.fixture(scope="module")
+def lib(tmp_path_factory):
+    return kv_host.build(tmp_path_factory.mktemp("kv_host"))
+
+
+@pytest.fixture
+def cache(lib):
+    for i in range(16):
+        lib.fake_identity(i, 100 + i)
+        lib.fake_capturing(i, 0)
+    c = kv_host.Cache(lib)
+    yield c
+    lib.moe_kv_destroy(c.h)
+
+
+def waits(log):
+    return [x for x in log if x.startswith("wait")]
+
+
+def test_another_stream_waits_and_the_same_one_does_not(cache):
+    for s in (4, 4):
+        assert cache.attention(s) == 0
+    assert not waits(cache.log())
+    assert cache.attention(5) == 0
+    log = cache.log()
+    assert log.index("wait 5") < log.index("attention 5")
+    assert cache.select(4, pages=600) == 0  # scores in the workspace
+    assert waits(cache.log()) == ["wait 4"]
+    assert cache.select(5, pages=4) == 0  # none
+    assert not waits(cache.log())
+
+
+def test_default_stream_is_recorded_when_another_follows(cache):
+    assert cache.attention(0) == 0 and cache.attention(0) == 0
+    assert cache.log() == ["attention 0", "attention 0"]
+    assert cache.attention(4) == 0
+    assert cache.log()[:3] == ["record 0", "wait 4", "attention 4"]
+
+
+def test_a_handle_value_that_names_a_new_stream_waits(cache, lib):
+    """A stream that was destroyed (its work goes on) and whose handle value another one got; the
+    per-thread default stream (handle 2), one stream in each thread."""
+    for handle in (4, 2):
+        lib.fake_identity(handle, 1000 + handle)
+        assert cache.attention(handle) == 0
+        cache.log()
+        lib.fake_identity(handle, 2000 + handle)
+        assert cache.attention(handle) == 0
+        assert waits(cache.log()) == [f"wait {handle}"]
+
+
+def test_a_capture_neither_waits_nor_records(cache, lib):
+    assert cache.attention(4) == 0
+    lib.fake_capturing(5, 1)
+    cache.log()
+    assert cache.attention(5) == 0
+    assert cache.log() == ["attention 5"]
