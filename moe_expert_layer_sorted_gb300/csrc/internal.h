@@ -149,7 +149,7 @@ struct Plan {
   // streams
   cudaStream_t aux = nullptr;  // second stream (placement, host-resident experts)
   cudaEvent_t ev_fork = nullptr, ev_join = nullptr, ev_done = nullptr;
-  cudaStream_t last_stream = nullptr;
+  unsigned long long last_stream = 0;  // identity of the last forward's
   bool have_last = false;
 
   // decode launch configuration per batch size T (computed on first use)

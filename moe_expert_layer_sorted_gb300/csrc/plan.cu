@@ -481,20 +481,21 @@ void release(Plan* p) {
 // stream is being captured into a graph nothing is waited on or recorded --
 // the graph's edges order its nodes, and an event recorded inside a capture
 // could not be waited on by a later forward outside it.
-cudaError_t order_before(Plan* p, cudaStream_t s, bool& capturing) {
-  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-  cudaError_t e = cudaStreamIsCapturing(s, &st);
-  if (e != cudaSuccess) return e;
-  capturing = st != cudaStreamCaptureStatusNone;
-  if (!capturing && p->have_last && p->last_stream != s) return cudaStreamWaitEvent(s, p->ev_done, 0);
-  return cudaSuccess;
+struct Order {
+  bool capturing = false;
+  unsigned long long stream = 0;
+};
+cudaError_t order_before(Plan* p, cudaStream_t s, Order& o) {
+  const cudaError_t e = stream_identity(s, o.capturing, o.stream);
+  if (e != cudaSuccess || o.capturing || !p->have_last || p->last_stream == o.stream) return e;
+  return cudaStreamWaitEvent(s, p->ev_done, 0);
 }
 
-cudaError_t order_after(Plan* p, cudaStream_t s, bool capturing) {
-  if (capturing) return cudaSuccess;
+cudaError_t order_after(Plan* p, cudaStream_t s, const Order& o) {
+  if (o.capturing) return cudaSuccess;
   const cudaError_t e = cudaEventRecord(p->ev_done, s);
   if (e == cudaSuccess) {
-    p->last_stream = s;
+    p->last_stream = o.stream;
     p->have_last = true;
   }
   return e;
@@ -935,8 +936,8 @@ moe_status layer_forward(moe_plan* plan, int layer, const void* x, int T, void* 
   }
   if (take_overflow(p)) return fail(p, MOE_ERR_STATE, kOverflowMsg);
   cudaStream_t s = (cudaStream_t)stream;
-  bool capturing = false;
-  CK(p, order_before(p, s, capturing));
+  Order order;
+  CK(p, order_before(p, s, order));
   cudaError_t e;
   if (T <= kDecodeMaxTokens)
     e = decode_forward(*p, layer, (const uint16_t*)x, T, (uint16_t*)y, s, dbg, res, (uint16_t*)ysum);
@@ -944,7 +945,7 @@ moe_status layer_forward(moe_plan* plan, int layer, const void* x, int T, void* 
     e = prefill_forward(*p, layer, (const uint16_t*)x, T, (uint16_t*)y, s, dbg, true, nullptr, res,
                         (uint16_t*)ysum);
   if (e != cudaSuccess) return forward_fail(p, e, "forward launch");
-  CK(p, order_after(p, s, capturing));
+  CK(p, order_after(p, s, order));
   return MOE_OK;
 }
 }  // namespace
@@ -982,8 +983,8 @@ extern "C" moe_status moe_prefill_forward(moe_plan* plan, int layer, const void*
   if (*p->err_host) return fail(p, MOE_ERR_STATE, "a latched device error is pending: call moe_layer_forward");
   if (take_overflow(p)) return fail(p, MOE_ERR_STATE, kOverflowMsg);
   cudaStream_t s = (cudaStream_t)stream;
-  bool capturing = false;
-  CK(p, order_before(p, s, capturing));
+  Order order;
+  CK(p, order_before(p, s, order));
   const int64_t chunk = std::min<int64_t>(8192, d.max_tokens), H = d.hidden;
   // Staging pays back only over several chunks (it moves each host expert
   // over the link once instead of once per chunk): with one chunk every
@@ -1000,7 +1001,7 @@ extern "C" moe_status moe_prefill_forward(moe_plan* plan, int layer, const void*
                         stage ? p->pf_blob : nullptr);
     if (e != cudaSuccess) return forward_fail(p, e, "prefill chunk");
   }
-  CK(p, order_after(p, s, capturing));
+  CK(p, order_after(p, s, order));
   return MOE_OK;
 }
 
