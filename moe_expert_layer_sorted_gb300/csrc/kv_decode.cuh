@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
   __shared__ int sh_base, sh_group;
   __shared__ Item sh_item;
   __shared__ unsigned sh_last;
+  __shared__ float sh_lift[C];  // of the item's columns; every warp writes the same
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
 
@@ -328,6 +329,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
       float factor[NT][2];       // what makes the columns' sums scores (log2)
       int seen[NT][2];           // tokens that the columns see
       int least = 0x7fffffff, most = 0;  // over the columns
+      bool lifted = false;               // some column's scores are taken times a power of two first (sh_lift)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int s = it.s, h = it.head, row_lo = it.row_lo, ncols = it.cols;
@@ -351,7 +353,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int ex = (int)(top >> 23) - 127;  // the largest element to 2^14; an infinity or a NaN stays what it is
-        const int by = top == 0u || ex > 127 ? 0 : min(max(14 - ex, -102), 113);
+        const int by = top == 0u || ex > 127 ? 0 : min(14 - ex, 113);
         const float up = pow2(by), up16 = pow2(by - 4);  // the odd fields are 16 u
         float sum[NG];
 #pragma unroll
@@ -375,7 +377,13 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
         }
         const int64_t pos = (int64_t)q.len - q.rows + i;
         const int see = (int)min(max(a.causal ? pos + 1 : (int64_t)q.len, (int64_t)0), (int64_t)cap);
-        const float back = a.scale * 1.4426950408889634f * pow2(24 - by);
+        // scale log2 e 2^(24 - by), of which what would leave fp32's range stays with the scores
+        const float base = a.scale * 1.4426950408889634f;
+        const int over = min(max((int)(__float_as_uint(fabsf(base)) >> 23) - 127 + 24 - by - 126, 0), 126);
+        const int pw = 24 - by - over;  // -89..137: in two steps
+        const float back = base * pow2(pw / 2) * pow2(pw - pw / 2);
+        if (c == 0) sh_lift[nt * 8 + r] = pow2(over);
+        lifted |= __any_sync(0xffffffffu, over > 0);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           factor[nt][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * c + e));
@@ -384,6 +392,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
         least = min(least, __reduce_min_sync(0xffffffffu, see));
         most = max(most, __reduce_max_sync(0xffffffffu, see));
       }
+      __syncwarp();  // sh_lift
 
       float acc[D / 16][NT][4];  // O^T: channel tiles by columns
       float oc[NT][NG][2];       // this lane's tokens' part of sum P (c - 8 s), or of sum P c
@@ -598,6 +607,12 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
         if (pos >= 0) {
           float sc[NT][4];
           scores(blk, sc);
+          if (lifted) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sc[nt][e] *= sh_lift[nt * 8 + 2 * c + (e & 1)];
+          }
           if (pos + 16 > least) block(blk, pos, sc, std::true_type());
           else block(blk, pos, sc, std::false_type());
         }
