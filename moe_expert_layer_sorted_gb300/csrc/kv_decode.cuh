@@ -19,9 +19,14 @@
 //
 // Softmax: weights are 2^(score - reference) with a running reference per
 // column, raised only when a score passes it by 4, so that most blocks rescale
-// nothing; sums are fp32.  O is carried times 2^-E, E raised when a token's
-// values need it: weights times values of any size stay inside fp16's and,
-// summed, fp32's range.  A column that sees no token keeps the sum 0.
+// nothing; sums are fp32.  O is carried times 2^-E, with E for values of
+// ordinary size.  In a block that holds other sizes the reference goes by weight
+// times value: a huge value that a column does not see, or hardly weighs, takes
+// nothing from its other tokens, and a token of nearly all the weight and hardly
+// any value leaves room for the rest.  What is rounded to fp16 is then below
+// 2^-24 of the column's largest product.  (The groups of a token share this:
+// one whose values are 2^16 times smaller than another's begins to lose bits.)
+// A column that sees no token keeps the sum 0.
 //
 // Work split: all rounds (8 blocks of 16 tokens of one kv head and column tile)
 // of the batch in one line, cut into equal shares, one per CTA; a share covers
@@ -64,7 +69,9 @@ struct DecRegs {
 };
 constexpr int kDecMaxParts = kDecWarps * (64 + 4);  // CTAs, so parts of an item, whose references fit the merge buffer
 constexpr float kDecSlack = 4.0f;      // weights reach 2^4
-constexpr float kDecValues = 8192.0f;  // bound of |c| + 8 s times 2^-E
+constexpr int kDecRoom = 14;           // |c| + 8 s stays below 2^(E + 14): weights times steps below 2^15
+constexpr int kDecAim = 10;            // a column's largest weight times value is raised to about 2^(E + 10)
+constexpr float kDecPartScale = 0x1p-16f;  // of parts' weights (below 2^4 each): their sum with values stays in range
 
 __device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kDecWarps * 32) : "memory"); }
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -170,7 +177,9 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
   __shared__ int sh_base, sh_group;
   __shared__ Item sh_item;
   __shared__ unsigned sh_last;
-  __shared__ float sh_lift[C];  // of the item's columns; every warp writes the same
+  __shared__ int2 sh_exp[kDecWarps];  // a warp's E, exponent of the largest value it has seen
+  __shared__ float sh_up[kDecWarps * C];
+  __shared__ float sh_lift[C];        // of the item's columns; every warp writes the same
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
 
@@ -392,13 +401,13 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
         least = min(least, __reduce_min_sync(0xffffffffu, see));
         most = max(most, __reduce_max_sync(0xffffffffu, see));
       }
-      __syncwarp();  // sh_lift
+      if (lane == 0) sh_exp[warp] = make_int2(0, -127);
+      __syncwarp();  // sh_lift, sh_exp
 
       float acc[D / 16][NT][4];  // O^T: channel tiles by columns
       float oc[NT][NG][2];       // this lane's tokens' part of sum P (c - 8 s), or of sum P c
       float m[NT][2], l[NT][2];
-      int vexp = 0;                    // E
-      float vlimit = -1.0f;            // the values' bound for this E; negative before the first block
+      float vlimit = -1.0f;            // the values' bound for this E; negative before the first value
       float vdown = 0.0f;              // 2^-E
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -487,14 +496,14 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
             }
         };
         exponents();
-        float vs[2][NG], vc[2][NG], big = 0.0f;
+        float vs[2][NG], vc[2][NG], big[2] = {0.0f, 0.0f};  // bounds of tokens r and r + 8 (of NaN groups: none)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
             vs[e][g] = KvType<T>::lo(vp[e][g]);
             vc[e][g] = KvType<T>::hi(vp[e][g]);
-            big = fmaxf(big, fmaf(8.0f, vs[e][g], fabsf(vc[e][g])));
+            big[e] = fmaxf(big[e], fmaf(8.0f, vs[e][g], fabsf(vc[e][g])));
             if constexpr (!kCentred) vc[e][g] = fmaf(-8.0f, vs[e][g], vc[e][g]);
           }
         float top = ex[0][0];
@@ -502,42 +511,93 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) top = fmaxf(top, ex[nt][e]);
-        if (__any_sync(0xffffffffu, top > kDecSlack || big > vlimit)) {
-          const float vtop = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
-          float fv = 1.0f;      // for what was summed with the E before
-          if (vtop > vlimit) {  // values to about 2^5, room for 2^13
-            const int to = min(max((int)(__float_as_uint(vtop) >> 23) - 127 - 5, -90), 120);
-            fv = vlimit < 0.0f ? 0.0f : pow2(max(vexp - to, -126));
-            vexp = to;
-            vdown = pow2(-to);
-            vlimit = kDecValues * pow2(min(to, 113));
-          }
+        if (__any_sync(0xffffffffu, top > kDecSlack || fmaxf(big[0], big[1]) > vlimit)) {
+          auto score = [&](int nt, int x, float (&y)[2]) {  // of the column's two tokens here, and the block's largest
+            float t = kNone;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              float t = kNone;
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float y = sc[nt][2 * e + x] * factor[nt][x];
-                if constexpr (part)
-                  if (hidden[nt][2 * e + x]) y = kNone;
-                t = fmaxf(t, y);
-              }
-#pragma unroll
-              for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-              t = fmaxf(t, m[nt][x]);
-              const float f = exp2_fast(m[nt][x] - t), fo = f * fv;
-              m[nt][x] = t;
-              l[nt][x] *= f;
-#pragma unroll
-              for (int g = 0; g < NG; ++g) oc[nt][g][x] *= fo;
-#pragma unroll
-              for (int j = 0; j < D / 16; ++j) {
-                acc[j][nt][x] *= fo;
-                acc[j][nt][2 + x] *= fo;
-              }
+            for (int e = 0; e < 2; ++e) {
+              y[e] = sc[nt][2 * e + x] * factor[nt][x];
+              if constexpr (part)
+                if (hidden[nt][2 * e + x]) y[e] = kNone;
+              t = fmaxf(t, y[e]);
             }
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+            return t;
+          };
+          auto rescale = [&](int nt, int x, float f, float fo) {  // sum, O
+            l[nt][x] *= f;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) oc[nt][g][x] *= fo;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              acc[j][nt][x] *= fo;
+              acc[j][nt][2 + x] *= fo;
+            }
+          };
+          // values of ordinary size, within 2^16 of the limit (at first: within 2^12 of each other)?
+          bool ordinary = !__any_sync(0xffffffffu, fmaxf(big[0], big[1]) > vlimit || fminf(big[0], big[1]) < vlimit * 0x1p-16f);
+          float shift = 0.0f;
+          int to = 0;
+          if (!ordinary) {
+            // E becomes that of what is of ordinary size: an even block's largest value, at first also
+            // an uneven one's smallest; within 2^64 of the largest ever
+            const uint32_t b0 = __float_as_uint(big[0]), b1 = __float_as_uint(big[1]);
+            const uint32_t vtop = __reduce_max_sync(0xffffffffu, max(b0, b1));
+            const int hi_e = exponent(vtop);
+            const int lo_e = exponent(__reduce_min_sync(0xffffffffu, min(b0 - 1u, b1 - 1u)));  // zero counts as none
+            const int2 was = sh_exp[warp];
+            to = was.x;
+            if (vtop) {
+              const bool even = hi_e - lo_e <= 12;
+              if (vlimit < 0.0f) to = (even ? hi_e : lo_e) - kDecAim;
+              else if (even && (hi_e >= was.x + kDecRoom || hi_e < was.x + kDecAim - 8)) to = hi_e - kDecAim;
+              to = min(max(to, max(max(was.y, hi_e) - kDecAim - 64, -60)), 115);
+              ordinary = vlimit < 0.0f && even && to == hi_e - kDecAim;
+              if (vlimit >= 0.0f) shift = (float)(was.x - to);
+              vdown = pow2(-to);
+              vlimit = pow2(min(to + kDecRoom, 127));
+            }
+            __syncwarp();
+            if (lane == 0) sh_exp[warp] = make_int2(to, max(was.y, hi_e));
+          }
+          if (ordinary) {  // the reference rises to the largest score
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                float y[2];
+                const float ref = fmaxf(score(nt, x, y), m[nt][x]), f = exp2_fast(m[nt][x] - ref);
+                m[nt][x] = ref;
+                rescale(nt, x, f, f);
+              }
+          } else {
+            // the reference takes over what E gives up (O stays as it is) and rises by weight times
+            // value, within 2^60 of the weights'
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                float y[2];
+                const float t = score(nt, x, y);
+                // the weights so far, and the largest weight times value
+                float w = l[nt][x] > 0.0f ? m[nt][x] + (float)exponent(__float_as_uint(l[nt][x])) : kNone, z = kNone;
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (big[e] > 0.0f) z = fmaxf(z, y[e] + (float)(exponent(__float_as_uint(big[e])) - to));
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                  w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, o));
+                  z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, o));
+                }
+                const float cur = m[nt][x] + shift;
+                float ref = fmaxf(fmaxf(cur, z - kDecAim), fmaxf(t, w) - 60.0f);
+                if (t - ref <= 12.0f) ref = fmaxf(ref, t);  // so that the next blocks pass
+                const float f = exp2_fast(m[nt][x] - ref);
+                m[nt][x] = ref;
+                rescale(nt, x, f, exp2_fast(cur - ref));
+              }
+          }
           exponents();
         }
         // ---- weights, their sums, and P s as the second product's operand
@@ -637,9 +697,12 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
           for (int g = 0; g < NG; ++g)
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) oc[nt][g][x] += __shfl_xor_sync(0xffffffffu, oc[nt][g][x], o);
-          if (r == 0) {  // from here on E is part of the reference: the sum is scaled as O is
-            mm[warp * C + col] = m[nt][x] + (float)vexp;
-            ml[warp * C + col] = l[nt][x] * pow2(-vexp);
+          // the sum between 1 and 2, with a reference to suit; O with the power of two that goes with both
+          const int by = l[nt][x] > 0.0f ? min(exponent(__float_as_uint(l[nt][x])), 126) : 0, up = sh_exp[warp].x - by;
+          if (r == 0) {
+            mm[warp * C + col] = l[nt][x] > 0.0f ? m[nt][x] + (float)by : kNone;
+            ml[warp * C + col] = l[nt][x] * pow2(-by);
+            sh_up[warp * C + col] = up < -126 ? 0.0f : pow2(min(up, 127));
           }
           float* dst = mo + (warp * C + col) * (D + 4);
 #pragma unroll
@@ -660,12 +723,16 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
         if (x >= it.cols) return;
         const int i = it.row_lo + x / p.per, hq = it.head * p.per + x % p.per;
         const KvSeq q = it.seq();
-        const float inv = L == 0.0f ? 0.0f : 1.0f / L;  // a row that sees nothing is zero
         *reinterpret_cast<uint2*>(a.out + kv_row_offset(a.b, a.os, s, q.row0, i) + (int64_t)hq * a.os.head + 4 * d4) =
-            make_uint2(KvType<T>::pack(o.x * inv, o.y * inv), KvType<T>::pack(o.z * inv, o.w * inv));
+            make_uint2(KvType<T>::pack(o.x, o.y), KvType<T>::pack(o.z, o.w));
         if (a.lse && d4 == 0)
           a.lse[kv_row_index(a.b, s, q.row0, i) * a.q_heads + hq] =
               L == 0.0f ? -__int_as_float(0x7f800000) : (M + log2f(L)) * 0.6931471805599453f;
+      };
+      auto normalise = [&](float4& o, float& L) {  // a row that sees nothing is zero
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        L *= 1.0f / kDecPartScale;
       };
       for (int x = tid; x < C * (D / 4); x += kDecWarps * 32) {
         const int col = x / (D / 4), d4 = x % (D / 4);
@@ -676,14 +743,15 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
         float L = 0.0f;
 #pragma unroll
         for (int w = 0; w < kDecWarps; ++w) {
-          const float f = exp2_fast(mm[w * C + col] - M);
+          const float p = exp2_fast(mm[w * C + col] - M) * kDecPartScale, f = p * sh_up[w * C + col];
           const float4 v = *reinterpret_cast<const float4*>(mo + (w * C + col) * (D + 4) + 4 * d4);
           o.x = fmaf(f, v.x, o.x);
           o.y = fmaf(f, v.y, o.y);
           o.z = fmaf(f, v.z, o.z);
           o.w = fmaf(f, v.w, o.w);
-          L = fmaf(f, ml[w * C + col], L);
+          L = fmaf(p, ml[w * C + col], L);
         }
+        normalise(o, L);
         if (whole) {
           finish(col, d4, o, M, L);
         } else {
@@ -716,13 +784,14 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
             for (int y = c0; y <= c1; ++y) {
               const float* src = slot_of(y);
               const float4 v = __ldcg(reinterpret_cast<const float4*>(src) + x);
-              const float w = __ldcg(src + C * D + C + col), f = exp2_fast(mo[(y - c0) * C + col] - M);
+              const float w = __ldcg(src + C * D + C + col), f = exp2_fast(mo[(y - c0) * C + col] - M) * (w * kDecPartScale);
               o.x = fmaf(f, v.x, o.x);
               o.y = fmaf(f, v.y, o.y);
               o.z = fmaf(f, v.z, o.z);
               o.w = fmaf(f, v.w, o.w);
-              L = fmaf(f, w, L);
+              L += f;
             }
+            normalise(o, L);
             finish(col, d4, o, M, L);
           }
           if (tid == 0) counters[c0] = 0;  // for the next call

@@ -6,6 +6,8 @@ constexpr float kNone = -1e30f;  // softmax reference of a row that has seen no 
 
 // 2^e, e in -126..127
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+// floor(log2) of a positive normal fp32's bits (-127 of zero and subnormals, 128 of an infinity)
+__device__ __forceinline__ int exponent(uint32_t bits) { return (int)(bits >> 23) - 127; }
 __device__ __forceinline__ float exp2_fast(float x) {
   float d;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));

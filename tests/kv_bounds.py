@@ -6,8 +6,8 @@ import torch
 import kv_reference as ref
 
 
-def attention(q, k, v, seen, scale):
-    """q [R, Hq, D] 16-bit, k, v [L, H, D] in 64 bits, seen [R, L] bool -> out, lse and their bounds.
+def attention(q, k, v, seen, scale, group):
+    """q [R, Hq, D] 16-bit, k, v [L, H, D] in 64 bits, in groups of `group` channels, seen [R, L] bool -> out, lse and their bounds.
 
     A score is off by at most ds, the unit of the keys' rounding (or of fp16, the coarser) and
     2^-16 for fp32 sums, times its terms' magnitude; a weight by twice that, relatively; weights
@@ -31,7 +31,7 @@ def attention(q, k, v, seen, scale):
     lse = torch.where(tot[..., 0] > 0, top[..., 0] + torch.log(tot[..., 0].clamp_min(1e-300)), top[..., 0])
     out = torch.einsum("rhgl,lhd->rhgd", p, v)
     ds = torch.where(seen & (p > 2.0 ** -60), mag, torch.zeros_like(mag)).amax(-1) * (u16 / 2 + 2.0 ** -16) + 2.0 ** -16
-    big = v.abs().unflatten(-1, (-1, 32)).amax(-1, keepdim=True).expand(L, H, D // 32, 32).flatten(2)
+    big = v.abs().unflatten(-1, (-1, group)).amax(-1, keepdim=True).expand(L, H, D // group, group).flatten(2)
     terms = torch.einsum("rhgl,lhd->rhgd", p, big)
     tol = (2.2 * ds + 2.0 ** -9)[..., None] * terms + 1.1 * u * out.abs() + 2.0 ** -134
     if q.dtype == torch.float16:
