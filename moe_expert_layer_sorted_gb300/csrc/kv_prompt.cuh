@@ -23,7 +23,12 @@
 // nothing leaves fp16's range, powers of two are taken out and put back: of a query
 // row, to its largest element (back in the row's factor scale log2 e); of a token
 // whose keys are all tiny or huge (back on its column, in tiles that hold one); of
-// all values, 2^E with E raised when a token needs it (O is rescaled as for m).
+// all values, 2^E with E for a tile's ordinary size; of a token whose values are far
+// larger or smaller than that, another one (back in its weights, which are computed
+// once for the sums and once with it).  A row's reference goes by weight times that
+// power, so that a huge value that the row does not see or hardly weighs takes
+// nothing from its other tokens.  (A token's groups share its power: one whose
+// values are 2^16 times smaller than another's begins to lose bits.)
 //
 // Where there are fewer tiles of rows than half the SMs, the tokens are cut into as
 // many stretches as fill them, and a second kernel joins a tile's parts, in the order
@@ -66,6 +71,7 @@ constexpr int kPrTile = 128;  // rows of a row tile, tokens of a token tile
 // raised when a tile's weights sum to kPrLimit; so no weight passes 2^15 and fp16 holds those
 // 2^-31 of the largest
 constexpr float kPrDrop = 7.0f, kPrLimit = 32768.0f;
+constexpr float kPrJoin = 0x1p-10f;  // of the stretches' weights: their sum with values of any size stays in range
 
 // K-major operand, 128-byte swizzle: 8-row groups 1024 bytes apart.
 __device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
@@ -207,9 +213,10 @@ struct PromptTile {
     return (int)min(max(p.a.causal ? first + x / p.per + 1 : (int64_t)q.len, (int64_t)0), (int64_t)cap);
   }
 };
-// Floats of a stretch's part: O [D / 4][row] of four channels, then references, sums, poisoned groups.
+// Floats of a stretch's part: O [D / 4][row] of four channels, then references, sums, poisoned
+// groups, O's powers of two.
 template <int D>
-constexpr int64_t kPrPart = 2 * kPrTile * (D + 3);
+constexpr int64_t kPrPart = 2 * kPrTile * (D + 4);
 
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_constant__ PromptArgs p) {
@@ -220,11 +227,12 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t kFull[2], kEmpty[2], vFull[2], vEmpty[2], sFull[2], pFull[2], qFull, oFull;
   __shared__ uint32_t tmem_base;
-  // per token tile (ring of 4): tokens that exist, tokens with a poisoned value, tokens with scaled keys
+  // per token tile (ring of 4): tokens that exist, tokens with a poisoned value, tokens with scaled keys or values
   __shared__ uint4 sh_valid[4], sh_poison[4], sh_scaled[4];
   __shared__ float sh_kscale[4][kPrTile];      // what the scaled keys' scores are multiplied by
+  __shared__ float sh_vshift[4][kPrTile];      // log2 of what the scaled values' weights are multiplied by
   __shared__ int sh_vtop[4][kPrDequant];       // exponents of the tile's largest values, one per warp
-  __shared__ int sh_vexp[4];                   // E of the tile
+  __shared__ int sh_vexp[4];                   // E from the tile on
   __shared__ float sh_qscale[2 * kPrTile];     // what a query row's scores are multiplied by
   __shared__ uint8_t sh_pgroups[4][kPrTile];   // the poisoned groups of a token
   const KvAttnArgs& a = p.a;
@@ -345,7 +353,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
         const int n = seen - (j * kPrTile + 32 * k);
         return valid[k] & (n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u);
       };
-      auto load = [&](int k, uint32_t (&v)[32]) {  // the k-th 32 scores, masked ones -infinity (in the sign of scale)
+      // the k-th 32 scores, masked ones -infinity; shifted: of the weights with their tokens' powers of two
+      auto load = [&](int k, uint32_t (&v)[32], bool shifted) {
         tmem_ld32(ts + 32 * k, v);
         tmem_wait_ld();
         const uint32_t mask = mask_of(k);
@@ -355,8 +364,12 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
         }
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = (mask >> i) & 1u ? __float_as_uint(__uint_as_float(v[i]) * kappa) : 0xff800000u;
+        if (shifted) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + sh_vshift[j & 3][32 * k + i]);
+        }
       };
-      uint64_t sum = 0;
+      uint64_t sum = 0, whole = 0;  // of the weights as operands, as they are
       auto weights = [&](const uint32_t (&v)[32], int k, uint64_t factor, uint64_t neg) {
         float e[32];  // step by step over all 32: independent instructions side by side
 #pragma unroll
@@ -374,27 +387,40 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
         sum = add2(sum, add2(add2(part[0], part[1]), add2(part[2], part[3])));
       };
       // weights against the reference as it stands, and once more where it has to rise: for the
-      // first tile, with E, or where a weight is above the limit, which shows in the sum (that may
-      // reach the limit without one: no harm)
+      // first tile, with E, or where a weight (times its token's power of two) is above the limit,
+      // which shows in the sum (that may reach the limit without one: no harm)
       bool raise = j == 0 || sh_vexp[j & 3] != vexp, asked = true;
       while (true) {
         if (raise) {
-          // the row's largest score of this tile becomes its reference; what was summed so far shrinks
-          float best = kNone;
+          // the reference takes over what E gives up (O stays as it is) and rises to the tile's largest
+          // weight times its token's power of two, within 2^60 of the weights'; the sums shrink
+          float best = kNone, top = kNone;
 #pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            load(k, v[0]);
+          for (int k = 0; k < (scaled ? 8 : 4); ++k) {
+            load(k & 3, v[0], k < 4 && scaled);
+            if (k == 4) {
+              top = best;  // of the shifted ones
+              best = kNone;
+            }
 #pragma unroll
             for (int i = 0; i < 32; ++i) best = fmaxf(best, __uint_as_float(v[0][i]));
           }
+          if (scaled) {
+            const float t = best;
+            best = top;
+            top = t;
+          }
           asked = false;
-          best = fmaxf(best - kPrDrop, m);
-          const float f = exp2_fast(m - best), fo = f * pow2(max(vexp - sh_vexp[j & 3], -126));
+          float l0, l1;
+          split2(l2, l0, l1);
+          if (l0 + l1 > 0.0f) top = fmaxf(top, m + (float)exponent(__float_as_uint(l0 + l1)));
+          const int now = sh_vexp[j & 3];
+          const float cur = m + (float)(vexp - now);
+          best = fmaxf(fmaxf(best - kPrDrop, top - 60.0f), cur);
+          const float f = exp2_fast(m - best), fo = exp2_fast(cur - best);
           m = best;
-          vexp = sh_vexp[j & 3];
-          float s0, s1;
-          split2(l2, s0, s1);
-          l2 = pair2(s0 * f, s1 * f);
+          vexp = now;
+          l2 = pair2(l0 * f, l1 * f);
           if (j > 0) {
 #pragma unroll 1
             for (int k = 0; k < D / 32; ++k) {
@@ -419,19 +445,26 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
           }
         } else {
           const uint64_t one = pair2(1.0f, 1.0f);
+#pragma unroll 1
+          for (bool shifted = false;; shifted = true) {  // scaled values: sums by the weights, operands by the shifted
+            sum = 0;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            load(k, v[0]);
-            weights(v[0], k, one, neg);
+            for (int k = 0; k < 4; ++k) {
+              load(k, v[0], shifted);
+              weights(v[0], k, one, neg);
+            }
+            if (!shifted) whole = sum;
+            if (shifted || !scaled) break;
           }
         }
+        if (plain) whole = sum;
         if (raise) break;
         float s0, s1;
         split2(sum, s0, s1);
         raise = __any_sync(0xffffffffu, fmaxf(s0, s1) > kPrLimit);
         if (!raise) break;
       }
-      l2 = add2(l2, sum);
+      l2 = add2(l2, whole);
       tmem_st32(ts, pr);
       tmem_st32(ts + 32, pr + 32);
       if (poison[0] | poison[1] | poison[2] | poison[3]) {
@@ -468,10 +501,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
     auto write = [&](int k, const uint32_t (&v)[32], float f0, float f1) {  // 32 channels, times both factors
       // the groups of a poisoned value are NaN
       if ((poisoned >> (32 * k / G)) & 1u) f0 = __int_as_float(0x7fffffff);
-      f0 *= f1;
       uint32_t o[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) o[e] = KvType<T>::pack(__uint_as_float(v[2 * e]) * f0, __uint_as_float(v[2 * e + 1]) * f0);
+      for (int e = 0; e < 16; ++e)
+        o[e] = KvType<T>::pack(__uint_as_float(v[2 * e]) * f0 * f1, __uint_as_float(v[2 * e + 1]) * f0 * f1);
       if (reinterpret_cast<uintptr_t>(dst) & 31) {
 #pragma unroll
         for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(dst + 32 * k + 2 * e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
@@ -496,7 +529,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
       if (dst && a.lse)
         a.lse[kv_row_index(a.b, s, q.row0, i) * a.q_heads + hq] =
             l == 0.0f ? -__int_as_float(0x7f800000) : (m + log2f(l)) * 0.6931471805599453f;
-    } else if (has) {  // a stretch's part; from here on E is part of the reference
+    } else if (has) {  // a stretch's part
       float* part = p.ws + ((int64_t)blockIdx.x * p.splits + z) * kPrPart<D>;
 #pragma unroll 1
       for (int k = 0; k < D / 32; ++k) {
@@ -508,9 +541,12 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
               make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
       }
       float* ends = part + 2 * kPrTile * D + row;
-      ends[0] = m + (float)vexp;
-      ends[2 * kPrTile] = l * pow2(-vexp);
+      // the sum between 1 and 2, with a reference to suit; the power of two that goes with O
+      const int by = l > 0.0f ? min(exponent(__float_as_uint(l)), 126) : 0, up = vexp - by;
+      ends[0] = l > 0.0f ? m + (float)by : kNone;
+      ends[2 * kPrTile] = l * pow2(-by);
       ends[4 * kPrTile] = __uint_as_float(poisoned);
+      ends[6 * kPrTile] = up < -126 ? 0.0f : pow2(min(up, 127));
     }
   } else if (warp < kPrMma) {
     // ------------------------------------------------------------------ codes to K and V tiles
@@ -524,6 +560,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
     const uint8_t* at = nullptr;  // its block
     constexpr int kNoExp = -1000;
     int vexp = kNoExp;            // E
+    int vever = kNoExp;           // exponent of the largest value so far
     int64_t pid = -1;             // page of the token one tile on
     auto page_of = [&](int j) {
       const int pos = base + j * kPrTile + t;
@@ -575,6 +612,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
       uint8_t* tk = gen + 2 * kTileBytes + st * kTileBytes;
       uint32_t bad = 0;  // the token's poisoned groups
       float kscale = 1.0f, vbig = 0.0f;
+      int vown;  // the power of two that its values are divided by
       if (ok) {
         float kbig = 0.0f;  // bound of the token's keys
 #pragma unroll
@@ -612,23 +650,34 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
         for (int ch = 0; ch < D; ch += 8) put(tk, ch, make_uint4(0, 0, 0, 0));
       }
       const uint32_t bv = __ballot_sync(0xffffffffu, ok), bp = __ballot_sync(0xffffffffu, bad != 0);
-      const uint32_t bs = __ballot_sync(0xffffffffu, kscale != 1.0f);
       sh_kscale[j & 3][t] = kscale;
       if (lane == 0) {
-        reinterpret_cast<uint32_t*>(&sh_scaled[j & 3])[dw] = bs;
         reinterpret_cast<uint32_t*>(&sh_valid[j & 3])[dw] = bv;
         reinterpret_cast<uint32_t*>(&sh_poison[j & 3])[dw] = bp;
       }
       if (bp) sh_pgroups[j & 3][t] = (uint8_t)bad;
-      // E: first so that the tile's largest value is about 2^7, then raised where one would pass 2^15
+      // E: the tile's ordinary size (the smallest of its warps' largest values) to about 2^7, changed
+      // where that would pass 2^15 or fall below 2^-1, within 2^60 of the largest value ever
       const uint32_t vtop = __reduce_max_sync(0xffffffffu, __float_as_uint(vbig));
-      if (lane == 0) sh_vtop[j & 3][dw] = vtop == 0 ? -1000 : (int)(vtop >> 23) - 127;
+      if (lane == 0) sh_vtop[j & 3][dw] = vtop == 0 ? kNoExp : exponent(vtop);
       asm volatile("bar.sync 1, %0;" ::"n"(kPrDequant * 32) : "memory");
-      int e = sh_vtop[j & 3][0];
+      int usual = -kNoExp;
 #pragma unroll
-      for (int i = 1; i < kPrDequant; ++i) e = max(e, sh_vtop[j & 3][i]);
-      if (e > -1000 && (vexp == kNoExp || e > vexp + 14)) vexp = min(max(e - 7, -110), 120);
-      if (t == 0) sh_vexp[j & 3] = vexp == kNoExp ? 0 : vexp;
+      for (int i = 0; i < kPrDequant; ++i) {
+        const int e = sh_vtop[j & 3][i];
+        vever = max(vever, e);
+        if (e != kNoExp) usual = min(usual, e);
+      }
+      if (usual != -kNoExp && (vexp == kNoExp || usual > vexp + 14 || usual < vexp - 1)) vexp = usual - 7;
+      if (vexp != kNoExp) vexp = min(max(vexp, max(vever - 67, -60)), 120);
+      // a token whose largest value would leave that range has a power of two of its own, which
+      // goes with its weights (a token without values: the smallest)
+      const int e = vbig > 0.0f ? exponent(__float_as_uint(vbig)) : -126, base = vexp == kNoExp ? 0 : vexp;
+      vown = e > base + 14 || e < base - 1 ? max(e - 7, base - 60) : base;
+      sh_vshift[j & 3][t] = (float)(vown - base);
+      const uint32_t bs = __ballot_sync(0xffffffffu, kscale != 1.0f || (ok && vown != base));
+      if (lane == 0) reinterpret_cast<uint32_t*>(&sh_scaled[j & 3])[dw] = bs;
+      if (t == 0) sh_vexp[j & 3] = base;
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&kFull[st]));
@@ -638,7 +687,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
       mbar_wait<false>(smem_addr(&vEmpty[st]), free_parity, p.err);
       uint8_t* tv = gen + 4 * kTileBytes + st * kTileBytes;
       if (okv) {
-        const float to = pow2(vexp == kNoExp ? 0 : -vexp);
+        const float to = pow2(-vown);
         uint32_t w[D / 8];
 #pragma unroll
         for (int g = 0; g < NG; ++g) vp[g] = KvType<__half>::pack(KvType<T>::lo(vp[g]) * to, KvType<T>::hi(vp[g]) * to);
@@ -725,7 +774,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Pr
   for (int y = 0; y < tile.splits; ++y) m = fmaxf(m, __ldcg(ends + y * kPrPart<D>));
 #pragma unroll 4
   for (int y = 0; y < tile.splits; ++y) {
-    l = fmaf(exp2_fast(__ldcg(ends + y * kPrPart<D>) - m), __ldcg(ends + y * kPrPart<D> + 2 * kPrTile), l);
+    l = fmaf(exp2_fast(__ldcg(ends + y * kPrPart<D>) - m) * kPrJoin, __ldcg(ends + y * kPrPart<D> + 2 * kPrTile), l);
     poisoned |= __float_as_uint(__ldcg(ends + y * kPrPart<D> + 4 * kPrTile));
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row that sees nothing is zero
@@ -737,7 +786,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Pr
   for (int k = 0; k < kQuads; ++k) o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
   for (int y = 0; y < tile.splits; ++y) {
-    const float f = exp2_fast(__ldcg(ends + y * kPrPart<D>) - m);
+    const float f = exp2_fast(__ldcg(ends + y * kPrPart<D>) - m) * kPrJoin * __ldcg(ends + y * kPrPart<D> + 6 * kPrTile);
 #pragma unroll
     for (int k = 0; k < kQuads; ++k) {
       const int d4 = (threadIdx.x >> 5) * kQuads + k;
@@ -757,7 +806,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(const __grid_constant__ Pr
   }
   if (a.lse && threadIdx.x < 32)
     a.lse[kv_row_index(a.b, tile.s, tile.q.row0, i) * a.q_heads + hq] =
-        l == 0.0f ? -__int_as_float(0x7f800000) : (m + log2f(l)) * 0.6931471805599453f;
+        l == 0.0f ? -__int_as_float(0x7f800000) : (m + log2f(l * (1.0f / kPrJoin))) * 0.6931471805599453f;
 }
 
 template <typename T, int D, int G>
@@ -782,7 +831,7 @@ cudaError_t prompt(Kv& kv, const KvAttnArgs& a, cudaStream_t s) {
     return cudaErrorInvalidConfiguration;
   p.tiles = (int)tiles;
   // the SMs hold one CTA each; the parts have to fit the workspace
-  const int64_t slots = Kv::kPartsBytes / (2 * kPrTile * (kv.d.head_dim + 3) * sizeof(float));
+  const int64_t slots = Kv::kPartsBytes / (2 * kPrTile * (kv.d.head_dim + 4) * sizeof(float));
   p.splits = (int)std::max<int64_t>(std::min<int64_t>(kv.sms, slots) / ctas, 1);
   cudaError_t e = cudaErrorInvalidValue;
   const int dg = kv.d.head_dim * 1000 + kv.d.group_size;

@@ -9,8 +9,9 @@ import kv_reference as ref
 def attention(q, k, v, seen, scale, group):
     """q [R, Hq, D] 16-bit, k, v [L, H, D] in 64 bits, in groups of `group` channels, seen [R, L] bool -> out, lse and their bounds.
 
-    A score is off by at most ds, the unit of the keys' rounding (or of fp16, the coarser) and
-    2^-16 for fp32 sums, times its terms' magnitude; a weight by twice that, relatively; weights
+    A score is off by at most ds, 2^-11 for keys rounded to fp16 (half a unit in the last place of
+    11 bits, relative to a number just above a power of two) and 2^-16 for fp32 sums, times its
+    terms' magnitude; a weight by twice that, relatively; weights
     (times steps) and values are rounded once each to 11 bits.  So a channel is off by that part
     of sum p |v|, with |v| up to the largest stored value of its group (codes are what is
     multiplied, so a small value of a group carries the group's rounding), and by the output's
@@ -30,7 +31,7 @@ def attention(q, k, v, seen, scale, group):
     p = p / tot.clamp_min(1e-300)
     lse = torch.where(tot[..., 0] > 0, top[..., 0] + torch.log(tot[..., 0].clamp_min(1e-300)), top[..., 0])
     out = torch.einsum("rhgl,lhd->rhgd", p, v)
-    ds = torch.where(seen & (p > 2.0 ** -60), mag, torch.zeros_like(mag)).amax(-1) * (u16 / 2 + 2.0 ** -16) + 2.0 ** -16
+    ds = torch.where(seen & (p > 2.0 ** -60), mag, torch.zeros_like(mag)).amax(-1) * (u16 + 2.0 ** -16) + 2.0 ** -16
     big = v.abs().unflatten(-1, (-1, group)).amax(-1, keepdim=True).expand(L, H, D // group, group).flatten(2)
     terms = torch.einsum("rhgl,lhd->rhgd", p, big)
     tol = (2.2 * ds + 2.0 ** -9)[..., None] * terms + 1.1 * u * out.abs() + 2.0 ** -134

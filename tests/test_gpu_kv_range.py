@@ -45,7 +45,7 @@ def times(x, factor, dtype):
 
 
 @pytest.mark.parametrize("D,G,P,dtype", SHAPES)
-@pytest.mark.parametrize("n", [2, 5])
+@pytest.mark.parametrize("n", [2, 5, 80, 200])
 def test_a_huge_value_that_only_the_last_row_sees(D, G, P, dtype, n):
     """The rows before it are what they are without it."""
     w = World(D, G, P, dtype, 2, [n, 333, 1500], seed=n)
@@ -58,7 +58,7 @@ def test_a_huge_value_that_only_the_last_row_sees(D, G, P, dtype, n):
 
 
 @pytest.mark.parametrize("D,G,P,dtype", SHAPES)
-@pytest.mark.parametrize("n", [1, 3])
+@pytest.mark.parametrize("n", [1, 3, 80])
 @pytest.mark.parametrize("at", [0, 5, 40])
 def test_a_huge_value_of_no_weight(D, G, P, dtype, n, at):
     """A token that every row sees, its score some 100 below the others'."""
@@ -74,7 +74,7 @@ def test_a_huge_value_of_no_weight(D, G, P, dtype, n, at):
 
 
 @pytest.mark.parametrize("D,G,P,dtype", SHAPES)
-@pytest.mark.parametrize("n", [1, 3])
+@pytest.mark.parametrize("n", [1, 3, 80])
 @pytest.mark.parametrize("at", [0, 7, 300])
 @pytest.mark.parametrize("size", [0.0, 2.0 ** -30, 2.0 ** -9])
 def test_a_token_of_nearly_all_the_weight_and_hardly_any_value(D, G, P, dtype, n, at, size):
@@ -89,7 +89,7 @@ def test_a_token_of_nearly_all_the_weight_and_hardly_any_value(D, G, P, dtype, n
 
 
 @pytest.mark.parametrize("D,G,P,dtype", SHAPES)
-@pytest.mark.parametrize("n", [1, 3])
+@pytest.mark.parametrize("n", [1, 3, 80])
 @pytest.mark.parametrize("kind", ["tokens", "blocks", "up", "down", "zeros"])
 def test_values_of_all_sizes(D, G, P, dtype, n, kind):
     w = World(D, G, P, dtype, 2, [n, 333, 2100], seed=n)
@@ -111,7 +111,7 @@ def test_values_of_all_sizes(D, G, P, dtype, n, kind):
     run(w, n, scale=0.0)
 
 
-@pytest.mark.parametrize("n", [1, 4])
+@pytest.mark.parametrize("n", [1, 4, 60])
 def test_parts_whose_values_are_far_apart(n):
     """One value near the type's largest among many parts of ordinary, tiny or zero values: every
     part keeps its share of the weights."""
@@ -125,7 +125,7 @@ def test_parts_whose_values_are_far_apart(n):
 
 
 @pytest.mark.parametrize("D,G,P,dtype", SHAPES[:3])
-@pytest.mark.parametrize("n", [1, 3])
+@pytest.mark.parametrize("n", [1, 3, 80])
 def test_groups_of_channels_far_apart(D, G, P, dtype, n):
     """Groups 2^16 apart, in every token or in some of any weight."""
     w = World(D, G, P, dtype, 2, [n + 300, 700], seed=n)
