@@ -50,7 +50,7 @@ typedef enum moe_status {
   MOE_ERR_INVALID = 1,     /* bad argument, shape or index */
   MOE_ERR_OOM = 2,         /* HBM or pinned host memory not available for the request */
   MOE_ERR_CUDA = 3,        /* a CUDA call failed (text in moe_last_error) */
-  MOE_ERR_TIMEOUT = 4,     /* a bounded device-side wait gave up (latched; see moe_layer_forward) */
+  MOE_ERR_TIMEOUT = 4,     /* a bounded device-side wait gave up (latched; see moe_layer_forward, moe_kv_status) */
   MOE_ERR_STATE = 5,       /* call not valid in the plan's current state */
   MOE_ERR_UNSUPPORTED = 6  /* well-formed request outside what the library implements */
 } moe_status;
@@ -412,8 +412,24 @@ moe_status moe_kv_sizes(const moe_kv_desc* desc, int64_t* page_bytes_per_layer, 
  * handle.  Ordering writes to the pages before reads of them is the caller's,
  * as for any device memory. */
 moe_status moe_kv_create(const moe_kv_desc* desc, moe_kv_cache** out);
-/* Waits for the last call that used the workspace and frees it. */
+/* Waits for the last call that used the workspace and frees the handle.
+ * MOE_ERR_TIMEOUT: as below, and the handle is gone all the same.
+ * MOE_ERR_STATE: another thread's call is running, nothing was done. */
 moe_status moe_kv_destroy(moe_kv_cache* kv);
+
+/* Every wait on the device is bounded (some seconds).  Where one of an
+ * attention gives up its results are wrong, and the next moe_kv_* call on the
+ * handle (any of them, or this one, which does nothing else) returns
+ * MOE_ERR_TIMEOUT, once, without doing its work: what was computed since the
+ * last call that was seen to be done before it is suspect.  Later launches are
+ * not touched.  The word is written when the kernel runs: ask after a
+ * synchronisation, and after the replays of a captured graph, which make no
+ * host call of their own. */
+moe_status moe_kv_status(moe_kv_cache* kv);
+
+/* Test hook: one wait of the next moe_kv_attention runs out (it faults nothing
+ * and ends by itself after some seconds). */
+moe_status moe_kv_debug_fail_next_attention(moe_kv_cache* kv);
 
 /* Quantise the rows k, v into the pages of `layer`, and with bounds update the
  * bounds of the pages written to: a page whose first token is among the rows

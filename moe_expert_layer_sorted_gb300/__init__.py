@@ -34,7 +34,7 @@ EXPORTS = ["moe_plan_create", "moe_plan_destroy", "moe_set_router", "moe_update_
            "moe_cache_stats", "moe_residence_table", "moe_quantize", "moe_probe_bandwidth",
            "moe_route_noalloc", "moe_status_string", "moe_last_error",
            "moe_kv_sizes", "moe_kv_create", "moe_kv_destroy", "moe_kv_append", "moe_kv_read", "moe_kv_attention",
-           "moe_kv_select", "moe_kv_last_error"]
+           "moe_kv_select", "moe_kv_status", "moe_kv_debug_fail_next_attention", "moe_kv_last_error"]
 
 _P = ctypes.c_void_p
 

@@ -146,7 +146,18 @@ moe_status guarded(F&& f) noexcept {
   }
 }
 
-// The frame of a call on a handle: one at a time, its device current.
+// Whether a kernel's bounded wait gave up since this was last asked (for every wait of a launch
+// counts its own CTA's state alone, nothing on the device needs to be put right).
+bool take_timeout(Kv* kv) {
+  if (!*kv->err_host) return false;
+  *kv->err_host = 0;
+  return true;
+}
+constexpr char kTimeoutMsg[] =
+    "a bounded wait of an attention gave up: results of the calls since the last one that was reported as done are suspect; "
+    "this call did nothing";
+
+// The frame of a call on a handle: one at a time, its device current, no timeout unreported.
 template <typename F>
 moe_status on_handle(moe_kv_cache* h, F&& f) noexcept {
   return guarded([&]() -> moe_status {
@@ -156,6 +167,7 @@ moe_status on_handle(moe_kv_cache* h, F&& f) noexcept {
     if (!busy.ok) return MOE_ERR_STATE;  // the text is the other thread's to write
     DeviceScope ds(kv->d.device);
     if (!ds.ok) return fail(kv, MOE_ERR_CUDA, "cudaSetDevice failed");
+    if (take_timeout(kv)) return fail(kv, MOE_ERR_TIMEOUT, kTimeoutMsg);
     return f(kv);
   });
 }
@@ -227,7 +239,20 @@ extern "C" moe_status moe_kv_destroy(moe_kv_cache* h) {
     DeviceScope ds(kv->d.device);
     if (kv->have_last && (kv->last_stream != kDefaultStream || cudaEventRecord(kv->ev_done, nullptr) == cudaSuccess))
       cudaEventSynchronize(kv->ev_done);
+    const bool late = take_timeout(kv);
     release(kv);
+    return late ? fail(nullptr, MOE_ERR_TIMEOUT, "a bounded wait of an attention gave up: the last results are suspect; the handle is gone")
+                : MOE_OK;
+  });
+}
+
+extern "C" moe_status moe_kv_status(moe_kv_cache* h) {
+  return on_handle(h, [](Kv*) { return MOE_OK; });
+}
+
+extern "C" moe_status moe_kv_debug_fail_next_attention(moe_kv_cache* h) {
+  return on_handle(h, [](Kv* kv) {
+    kv->fail_next = true;
     return MOE_OK;
   });
 }
@@ -278,15 +303,8 @@ extern "C" moe_status moe_kv_attention(moe_kv_cache* h, int layer, const moe_kv_
                  pages, pages ? budget : 0};
     Order order;
     cudaError_t e = order_before(kv, s, order);
-    if (e == cudaSuccess && *kv->err_host) {  // reported once; the counters start afresh behind the failed call
-      if (!order.capturing) {  // (a capture would only record it: the next call outside reports again and does it)
-        *kv->err_host = 0;
-        e = cudaMemsetAsync(kv->counters(), 0, Kv::kCounterBytes, s);
-        if (e == cudaSuccess) e = order_after(kv, s, order);
-      }
-      if (e == cudaSuccess) return fail(kv, MOE_ERR_TIMEOUT, "a bounded wait of an earlier moe_kv_attention gave up: its results are wrong");
-    }
     if (e == cudaSuccess) e = kv_attention(*kv, a, s);
+    kv->fail_next = false;
     if (e == cudaSuccess) e = order_after(kv, s, order);
     return e == cudaSuccess ? MOE_OK : cuda_fail(kv, e, "moe_kv_attention");
   });

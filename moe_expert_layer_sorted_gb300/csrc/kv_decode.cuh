@@ -108,6 +108,7 @@ struct DecPlan {
   int ctiles;      // column tiles
   int per;         // query heads per kv head
   int min_rounds;  // a CTA's share is not made smaller than this
+  int fail;        // test hook: the first CTA's last round is not fetched
 };
 
 __device__ __forceinline__ int group_rounds(const KvAttnArgs& a, int gi) {
@@ -177,12 +178,14 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
   __shared__ int sh_base, sh_group;
   __shared__ Item sh_item;
   __shared__ unsigned sh_last;
+  __shared__ uint32_t sh_gone;  // a wait gave up: results are wrong, the next call says so
   __shared__ int2 sh_exp[kDecWarps];  // a warp's E, exponent of the largest value it has seen
   __shared__ float sh_up[kDecWarps * C];
   __shared__ float sh_lift[C];        // of the item's columns; every warp writes the same
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
 
+  if (tid == 0) sh_gone = 0;
   if (tid < kStages) {
     mbar_init(smem_addr(&full[tid]), 1);
     mbar_init(smem_addr(&empty[tid]), kDecWarps);
@@ -289,7 +292,8 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
         const int at = ok ? pos : -1;
         look(u + 1);
         const uint32_t there = __ballot_sync(0xffffffffu, ok);
-        mbar_wait<false>(smem_addr(&empty[stage]), parity, err);
+        if (!kv_wait(smem_addr(&empty[stage]), parity, &sh_gone, err)) break;
+        if (p.fail && me == 0 && u == last - 1) break;
         if (lane < kDecWarps) spos[stage * kDecWarps + lane] = at;
         __syncwarp();
         const uint32_t bar = smem_addr(&full[stage]);
@@ -302,6 +306,13 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
         if (++stage == kStages) {
           stage = 0;
           parity ^= 1u;
+        }
+      }
+      // whoever gave up no longer waits for what was fetched: it has landed before the CTA ends
+      if (*static_cast<volatile uint32_t*>(&sh_gone)) {
+        for (int st = 0; st < kStages; ++st) {
+          const uint32_t fill = st < stage ? parity ^ 1u : parity;  // of its last fill; a barrier never filled is passed
+          mbar_drain(smem_addr(&full[st]), fill);
         }
       }
       }
@@ -657,8 +668,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
       // a round's stage, once it is there: this warp's block and its position
       auto arrive = [&](int st, uint32_t par, int& pos) {
         const uint32_t bar = smem_addr(&full[st]);
-        if (!mbar_wait<false>(bar, par, err)) mbar_drain(bar, par);
-        pos = spos[st * kDecWarps + warp];
+        pos = kv_wait(bar, par, &sh_gone, err) ? spos[st * kDecWarps + warp] : -1;
         return smem + (st * kDecWarps + warp) * Geo::kBytes;
       };
       for (int cu = seg; cu < seg_end; ++cu) {
@@ -852,6 +862,7 @@ cudaError_t decode(Kv& kv, const KvAttnArgs& a, cudaStream_t s) {
     return cudaErrorInvalidConfiguration;  // rounds are numbered in 32 bits
   p.items = (int)items;
   p.min_rounds = 1;
+  p.fail = kv.fail_next;
   cudaError_t e = cudaErrorInvalidValue;
   const int dg = kv.d.head_dim * 1000 + kv.d.group_size;
 #define KV_CASE(DD, GG)                                                        \

@@ -26,6 +26,7 @@ struct Kv {
   unsigned* counters() const { return reinterpret_cast<unsigned*>(ws + kScoreBytes + kPartsBytes); }
   volatile uint32_t* err_host = nullptr;  // mapped pinned word: set by a kernel whose bounded wait gave up
   uint32_t* err_dev = nullptr;
+  bool fail_next = false;         // test hook: a wait of the next attention runs out
   cudaEvent_t ev_done = nullptr;  // end of the last call that used the workspace
   unsigned long long last_stream = 0;  // its identity
   bool have_last = false;

@@ -36,6 +36,27 @@ __device__ __forceinline__ uint32_t centred_pair(uint32_t x) {
   return d;
 }
 
+// Bounded wait for phase `parity` of bar.  One that gives up sets the handle's word, which the
+// next call reports, and `gone` of its CTA, whose later waits then give up soon; no other CTA
+// and no later launch is touched.
+__device__ __forceinline__ bool kv_wait(uint32_t bar, uint32_t parity, volatile uint32_t* gone, uint32_t* err) {
+  for (uint32_t it = 0; it < (1u << 20); ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((it & 255u) == 255u && *gone) return false;
+  }
+  *gone = 1;
+  *reinterpret_cast<volatile uint32_t*>(err) = kErrTimeout;
+  __threadfence_system();
+  return false;
+}
+
 // Registers of a warpgroup's threads from here on.
 // `Launch`: what the block was launched with; the direction of the change has to match it.
 template <int Launch, int R>

@@ -183,6 +183,7 @@ struct PromptArgs {
   int splits;     // stretches of tokens per row-tile pair, at most
   float* ws;      // [pair][split] partial results
   uint32_t* err;
+  int fail;       // test hook: the first CTA's last values are not announced
 };
 
 // A pair of row tiles: its rows x0 .. of the nx of sequence s and kv head h, and its tokens.
@@ -227,6 +228,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t kFull[2], kEmpty[2], vFull[2], vEmpty[2], sFull[2], pFull[2], qFull, oFull;
   __shared__ uint32_t tmem_base;
+  __shared__ uint32_t sh_gone;  // a wait gave up: results are wrong, the next call says so
   // per token tile (ring of 4): tokens that exist, tokens with a poisoned value, tokens with scaled keys or values
   __shared__ uint4 sh_valid[4], sh_poison[4], sh_scaled[4];
   __shared__ float sh_kscale[4][kPrTile];      // what the scaled keys' scores are multiplied by
@@ -252,6 +254,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
   uint8_t* gen = smem_raw + (smem - smem_addr(smem_raw));  // the same places as a generic pointer
 
   if (tid == 0) {
+    sh_gone = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&kFull[i]), kPrDequant);
       mbar_init(smem_addr(&kEmpty[i]), 1);
@@ -337,7 +340,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
     uint32_t poisoned = 0;  // groups with a NaN value that the row sees
     int vexp = 0;           // E so far
     for (int j = 0; j < (t == 0 || two ? ntiles : 0); ++j) {
-      mbar_wait<false>(smem_addr(&sFull[t]), (uint32_t)j & 1u, p.err);
+      kv_wait(smem_addr(&sFull[t]), (uint32_t)j & 1u, &sh_gone, p.err);
       fence_after();
       uint32_t v[2][32];  // asked for before what the tile needs is known: nearly always the unmasked pass
       tmem_ld32(ts, v[0]);
@@ -479,7 +482,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
     }
     // ---- output
     if (ntiles > 0) {
-      mbar_wait<false>(smem_addr(&oFull), 0, p.err);
+      kv_wait(smem_addr(&oFull), 0, &sh_gone, p.err);
       fence_after();
     }
     float s0, s1;
@@ -608,7 +611,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
       load_v();
 #pragma unroll
       for (int g = 0; g < NG; ++g) vp[g] = vpn[g];
-      mbar_wait<false>(smem_addr(&kEmpty[st]), free_parity, p.err);
+      kv_wait(smem_addr(&kEmpty[st]), free_parity, &sh_gone, p.err);
       uint8_t* tk = gen + 2 * kTileBytes + st * kTileBytes;
       uint32_t bad = 0;  // the token's poisoned groups
       float kscale = 1.0f, vbig = 0.0f;
@@ -684,7 +687,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
       // the next tile's keys
       load_k(j + 1);
       page_of(j + 2);
-      mbar_wait<false>(smem_addr(&vEmpty[st]), free_parity, p.err);
+      kv_wait(smem_addr(&vEmpty[st]), free_parity, &sh_gone, p.err);
       uint8_t* tv = gen + 4 * kTileBytes + st * kTileBytes;
       if (okv) {
         const float to = pow2(-vown);
@@ -708,7 +711,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&vFull[st]));
+      const bool held = p.fail && blockIdx.x == 0 && z == 0 && j == ntiles - 1 && dw == 0;
+      if (lane == 0 && !held) mbar_arrive(smem_addr(&vFull[st]));
     }
   } else {
     set_registers<kPrRegs, kPrMmaRegs>();
@@ -726,16 +730,16 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
       if (t == nt - 1) commit(leader, &kEmpty[j & 1]);
     };
     if (warp == kPrMma && ntiles > 0) {
-      mbar_wait<false>(smem_addr(&qFull), 0, p.err);
-      mbar_wait<false>(smem_addr(&kFull[0]), 0, p.err);
+      kv_wait(smem_addr(&qFull), 0, &sh_gone, p.err);
+      kv_wait(smem_addr(&kFull[0]), 0, &sh_gone, p.err);
       fence_after();
       for (int t = 0; t < nt; ++t) scores(t, 0);
       for (int j = 0; j < ntiles; ++j) {
         // both operands of this round are usually there long before the weights
-        mbar_wait<false>(smem_addr(&vFull[j & 1]), (uint32_t)(j >> 1) & 1u, p.err);
-        if (j + 1 < ntiles) mbar_wait<false>(smem_addr(&kFull[(j + 1) & 1]), (uint32_t)((j + 1) >> 1) & 1u, p.err);
+        kv_wait(smem_addr(&vFull[j & 1]), (uint32_t)(j >> 1) & 1u, &sh_gone, p.err);
+        if (j + 1 < ntiles) kv_wait(smem_addr(&kFull[(j + 1) & 1]), (uint32_t)((j + 1) >> 1) & 1u, &sh_gone, p.err);
         for (int t = 0; t < nt; ++t) {
-          mbar_wait<false>(smem_addr(&pFull[t]), (uint32_t)j & 1u, p.err);
+          kv_wait(smem_addr(&pFull[t]), (uint32_t)j & 1u, &sh_gone, p.err);
           fence_after();
           const uint32_t vb = sv + (j & 1) * kTileBytes;
 #pragma unroll
@@ -824,7 +828,7 @@ cudaError_t launch_prompt(const PromptArgs& p, unsigned ctas, cudaStream_t s) {
 
 template <typename T>
 cudaError_t prompt(Kv& kv, const KvAttnArgs& a, cudaStream_t s) {
-  PromptArgs p{a, a.q_heads / a.c.heads, 0, 1, kv.parts(), kv.err_dev};
+  PromptArgs p{a, a.q_heads / a.c.heads, 0, 1, kv.parts(), kv.err_dev, kv.fail_next};
   const int64_t tiles = ((int64_t)a.b.max_new * p.per + 2 * kPrTile - 1) / (2 * kPrTile);
   const int64_t ctas = tiles * a.c.heads * a.b.batch;
   if (ctas > 0x7fffffff || (int64_t)a.c.heads * a.b.batch > 0x7fffffff || tiles * 2 * kPrTile > 0x7fffffff)

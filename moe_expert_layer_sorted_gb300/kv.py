@@ -26,6 +26,8 @@ def declare(L):
     L.moe_kv_read.argtypes = [_P, i32, _P, _P, _P, _P]
     L.moe_kv_attention.argtypes = [_P, i32, _P, _P, i32, ctypes.c_float, i32, _P, _P, _P, i32, _P]
     L.moe_kv_select.argtypes = [_P, i32, _P, _P, i32, i32, i32, i32, _P, _P]
+    L.moe_kv_status.argtypes = [_P]
+    L.moe_kv_debug_fail_next_attention.argtypes = [_P]
     L.moe_kv_last_error.argtypes = [_P]
     L.moe_kv_last_error.restype = ctypes.c_char_p
 
@@ -134,6 +136,23 @@ class KVCache:
             self.close()
         except Exception:
             pass
+
+    def _call(self, f):
+        from . import MoeError
+        if not self._h:
+            _bad("the cache is closed")
+        rc = f(self._h)
+        if rc:
+            raise MoeError(rc, self._lib.moe_kv_last_error(self._h).decode())
+
+    def check(self):
+        """Raises MoeError (MOE_ERR_TIMEOUT) where a bounded wait on the device gave up, in a call
+        or in a replayed graph that holds one; after a synchronisation."""
+        self._call(self._lib.moe_kv_status)
+
+    def debug_fail_next_attention(self):
+        """Test hook: a wait of the next attention runs out (see moe.h)."""
+        self._call(self._lib.moe_kv_debug_fail_next_attention)
 
     # The tensors are checked and unpacked in csrc/kv_binding.cpp.
 

@@ -61,3 +61,30 @@ def test_a_capture_neither_waits_nor_records(cache, lib):
     cache.log()
     assert cache.attention(5) == 0
     assert cache.log() == ["attention 5"]
+
+
+@pytest.mark.parametrize("call", ["append", "read", "attention", "select", "status"])
+def test_a_wait_that_gave_up_is_reported_once_by_whichever_call_is_next(cache, lib, call):
+    def run():
+        return lib.moe_kv_status(cache.h) if call == "status" else getattr(cache, call)(4)
+
+    assert run() == 0
+    cache.log()
+    lib.fake_raise(cache.h)
+    assert run() == 4 and b"gave up" in lib.moe_kv_last_error(cache.h)
+    assert cache.log() == []
+    assert run() == 0
+    assert lib.moe_kv_status(cache.h) == 0
+
+
+def test_a_wait_that_gave_up_is_reported_to_a_capture_and_by_destroy(lib):
+    c = kv_host.Cache(lib)
+    assert c.attention(4) == 0
+    lib.fake_capturing(5, 1)
+    lib.fake_raise(c.h)
+    c.log()
+    assert c.attention(5) == 4 and c.log() == []
+    lib.fake_capturing(5, 0)
+    lib.fake_raise(c.h)
+    assert lib.moe_kv_destroy(c.h) == 4 and b"gone" in lib.moe_kv_last_error(None)
+    assert "free" in c.log()
