@@ -32,11 +32,14 @@ def _deps():
     return max(os.path.getmtime(h) for h in hdrs)
 
 
-def _binding_cmd(header_time: float) -> list | None:
-    """g++ command of the key/value cache's Python binding, or None where it is up to date."""
+def _binding_fresh(header_time: float) -> bool:
     src = os.path.join(CSRC, "kv_binding.cpp")
-    if os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(src), header_time):
-        return None
+    return os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(src), header_time)
+
+
+def _binding_cmd(out: str, lib: str = LIB) -> list:
+    """g++ command of the key/value cache's Python binding over `lib`, into `out`."""
+    src = os.path.join(CSRC, "kv_binding.cpp")
     import sysconfig
 
     import torch
@@ -45,7 +48,7 @@ def _binding_cmd(header_time: float) -> list | None:
     inc = [INCLUDE, os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-            *[f"-I{i}" for i in inc], src, "-o", BINDING + ".tmp", f"-L{PKG}", f"-L{os.path.join(t, 'lib')}", "-l:libmoe_gb300.so",
+            *[f"-I{i}" for i in inc], src, "-o", out, f"-L{os.path.dirname(lib)}", f"-L{os.path.join(t, 'lib')}", f"-l:{os.path.basename(lib)}",
             "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
 
 
@@ -81,8 +84,8 @@ def build(verbose: bool = False, force: bool = False) -> str:
             print(r.stdout + r.stderr)
             raise RuntimeError("link failed")
         os.replace(LIB + ".tmp", LIB)
-    cmd = _binding_cmd(os.path.getmtime(os.path.join(INCLUDE, "moe.h")))
-    if cmd:
+    if not _binding_fresh(os.path.getmtime(os.path.join(INCLUDE, "moe.h"))):
+        cmd = _binding_cmd(BINDING + ".tmp")
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode:
             print(" ".join(cmd))

@@ -39,6 +39,7 @@ void check(bool ok, const char* text) {
 struct Cache {
   PyObject_HEAD moe_kv_cache* h;
   int device;
+  int running;  // calls inside the library (counted under the interpreter's lock)
   at::ScalarType type;
   int64_t kv_heads, head_dim;
 };
@@ -143,16 +144,20 @@ int32_t* choice_of(const Cache* c, PyObject* o, int64_t rows, int* budget) {
   return static_cast<int32_t*>(const_cast<void*>(t.const_data_ptr()));
 }
 
+constexpr char kInUse[] = "the cache is in use by another thread";
+
 // Runs f, a call of the C ABI, without the interpreter's lock: a launch can wait
 // for room in the stream's queue.
 template <typename F>
-void run(const Cache* c, F&& f) {
+void run(Cache* c, F&& f) {
+  ++c->running;
   PyThreadState* state = PyEval_SaveThread();
   const moe_status rc = f();
   PyEval_RestoreThread(state);
+  --c->running;
   if (rc == MOE_OK) return;
   // a busy handle's text is the running call's
-  raise(rc, rc == MOE_ERR_STATE ? "the cache is in use by another thread" : moe_kv_last_error(c->h));
+  raise(rc, rc == MOE_ERR_STATE ? kInUse : moe_kv_last_error(c->h));
 }
 
 // Runs a call's body; what it throws becomes a Python exception.
@@ -163,7 +168,7 @@ PyObject* call(PyObject* self, Py_ssize_t given, Py_ssize_t wanted, F&& f) {
       PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
       return nullptr;
     }
-    const Cache* c = reinterpret_cast<Cache*>(self);
+    Cache* c = reinterpret_cast<Cache*>(self);
     check(c->h != nullptr, "the cache is closed");
     f(c);
     Py_RETURN_NONE;
@@ -182,7 +187,7 @@ PyObject* call(PyObject* self, Py_ssize_t given, Py_ssize_t wanted, F&& f) {
 // append / read (k, v, table, lens, starts, max_new, layer, stream)
 template <bool Write>
 PyObject* rows_call(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  return call(self, n, 8, [&](const Cache* c) {
+  return call(self, n, 8, [&](Cache* c) {
     const at::Tensor &k = leading(c, a[0], "k", true), &v = tensor(a[1], "v");
     const moe_kv_batch b = batch_of(c, k.sizes(), a[2], a[3], a[4], a[5]);
     const moe_kv_tensor kt = rows_of(c, k, "k", k.sizes(), !Write), vt = rows_of(c, v, "v", k.sizes(), !Write);
@@ -194,7 +199,7 @@ PyObject* rows_call(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 
 // attention (q, out, table, lens, starts, max_new, layer, stream, scale, causal, lse, pages)
 PyObject* attention(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  return call(self, n, 12, [&](const Cache* c) {
+  return call(self, n, 12, [&](Cache* c) {
     const at::Tensor &q = leading(c, a[0], "q", false), &out = tensor(a[1], "out");
     const moe_kv_batch b = batch_of(c, q.sizes(), a[2], a[3], a[4], a[5]);
     const moe_kv_tensor qt = rows_of(c, q, "q", q.sizes(), false), ot = rows_of(c, out, "out", q.sizes(), true);
@@ -224,7 +229,7 @@ PyObject* attention(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 
 // select (q, pages, table, lens, starts, max_new, layer, stream, keep_first, keep_last)
 PyObject* select(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  return call(self, n, 10, [&](const Cache* c) {
+  return call(self, n, 10, [&](Cache* c) {
     const at::Tensor& q = leading(c, a[0], "q", false);
     const moe_kv_batch b = batch_of(c, q.sizes(), a[2], a[3], a[4], a[5]);
     const moe_kv_tensor qt = rows_of(c, q, "q", q.sizes(), false);
@@ -238,9 +243,27 @@ PyObject* select(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-PyObject* closed(PyObject* self, PyObject*) {  // the handle is gone
-  reinterpret_cast<Cache*>(self)->h = nullptr;
-  Py_RETURN_NONE;
+PyObject* status(PyObject* self, PyObject*) {
+  return call(self, 0, 0, [&](Cache* c) { run(c, [h = c->h] { return moe_kv_status(h); }); });
+}
+PyObject* fail_next(PyObject* self, PyObject*) {
+  return call(self, 0, 0, [&](Cache* c) { run(c, [h = c->h] { return moe_kv_debug_fail_next_attention(h); }); });
+}
+
+// Destroys the handle; not while a call is inside the library (which may not have reached the
+// handle's own guard yet): the cache then stays as it is.
+PyObject* close(PyObject* self, PyObject*) {
+  if (!reinterpret_cast<Cache*>(self)->h) Py_RETURN_NONE;
+  return call(self, 0, 0, [&](Cache* c) {
+    if (c->running) raise(MOE_ERR_STATE, kInUse);
+    moe_kv_cache* h = c->h;
+    c->h = nullptr;  // no call begins from here on
+    PyThreadState* state = PyEval_SaveThread();
+    const moe_status rc = moe_kv_destroy(h);
+    PyEval_RestoreThread(state);
+    if (rc == MOE_ERR_STATE) c->h = h;  // in use through the C ABI
+    if (rc != MOE_OK) raise(rc, rc == MOE_ERR_STATE ? kInUse : moe_kv_last_error(nullptr));
+  });
 }
 
 // Cache(MoeError, handle, device, bfloat16, kv_heads, head_dim)
@@ -256,6 +279,7 @@ int cache_init(PyObject* self, PyObject* args, PyObject*) {
   Cache* c = reinterpret_cast<Cache*>(self);
   c->h = static_cast<moe_kv_cache*>(h);
   c->device = device;
+  c->running = 0;
   c->type = bf16 ? at::kBFloat16 : at::kHalf;
   c->kv_heads = kv_heads;
   c->head_dim = head_dim;
@@ -273,7 +297,9 @@ PyMethodDef cache_methods[] = {
     {"read", fast(&rows_call<false>), METH_FASTCALL, nullptr},
     {"attention", fast(&attention), METH_FASTCALL, nullptr},
     {"select", fast(&select), METH_FASTCALL, nullptr},
-    {"closed", closed, METH_NOARGS, nullptr},
+    {"check", status, METH_NOARGS, nullptr},
+    {"debug_fail_next_attention", fail_next, METH_NOARGS, nullptr},
+    {"close", close, METH_NOARGS, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyType_Slot cache_slots[] = {{Py_tp_init, reinterpret_cast<void*>(&cache_init)},

@@ -77,7 +77,7 @@ class KVCache:
     def __init__(self, pages, *, page_size, head_dim, group_size=64, dtype=None, bounds=None):
         import torch
         from . import MoeError
-        self._h = None
+        self._h = self._c = None
         self._lib = _lib()
         dtype = torch.bfloat16 if dtype is None else dtype
         if not (pages.is_cuda and pages.dtype == torch.uint8 and pages.dim() in (4, 5) and pages.is_contiguous()):
@@ -125,11 +125,20 @@ class KVCache:
         return cls(pages, page_size=page_size, head_dim=head_dim, group_size=group_size, dtype=dtype, bounds=ends)
 
     def close(self):
-        if getattr(self, "_h", None):
-            if getattr(self, "_c", None):
-                self._c.closed()
-            self._lib.moe_kv_destroy(self._h)
+        """Frees the handle.  MoeError with MOE_ERR_STATE: a call of another thread is running, and the
+        cache stays as it is; with MOE_ERR_TIMEOUT: see `check`, and the cache is closed."""
+        from . import MoeError
+        try:
+            if self._c is not None:
+                self._c.close()
+            elif self._h:
+                self._lib.moe_kv_destroy(self._h)
+        except MoeError as e:
+            if e.status == 5:  # MOE_ERR_STATE
+                raise
             self._h = None
+            raise
+        self._h = None
 
     def __del__(self):
         try:
@@ -137,22 +146,14 @@ class KVCache:
         except Exception:
             pass
 
-    def _call(self, f):
-        from . import MoeError
-        if not self._h:
-            _bad("the cache is closed")
-        rc = f(self._h)
-        if rc:
-            raise MoeError(rc, self._lib.moe_kv_last_error(self._h).decode())
-
     def check(self):
         """Raises MoeError (MOE_ERR_TIMEOUT) where a bounded wait on the device gave up, in a call
         or in a replayed graph that holds one; after a synchronisation."""
-        self._call(self._lib.moe_kv_status)
+        self._c.check()
 
     def debug_fail_next_attention(self):
         """Test hook: a wait of the next attention runs out (see moe.h)."""
-        self._call(self._lib.moe_kv_debug_fail_next_attention)
+        self._c.debug_fail_next_attention()
 
     # The tensors are checked and unpacked in csrc/kv_binding.cpp.
 

@@ -6,6 +6,8 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <condition_variable>
+#include <mutex>
 #include <string>
 
 namespace {
@@ -13,6 +15,9 @@ namespace {
 std::string g_log;
 unsigned long long g_id[16];   // identity of the stream behind a handle value
 bool g_capturing[16];
+std::mutex g_mu;
+std::condition_variable g_cv;
+bool g_blocking = false, g_inside = false;
 
 int slot(cudaStream_t s) { return (int)((uintptr_t)s & 15); }
 
@@ -35,7 +40,25 @@ cudaError_t cudaHostGetDevicePointer(void** d, void* h, unsigned) { *d = h; retu
 cudaError_t cudaMemset(void* p, int v, size_t n) { memset(p, v, n); return cudaSuccess; }
 cudaError_t cudaMemsetAsync(void* p, int v, size_t n, cudaStream_t s) { memset(p, v, n); say("memset", s); return cudaSuccess; }
 cudaError_t cudaGetDeviceCount(int* n) { *n = 1; return cudaSuccess; }
-cudaError_t cudaGetDevice(int* d) { *d = 0; return cudaSuccess; }
+cudaError_t cudaGetDevice(int* d) {
+  std::unique_lock<std::mutex> l(g_mu);
+  if (g_blocking) {
+    g_blocking = false;  // the one call
+    g_inside = true;
+    g_cv.notify_all();
+    g_cv.wait(l, [] { return !g_inside; });
+  }
+  *d = 0;
+  return cudaSuccess;
+}
+// 1: the next call stays inside the library until 0; 2: waits until it is there
+void fake_block(int what) {
+  std::unique_lock<std::mutex> l(g_mu);
+  if (what == 2) g_cv.wait(l, [] { return g_inside; });
+  else if (what == 1) g_blocking = true;
+  else g_inside = false;
+  g_cv.notify_all();
+}
 cudaError_t cudaSetDevice(int) { return cudaSuccess; }
 cudaError_t cudaGetLastError() { return cudaSuccess; }
 const char* cudaGetErrorString(cudaError_t) { return "an error"; }

@@ -1,29 +1,7 @@
 // The launchers that csrc/kv.cu calls, without kernels: each call goes to the log of fake_cuda.cpp.
-#include <condition_variable>
-#include <mutex>
-
 #include "kv_internal.h"
 
 void say(const char* what, cudaStream_t s);
-
-namespace {
-
-std::mutex g_mu;
-std::condition_variable g_cv;
-bool g_blocking = false, g_inside = false;
-
-}  // namespace
-
-// 1: the next append stays inside its call until 0; 2: waits until one is inside
-extern "C" void fake_block(int what) {
-  std::unique_lock<std::mutex> l(g_mu);
-  if (what == 2) {
-    g_cv.wait(l, [] { return g_inside; });
-    return;
-  }
-  g_blocking = what;
-  g_cv.notify_all();
-}
 
 // what a kernel's wait that gave up leaves behind
 extern "C" void fake_raise(moe_kv_cache* h) { *reinterpret_cast<moe::Kv*>(h)->err_host = 1; }
@@ -32,13 +10,6 @@ namespace moe {
 
 cudaError_t kv_append(const Kv&, const KvView&, const KvBatch&, const uint16_t*, const KvRows&, const uint16_t*,
                       const KvRows&, cudaStream_t s) {
-  std::unique_lock<std::mutex> l(g_mu);
-  if (g_blocking) {
-    g_inside = true;
-    g_cv.notify_all();
-    g_cv.wait(l, [] { return !g_blocking; });
-    g_inside = false;
-  }
   say("append", s);
   return cudaSuccess;
 }

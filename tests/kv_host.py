@@ -36,6 +36,23 @@ def build(folder):
     return L
 
 
+def folder_of(L):
+    return os.path.dirname(L._name)
+
+
+def build_binding(folder):
+    """The Python binding over that library: a module."""
+    import importlib.util
+
+    from moe_expert_layer_sorted_gb300 import _build as b
+    out = os.path.join(str(folder), "_kv_binding.so")
+    subprocess.run(b._binding_cmd(out, os.path.join(str(folder), "libkv_host.so")), check=True)
+    spec = importlib.util.spec_from_file_location("_kv_binding", out)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
 class Cache:
     """A handle over nothing: 1 kv head, 4 pages."""
 

@@ -88,3 +88,38 @@ def test_a_wait_that_gave_up_is_reported_to_a_capture_and_by_destroy(lib):
     lib.fake_raise(c.h)
     assert lib.moe_kv_destroy(c.h) == 4 and b"gone" in lib.moe_kv_last_error(None)
     assert "free" in c.log()
+
+
+class Error(RuntimeError):
+    def __init__(self, status, text):
+        super().__init__(text)
+        self.status = status
+
+
+def test_close_while_another_thread_is_in_a_call(lib, tmp_path_factory):
+    """The cache stays open and usable, nothing is freed, and a later close frees it."""
+    import threading
+
+    c = kv_host.Cache(lib)
+    m = kv_host.build_binding(kv_host.folder_of(lib))
+    cache = m.Cache(Error, c.h.value, 0, True, 1, 64)
+    cache.check()
+    lib.fake_block(1)
+    t = threading.Thread(target=cache.check)
+    t.start()
+    lib.fake_block(2)
+    with pytest.raises(Error) as e:
+        cache.close()
+    assert e.value.status == 5
+    with pytest.raises(Error) as e:  # one call at a time
+        cache.check()
+    assert e.value.status == 5
+    assert "free" not in c.log()
+    lib.fake_block(0)
+    t.join()
+    cache.check()
+    cache.close()
+    assert "free" in c.log()
+    cache.close()
+    with pytest.raises(Error, match="closed"):
+        cache.check()
