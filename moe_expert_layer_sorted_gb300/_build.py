@@ -1,11 +1,15 @@
 """Build of the CUDA library (sm_103a only): one nvcc per translation unit, in
-parallel, then one shared-library link.  Output:
-moe_expert_layer_sorted_gb300/libmoe_gb300.so (git-ignored, rebuilt per box)."""
+parallel, then one shared-library link, and of the key/value cache's Python
+binding where torch is installed.  Output: libmoe_gb300.so and _kv_binding.so in
+moe_expert_layer_sorted_gb300/ (git-ignored, rebuilt per box)."""
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
+import importlib.util
 import os
 import subprocess
+import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -32,9 +36,25 @@ def _deps():
     return max(os.path.getmtime(h) for h in hdrs)
 
 
-def _binding_fresh(header_time: float) -> bool:
-    src = os.path.join(CSRC, "kv_binding.cpp")
-    return os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(src), header_time)
+def _binding_for() -> str | None:
+    """What a binding is built for (it holds torch's and the interpreter's layouts); None without torch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:  # not installed as a package: by its files
+        version = f"{spec.origin} of {os.path.getmtime(spec.origin)}"
+    return f"torch {version}, python {sys.version}"
+
+
+def _binding_fresh(made_for: str) -> bool:
+    files = [os.path.join(CSRC, "kv_binding.cpp"), os.path.join(INCLUDE, "moe.h")]
+    try:
+        with open(BINDING + ".for") as f:
+            return f.read() == made_for and os.path.getmtime(BINDING) >= max(os.path.getmtime(x) for x in files)
+    except OSError:
+        return False
 
 
 def _binding_cmd(out: str, lib: str = LIB) -> list:
@@ -84,7 +104,8 @@ def build(verbose: bool = False, force: bool = False) -> str:
             print(r.stdout + r.stderr)
             raise RuntimeError("link failed")
         os.replace(LIB + ".tmp", LIB)
-    if not _binding_fresh(os.path.getmtime(os.path.join(INCLUDE, "moe.h"))):
+    made_for = _binding_for()  # without torch there is the C library alone
+    if made_for and not _binding_fresh(made_for):
         cmd = _binding_cmd(BINDING + ".tmp")
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode:
@@ -92,6 +113,8 @@ def build(verbose: bool = False, force: bool = False) -> str:
             print(r.stdout + r.stderr)
             raise RuntimeError("the Python binding did not build")
         os.replace(BINDING + ".tmp", BINDING)
+        with open(BINDING + ".for", "w") as f:
+            f.write(made_for)
     return LIB
 
 

@@ -76,7 +76,7 @@ class KVCache:
 
     def __init__(self, pages, *, page_size, head_dim, group_size=64, dtype=None, bounds=None):
         import torch
-        from . import MoeError
+        from . import MoeError, _kv_binding
         self._h = self._c = None
         self._lib = _lib()
         dtype = torch.bfloat16 if dtype is None else dtype
@@ -104,7 +104,6 @@ class KVCache:
         self.dtype, self.device = dtype, pages.device
         self.layers, self.kv_heads, self.head_dim = layers, kv_heads, head_dim
         self.page_size, self.group_size = page_size, group_size
-        from . import _kv_binding
         self._c = _kv_binding.Cache(MoeError, h.value, d.device, dtype == torch.bfloat16, kv_heads, head_dim)
 
     @staticmethod
