@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
           for (int e = 0; e < 2; ++e) qsum[nt][g][e] = __shfl_sync(0xffffffffu, sum[g], 4 * (2 * c + e));
         }
         const int64_t pos = (int64_t)q.len - q.rows + i;
-        const int see = (int)min(max(a.causal ? pos + 1 : (int64_t)q.len, (int64_t)0), (int64_t)cap);
+        const int see = pos < 0 ? 0 : (int)min(a.causal ? pos + 1 : (int64_t)q.len, (int64_t)cap);
         // scale log2 e 2^(24 - by), of which what would leave fp32's range stays with the scores
         const float base = a.scale * 1.4426950408889634f;
         const int over = min(max((int)(__float_as_uint(fabsf(base)) >> 23) - 127 + 24 - by - 126, 0), 126);

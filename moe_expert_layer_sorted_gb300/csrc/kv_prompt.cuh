@@ -211,7 +211,8 @@ struct PromptTile {
     splits = min(p.splits, max(all / 2, 1));
   }
   __device__ __forceinline__ int seen(const PromptArgs& p, int x) const {  // tokens that row x sees
-    return (int)min(max(p.a.causal ? first + x / p.per + 1 : (int64_t)q.len, (int64_t)0), (int64_t)cap);
+    const int64_t pos = first + x / p.per;
+    return pos < 0 ? 0 : (int)min(p.a.causal ? pos + 1 : (int64_t)q.len, (int64_t)cap);
   }
 };
 // Floats of a stretch's part: O [D / 4][row] of four channels, then references, sums, poisoned
