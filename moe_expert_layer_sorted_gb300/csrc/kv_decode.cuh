@@ -71,7 +71,7 @@ constexpr int kDecMaxParts = kDecWarps * (64 + 4);  // CTAs, so parts of an item
 constexpr float kDecSlack = 4.0f;      // weights reach 2^4
 constexpr int kDecRoom = 14;           // |c| + 8 s stays below 2^(E + 14): weights times steps below 2^15
 constexpr int kDecAim = 10;            // a column's largest weight times value is raised to about 2^(E + 10)
-constexpr float kDecPartScale = 0x1p-16f;  // of parts' weights (below 2^4 each): their sum with values stays in range
+constexpr float kDecPartScale = 0x1p-40f;  // of parts' weights (up to 2^30 each): their sum with values stays in range
 
 __device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kDecWarps * 32) : "memory"); }
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
   __shared__ uint32_t sh_gone;  // a wait gave up: results are wrong, the next call says so
   __shared__ int2 sh_exp[kDecWarps];  // a warp's E, exponent of the largest value it has seen
   __shared__ float sh_up[kDecWarps * C];
-  __shared__ float sh_lift[C];        // of the item's columns; every warp writes the same
+  __shared__ float2 sh_lift[C];       // of the item's columns; every warp writes the same
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
 
@@ -349,7 +349,9 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
       float factor[NT][2];       // what makes the columns' sums scores (log2)
       int seen[NT][2];           // tokens that the columns see
       int least = 0x7fffffff, most = 0;  // over the columns
-      bool lifted = false;               // some column's scores are taken times a power of two first (sh_lift)
+      // the scores are multiplied by sh_lift and the factor (then 1) before anything else: where a
+      // factor would leave fp32's range, and where they are as large as kCoarse
+      bool lifted = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int s = it.s, h = it.head, row_lo = it.row_lo, ncols = it.cols;
@@ -402,7 +404,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
         const int over = min(max((int)(__float_as_uint(fabsf(base)) >> 23) - 127 + 24 - by - 126, 0), 126);
         const int pw = 24 - by - over;  // -89..137: in two steps
         const float back = base * pow2(pw / 2) * pow2(pw - pw / 2);
-        if (c == 0) sh_lift[nt * 8 + r] = pow2(over);
+        if (c == 0) sh_lift[nt * 8 + r] = make_float2(pow2(over), back);
         lifted |= __any_sync(0xffffffffu, over > 0);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -414,6 +416,20 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
       }
       if (lane == 0) sh_exp[warp] = make_int2(0, -127);
       __syncwarp();  // sh_lift, sh_exp
+      auto lift = [&](float (&sc)[NT][4]) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 by = sh_lift[nt * 8 + 2 * c + (e & 1)];
+            sc[nt][e] = sc[nt][e] * by.x * by.y;
+          }
+      };
+      auto factor_one = [&]() {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) factor[nt][0] = factor[nt][1] = 1.0f;
+      };
+      if (lifted) factor_one();
 
       float acc[D / 16][NT][4];  // O^T: channel tiles by columns
       float oc[NT][NG][2];       // this lane's tokens' part of sum P (c - 8 s), or of sum P c
@@ -474,7 +490,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
         }
       };
       // One block from its scores.  part: some column does not see some of its tokens.
-      auto block = [&](const uint8_t* blk, int pos, const float (&sc)[NT][4], auto part_) {
+      auto block = [&](const uint8_t* blk, int pos, float (&sc)[NT][4], auto part_) {
         constexpr bool part = decltype(part_)::value;
         // params of tokens r and r + 8, values' codes of tokens 2c, 2c + 1, 2c + 8, 2c + 9
         uint32_t vp[2][NG], vw[4][D / 64];
@@ -609,6 +625,16 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
                 rescale(nt, x, f, exp2_fast(cur - ref));
               }
           }
+          float far = 0.0f;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) far = fmaxf(far, m[nt][x] == kNone ? 0.0f : fabsf(m[nt][x]));
+          if (!lifted && __any_sync(0xffffffffu, far >= kCoarse)) {
+            lifted = true;
+            lift(sc);
+            factor_one();
+          }
           exponents();
         }
         // ---- weights, their sums, and P s as the second product's operand
@@ -677,12 +703,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
         if (pos >= 0) {
           float sc[NT][4];
           scores(blk, sc);
-          if (lifted) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) sc[nt][e] *= sh_lift[nt * 8 + 2 * c + (e & 1)];
-          }
+          if (lifted) lift(sc);
           if (pos + 16 > least) block(blk, pos, sc, std::true_type());
           else block(blk, pos, sc, std::false_type());
         }
@@ -707,10 +728,9 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
           for (int g = 0; g < NG; ++g)
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) oc[nt][g][x] += __shfl_xor_sync(0xffffffffu, oc[nt][g][x], o);
-          // the sum between 1 and 2, with a reference to suit; O with the power of two that goes with both
-          const int by = l[nt][x] > 0.0f ? min(exponent(__float_as_uint(l[nt][x])), 126) : 0, up = sh_exp[warp].x - by;
+          const int by = excess<30>(l[nt][x]), up = sh_exp[warp].x - by;  // up: the power of two that goes with O
           if (r == 0) {
-            mm[warp * C + col] = l[nt][x] > 0.0f ? m[nt][x] + (float)by : kNone;
+            mm[warp * C + col] = m[nt][x] + (float)by;
             ml[warp * C + col] = l[nt][x] * pow2(-by);
             sh_up[warp * C + col] = up < -126 ? 0.0f : pow2(min(up, 127));
           }

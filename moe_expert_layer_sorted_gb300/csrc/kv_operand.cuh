@@ -8,11 +8,23 @@ constexpr float kNone = -1e30f;  // softmax reference of a row that has seen no 
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 // floor(log2) of a positive normal fp32's bits (-127 of zero and subnormals, 128 of an infinity)
 __device__ __forceinline__ int exponent(uint32_t bits) { return (int)(bits >> 23) - 127; }
+// A partial result leaves with its reference m and its sum l as they are, so that equal scores of
+// any size weigh the same in every part; where l is outside 2^-Span..2^Span its exponent, which
+// this is, goes from l to m (there the reference went by the sizes of values).
+template <int Span>
+__device__ __forceinline__ int excess(float l) {
+  const int e = exponent(__float_as_uint(l));
+  return l > 0.0f && (e >= Span || e < -Span) ? min(e, 126) : 0;
+}
 __device__ __forceinline__ float exp2_fast(float x) {
   float d;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
   return d;
 }
+
+// Scores from here on are rounded before the reference is taken off: the exact product differs
+// from its rounded self, which the reference is, by a sixteenth there, and by any amount above.
+constexpr float kCoarse = 1048576.0f;
 
 // Fields I of both half-words of a word (4 bits each at bit 4 I) as a pair of fp16.
 //   raw:     the bits themselves, a subnormal: u 2^-24, or for odd I u 2^-20.  One mask

@@ -71,7 +71,7 @@ constexpr int kPrTile = 128;  // rows of a row tile, tokens of a token tile
 // raised when a tile's weights sum to kPrLimit; so no weight passes 2^15 and fp16 holds those
 // 2^-31 of the largest
 constexpr float kPrDrop = 7.0f, kPrLimit = 32768.0f;
-constexpr float kPrJoin = 0x1p-10f;  // of the stretches' weights: their sum with values of any size stays in range
+constexpr float kPrJoin = 0x1p-50f;  // of the stretches' weights (up to 2^40 each): their sum with values stays in range
 
 // K-major operand, 128-byte swizzle: 8-row groups 1024 bytes apart.
 __device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
@@ -340,6 +340,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
     uint64_t l2 = 0;        // the two halves of the row's sum
     uint32_t poisoned = 0;  // groups with a NaN value that the row sees
     int vexp = 0;           // E so far
+    bool coarse = false;    // a row's scores are as large as kCoarse
     for (int j = 0; j < (t == 0 || two ? ntiles : 0); ++j) {
       kv_wait(smem_addr(&sFull[t]), (uint32_t)j & 1u, &sh_gone, p.err);
       fence_after();
@@ -350,8 +351,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
       const uint32_t valid[4] = {valid4.x, valid4.y, valid4.z, valid4.w};
       const uint32_t poison[4] = {poison4.x, poison4.y, poison4.z, poison4.w};
       // a tile that every row of the warp sees in full takes no masks
-      const bool plain = __all_sync(0xffffffffu, seen >= (j + 1) * kPrTile) &&
-                         (valid4.x & valid4.y & valid4.z & valid4.w) == 0xffffffffu && !scaled;
+      bool plain = __all_sync(0xffffffffu, seen >= (j + 1) * kPrTile) &&
+                   (valid4.x & valid4.y & valid4.z & valid4.w) == 0xffffffffu && !scaled && !coarse;
       uint32_t pr[kPrTile / 2];
       auto mask_of = [&](int k) {  // tokens of the k-th 32 that the row sees
         const int n = seen - (j * kPrTile + 32 * k);
@@ -424,6 +425,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
           const float f = exp2_fast(m - best), fo = exp2_fast(cur - best);
           m = best;
           vexp = now;
+          coarse = coarse || __any_sync(0xffffffffu, m != kNone && fabsf(m) >= kCoarse);
+          plain = plain && !coarse;
           l2 = pair2(l0 * f, l1 * f);
           if (j > 0) {
 #pragma unroll 1
@@ -545,9 +548,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv_prompt_kernel(const __grid_c
               make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
       }
       float* ends = part + 2 * kPrTile * D + row;
-      // the sum between 1 and 2, with a reference to suit; the power of two that goes with O
-      const int by = l > 0.0f ? min(exponent(__float_as_uint(l)), 126) : 0, up = vexp - by;
-      ends[0] = l > 0.0f ? m + (float)by : kNone;
+      const int by = excess<40>(l), up = vexp - by;  // up: the power of two that goes with O
+      ends[0] = m + (float)by;
       ends[2 * kPrTile] = l * pow2(-by);
       ends[4 * kPrTile] = __uint_as_float(poisoned);
       ends[6 * kPrTile] = up < -126 ? 0.0f : pow2(min(up, 127));

@@ -22,3 +22,42 @@ def test_rows_before_a_sequence_attend_to_nothing_without_causal_mask_too(D, G, 
     for i, L in enumerate(w.lens):
         seen = (torch.arange(L - n, L, device="cuda") >= 0)[:, None].expand(n, L)
         kv_bounds.check(out[i], lse[i * n:(i + 1) * n], kv_bounds.attention(q[i], *w.values(i), seen, 1 / math.sqrt(D), G))
+
+
+@pytest.mark.parametrize("n", [1, 4, 90])
+@pytest.mark.parametrize("length", [200, 5000])
+@pytest.mark.parametrize("size", [2.0 ** 11, 2.0 ** 13, 2.0 ** 16, -2.0 ** 13])
+def test_scores_of_millions_and_more(n, length, size):
+    """Where a score's last place is above one: a row is the mean of the tokens that score the
+    same and more than all others."""
+    w = World(128, 64, 64, BF, 2, [length], seed=n)
+    u = w.rand(2, 128).sign()
+    w.k[0].copy_((w.k[0].float().clamp(-1, 1) * 0.3 * abs(size)).to(BF))
+    best = torch.arange(7, length - n, 31, device="cuda")
+    w.k[0][best] = u * size
+    w.fill()
+    q = (u * abs(size)).expand(1, n, 2, 128).to(BF) * (1 if size > 0 else -1)
+    out, lse = torch.full((1, n, 2, 128), 9.0, dtype=BF, device="cuda"), torch.empty(n, 2, device="cuda")
+    w.cache.attention(q, out, lse=lse, **w.batch)
+    k, v = w.values(0)
+    score = (q[0, 0].double() * k[best[0]]).sum(-1) / math.sqrt(128)
+    assert (score > 1e6).all()
+    want = v[best].mean(0)
+    assert ((out[0].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -8).all()
+    assert ((lse.double() / score - 1).abs() < 2.0 ** -11).all()
+
+
+@pytest.mark.parametrize("n", [1, 4, 90])
+@pytest.mark.parametrize("size", [2.0 ** 12, 2.0 ** 15, 2.0 ** 40])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_equal_scores_of_millions_and_more(n, size, sign):
+    w = World(128, 64, 64, BF, 1, [3000], seed=n)
+    w.k[0].copy_((w.k[0][:1].float() * size).to(BF).expand(3000, 1, 128))
+    w.fill()
+    q = (w.k[0][:1].float() * sign).to(BF).expand(1, n, 4, 128)
+    out = torch.full((1, n, 4, 128), 9.0, dtype=BF, device="cuda")
+    w.cache.attention(q, out, **w.batch)
+    _, v = w.values(0)
+    for i in range(n):
+        want = v[:3000 - n + i + 1].mean(0)
+        assert ((out[0, i].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -9).all()
