@@ -2,7 +2,7 @@
 // anonymous namespace after device_common.cuh).
 #pragma once
 
-constexpr float kNone = -1e30f;  // softmax reference of a row that has seen no token
+constexpr float kNone = -3.402823466e38f;  // softmax reference of a row that has seen no token: the lowest finite score
 
 // 2^e, e in -126..127
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }

@@ -61,3 +61,22 @@ def test_equal_scores_of_millions_and_more(n, size, sign):
     for i in range(n):
         want = v[:3000 - n + i + 1].mean(0)
         assert ((out[0, i].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -9).all()
+
+
+@pytest.mark.parametrize("n", [1, 4, 90])
+@pytest.mark.parametrize("length", [200, 5000])
+def test_scores_near_the_lowest_fp32(n, length):
+    """Every token scores the same, some -10^36: the row is the mean of what it sees."""
+    w = World(128, 64, 64, BF, 1, [length], seed=n)
+    w.k[0].copy_((w.k[0][:1].float() * 2.0 ** 64).to(BF).expand(length, 1, 128))
+    w.fill()
+    q = (-w.k[0][:1].float() * 2.0 ** -10).to(BF).expand(1, n, 4, 128)
+    out, lse = torch.full((1, n, 4, 128), 9.0, dtype=BF, device="cuda"), torch.empty(n, 4, device="cuda")
+    w.cache.attention(q, out, lse=lse, **w.batch)
+    k, v = w.values(0)
+    score = float((q[0, 0, 0].double() @ k[0, 0])) / math.sqrt(128)
+    assert -3e38 < score < -1e34
+    for i in range(n):
+        want = v[:length - n + i + 1].mean(0)
+        assert ((out[0, i].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -9).all()
+    assert ((lse.double() / score - 1).abs() < 2.0 ** -16).all()
