@@ -30,7 +30,7 @@ __device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
 constexpr uint32_t kNegate = 0x80008000u;
 
 // x / 15 rounded to nearest: the product with the reciprocal and Markstein's correction of it by
-// its remainder.  Equal to the division for every finite 16-bit x (compared for all of them).
+// its remainder.  Equal to the division for every finite 16-bit x (tests/test_kv_division.py).
 __device__ __forceinline__ float over15(float x) {
   constexpr float kInv = 1.0f / 15.0f;
   const float q = __fmul_rn(x, kInv);
