@@ -273,7 +273,11 @@ cudaError_t moe::kv_append(const Kv& kv, const KvView& c, const KvBatch& b, cons
   const int per_seq = (int)(((int64_t)b.max_new + c.page_size - 2) / c.page_size) + 1;
   const int64_t ctas = (int64_t)b.batch * per_seq * c.heads;
   if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  const int half = b.max_new == 1 ? 1 : 4;  // key warps
+  // key warps: as few as the rows of a page keep busy.  Measured with 1 / 2 / 4 (8 heads of 128
+  // channels, us): 256 sequences of 1 row 5.2 / 7.0 / -, of 2 rows 7.6 / 8.7 / 14.5, of 4 rows
+  // 9.9 / 9.9 / 15.7, of 8 rows 14.4 / 13.2 / 17.9, of 64 rows 69 / 60 / 64; 1 sequence of 4 rows
+  // 4.5 / 3.2 / 3.5, of 8 rows 6.2 / 4.2 / 3.6, of 64 rows 14.7 / 11.9 / 8.8.
+  const int half = b.max_new == 1 ? 1 : b.max_new <= 4 ? 2 : 4;
   cudaError_t e = cudaSuccess;
   KV_DISPATCH(kv.d, {
     kv_append_kernel<T, D, G><<<(unsigned)ctas, half * 64, half * D * sizeof(uint32_t), s>>>(c, b, k, ks, v, vs, per_seq);

@@ -321,6 +321,9 @@ cudaError_t select(Kv& kv, const KvSelectArgs& a, cudaStream_t s) {
   for (int64_t r = 0; r < rows; r += step) {  // as many rows at a time as the workspace holds scores for
     const int64_t n = std::min(step, rows - r);
     kv_score_kernel<T, D><<<dim3((unsigned)(n * chunks), head_tiles), kSelThreads, 0, s>>>(a, r, chunks, keys);
+    // keys in registers / read again each step (us, 1 and 16 rows): tables of 1,024 pages 10.7 / 11.7,
+    // 16.5 / 17.9; of 4,096 13.5 / 18.5, 56.8 / 63.9.  32 keys a thread cost tables of 1,024 2.8 us
+    // (and would take 11.6 off 34.1 at 8,192 pages).
     const auto pick_kernel = a.b.table_pages <= 16 * kSelThreads ? kv_pick_kernel<16> : kv_pick_kernel<0>;
     pick_kernel<<<(unsigned)(n * a.c.heads), kSelThreads, 0, s>>>(a, r, keys);
     const cudaError_t e = cudaGetLastError();

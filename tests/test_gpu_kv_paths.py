@@ -34,6 +34,20 @@ def test_every_instantiation(D, G, dtype, per, counts):
     run(World(D, G, 32, dtype, 2, [777, 40, 130], seed=per).fill(), counts, 2 * per)
 
 
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 9])
+@pytest.mark.parametrize("D,G,dtype", [(128, 64, BF), (64, 32, FP)])
+def test_writes_of_a_few_rows_and_one_write_are_the_same_bytes(D, G, dtype, n):
+    a, b = (World(D, G, 32, dtype, 2, [75, 40, 3], seed=5) for _ in "ab")
+    a.fill()
+    for have in range(n, 75 + n, n):
+        lens = torch.tensor([min(have, L) for L in a.lens], dtype=torch.int32, device="cuda")
+        counts = [max(min(have, L) - (have - n), 0) for L in a.lens]
+        rows = [torch.cat([x[i][have - n:have - n + c] for i, c in enumerate(counts)]) for x in (b.k, b.v)]
+        b.cache.append(*rows, table=b.table, lens=lens, starts=starts_of(counts), max_new=n)
+    assert torch.equal(a.cache.pages, b.cache.pages)
+    assert torch.equal(a.cache.bounds.view(torch.int16), b.cache.bounds.view(torch.int16))
+
+
 def test_more_sequences_than_threads():
     g = torch.Generator().manual_seed(0)
     lens = torch.randint(1, 60, (500,), generator=g).tolist()
