@@ -294,6 +294,8 @@ extern "C" moe_status moe_kv_attention(moe_kv_cache* h, int layer, const moe_kv_
     if (!why && pages && budget < 1) why = "budget must be >= 1 with pages";
     if (!why && !(scale == scale && scale - scale == 0.0f)) why = "scale must be finite";
     if (why) return fail(kv, MOE_ERR_INVALID, why);
+    if (pages && (int64_t)budget * (kv->d.page_size / kKvBlock) > 0x7fffff00)  // blocks are counted in 32 bits
+      return fail(kv, MOE_ERR_UNSUPPORTED, "budget * page_size above 2^35 tokens");
     if (empty(batch)) return MOE_OK;
     if ((why = check_tensor(q)) || (why = check_tensor(out))) return fail(kv, MOE_ERR_INVALID, why);
     if (q->data == out->data) return fail(kv, MOE_ERR_INVALID, "q and out must not overlap");

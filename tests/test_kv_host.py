@@ -123,3 +123,18 @@ def test_close_while_another_thread_is_in_a_call(lib, tmp_path_factory):
     cache.close()
     with pytest.raises(Error, match="closed"):
         cache.check()
+
+
+def test_budgets_that_rounds_cannot_number_are_refused(cache):
+    """A chosen page is page_size / 16 blocks, which are counted in 32 bits."""
+    import ctypes
+
+    def attention(budget):
+        return cache.L.moe_kv_attention(cache.h, 0, ctypes.byref(cache.batch()), ctypes.byref(cache.t), 1, ctypes.c_float(1.0), 1,
+                                        ctypes.byref(cache.o), None, kv_host.P(4096), budget, kv_host.P(4))
+
+    assert attention(1 << 20) == 0
+    cache.log()
+    for budget in (0x7fffffff, 0x7ffffff9):
+        assert attention(budget) == 6 and b"budget" in cache.L.moe_kv_last_error(cache.h)
+    assert cache.log() == []
