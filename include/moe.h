@@ -450,7 +450,15 @@ moe_status moe_kv_read(moe_kv_cache* kv, int layer, const moe_kv_batch* batch, c
  * skipped): only the tokens of these pages are attended to.  lse: NULL, or
  * [rows][q_heads] fp32, the natural logarithm of the sum of exponentials (-inf
  * where a row sees nothing).  q and out must not overlap.  Rows that are no
- * sequence's are not written. */
+ * sequence's are not written.
+ * Accuracy: scores, weights and sums are fp32; on the tensor cores a weight
+ * times its value's step (or a weight and a value, and for more than 32 rows
+ * times query heads of a kv head also a key) enters with 11 bits, powers of two
+ * taken out: a channel is off by at most 2^-9 of the sum of weight times the
+ * largest value of the channel's group, beside its own rounding and what the
+ * keys' 11 bits do to the scores.  The values of a kv head's tokens may lie 2^60
+ * apart, seen or not, at any weights; within one token, groups of channels
+ * 2^16 (beyond, the smaller one loses bits). */
 moe_status moe_kv_attention(moe_kv_cache* kv, int layer, const moe_kv_batch* batch, const moe_kv_tensor* q,
                             int q_heads, float scale, int causal, const moe_kv_tensor* out, float* lse,
                             const int32_t* pages, int budget, void* stream);
@@ -460,7 +468,9 @@ moe_status moe_kv_attention(moe_kv_cache* kv, int layer, const moe_kv_batch* bat
  *     sum over d of max(qs[d] max[d], qs[d] min[d]),
  * qs the sum of the group's query heads (fp32, ascending), the products and
  * their sum in fp32, the sum by adjacent pairs level by level; ties go to the
- * lower page, a NaN score counts as -infinity.  pages_out [rows][kv_heads]
+ * lower page, a NaN score counts as -infinity.  (The sum is an upper bound of
+ * qs . k: heads that point opposite ways cancel in it, and a page that one of
+ * them alone needs is not favoured.)  pages_out [rows][kv_heads]
  * [budget]: page indices ascending, -1 after them where the row sees fewer.
  * keep_first + keep_last <= budget, keep_last >= 1; needs bounds. */
 moe_status moe_kv_select(moe_kv_cache* kv, int layer, const moe_kv_batch* batch, const moe_kv_tensor* q,

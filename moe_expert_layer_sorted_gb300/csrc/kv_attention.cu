@@ -8,10 +8,10 @@ using namespace moe;
 // once per 256 but turns every code into shared memory first.  Measured, both kernels, us
 // (8 kv heads of 128 channels, bf16; decode / prompt):
 //     columns                       16          32          64         128
-//     1 sequence of 2,048       14.5 / 24   14.7 / 25   21 / 25     23 / 25
-//     1 of 131,072                58 / 129   103 / 130  187 / 131   359 / 132
-//     16 of 4,096                 39 / 60     62 / 60   112 / 62    209 / 62
-//     64 of 2,048                 75 / 148   130 / 148  245 / 152   470 / 158
+//     1 sequence of 2,048       14.5 / 19   14.9 / 21   23 / 21     25 / 21
+//     1 of 131,072                61 / 115   106 / 115  193 / 115   369 / 117
+//     16 of 4,096                 41 / 60     66 / 60   117 / 60    219 / 62
+//     64 of 2,048                 80 / 135   138 / 135  260 / 137   498 / 143
 // so 32 is the last count that the decode kernel takes.  Rows with pages of their own have
 // no tiles to share and always go there.
 cudaError_t moe::kv_attention(Kv& kv, const KvAttnArgs& a, cudaStream_t s) {

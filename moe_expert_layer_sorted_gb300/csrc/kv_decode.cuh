@@ -39,12 +39,13 @@
 // not depend on timing.
 //
 // Measured (8 kv heads of 128 channels): 64 sequences of up to 8,191 tokens, 32
-// query heads, bf16, groups of 64: 88.6 us, 4.1 TB/s; 2 of 131,072, 64 query
-// heads, fp16, groups of 32: 80 us, 4.2 TB/s; one of 777: 10.4 us.  The fetch alone
-// takes 72 and 61 us, the bytes at the memory's rate and some 11 us of launch,
-// shares, first round, joins; the rest is the blocks' own work that the fetch does
-// not cover: some 330 instructions a block and warp, 56 and 64 % of the issue
-// slots, the integer pipe (the masks that make operands of codes) 47 and 41 %.
+// query heads, bf16, groups of 64: 92.5 us, 4.0 TB/s; 2 of 131,072, 64 query
+// heads, fp16, groups of 32: 82 us, 4.1 TB/s; one of 777: 11.4 us.  The fetch alone
+// takes 72 and 61 us: the bytes at the memory's rate (54 and 50) and launch, shares,
+// first round, joins; the rest is the blocks' own work that the fetch does not
+// cover: some 350 instructions a block and warp, 57 and 65 % of the issue slots,
+// the integer pipe (the masks that make operands of codes) 48 and 42 %.  Telling
+// sizes of values and scores apart where the reference rises costs 4 and 2 us of it.
 // Two blocks at once a warp, or the next block's scores early, need more than the
 // 104 registers that two CTAs per SM leave, and lose (104 and 105 us for the first).
 #pragma once

@@ -18,7 +18,7 @@
 // Rounding: k, v and P to fp16, in caches of both types, k and v from c + s (u - 8)
 // by one fma on exact operands; the sums are fp32.  (bf16's 2^-9 would be seen: in a
 // score of several hundred, and in P and v as much as in a bf16 output.  What is
-// left shows in an fp16 output only: 5.1e-4 of its norm at scores of a standard
+// left shows in an fp16 output only: 4.9e-4 of its norm at scores of a standard
 // deviation of 1.5, 4.5e-4 by the keys, where its own rounding is 2.1e-4.)  So that
 // nothing leaves fp16's range, powers of two are taken out and put back: of a query
 // row, to its largest element (back in the row's factor scale log2 e); of a token
@@ -40,14 +40,14 @@
 // the token.
 //
 // Measured (bf16, 32 query and 8 kv heads of 128 channels, groups of 64): 8,192
-// rows at the end of 16,384 tokens 1,160 us, 1,421 TFLOP/s, the tensor pipe busy
+// rows at the end of 16,384 tokens 1,170 us, 1,410 TFLOP/s, the tensor pipe busy
 // 61 % of the time.  Bound by the chain of one token tile, scores -> weights ->
 // product, of which two row tiles alternate: 1.8 us a token tile where the products
-// alone take 1.1; issue slots 54 %, exponents 31 %.  16 softmax warps, two threads
+// alone take 1.1; issue slots 55 %, exponents 31 %.  16 softmax warps, two threads
 // a row, have too few registers (1,780 us against 1,400 before other steps); halves
 // of 64 tokens, the next one's scores computed during the weights of one, need
 // products of N = 64 and twice the hand-overs (1,497 us).  Three ragged prompts of
-// up to 333 rows over up to 2,500 tokens (fp16, 12 heads of 64): 32 us, some ten
+// up to 333 rows over up to 2,500 tokens (fp16, 12 heads of 64): 33 us, some ten
 // token tiles one after the other, launch and join.
 #pragma once
 

@@ -15,8 +15,9 @@
 //
 // Measured, 16 rows of contexts up to 131,072 (pages of 64, 8 kv heads of 128
 // channels): scores 27 us for 104 MB of bounds, 3.8 TB/s, at 48 % of the issue
-// slots: every CTA starts with the chain length -> page numbers -> bounds and all
-// fit the SMs at once (16, 32 and 64 pages a CTA are within 1 us of each other);
+// slots: every CTA starts with the chain length -> page numbers -> bounds, and the
+// some 800 that have pages are just above the 760 that the SMs hold at once (16, 32
+// and 64 pages a CTA are within 1 us of each other);
 // choice 8 us, one CTA a row and head, a barrier a step of the bisection: latency.
 // One row of 6,001 tokens, with the attention over its 16 pages: 16.4 us.
 #include "kv_internal.h"

@@ -69,10 +69,12 @@ class KVCache:
       starts  None: tensors are [sequences, rows, heads, head_dim], the rows being the last
               tokens of each sequence.  int32 [sequences + 1]: tensors are [rows, heads,
               head_dim], rows starts[s] .. starts[s + 1] being sequence s's; max_new is then
-              the most rows of any sequence (None: all rows).
+              the most rows of any sequence (None: all rows; which kernel takes the call and how
+              it is cut goes by max_new, so it is worth giving).
     These are CUDA tensors and are read on the device only.  Row tensors may be strided
     (16-byte aligned rows and heads, contiguous channels).  Work goes to `stream` (None:
-    torch's current stream)."""
+    torch's current stream); where that is not the stream that torch allocated a tensor for, keeping
+    the tensor until the work is done is the caller's (Tensor.record_stream)."""
 
     def __init__(self, pages, *, page_size, head_dim, group_size=64, dtype=None, bounds=None):
         import torch
