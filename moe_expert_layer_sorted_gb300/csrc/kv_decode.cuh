@@ -563,7 +563,8 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
               acc[j][nt][2 + x] *= fo;
             }
           };
-          // values of ordinary size, within 2^16 of the limit (at first: within 2^12 of each other)?
+          // values of ordinary size, within 2^16 of the limit (at first: within 2^12 of each other), and
+          // no token without any?
           bool ordinary = !__any_sync(0xffffffffu, fmaxf(big[0], big[1]) > vlimit || fminf(big[0], big[1]) < vlimit * 0x1p-16f);
           float shift = 0.0f;
           int to = 0;
@@ -581,7 +582,8 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
               if (vlimit < 0.0f) to = (even ? hi_e : lo_e) - kDecAim;
               else if (even && (hi_e >= was.x + kDecRoom || hi_e < was.x + kDecAim - 8)) to = hi_e - kDecAim;
               to = min(max(to, max(max(was.y, hi_e) - kDecAim - 64, -60)), 115);
-              ordinary = vlimit < 0.0f && even && to == hi_e - kDecAim;
+              ordinary = vlimit < 0.0f && even && to == hi_e - kDecAim &&
+                         __all_sync(0xffffffffu, fminf(big[0], big[1]) > 0.0f);
               if (vlimit >= 0.0f) shift = (float)(was.x - to);
               vdown = pow2(-to);
               vlimit = pow2(min(to + kDecRoom, 127));

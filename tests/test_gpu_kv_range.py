@@ -132,3 +132,21 @@ def test_groups_of_channels_far_apart(D, G, P, dtype, n):
     for i, v in enumerate(w.v):
         v[:: 1 if i else 7, :, :G] = times(v[:: 1 if i else 7, :, :G], 2.0 ** -16, dtype)
     run(w.fill(), n)
+
+
+@pytest.mark.parametrize("D,G,P,dtype", SHAPES)
+@pytest.mark.parametrize("n", [1, 3, 40])
+@pytest.mark.parametrize("above", [20, 27, 34])
+def test_all_the_weight_on_tokens_without_values(D, G, P, dtype, n, above):
+    """Half of the tokens have no values, one of them scores `above` more than any other token;
+    what the others weigh, down to 2^-50, carries the result."""
+    w = World(D, G, P, dtype, 2, [n + 3, n + 17, 200, 1000], seed=n + above)
+    q = (0.3 * w.rand(4, n, 8, D).float()).to(dtype)
+    q[..., 0] = 8.0
+    for k, v in zip(w.k, w.v):
+        k[:, :, 0] *= 0.1
+        k[len(k) // 3, :, 0] = above * math.sqrt(D) / 8
+        v[torch.arange(len(v), device="cuda") % 2 == len(v) // 3 % 2] = 0
+        if dtype == FP:  # so that the results are above fp16's smallest
+            v.copy_(times(v, 2.0 ** 12, dtype))
+    run(w.fill(), n, q)
