@@ -457,8 +457,9 @@ moe_status moe_kv_read(moe_kv_cache* kv, int layer, const moe_kv_batch* batch, c
  * taken out: a channel is off by at most 2^-9 of the sum of weight times the
  * largest value of the channel's group, beside its own rounding and what the
  * keys' 11 bits do to the scores.  The values of a kv head's tokens may lie 2^60
- * apart, seen or not, at any weights; within one token, groups of channels
- * 2^16 (beyond, the smaller one loses bits). */
+ * apart, seen or not, and tokens that weigh 2^-60 of a row's most still make up
+ * its result where the others have no values; within one token, groups of
+ * channels may lie 2^16 apart.  Beyond that what is smaller loses bits. */
 moe_status moe_kv_attention(moe_kv_cache* kv, int layer, const moe_kv_batch* batch, const moe_kv_tensor* q,
                             int q_heads, float scale, int causal, const moe_kv_tensor* out, float* lse,
                             const int32_t* pages, int budget, void* stream);
