@@ -44,3 +44,23 @@ def test_per_thread_default_streams_of_two_threads():
     torch.cuda.synchronize()
     assert not errors
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_calls_on_other_streams_beside_a_capture():
+    """Asking for a stream's identity does not end the capture of another."""
+    a, b = (World(128, 64, 64, BF, 2, [3000], seed=s).fill() for s in (4, 5))
+    q = a.rand(1, 1, 16, 128)
+    want, outs = [torch.empty_like(q) for _ in "ab"], [torch.zeros_like(q) for _ in "abcd"]
+    for w, o in zip((a, b), want):
+        w.cache.attention(q, o, **w.batch)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        a.cache.attention(q, outs[0], **a.batch)
+        for s, o in zip(streams, outs[1:]):
+            b.cache.attention(q, o, stream=s, **b.batch)
+    g.replay()
+    torch.cuda.synchronize()
+    b.cache.attention(q, outs[3], **b.batch)
+    assert torch.equal(outs[0], want[0]) and all(torch.equal(o, want[1]) for o in outs[1:])
