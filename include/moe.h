@@ -480,6 +480,103 @@ moe_status moe_kv_select(moe_kv_cache* kv, int layer, const moe_kv_batch* batch,
 /* Last error text of `kv` (or of the last call that had no handle, for NULL). */
 const char* moe_kv_last_error(const moe_kv_cache* kv);
 
+/* ------------------------------------------------------------------ 8-bit key/value cache
+ *
+ * The same attention over keys and values in 8 bits, for models whose answers
+ * suffer at 4, with what keeps the KV that stays in VRAM ("763B MoE in two 96 GB
+ * cards", KV side-box of section "Where the VRAM gap comes from") at a budget: the
+ * weight that attention has given to every token, and the eviction of those that
+ * got least.  moe_kv_batch and moe_kv_tensor are as above.
+ *
+ * Caller-owned device memory:
+ *   pages   [layer][page][kv head][page_size / 16 blocks][32 D + 16 bytes]; a block
+ *           of 16 tokens is K codes [16][D] | V codes [8 token pairs][D][2] | params
+ *           (order of the codes: csrc/kv8_common.cuh).  A stored value is s u, u in
+ *           -127..127, s one fp32 step for the block's keys and one for its values:
+ *           s = rn(max |x| / 127), u = x / s to the nearest whole number (ties to
+ *           even; no rounding before that).  A token and head whose keys (values)
+ *           hold an infinity or a NaN reads as NaN in all channels of its keys
+ *           (values) and has no part in s.
+ *   mass    [layer][page][kv head][page_size] fp32, or NULL: the weight of each
+ *           token, which moe_kv8_append sets to 0, an attention with `weigh` adds to
+ *           and moe_kv8_evict goes by. */
+typedef struct moe_kv8_cache moe_kv8_cache;
+
+typedef struct moe_kv8_desc {
+  uint32_t struct_size; /* sizeof(moe_kv8_desc) */
+  int32_t device;       /* CUDA device ordinal */
+  int32_t dtype;        /* moe_kv_dtype: keys, values, queries and outputs */
+  int32_t num_layers;   /* >= 1 */
+  int32_t kv_heads;     /* 1..1024 */
+  int32_t head_dim;     /* D: 64 or 128 */
+  int32_t page_size;    /* tokens per page: 16, 32, 64, 128 or 256 */
+  int32_t reserved0;    /* must be zero */
+  int64_t num_pages;    /* 1 .. 2^31 - 1 */
+  void* pages;          /* 16-byte aligned device memory */
+  float* mass;          /* 16-byte aligned device memory, or NULL */
+  int64_t reserved[2];  /* must be zero */
+} moe_kv8_desc;
+
+/* Bytes of one layer's pages and mass for desc (pages and mass not read). */
+moe_status moe_kv8_sizes(const moe_kv8_desc* desc, int64_t* page_bytes_per_layer, int64_t* mass_bytes_per_layer);
+
+/* As moe_kv_create, moe_kv_destroy, moe_kv_status and
+ * moe_kv_debug_fail_next_attention (a workspace of 24 MB). */
+moe_status moe_kv8_create(const moe_kv8_desc* desc, moe_kv8_cache** out);
+moe_status moe_kv8_destroy(moe_kv8_cache* kv);
+moe_status moe_kv8_status(moe_kv8_cache* kv);
+moe_status moe_kv8_debug_fail_next_attention(moe_kv8_cache* kv);
+
+/* Quantise the rows k, v into the pages of `layer`; with mass, set theirs to 0.
+ * Where a sequence's first row falls into a block that holds older tokens of it, the
+ * block's step becomes the larger of the old one and the rows', and if it grew the
+ * older codes are turned: u s_old / s to the nearest whole number.  (So what is
+ * stored depends on how the tokens were grouped into calls, by a step at most for
+ * every time that it grew.)  Pages written to must not be shared between the
+ * sequences of a call. */
+moe_status moe_kv8_append(moe_kv8_cache* kv, int layer, const moe_kv_batch* batch, const moe_kv_tensor* k,
+                          const moe_kv_tensor* v, void* stream);
+
+/* The stored values of the rows, rounded to the cache's type. */
+moe_status moe_kv8_read(moe_kv8_cache* kv, int layer, const moe_kv_batch* batch, const moe_kv_tensor* k,
+                        const moe_kv_tensor* v, void* stream);
+
+/* Attention as moe_kv_attention without chosen pages (head h reads kv head
+ * h / (q_heads / kv_heads), causal, lse, rows that see nothing).  A row that sees a
+ * token of NaN keys or values is NaN.  weigh = 1: after it, every token's softmax
+ * weights of this call, summed over the rows and query heads that see it (in fp32,
+ * in an order that does not depend on timing), are added to its mass; needs mass and lse.  Rows whose lse is
+ * not finite add nothing.
+ * Accuracy: scores, weights and sums are fp32 and the codes are exact operands; a weight enters the
+ * product with the values with 11 bits, relative to the largest weight times step of its row (below 2^-24 of
+ * that it loses bits).  For more than 32 rows times query heads of a kv head the values'
+ * steps of 128 tokens may lie 2^40 apart; beyond that what is smaller loses bits. */
+moe_status moe_kv8_attention(moe_kv8_cache* kv, int layer, const moe_kv_batch* batch, const moe_kv_tensor* q,
+                             int q_heads, float scale, int causal, const moe_kv_tensor* out, float* lse, int weigh,
+                             void* stream);
+
+/* Bring every sequence of the batch that holds more than `budget` tokens back to
+ * that many: of each kv head stay the first keep_first tokens, the last keep_last,
+ * and of the others those of the largest mass (ties go to the lower position; NaN
+ * and tokens in no page count below everything), in their order.  They move to
+ * positions 0 .. budget - 1 of the sequence's pages, their mass with them; a block
+ * of moved tokens gets the largest of their steps, and a code of a smaller step is
+ * turned: u s_old / s to the nearest whole number.  Heads keep different tokens, so
+ * a position then names other tokens in each head; attention does not mind, since
+ * what a row sees goes by order alone.  The rest of the last block is zeros, what
+ * lies beyond stays as it is.  The sequence's length is then min(len, budget): lens
+ * is not written (layers share it), that is the caller's to set when all layers are
+ * done.  kept [batch][kv_heads][budget] int32 (device): the positions that stayed,
+ * ascending, -1 after them where a sequence held fewer (such a sequence is not
+ * touched).  batch's rows, max_new and starts are not used; rows must be batch * max_new
+ * without starts all the same.  Pages must not be shared between sequences.  keep_first + keep_last <=
+ * budget. */
+moe_status moe_kv8_evict(moe_kv8_cache* kv, int layer, const moe_kv_batch* batch, int budget, int keep_first,
+                         int keep_last, int32_t* kept, void* stream);
+
+/* Last error text of `kv` (or of the last call that had no handle, for NULL). */
+const char* moe_kv8_last_error(const moe_kv8_cache* kv);
+
 const char* moe_status_string(moe_status s);
 /* Last error text of `plan` (or of the last call that had no plan, for NULL). */
 const char* moe_last_error(const moe_plan* plan);

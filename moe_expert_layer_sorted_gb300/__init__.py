@@ -14,7 +14,9 @@ import os
 import numpy as np
 
 from . import kv as _kv
+from . import kv8 as _kv8
 from .kv import KVCache
+from .kv8 import KVCache8
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoe_gb300.so")
@@ -34,7 +36,9 @@ EXPORTS = ["moe_plan_create", "moe_plan_destroy", "moe_set_router", "moe_update_
            "moe_cache_stats", "moe_residence_table", "moe_quantize", "moe_probe_bandwidth",
            "moe_route_noalloc", "moe_status_string", "moe_last_error",
            "moe_kv_sizes", "moe_kv_create", "moe_kv_destroy", "moe_kv_append", "moe_kv_read", "moe_kv_attention",
-           "moe_kv_select", "moe_kv_status", "moe_kv_debug_fail_next_attention", "moe_kv_last_error"]
+           "moe_kv_select", "moe_kv_status", "moe_kv_debug_fail_next_attention", "moe_kv_last_error",
+           "moe_kv8_sizes", "moe_kv8_create", "moe_kv8_destroy", "moe_kv8_append", "moe_kv8_read", "moe_kv8_attention",
+           "moe_kv8_evict", "moe_kv8_status", "moe_kv8_debug_fail_next_attention", "moe_kv8_last_error"]
 
 _P = ctypes.c_void_p
 
@@ -107,6 +111,7 @@ def lib():
         L.moe_last_error.restype = ctypes.c_char_p
         L.moe_last_error.argtypes = [_P]
         _kv.declare(L)
+        _kv8.declare(L)
         _lib = L
     return _lib
 

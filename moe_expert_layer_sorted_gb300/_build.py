@@ -1,5 +1,5 @@
 """Build of the CUDA library (sm_103a only): one nvcc per translation unit, in
-parallel, then one shared-library link, and of the key/value cache's Python
+parallel, then one shared-library link, and of the key/value caches' Python
 binding where torch is installed.  Output: libmoe_gb300.so and _kv_binding.so in
 moe_expert_layer_sorted_gb300/ (git-ignored, rebuilt per box)."""
 from __future__ import annotations
@@ -20,7 +20,9 @@ LIB = os.path.join(PKG, "libmoe_gb300.so")
 BINDING = os.path.join(PKG, "_kv_binding.so")
 SOURCES = ["plan.cu", "decode.cu", "prefill.cu", "cache.cu", "noalloc.cu", "kv.cu", "kv_append.cu",
            "kv_attention.cu", "kv_select.cu", "kv_decode_bf16.cu", "kv_decode_f16.cu",
-           "kv_prompt_bf16.cu", "kv_prompt_f16.cu"]
+           "kv_prompt_bf16.cu", "kv_prompt_f16.cu",
+           "kv8.cu", "kv8_append.cu", "kv8_attention.cu", "kv8_decode_bf16.cu", "kv8_decode_f16.cu",
+           "kv8_weigh.cu", "kv8_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

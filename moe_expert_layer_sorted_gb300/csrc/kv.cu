@@ -8,40 +8,7 @@ using namespace moe;
 
 namespace {
 
-thread_local std::string g_kv_error;
-
-moe_status fail(Kv* kv, moe_status s, const char* msg) {
-  (kv ? kv->last_error : g_kv_error) = msg;
-  return s;
-}
-moe_status cuda_fail(Kv* kv, cudaError_t e, const char* what) {
-  (kv ? kv->last_error : g_kv_error) = std::string(what) + ": " + cudaGetErrorString(e);
-  return e == cudaErrorMemoryAllocation ? MOE_ERR_OOM : MOE_ERR_CUDA;
-}
-
-struct DeviceScope {  // makes `dev` current for a call and restores the caller's device
-  int prev = -1;
-  bool ok = true;
-  explicit DeviceScope(int dev) {
-    if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-    if (prev != dev) ok = cudaSetDevice(dev) == cudaSuccess;
-    else prev = -1;  // nothing to restore
-  }
-  ~DeviceScope() {
-    if (prev >= 0) cudaSetDevice(prev);
-  }
-};
-
-struct Busy {  // one call at a time per handle
-  Kv* kv;
-  bool ok;
-  explicit Busy(Kv* k) : kv(k), ok(k->busy.exchange(1) == 0) {}
-  ~Busy() {
-    if (ok) kv->busy.store(0);
-  }
-};
-
-bool aligned16(const void* p) { return !(reinterpret_cast<uintptr_t>(p) & 15); }
+#include "kv_entry.h"
 
 const char* check_desc(const moe_kv_desc* d) {
   if (!d) return "desc is NULL";
@@ -68,25 +35,6 @@ void set_sizes(Kv* kv) {
   kv->bounds_layer = (int64_t)d.num_pages * d.kv_heads * 2 * d.head_dim;
 }
 
-const char* check_batch(const Kv* kv, int layer, const moe_kv_batch* b) {
-  if (layer < 0 || layer >= kv->d.num_layers) return "bad layer";
-  if (!b || b->struct_size != sizeof(moe_kv_batch)) return "batch is NULL or its struct_size is not sizeof(moe_kv_batch)";
-  if (b->batch < 0 || b->max_new < 0) return "batch and max_new must be >= 0";
-  if (b->table_pages < 1 || b->table_stride < b->table_pages) return "table_pages must be >= 1 and table_stride >= table_pages";
-  if (b->rows < 0 || (!b->starts && b->rows != (int64_t)b->batch * b->max_new)) return "rows must be batch * max_new without starts";
-  if (b->batch > 0 && (!b->table || !b->lens)) return "table or lens is NULL";
-  return nullptr;
-}
-
-const char* check_tensor(const moe_kv_tensor* t) {
-  if (!t || !t->data) return "a tensor is NULL";
-  if (!aligned16(t->data)) return "tensors must be 16-byte aligned";
-  if ((t->batch_stride | t->row_stride | t->head_stride) & 7) return "strides must be multiples of 8 elements";
-  return nullptr;
-}
-
-bool empty(const moe_kv_batch* b) { return b->batch == 0 || b->max_new == 0 || b->rows == 0; }
-
 KvView view(const Kv* kv, int layer) {
   const moe_kv_desc& d = kv->d;
   KvView c;
@@ -100,35 +48,6 @@ KvView view(const Kv* kv, int layer) {
   c.heads = d.kv_heads;
   return c;
 }
-KvBatch batch_of(const moe_kv_batch* b) {
-  return {b->table, b->lens, b->starts, b->table_stride, b->rows, b->batch, b->table_pages, b->max_new};
-}
-KvRows rows_of(const moe_kv_tensor* t) { return {t->batch_stride, t->row_stride, t->head_stride}; }
-
-// Calls that share the workspace follow one another across streams; inside a
-// capture the graph's own edges order its nodes.  A stream may be gone by the
-// next call, so its work is recorded at once, but for the default stream, which
-// stays and is never captured: that one is recorded when another stream follows.
-struct Order {
-  bool capturing = false;
-  unsigned long long stream = 0;
-};
-cudaError_t order_before(Kv* kv, cudaStream_t s, Order& o) {
-  cudaError_t e = stream_identity(s, o.capturing, o.stream);
-  if (e != cudaSuccess || o.capturing || !kv->have_last || kv->last_stream == o.stream) return e;
-  if (kv->last_stream == kDefaultStream && (e = cudaEventRecord(kv->ev_done, nullptr)) != cudaSuccess) return e;
-  return cudaStreamWaitEvent(s, kv->ev_done, 0);
-}
-cudaError_t order_after(Kv* kv, cudaStream_t s, const Order& o) {
-  if (o.capturing) return cudaSuccess;
-  const cudaError_t e = o.stream != kDefaultStream ? cudaEventRecord(kv->ev_done, s) : cudaSuccess;
-  if (e == cudaSuccess) {
-    kv->last_stream = o.stream;
-    kv->have_last = true;
-  }
-  return e;
-}
-
 void release(Kv* kv) {
   if (kv->ws) cudaFree(kv->ws);
   if (kv->err_host) cudaFreeHost(const_cast<uint32_t*>(kv->err_host));
@@ -136,48 +55,12 @@ void release(Kv* kv) {
   delete kv;
 }
 
-// Runs f with no C++ exception leaving the library.
-template <typename F>
-moe_status guarded(F&& f) noexcept {
-  try {
-    return f();
-  } catch (...) {
-    return MOE_ERR_OOM;  // the only exceptions here are failed host allocations
-  }
-}
-
-// Whether a kernel's bounded wait gave up since this was last asked (for every wait of a launch
-// counts its own CTA's state alone, nothing on the device needs to be put right).
-bool take_timeout(Kv* kv) {
-  if (!*kv->err_host) return false;
-  *kv->err_host = 0;
-  return true;
-}
-constexpr char kTimeoutMsg[] =
-    "a bounded wait of an attention gave up: results of the calls since the last one that was reported as done are suspect; "
-    "this call did nothing";
-
-// The frame of a call on a handle: one at a time, its device current, no timeout unreported.
-template <typename F>
-moe_status on_handle(moe_kv_cache* h, F&& f) noexcept {
-  return guarded([&]() -> moe_status {
-    Kv* kv = reinterpret_cast<Kv*>(h);
-    if (!kv) return fail(nullptr, MOE_ERR_INVALID, "handle is NULL");
-    Busy busy(kv);
-    if (!busy.ok) return MOE_ERR_STATE;  // the text is the other thread's to write
-    DeviceScope ds(kv->d.device);
-    if (!ds.ok) return fail(kv, MOE_ERR_CUDA, "cudaSetDevice failed");
-    if (take_timeout(kv)) return fail(kv, MOE_ERR_TIMEOUT, kTimeoutMsg);
-    return f(kv);
-  });
-}
-
 }  // namespace
 
 extern "C" moe_status moe_kv_sizes(const moe_kv_desc* desc, int64_t* pages, int64_t* bounds) {
   return guarded([&]() -> moe_status {
     const char* why = check_desc(desc);
-    if (why) return fail(nullptr, MOE_ERR_INVALID, why);
+    if (why) return fail<Kv>(nullptr, MOE_ERR_INVALID, why);
     Kv kv;
     kv.d = *desc;
     set_sizes(&kv);
@@ -189,23 +72,23 @@ extern "C" moe_status moe_kv_sizes(const moe_kv_desc* desc, int64_t* pages, int6
 
 extern "C" moe_status moe_kv_create(const moe_kv_desc* desc, moe_kv_cache** out) {
   return guarded([&]() -> moe_status {
-    if (!out) return fail(nullptr, MOE_ERR_INVALID, "out is NULL");
+    if (!out) return fail<Kv>(nullptr, MOE_ERR_INVALID, "out is NULL");
     *out = nullptr;
     const char* why = check_desc(desc);
     if (!why && !desc->pages) why = "pages is NULL";
     if (!why && (!aligned16(desc->pages) || !aligned16(desc->bounds))) why = "pages and bounds must be 16-byte aligned";
-    if (why) return fail(nullptr, MOE_ERR_INVALID, why);
+    if (why) return fail<Kv>(nullptr, MOE_ERR_INVALID, why);
     int ndev = 0;
     if (cudaGetDeviceCount(&ndev) != cudaSuccess || desc->device < 0 || desc->device >= ndev) {
       cudaGetLastError();
-      return fail(nullptr, MOE_ERR_INVALID, "no such CUDA device");
+      return fail<Kv>(nullptr, MOE_ERR_INVALID, "no such CUDA device");
     }
     DeviceScope ds(desc->device);
-    if (!ds.ok) return fail(nullptr, MOE_ERR_CUDA, "cudaSetDevice failed");
+    if (!ds.ok) return fail<Kv>(nullptr, MOE_ERR_CUDA, "cudaSetDevice failed");
     int major = 0, minor = 0;
     cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, desc->device);
     cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, desc->device);
-    if (major != 10 || minor != 3) return fail(nullptr, MOE_ERR_UNSUPPORTED, "the library targets sm_103a (GB300) only");
+    if (major != 10 || minor != 3) return fail<Kv>(nullptr, MOE_ERR_UNSUPPORTED, "the library targets sm_103a (GB300) only");
     Kv* kv = new Kv();
     kv->d = *desc;
     set_sizes(kv);
@@ -224,7 +107,7 @@ extern "C" moe_status moe_kv_create(const moe_kv_desc* desc, moe_kv_cache** out)
     if (e != cudaSuccess) {
       cudaGetLastError();
       release(kv);
-      return cuda_fail(nullptr, e, "key/value cache workspace");
+      return cuda_fail<Kv>(nullptr, e, "key/value cache workspace");
     }
     *out = reinterpret_cast<moe_kv_cache*>(kv);
     return MOE_OK;
@@ -234,24 +117,24 @@ extern "C" moe_status moe_kv_create(const moe_kv_desc* desc, moe_kv_cache** out)
 extern "C" moe_status moe_kv_destroy(moe_kv_cache* h) {
   return guarded([&]() -> moe_status {
     Kv* kv = reinterpret_cast<Kv*>(h);
-    if (!kv) return fail(nullptr, MOE_ERR_INVALID, "handle is NULL");
+    if (!kv) return fail<Kv>(nullptr, MOE_ERR_INVALID, "handle is NULL");
     if (kv->busy.exchange(1)) return MOE_ERR_STATE;  // another call is running: stays as it is
     DeviceScope ds(kv->d.device);
     if (kv->have_last && (kv->last_stream != kDefaultStream || cudaEventRecord(kv->ev_done, nullptr) == cudaSuccess))
       cudaEventSynchronize(kv->ev_done);
     const bool late = take_timeout(kv);
     release(kv);
-    return late ? fail(nullptr, MOE_ERR_TIMEOUT, "a bounded wait of an attention gave up: the last results are suspect; the handle is gone")
+    return late ? fail<Kv>(nullptr, MOE_ERR_TIMEOUT, "a bounded wait of an attention gave up: the last results are suspect; the handle is gone")
                 : MOE_OK;
   });
 }
 
 extern "C" moe_status moe_kv_status(moe_kv_cache* h) {
-  return on_handle(h, [](Kv*) { return MOE_OK; });
+  return on_handle<Kv>(h, [](Kv*) { return MOE_OK; });
 }
 
 extern "C" moe_status moe_kv_debug_fail_next_attention(moe_kv_cache* h) {
-  return on_handle(h, [](Kv* kv) {
+  return on_handle<Kv>(h, [](Kv* kv) {
     kv->fail_next = true;
     return MOE_OK;
   });
@@ -259,8 +142,8 @@ extern "C" moe_status moe_kv_debug_fail_next_attention(moe_kv_cache* h) {
 
 extern "C" moe_status moe_kv_append(moe_kv_cache* h, int layer, const moe_kv_batch* batch, const moe_kv_tensor* k,
                                     const moe_kv_tensor* v, void* stream) {
-  return on_handle(h, [&](Kv* kv) -> moe_status {
-    const char* why = check_batch(kv, layer, batch);
+  return on_handle<Kv>(h, [&](Kv* kv) -> moe_status {
+    const char* why = check_batch(kv->d.num_layers, layer, batch);
     if (why) return fail(kv, MOE_ERR_INVALID, why);
     if (empty(batch)) return MOE_OK;
     if ((why = check_tensor(k)) || (why = check_tensor(v))) return fail(kv, MOE_ERR_INVALID, why);
@@ -273,8 +156,8 @@ extern "C" moe_status moe_kv_append(moe_kv_cache* h, int layer, const moe_kv_bat
 
 extern "C" moe_status moe_kv_read(moe_kv_cache* h, int layer, const moe_kv_batch* batch, const moe_kv_tensor* k,
                                   const moe_kv_tensor* v, void* stream) {
-  return on_handle(h, [&](Kv* kv) -> moe_status {
-    const char* why = check_batch(kv, layer, batch);
+  return on_handle<Kv>(h, [&](Kv* kv) -> moe_status {
+    const char* why = check_batch(kv->d.num_layers, layer, batch);
     if (why) return fail(kv, MOE_ERR_INVALID, why);
     if (empty(batch)) return MOE_OK;
     if ((why = check_tensor(k)) || (why = check_tensor(v))) return fail(kv, MOE_ERR_INVALID, why);
@@ -287,8 +170,8 @@ extern "C" moe_status moe_kv_read(moe_kv_cache* h, int layer, const moe_kv_batch
 extern "C" moe_status moe_kv_attention(moe_kv_cache* h, int layer, const moe_kv_batch* batch, const moe_kv_tensor* q,
                                        int q_heads, float scale, int causal, const moe_kv_tensor* out, float* lse,
                                        const int32_t* pages, int budget, void* stream) {
-  return on_handle(h, [&](Kv* kv) -> moe_status {
-    const char* why = check_batch(kv, layer, batch);
+  return on_handle<Kv>(h, [&](Kv* kv) -> moe_status {
+    const char* why = check_batch(kv->d.num_layers, layer, batch);
     if (!why && (q_heads < 1 || q_heads % kv->d.kv_heads)) why = "q_heads must be a positive multiple of kv_heads";
     if (!why && (causal != 0 && causal != 1)) why = "causal must be 0 or 1";
     if (!why && pages && budget < 1) why = "budget must be >= 1 with pages";
@@ -315,8 +198,8 @@ extern "C" moe_status moe_kv_attention(moe_kv_cache* h, int layer, const moe_kv_
 extern "C" moe_status moe_kv_select(moe_kv_cache* h, int layer, const moe_kv_batch* batch, const moe_kv_tensor* q,
                                     int q_heads, int budget, int keep_first, int keep_last, int32_t* pages_out,
                                     void* stream) {
-  return on_handle(h, [&](Kv* kv) -> moe_status {
-    const char* why = check_batch(kv, layer, batch);
+  return on_handle<Kv>(h, [&](Kv* kv) -> moe_status {
+    const char* why = check_batch(kv->d.num_layers, layer, batch);
     if (!why && (q_heads < 1 || q_heads % kv->d.kv_heads)) why = "q_heads must be a positive multiple of kv_heads";
     if (!why && (budget < 1 || keep_first < 0 || keep_last < 1 || (int64_t)keep_first + keep_last > budget))
       why = "budget must hold keep_first >= 0 and keep_last >= 1 pages";

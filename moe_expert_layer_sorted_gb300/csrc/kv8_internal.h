@@ -1,0 +1,63 @@
+// The 8-bit key/value cache's handle and the launchers of its kernels.
+#pragma once
+
+#include "kv8_common.cuh"
+#include "kv_internal.h"
+
+namespace moe {
+
+struct Kv8 {
+  moe_kv8_desc d{};
+  int sms = 0;
+  int64_t block_bytes = 0, head_bytes = 0, page_bytes = 0, layer_bytes = 0, mass_layer = 0;  // mass_layer: elements
+  // workspace: partial results of attention items that are cut between CTAs; their counters, zero between calls
+  uint8_t* ws = nullptr;
+  static constexpr size_t kPartsBytes = size_t(24) << 20;
+  static constexpr int kCounters = 1024;
+  static constexpr size_t kCounterBytes = kCounters * sizeof(unsigned);
+  static constexpr size_t kWorkspace = kPartsBytes + kCounterBytes;
+  float* parts() const { return reinterpret_cast<float*>(ws); }
+  unsigned* counters() const { return reinterpret_cast<unsigned*>(ws + kPartsBytes); }
+  volatile uint32_t* err_host = nullptr;  // mapped pinned word: set by a kernel whose bounded wait gave up
+  uint32_t* err_dev = nullptr;
+  bool fail_next = false;         // test hook: a wait of the next attention runs out
+  cudaEvent_t ev_done = nullptr;  // end of the last call that used the workspace
+  unsigned long long last_stream = 0;  // its identity
+  bool have_last = false;
+  std::atomic<int> busy{0};
+  std::string last_error;
+};
+
+struct Kv8EvictArgs {
+  KvView c;
+  KvBatch b;      // max_new, rows and starts are not used
+  float* mass;    // the layer's
+  int budget, first, last;
+  int32_t* kept;  // [batch][heads][budget]
+};
+
+// mass: the layer's, or nullptr
+cudaError_t kv8_append(const Kv8& kv, const KvView& c, const KvBatch& b, const uint16_t* k, const KvRows& ks,
+                       const uint16_t* v, const KvRows& vs, float* mass, cudaStream_t s);
+cudaError_t kv8_read(const Kv8& kv, const KvView& c, const KvBatch& b, uint16_t* k, const KvRows& ks, uint16_t* v,
+                     const KvRows& vs, cudaStream_t s);
+cudaError_t kv8_decode_bf16(Kv8& kv, const KvAttnArgs& a, cudaStream_t s);
+cudaError_t kv8_decode_f16(Kv8& kv, const KvAttnArgs& a, cudaStream_t s);
+cudaError_t kv8_attention(Kv8& kv, const KvAttnArgs& a, cudaStream_t s);
+// Adds the weights of a's rows, whose lse the attention has written, to the layer's mass.
+cudaError_t kv8_weigh(Kv8& kv, const KvAttnArgs& a, float* mass, cudaStream_t s);
+cudaError_t kv8_evict(const Kv8& kv, const Kv8EvictArgs& a, cudaStream_t s);
+
+// Calls f with (T, D) of the cache as compile-time constants.
+#define KV8_DISPATCH(desc, ...)                                     \
+  do {                                                              \
+    auto run_ = [&](auto tag_) {                                    \
+      using T = decltype(tag_);                                     \
+      if ((desc).head_dim == 64) { constexpr int D = 64; __VA_ARGS__ } \
+      else { constexpr int D = 128; __VA_ARGS__ }                   \
+    };                                                              \
+    if ((desc).dtype == MOE_KV_BF16) run_(__nv_bfloat16());         \
+    else run_(__half());                                            \
+  } while (0)
+
+}  // namespace moe

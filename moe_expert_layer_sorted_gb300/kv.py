@@ -54,7 +54,53 @@ def _desc(dtype, num_layers, kv_heads, head_dim, group_size, page_size, num_page
     return d
 
 
-class KVCache:
+class Handle:
+    """What the key/value caches share: self._h, the library's handle, self._c, the binding's
+    object over it, and self._destroy, which frees a handle that has none."""
+
+    _h = _c = None
+
+    def close(self):
+        """Frees the handle.  MoeError with MOE_ERR_STATE: a call of another thread is running, and the
+        cache stays as it is; with MOE_ERR_TIMEOUT: see `check`, and the cache is closed."""
+        from . import MoeError
+        try:
+            if self._c is not None:
+                self._c.close()
+            elif self._h:
+                self._destroy(self._h)
+        except MoeError as e:
+            if e.status == 5:  # MOE_ERR_STATE
+                raise
+            self._h = None
+            raise
+        self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def check(self):
+        """Raises MoeError (MOE_ERR_TIMEOUT) where a bounded wait on the device gave up, in a call
+        or in a replayed graph that holds one; after a synchronisation."""
+        self._c.check()
+
+    def debug_fail_next_attention(self):
+        """Test hook: a wait of the next attention runs out (see moe.h)."""
+        self._c.debug_fail_next_attention()
+
+    def append(self, k, v, *, table, lens, starts=None, max_new=None, layer=0, stream=None):
+        """Quantise the rows k, v into the sequences' pages."""
+        self._c.append(k, v, table, lens, starts, max_new, layer, stream)
+
+    def read(self, k, v, *, table, lens, starts=None, max_new=None, layer=0, stream=None):
+        """The stored keys and values of the rows, into k and v."""
+        self._c.read(k, v, table, lens, starts, max_new, layer, stream)
+
+
+class KVCache(Handle):
     """A paged key/value cache in 4 bits for `num_layers` layers, with what writes it,
     reads it, attends over it and chooses its pages.
 
@@ -79,8 +125,8 @@ class KVCache:
     def __init__(self, pages, *, page_size, head_dim, group_size=64, dtype=None, bounds=None):
         import torch
         from . import MoeError, _kv_binding
-        self._h = self._c = None
         self._lib = _lib()
+        self._destroy = self._lib.moe_kv_destroy
         dtype = torch.bfloat16 if dtype is None else dtype
         if not (pages.is_cuda and pages.dtype == torch.uint8 and pages.dim() in (4, 5) and pages.is_contiguous()):
             _bad("pages: contiguous uint8 CUDA tensor [layers,] num_pages, kv_heads, blocks, block bytes")
@@ -125,46 +171,7 @@ class KVCache:
         ends = torch.zeros(shape + (2, head_dim), dtype=dtype, device=device) if bounds else None
         return cls(pages, page_size=page_size, head_dim=head_dim, group_size=group_size, dtype=dtype, bounds=ends)
 
-    def close(self):
-        """Frees the handle.  MoeError with MOE_ERR_STATE: a call of another thread is running, and the
-        cache stays as it is; with MOE_ERR_TIMEOUT: see `check`, and the cache is closed."""
-        from . import MoeError
-        try:
-            if self._c is not None:
-                self._c.close()
-            elif self._h:
-                self._lib.moe_kv_destroy(self._h)
-        except MoeError as e:
-            if e.status == 5:  # MOE_ERR_STATE
-                raise
-            self._h = None
-            raise
-        self._h = None
-
-    def __del__(self):
-        try:
-            self.close()
-        except Exception:
-            pass
-
-    def check(self):
-        """Raises MoeError (MOE_ERR_TIMEOUT) where a bounded wait on the device gave up, in a call
-        or in a replayed graph that holds one; after a synchronisation."""
-        self._c.check()
-
-    def debug_fail_next_attention(self):
-        """Test hook: a wait of the next attention runs out (see moe.h)."""
-        self._c.debug_fail_next_attention()
-
     # The tensors are checked and unpacked in csrc/kv_binding.cpp.
-
-    def append(self, k, v, *, table, lens, starts=None, max_new=None, layer=0, stream=None):
-        """Quantise the rows k, v into the sequences' pages and update the pages' bounds."""
-        self._c.append(k, v, table, lens, starts, max_new, layer, stream)
-
-    def read(self, k, v, *, table, lens, starts=None, max_new=None, layer=0, stream=None):
-        """The stored keys and values of the rows, into k and v."""
-        self._c.read(k, v, table, lens, starts, max_new, layer, stream)
 
     def attention(self, q, out, *, table, lens, starts=None, max_new=None, scale=None, causal=True, lse=None,
                   pages=None, layer=0, stream=None):
