@@ -549,8 +549,7 @@ moe_status moe_kv8_read(moe_kv8_cache* kv, int layer, const moe_kv_batch* batch,
  * not finite add nothing.
  * Accuracy: scores, weights and sums are fp32 and the codes are exact operands; a weight enters the
  * product with the values with 11 bits, relative to the largest weight times step of its row (below 2^-24 of
- * that it loses bits).  For more than 32 rows times query heads of a kv head the values'
- * steps of 128 tokens may lie 2^40 apart; beyond that what is smaller loses bits. */
+ * that it loses bits). */
 moe_status moe_kv8_attention(moe_kv8_cache* kv, int layer, const moe_kv_batch* batch, const moe_kv_tensor* q,
                              int q_heads, float scale, int causal, const moe_kv_tensor* out, float* lse, int weigh,
                              void* stream);

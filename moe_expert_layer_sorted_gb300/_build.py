@@ -22,6 +22,7 @@ SOURCES = ["plan.cu", "decode.cu", "prefill.cu", "cache.cu", "noalloc.cu", "kv.c
            "kv_attention.cu", "kv_select.cu", "kv_decode_bf16.cu", "kv_decode_f16.cu",
            "kv_prompt_bf16.cu", "kv_prompt_f16.cu",
            "kv8.cu", "kv8_append.cu", "kv8_attention.cu", "kv8_decode_bf16.cu", "kv8_decode_f16.cu",
+           "kv8_prompt_bf16.cu", "kv8_prompt_f16.cu",
            "kv8_weigh.cu", "kv8_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]

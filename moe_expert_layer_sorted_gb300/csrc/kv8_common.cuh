@@ -45,6 +45,13 @@ __device__ __forceinline__ uint32_t kv8_pair(uint32_t w) {
   asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(__byte_perm(w, 0x64646464u, I ? 0x4342 : 0x4140)), "r"(0xe480e480u));
   return d;
 }
+// The codes of the two channels of a word of values, of the pair's token I.
+template <int I>
+__device__ __forceinline__ uint32_t kv8_token(uint32_t w) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(__byte_perm(w, 0x64646464u, I ? 0x4341 : 0x4240)), "r"(0xe480e480u));
+  return d;
+}
 // Byte i of a word as u in fp32.
 __device__ __forceinline__ float kv8_code(uint32_t w, int i) {
   return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 | i)) - 8388736.0f;

@@ -43,6 +43,8 @@ cudaError_t kv8_read(const Kv8& kv, const KvView& c, const KvBatch& b, uint16_t*
                      const KvRows& vs, cudaStream_t s);
 cudaError_t kv8_decode_bf16(Kv8& kv, const KvAttnArgs& a, cudaStream_t s);
 cudaError_t kv8_decode_f16(Kv8& kv, const KvAttnArgs& a, cudaStream_t s);
+cudaError_t kv8_prompt_bf16(Kv8& kv, const KvAttnArgs& a, cudaStream_t s);
+cudaError_t kv8_prompt_f16(Kv8& kv, const KvAttnArgs& a, cudaStream_t s);
 cudaError_t kv8_attention(Kv8& kv, const KvAttnArgs& a, cudaStream_t s);
 // Adds the weights of a's rows, whose lse the attention has written, to the layer's mass.
 cudaError_t kv8_weigh(Kv8& kv, const KvAttnArgs& a, float* mass, cudaStream_t s);

@@ -86,45 +86,6 @@ __device__ __forceinline__ uint4 values8(uint32_t w, uint32_t par) {
                     fma_half2(centred_pair<2>(w), s2, c2), fma_half2(centred_pair<3>(w), s2, c2));
 }
 
-struct PromptArgs {
-  KvAttnArgs a;
-  int per;        // query heads per kv head
-  int tiles;      // row-tile pairs per sequence and head, at most
-  int splits;     // stretches of tokens per row-tile pair, at most
-  float* ws;      // [pair][split] partial results
-  uint32_t* err;
-  int fail;       // test hook: the first CTA's last values are not announced
-};
-
-// A pair of row tiles: its rows x0 .. of the nx of sequence s and kv head h, and its tokens.
-struct PromptTile {
-  int s, h;
-  KvSeq q;
-  int nx, x0;     // numbered in 32 bits
-  int64_t first;  // position of row 0
-  int cap, most;          // tokens that its last row sees
-  int all, splits;        // token tiles, stretches they are cut into
-
-  __device__ __forceinline__ PromptTile(const PromptArgs& p) {
-    // heavy tiles first: the last rows of every sequence see the most
-    const int hs = blockIdx.x % (p.a.c.heads * p.a.b.batch);
-    const int rt = p.tiles - 1 - blockIdx.x / (p.a.c.heads * p.a.b.batch);
-    h = hs % p.a.c.heads;
-    s = hs / p.a.c.heads;
-    q = kv_seq(p.a.b, s);
-    nx = q.rows * p.per;
-    x0 = rt * 2 * kPrTile;
-    cap = kv_capacity(p.a.c, p.a.b);
-    first = (int64_t)q.len - q.rows;
-    most = x0 < nx ? seen(p, min(x0 + 2 * kPrTile, nx) - 1) : 0;
-    all = (most + kPrTile - 1) / kPrTile;
-    splits = min(p.splits, max(all / 2, 1));
-  }
-  __device__ __forceinline__ int seen(const PromptArgs& p, int x) const {  // tokens that row x sees
-    const int64_t pos = first + x / p.per;
-    return pos < 0 ? 0 : (int)min(p.a.causal ? pos + 1 : (int64_t)q.len, (int64_t)cap);
-  }
-};
 // Floats of a stretch's part: O [D / 4][row] of four channels, then references, sums, poisoned
 // groups, O's powers of two.
 template <int D>

@@ -1,5 +1,5 @@
 // tcgen05 products of tiles of 128 rows and 128 tokens, for the attention kernels of prompts
-// (included into an anonymous namespace).
+// (included into an anonymous namespace after kv_operand.cuh).
 #pragma once
 
 constexpr int kPrTile = 128;  // rows of a row tile, tokens of a token tile
@@ -92,4 +92,91 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+
+struct PromptArgs {
+  KvAttnArgs a;
+  int per;        // query heads per kv head
+  int tiles;      // row-tile pairs per sequence and head, at most
+  int splits;     // stretches of tokens per row-tile pair, at most
+  float* ws;      // [pair][split] partial results
+  uint32_t* err;
+  int fail;       // test hook: the first CTA's last values are not announced
+};
+
+// A pair of row tiles: its rows x0 .. of the nx of sequence s and kv head h, and its tokens.
+struct PromptTile {
+  int s, h;
+  KvSeq q;
+  int nx, x0;     // numbered in 32 bits
+  int64_t first;  // position of row 0
+  int cap, most;          // tokens that its last row sees
+  int all, splits;        // token tiles, stretches they are cut into
+
+  __device__ __forceinline__ PromptTile(const PromptArgs& p) {
+    // heavy tiles first: the last rows of every sequence see the most
+    const int hs = blockIdx.x % (p.a.c.heads * p.a.b.batch);
+    const int rt = p.tiles - 1 - blockIdx.x / (p.a.c.heads * p.a.b.batch);
+    h = hs % p.a.c.heads;
+    s = hs / p.a.c.heads;
+    q = kv_seq(p.a.b, s);
+    nx = q.rows * p.per;
+    x0 = rt * 2 * kPrTile;
+    cap = kv_capacity(p.a.c, p.a.b);
+    first = (int64_t)q.len - q.rows;
+    most = x0 < nx ? seen(p, min(x0 + 2 * kPrTile, nx) - 1) : 0;
+    all = (most + kPrTile - 1) / kPrTile;
+    splits = min(p.splits, max(all / 2, 1));
+  }
+  __device__ __forceinline__ int seen(const PromptArgs& p, int x) const {  // tokens that row x sees
+    const int64_t pos = first + x / p.per;
+    return pos < 0 ? 0 : (int)min(p.a.causal ? pos + 1 : (int64_t)q.len, (int64_t)cap);
+  }
+};
+
+// 128 query rows from x0 on of a sequence and kv head (those from nx on as zeros) as a K-major fp16 tile, by 256
+// threads, two to a row; scale: what the rows' scores are multiplied by, since a row of bf16 is brought to 2^14 by
+// a power of two.
+template <typename T, int D>
+__device__ __forceinline__ void load_queries(uint8_t* tile, float* scale, const KvAttnArgs& a, int s, int h, const KvSeq& q, int per,
+                                             int x0, int nx, int tid) {
+  const int r = tid >> 1, side = tid & 1, x = x0 + r;
+  uint4 raw[D / 16];
+#pragma unroll
+  for (int n = 0; n < D / 16; ++n) raw[n] = make_uint4(0, 0, 0, 0);
+  if (x < nx) {
+    const uint4* src = reinterpret_cast<const uint4*>(a.q + kv_row_offset(a.b, a.qs, s, q.row0, x / per) +
+                                                      (int64_t)(h * per + x % per) * a.qs.head + side * (D / 2));
+#pragma unroll
+    for (int n = 0; n < D / 16; ++n) raw[n] = src[n];
+  }
+  float back = 1.0f;
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    uint32_t top = 0;  // largest magnitudes of the even and the odd channels (NaN above all)
+#pragma unroll
+    for (int n = 0; n < D / 16; ++n) {
+      const uint32_t w[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = __vmaxu2(top, w[e] & 0x7fff7fffu);
+    }
+    top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top >> 16, top & 0xffffu);
+    const int ex = (int)(top >> 7) - 127;  // an infinity or a NaN stays what it is
+    const int by = top == 0u || ex > 127 ? 0 : min(max(14 - ex, -113), 113);
+    const float up = pow2(by);
+    back = pow2(-by);
+#pragma unroll
+    for (int n = 0; n < D / 16; ++n) {
+      uint32_t w[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = KvType<__half>::pack(KvType<T>::lo(w[e]) * up, KvType<T>::hi(w[e]) * up);
+      raw[n] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  if (side == 0) scale[r] = back;
+#pragma unroll
+  for (int n = 0; n < D / 16; ++n) {
+    const int ch = side * (D / 16) + n;
+    *reinterpret_cast<uint4*>(tile + (ch / 8) * (kPrTile * 128) + r * 128 + ((ch % 8) ^ (r & 7)) * 16) = raw[n];
+  }
 }
