@@ -93,7 +93,7 @@ extern "C" moe_status moe_kv8_create(const moe_kv8_desc* desc, moe_kv8_cache** o
     kv->d = *desc;
     set_sizes(kv);
     cudaDeviceGetAttribute(&kv->sms, cudaDevAttrMultiProcessorCount, desc->device);
-    cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&kv->ws), Kv8::kWorkspace);
+    cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&kv->ws), kv->workspace());
     if (e == cudaSuccess) e = cudaMemset(kv->counters(), 0, Kv8::kCounterBytes);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();  // the memset is done before any stream's first call
     void* word = nullptr;
@@ -187,9 +187,8 @@ extern "C" moe_status moe_kv8_attention(moe_kv8_cache* h, int layer, const moe_k
                        static_cast<uint16_t*>(out->data), lse, rows_of(q), rows_of(out), q_heads, scale, causal, nullptr, 0};
     Order order;
     cudaError_t e = order_before(kv, s, order);
-    if (e == cudaSuccess) e = kv8_attention(*kv, a, s);
+    if (e == cudaSuccess) e = kv8_attention(*kv, a, weigh ? mass_of(kv, layer) : nullptr, s);
     kv->fail_next = false;
-    if (e == cudaSuccess && weigh) e = kv8_weigh(*kv, a, mass_of(kv, layer), s);
     if (e == cudaSuccess) e = order_after(kv, s, order);
     return e == cudaSuccess ? MOE_OK : cuda_fail(kv, e, "moe_kv8_attention");
   });

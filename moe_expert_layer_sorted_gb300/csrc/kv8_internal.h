@@ -10,12 +10,15 @@ struct Kv8 {
   moe_kv8_desc d{};
   int sms = 0;
   int64_t block_bytes = 0, head_bytes = 0, page_bytes = 0, layer_bytes = 0, mass_layer = 0;  // mass_layer: elements
-  // workspace: partial results of attention items that are cut between CTAs; their counters, zero between calls
+  // workspace: partial results of attention items that are cut between CTAs, or of tokens' weights; counters of
+  // the former, zero between calls; with mass, scores of single tokens whose weights are counted
   uint8_t* ws = nullptr;
   static constexpr size_t kPartsBytes = size_t(24) << 20;
   static constexpr int kCounters = 1024;
   static constexpr size_t kCounterBytes = kCounters * sizeof(unsigned);
-  static constexpr size_t kWorkspace = kPartsBytes + kCounterBytes;
+  static constexpr size_t kScoreBytes = size_t(128) << 20;
+  size_t workspace() const { return kPartsBytes + kCounterBytes + (d.mass ? kScoreBytes : 0); }
+  float* scores() const { return reinterpret_cast<float*>(ws + kPartsBytes + kCounterBytes); }
   float* parts() const { return reinterpret_cast<float*>(ws); }
   unsigned* counters() const { return reinterpret_cast<unsigned*>(ws + kPartsBytes); }
   volatile uint32_t* err_host = nullptr;  // mapped pinned word: set by a kernel whose bounded wait gave up
@@ -41,13 +44,18 @@ cudaError_t kv8_append(const Kv8& kv, const KvView& c, const KvBatch& b, const u
                        const uint16_t* v, const KvRows& vs, float* mass, cudaStream_t s);
 cudaError_t kv8_read(const Kv8& kv, const KvView& c, const KvBatch& b, uint16_t* k, const KvRows& ks, uint16_t* v,
                      const KvRows& vs, cudaStream_t s);
-cudaError_t kv8_decode_bf16(Kv8& kv, const KvAttnArgs& a, cudaStream_t s);
-cudaError_t kv8_decode_f16(Kv8& kv, const KvAttnArgs& a, cudaStream_t s);
+// Attention of few rows.  scores: nullptr, or room for every row's score of every token, log2 units:
+// [sequence][kv head][token of the table][score_width] by columns (row, query head), -infinity where not seen.
+cudaError_t kv8_decode_bf16(Kv8& kv, const KvAttnArgs& a, float* scores, cudaStream_t s);
+cudaError_t kv8_decode_f16(Kv8& kv, const KvAttnArgs& a, float* scores, cudaStream_t s);
+inline int score_width(const KvAttnArgs& a) { return (int)(((int64_t)a.b.max_new * (a.q_heads / a.c.heads) + 3) / 4 * 4); }
+// Attention of prompts.
 cudaError_t kv8_prompt_bf16(Kv8& kv, const KvAttnArgs& a, cudaStream_t s);
 cudaError_t kv8_prompt_f16(Kv8& kv, const KvAttnArgs& a, cudaStream_t s);
-cudaError_t kv8_attention(Kv8& kv, const KvAttnArgs& a, cudaStream_t s);
-// Adds the weights of a's rows, whose lse the attention has written, to the layer's mass.
-cudaError_t kv8_weigh(Kv8& kv, const KvAttnArgs& a, float* mass, cudaStream_t s);
+// mass: nullptr, or the layer's, to which the weights of the tokens are added (lse is then given).
+cudaError_t kv8_attention(Kv8& kv, const KvAttnArgs& a, float* mass, cudaStream_t s);
+// The weights of an attention whose lse is written; scores: as written by the single-token kernel, or nullptr.
+cudaError_t kv8_weigh(Kv8& kv, const KvAttnArgs& a, float* mass, const float* scores, cudaStream_t s);
 cudaError_t kv8_evict(const Kv8& kv, const Kv8EvictArgs& a, cudaStream_t s);
 
 // Calls f with (T, D) of the cache as compile-time constants.

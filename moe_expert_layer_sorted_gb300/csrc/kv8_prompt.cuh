@@ -10,7 +10,7 @@
 // The codes -127..127 are exact in fp16, and the blocks' steps cost nothing: s_K goes
 // into the factor of a block's 16 columns, s_V into what is added there.  Roles:
 //   warps 0-3, 4-7  softmax of tile 0, 1: a thread owns a row (a TMEM lane);
-//   warps 8-11      stored codes -> 16-bit K and V tiles, two blocks a warp;
+//   warps 8-11      stored codes -> 16-bit K and V tiles, two blocks of each a warp;
 //   warp 12         tcgen05.mma issue, TMEM allocation.
 // Rounding: P to 11 bits; everything else is exact or fp32 (a query row of bf16 is
 // scaled by the power of two that brings its largest element to 2^14).
@@ -56,6 +56,24 @@ constexpr float kPrNear = 60.0f;        // and of how far they may be from the r
 constexpr float kPrMaxSum = 0x1p60f;    // ry is raised when a tile's weights sum to this
 constexpr float kNoProduct = 1e38f;     // dz of a row that has seen no token
 
+// A block's constants, in order with the other asm statements: loaded where they are wanted, not all at once.
+__device__ __forceinline__ float4 load_block(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
+  return v;
+}
+
+__device__ __forceinline__ float log2_fast(float x) {
+  float d;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(d) : "f"(x));
+  return d;
+}
+__device__ __forceinline__ uint32_t load_word(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+
 // Floats of a stretch's part: results [D / 4][row] of four channels, then references, sums, 1 where a row is NaN.
 template <int D>
 constexpr int64_t kPr8Part = 2 * kPrTile * (D + 3);
@@ -71,9 +89,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv8_prompt_kernel(const __grid_
   __shared__ uint32_t sh_gone;  // a wait gave up: results are wrong, the next call says so
   // per token tile (ring of 4): tokens that exist, tokens with keys, values that are not finite
   __shared__ uint4 sh_valid[4], sh_kbad[4], sh_vbad[4];
-  // and its blocks: the keys' step, log2 of the values', the factor of a sum of P, and the values' step as stored
-  __shared__ float4 sh_ks[4][2], sh_lv[4][2], sh_c[4][2], sh_vs[4][2];
-  __shared__ float sh_lv0[4];                  // the largest log2 of the values' steps; NaN: not an ordinary tile
+  __shared__ uint32_t sh_any_bad[4];           // whether there are any of the latter
+  __shared__ float4 sh_block[4][8];            // and its blocks: the keys' step, log2 of the values', the factor of a sum of P
+  __shared__ float4 sh_vs[4][2];               // and the values' step
+  __shared__ float sh_lv0[4];                  // the largest log2 of the values' steps; NaN: not an ordinary tile, or not all there
   __shared__ float sh_qscale[2 * kPrTile];     // what a query row's scores are multiplied by
   const KvAttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -136,39 +155,35 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv8_prompt_kernel(const __grid_
     for (int j = 0; j < (t == 0 || two ? ntiles : 0); ++j) {
       kv_wait(smem_addr(&sFull[t]), (uint32_t)j & 1u, &sh_gone, p.err);
       fence_after();
-      uint32_t v[2][32];  // asked for before what the tile needs is known: nearly always the unmasked pass
-      tmem_ld32(ts, v[0]);
-      const uint4 valid4 = sh_valid[j & 3];
-      const uint32_t valid[4] = {valid4.x, valid4.y, valid4.z, valid4.w};
-      const float* const ks = reinterpret_cast<const float*>(sh_ks[j & 3]);
-      const float* const lv = reinterpret_cast<const float*>(sh_lv[j & 3]);
-      const float* const cs = reinterpret_cast<const float*>(sh_c[j & 3]);
+      uint32_t v[2][32];
+      const uint32_t blocks = smem_addr(&sh_block[j & 3][0]);
       const float lv0 = sh_lv0[j & 3];
       // an ordinary tile, which every row of the warp sees in full
       auto ordinary = [&]() {
-        return __all_sync(0xffffffffu, seen >= (j + 1) * kPrTile && fabsf(dz + lv0) <= kPrNear) && !coarse &&
-               (valid4.x & valid4.y & valid4.z & valid4.w) == 0xffffffffu;
+        return __all_sync(0xffffffffu, seen >= (j + 1) * kPrTile && fabsf(dz + lv0) <= kPrNear) && !coarse;
       };
       bool plain = ordinary();
       uint32_t pr[kPrTile / 2];
       auto mask_of = [&](int k) {  // tokens of the k-th 32 that the row sees
         const int n = seen - (j * kPrTile + 32 * k);
-        return valid[k] & (n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u);
+        return load_word(smem_addr(&sh_valid[j & 3]) + 4 * k) & (n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u);
       };
       // the k-th 32 scores, rounded, masked ones -infinity
       auto load = [&](int k, uint32_t (&v)[32]) {
         tmem_ld32(ts + 32 * k, v);
         tmem_wait_ld();
         const uint32_t mask = mask_of(k);
+        const float f[2] = {kappa * load_block(blocks + 32 * k).x, kappa * load_block(blocks + 32 * k + 16).x};
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          v[i] = (mask >> i) & 1u ? __float_as_uint(__uint_as_float(v[i]) * (kappa * ks[2 * k + i / 16])) : 0xff800000u;
+        for (int i = 0; i < 32; ++i) v[i] = (mask >> i) & 1u ? __float_as_uint(__uint_as_float(v[i]) * f[i / 16]) : 0xff800000u;
       };
       uint64_t sum = 0, whole = 0;  // of P, and of the weights (an ordinary tile's: times 2^(dz + lv0))
-      auto weights = [&](const uint32_t (&v)[32], int k, auto plain_) {  // v: sums of an ordinary tile, else rounded scores
+      // v: sums of an ordinary tile, else rounded scores; lo, hi: the two blocks
+      auto weights = [&](const uint32_t (&v)[32], int k, float4 lo, float4 hi, auto plain_) {
         constexpr bool plain = decltype(plain_)::value;
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
+          const float4 b = y ? hi : lo;
           float e[16];  // step by step: independent instructions side by side
           auto total = [&]() {
             uint64_t part[4];
@@ -177,13 +192,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv8_prompt_kernel(const __grid_
             return add2(add2(part[0], part[1]), add2(part[2], part[3]));
           };
           if constexpr (plain) {
-            const float f = kappa * ks[2 * k + y], add = (lv[2 * k + y] + dz) - ry;
+            const float f = kappa * b.x, add = (b.y + dz) - ry;
             const uint64_t f2 = pair2(f, f), plus = pair2(add, add);
 #pragma unroll
             for (int i = 0; i < 16; i += 2)
               split2(fma2(pair2(__uint_as_float(v[16 * y + i]), __uint_as_float(v[16 * y + i + 1])), f2, plus), e[i], e[i + 1]);
           } else {
-            const float plus = lv[2 * k + y] + dz;
+            const float plus = b.y + dz;
 #pragma unroll
             for (int i = 0; i < 16; ++i) e[i] = exp2_fast(__uint_as_float(v[16 * y + i]) - ry);
             whole = add2(whole, total());
@@ -196,13 +211,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv8_prompt_kernel(const __grid_
           for (int i = 0; i < 16; i += 2) pr[16 * k + 8 * y + i / 2] = KvType<__half>::pack(e[i], e[i + 1]);
           const uint64_t part = total();
           sum = add2(sum, part);
-          if constexpr (plain) whole = fma2(part, pair2(cs[2 * k + y], cs[2 * k + y]), whole);
+          if constexpr (plain) whole = fma2(part, pair2(b.z, b.z), whole);
         }
       };
       // P against the references as they stand, and once more where they have to rise: for the first
       // tile, or where a P or a weight is above its limit, which shows in the sum (that may reach the
       // limit without one: no harm)
-      bool raise = j == 0, asked = true;
+      bool raise = j == 0;
       while (true) {
         if (raise) {
           float top = kNone, most_z = -__int_as_float(0x7f800000);
@@ -216,10 +231,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv8_prompt_kernel(const __grid_
 #pragma unroll 1
           for (int k = 0; k < 4; ++k) {
             load(k, v[0]);
+            const float lv[2] = {load_block(blocks + 32 * k).y, load_block(blocks + 32 * k + 16).y};
 #pragma unroll
-            for (int i = 0; i < 32; ++i) most_z = fmaxf(most_z, (__uint_as_float(v[0][i]) - now) + lv[2 * k + i / 16]);
+            for (int i = 0; i < 32; ++i) most_z = fmaxf(most_z, (__uint_as_float(v[0][i]) - now) + lv[i / 16]);
           }
-          asked = false;
           l *= exp2_fast(ry - now);
           const float cur = fminf(dz - (ry - now), kNoProduct), want = kPrDrop - most_z;
           const float fo = want < cur ? exp2_fast(want - cur) : 1.0f;
@@ -241,37 +256,41 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv8_prompt_kernel(const __grid_
         }
         sum = whole = 0;
         if (plain) {
-          if (!asked) tmem_ld32(ts, v[0]);
+          tmem_ld32(ts, v[0]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {  // the next 32 scores arrive while these are worked on
+            const float4 lo = load_block(blocks + 32 * k), hi = load_block(blocks + 32 * k + 16);
             tmem_wait_ld();
             if (k < 3) tmem_ld32(ts + 32 * (k + 1), v[(k + 1) & 1]);
-            weights(v[k & 1], k, std::true_type());
+            weights(v[k & 1], k, lo, hi, std::true_type());
           }
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             load(k, v[0]);
-            weights(v[0], k, std::false_type());
+            weights(v[0], k, load_block(blocks + 32 * k), load_block(blocks + 32 * k + 16), std::false_type());
           }
         }
+        if (raise) break;
         float s0, s1, w0, w1;
         split2(sum, s0, s1);
         split2(whole, w0, w1);
-        if (!raise) {
-          raise = __any_sync(0xffffffffu, fmaxf(s0, s1) > kPrLimit || (!plain && w0 + w1 > kPrMaxSum));
-          if (raise) continue;
-        }
+        raise = __any_sync(0xffffffffu, fmaxf(s0, s1) > kPrLimit || (!plain && w0 + w1 > kPrMaxSum));
+        if (!raise) break;
+      }
+      {
+        float w0, w1;
+        split2(whole, w0, w1);
         l = plain ? fmaf(w0 + w1, exp2_fast(-dz - lv0), l) : l + (w0 + w1);
-        break;
       }
       tmem_st32(ts, pr);
       tmem_st32(ts + 32, pr + 32);
-      const uint4 kbad4 = sh_kbad[j & 3], vbad4 = sh_vbad[j & 3];
-      if (kbad4.x | kbad4.y | kbad4.z | kbad4.w | vbad4.x | vbad4.y | vbad4.z | vbad4.w) {
-        if ((kbad4.x & mask_of(0)) | (kbad4.y & mask_of(1)) | (kbad4.z & mask_of(2)) | (kbad4.w & mask_of(3)))
-          l = __int_as_float(0x7fffffff);
-        vnan = vnan || ((vbad4.x & mask_of(0)) | (vbad4.y & mask_of(1)) | (vbad4.z & mask_of(2)) | (vbad4.w & mask_of(3)));
+      if (load_word(smem_addr(&sh_any_bad[j & 3]))) {
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          if (load_word(smem_addr(&sh_kbad[j & 3]) + 4 * k) & mask_of(k)) l = __int_as_float(0x7fffffff);
+          if (load_word(smem_addr(&sh_vbad[j & 3]) + 4 * k) & mask_of(k)) vnan = true;
+        }
       }
       tmem_wait_st();
       fence_before();
@@ -294,8 +313,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv8_prompt_kernel(const __grid_
         for (int e = 0; e < 32; ++e) v[e] = 0;
       }
     };
-    const int i = x / p.per, hq = h * p.per + x % p.per;
-    uint16_t* dst = has && x < nx ? a.out + kv_row_offset(a.b, a.os, s, q.row0, i) + (int64_t)hq * a.os.head : nullptr;
+    const PromptTile end(p);  // asked for anew rather than kept in registers
+    const int xe = end.x0 + row, i = xe / p.per, hq = end.h * p.per + xe % p.per;
+    uint16_t* dst = has && xe < end.nx ? a.out + kv_row_offset(a.b, a.os, end.s, end.q.row0, i) + (int64_t)hq * a.os.head : nullptr;
     // 2^-dz / l, in two steps that stay in range; a row that sees nothing is zero
     const float f1 = dz >= kNoProduct ? 1.0f : exp2f(-0.5f * dz);
     const float f0 = vnan ? __int_as_float(0x7fffffff) : l == 0.0f ? 0.0f : f1 / l;
@@ -323,7 +343,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv8_prompt_kernel(const __grid_
         }
       }
       if (dst && a.lse)
-        a.lse[kv_row_index(a.b, s, q.row0, i) * a.q_heads + hq] =
+        a.lse[kv_row_index(a.b, end.s, end.q.row0, i) * a.q_heads + hq] =
             l == 0.0f ? -__int_as_float(0x7f800000) : (ry + log2f(l)) * 0.6931471805599453f;
     } else if (has) {  // a stretch's part
       float* part = p.ws + ((int64_t)blockIdx.x * p.splits + z) * kPr8Part<D>;
@@ -351,123 +371,147 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv8_prompt_kernel(const __grid_
     constexpr int kLoads = 16 / kKRows;  // of 16 bytes, per block, keys and values each
     static_assert(kLoads == 8 / kVPairs, "as many for both");
     const int kc = lane % kKLanes, kr = lane / kKLanes, vc = lane % kVLanes, vp = lane / kVLanes;
-    uint4 kq[2][kLoads], vq[2][kLoads], par[2], parn[2];
-    const uint8_t *at[2] = {nullptr, nullptr}, *atv[2] = {nullptr, nullptr};  // a tile's blocks
-    int64_t pid[2] = {-1, -1};  // pages of the blocks one tile on
+    uint4 kq[2][kLoads], vq[2][kLoads];
+    uint3 par[2];                           // steps and marks of a tile's blocks
+    uint32_t there = 0;                     // its tokens that are in a page
+    const uint8_t* at[2];                   // the blocks whose words are asked for next, nullptr: none
+    int pid[2];                             // pages of the blocks one tile on
     const uint4 none = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
     auto page_of = [&](int j) {
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int pos = base + j * kPrTile + 32 * dw + 16 * y;
-        pid[y] = j < ntiles && pos < most ? kv_page(a.c, a.b, s, pos >> a.c.page_shift) : -1;
+        pid[y] = j < ntiles && pos < most ? (int)kv_page(a.c, a.b, s, pos >> a.c.page_shift) : -1;
       }
     };
-    auto load_k = [&](int j) {
+    auto find = [&](int j) {
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int pos = base + j * kPrTile + 32 * dw + 16 * y;
         at[y] = pid[y] < 0 ? nullptr
                            : a.c.pages + pid[y] * a.c.page_stride + h * a.c.head_stride +
                                  ((pos & (a.c.page_size - 1)) >> 4) * (int64_t)Geo::kBytes;
-        parn[y] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const int r = i * kKRows + kr;
-          kq[y][i] = at[y] ? *reinterpret_cast<const uint4*>(at[y] + r * D + Geo::k_piece(r, kc) * 16) : none;
-        }
-        if (at[y]) parn[y] = *reinterpret_cast<const uint4*>(at[y] + Geo::kParams);
       }
     };
-    auto load_v = [&]() {
+    auto load_k = [&](auto y_) {
+      constexpr int y = decltype(y_)::value;
 #pragma unroll
-      for (int y = 0; y < 2; ++y)
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = i * kKRows + kr;
+        kq[y][i] = at[y] ? *reinterpret_cast<const uint4*>(at[y] + r * D + Geo::k_piece(r, kc) * 16) : none;
+      }
+    };
+    auto load_v = [&](auto y_) {
+      constexpr int y = decltype(y_)::value;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const int r = i * kVPairs + vp;
-          vq[y][i] = atv[y] ? *reinterpret_cast<const uint4*>(atv[y] + Geo::kVOff + r * 2 * D + Geo::v_piece(r, vc) * 16) : none;
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = i * kVPairs + vp;
+        vq[y][i] = at[y] ? *reinterpret_cast<const uint4*>(at[y] + Geo::kVOff + r * 2 * D + Geo::v_piece(r, vc) * 16) : none;
+      }
+    };
+    auto load_params = [&]() {
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        par[y] = make_uint3(0, 0, 0);
+        if (at[y]) {
+          const uint4 x = *reinterpret_cast<const uint4*>(at[y] + Geo::kParams);
+          par[y] = make_uint3(x.x, x.y, x.z);
         }
+      }
+      there = (at[0] ? 0xffffu : 0u) | (at[1] ? 0xffff0000u : 0u);
     };
     auto place = [&](uint8_t* tile, int r, int ch8) {  // channels 8 ch8 .. of token r
       return reinterpret_cast<uint4*>(tile + (ch8 / 8) * kSlab + r * 128 + ((ch8 % 8) ^ (r & 7)) * 16);
     };
+    auto put_k = [&](uint8_t* tile, auto y_) {
+      constexpr int y = decltype(y_)::value;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = 32 * dw + 16 * y + i * kKRows + kr;
+        uint4 w = kq[y][i];
+        // (128 channels: half of the lanes store the upper eight first, so that eight lanes hit all banks)
+        const bool turn = D == 128 && kc >= 4;
+        if (turn) w = make_uint4(w.z, w.w, w.x, w.y);
+        const uint4 lo = make_uint4(kv8_pair<0>(w.x), kv8_pair<1>(w.x), kv8_pair<0>(w.y), kv8_pair<1>(w.y));
+        const uint4 hi = make_uint4(kv8_pair<0>(w.z), kv8_pair<1>(w.z), kv8_pair<0>(w.w), kv8_pair<1>(w.w));
+        *place(tile, r, 2 * kc + turn) = lo;
+        *place(tile, r, 2 * kc + 1 - turn) = hi;
+      }
+    };
+    auto put_v = [&](uint8_t* tile, auto y_) {
+      constexpr int y = decltype(y_)::value;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = 32 * dw + 16 * y + 2 * (i * kVPairs + vp);
+        const uint32_t w[4] = {vq[y][i].x, vq[y][i].y, vq[y][i].z, vq[y][i].w};
+        *place(tile, r, vc) = make_uint4(kv8_token<0>(w[0]), kv8_token<0>(w[1]), kv8_token<0>(w[2]), kv8_token<0>(w[3]));
+        *place(tile, r + 1, vc) = make_uint4(kv8_token<1>(w[0]), kv8_token<1>(w[1]), kv8_token<1>(w[2]), kv8_token<1>(w[3]));
+      }
+    };
+    constexpr std::integral_constant<int, 0> b0;
+    constexpr std::integral_constant<int, 1> b1;
+    // what the softmax wants to know of the tile whose params are in hand; the tile's keys are announced later
+    auto tell = [&](int slot) {
+      if (lane < 2) reinterpret_cast<float*>(sh_vs[slot])[2 * dw + lane] = __uint_as_float(lane ? par[1].y : par[0].y);
+      if (lane == 0) {
+        reinterpret_cast<uint32_t*>(&sh_valid[slot])[dw] = there;
+        reinterpret_cast<uint32_t*>(&sh_kbad[slot])[dw] = (par[0].z & 0xffffu) | par[1].z << 16;
+        reinterpret_cast<uint32_t*>(&sh_vbad[slot])[dw] = par[0].z >> 16 | (par[1].z & 0xffff0000u);
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(kPrDequant * 32) : "memory");
+      // the tile's largest and smallest step of values
+      const float4 v0 = sh_vs[slot][0], v1 = sh_vs[slot][1];
+      const float big = fmaxf(fmaxf(fmaxf(v0.x, v0.y), fmaxf(v0.z, v0.w)), fmaxf(fmaxf(v1.x, v1.y), fmaxf(v1.z, v1.w)));
+      const float small = fminf(fminf(fminf(v0.x, v0.y), fminf(v0.z, v0.w)), fminf(fminf(v1.x, v1.y), fminf(v1.z, v1.w)));
+      const float lv0 = log2_fast(big);
+      if (lane < 2) {
+        const float lv = log2_fast(__uint_as_float(lane ? par[1].y : par[0].y));  // -infinity of zero
+        sh_block[slot][2 * dw + lane] = make_float4(__uint_as_float(lane ? par[1].x : par[0].x), lv, exp2_fast(lv0 - lv), 0.0f);
+      }
+      if (tid == kPrSoft * 32) {
+        sh_lv0[slot] = lv0 - log2_fast(small) <= kPrApart ? lv0 : __int_as_float(0x7fffffff);
+        const uint4 x = sh_kbad[slot], y = sh_vbad[slot];
+        sh_any_bad[slot] = x.x | x.y | x.z | x.w | y.x | y.y | y.z | y.w;
+      }
+    };
+    // the words of a tile are asked for as soon as the last one's are turned
     if (ntiles > 0) {
       page_of(0);
-      load_k(0);
+      find(0);
+      load_k(b0);
+      load_k(b1);
+      load_v(b0);
+      load_v(b1);
+      load_params();
       page_of(1);
+      tell(0);
     }
     for (int j = 0; j < ntiles; ++j) {
       const int st = j & 1;
       const uint32_t free_parity = ((uint32_t)(j >> 1) & 1u) ^ 1u;
-      // this tile's values can be asked for now: their words arrive while the keys are turned
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        atv[y] = at[y];
-        par[y] = parn[y];
-      }
-      load_v();
-      if (lane < 2) reinterpret_cast<float*>(sh_vs[j & 3])[2 * dw + lane] = __uint_as_float(lane ? par[1].y : par[0].y);
       kv_wait(smem_addr(&kEmpty[st]), free_parity, &sh_gone, p.err);
       uint8_t* tk = gen + 2 * kTileBytes + st * kTileBytes;
-#pragma unroll
-      for (int y = 0; y < 2; ++y)
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const int r = 32 * dw + 16 * y + i * kKRows + kr;
-          uint4 w = kq[y][i];
-          // (128 channels: half of the lanes store the upper eight first, so that eight lanes hit all banks)
-          const bool turn = D == 128 && kc >= 4;
-          if (turn) w = make_uint4(w.z, w.w, w.x, w.y);
-          const uint4 lo = make_uint4(kv8_pair<0>(w.x), kv8_pair<1>(w.x), kv8_pair<0>(w.y), kv8_pair<1>(w.y));
-          const uint4 hi = make_uint4(kv8_pair<0>(w.z), kv8_pair<1>(w.z), kv8_pair<0>(w.w), kv8_pair<1>(w.w));
-          *place(tk, r, 2 * kc + turn) = lo;
-          *place(tk, r, 2 * kc + 1 - turn) = hi;
-        }
-      asm volatile("bar.sync 1, %0;" ::"n"(kPrDequant * 32) : "memory");
-      // the tile's largest and smallest step of values
-      const float4 v0 = sh_vs[j & 3][0], v1 = sh_vs[j & 3][1];
-      const float big = fmaxf(fmaxf(fmaxf(v0.x, v0.y), fmaxf(v0.z, v0.w)), fmaxf(fmaxf(v1.x, v1.y), fmaxf(v1.z, v1.w)));
-      const float small = fminf(fminf(fminf(v0.x, v0.y), fminf(v0.z, v0.w)), fminf(fminf(v1.x, v1.y), fminf(v1.z, v1.w)));
-      const float lv0 = log2f(big);
-      if (lane < 2) {
-        const float lv = log2f(__uint_as_float(lane ? par[1].y : par[0].y));  // -infinity of zero
-        reinterpret_cast<float*>(sh_ks[j & 3])[2 * dw + lane] = __uint_as_float(lane ? par[1].x : par[0].x);
-        reinterpret_cast<float*>(sh_lv[j & 3])[2 * dw + lane] = lv;
-        reinterpret_cast<float*>(sh_c[j & 3])[2 * dw + lane] = exp2f(lv0 - lv);
-      }
-      if (lane == 0) {
-        reinterpret_cast<uint32_t*>(&sh_valid[j & 3])[dw] = (atv[0] ? 0xffffu : 0u) | (atv[1] ? 0xffff0000u : 0u);
-        reinterpret_cast<uint32_t*>(&sh_kbad[j & 3])[dw] = (par[0].z & 0xffffu) | par[1].z << 16;
-        reinterpret_cast<uint32_t*>(&sh_vbad[j & 3])[dw] = par[0].z >> 16 | (par[1].z & 0xffff0000u);
-        if (dw == 0) sh_lv0[j & 3] = lv0 - log2f(small) <= kPrApart ? lv0 : __int_as_float(0x7fffffff);
-      }
+      find(j + 1);
+      put_k(tk, b0);
+      load_k(b0);
+      put_k(tk, b1);
+      load_k(b1);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&kFull[st]));
-      // the next tile's keys
-      load_k(j + 1);
+      load_params();
       page_of(j + 2);
       kv_wait(smem_addr(&vEmpty[st]), free_parity, &sh_gone, p.err);
       uint8_t* tv = gen + 4 * kTileBytes + st * kTileBytes;
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const int r = 32 * dw + 16 * y + 2 * (i * kVPairs + vp);
-          const uint32_t w[4] = {vq[y][i].x, vq[y][i].y, vq[y][i].z, vq[y][i].w};
-          uint32_t o[2][4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            o[0][e] = kv8_token<0>(w[e]);
-            o[1][e] = kv8_token<1>(w[e]);
-          }
-          *place(tv, r, vc) = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
-          *place(tv, r + 1, vc) = make_uint4(o[1][0], o[1][1], o[1][2], o[1][3]);
-        }
-      }
+      put_v(tv, b0);
+      load_v(b0);
+      put_v(tv, b1);
+      load_v(b1);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       const bool held = p.fail && blockIdx.x == 0 && z == 0 && j == ntiles - 1 && dw == 0;
       if (lane == 0 && !held) mbar_arrive(smem_addr(&vFull[st]));
+      tell((j + 1) & 3);
     }
   } else {
     set_registers<kPrRegs, kPrMmaRegs>();

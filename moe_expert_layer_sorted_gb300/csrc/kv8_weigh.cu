@@ -1,11 +1,17 @@
-// The weight of every token: after an attention, the softmax weights of its rows, summed over the
-// rows and query heads that see the token, are added to the token's mass.
+// The weight of every token: the softmax weights of an attention's rows, summed over the rows and
+// query heads that see the token, are added to the token's mass.
 //
-// With lse from the attention a weight is 2^(y - lse log2 e), y the score in log2 units as the
-// attention computes it, so that a token's sum needs its keys and the queries alone: one warp per
-// block of 16 tokens and kv head holds the codes as the rows of mma.m16n8k16 and walks over the
-// columns (row, query head), eight at a time.  A token's sum is one lane's and its neighbours', in
-// the order of the columns: no atomics.
+// With lse from the attention a weight is 2^(y - lse log2 e), y the score in log2 units.  Where the
+// single-token kernel has written its scores (kv8_decode.cuh), a thread adds up a token's.  Otherwise the
+// scores are made again, transposed, on the tensor cores, and the sums run along registers:
+//     S^T = U_K Q^T   (128 tokens by 128 columns (row, query head) in TMEM),
+// a thread having a token (a TMEM lane) and half of the columns.  A column's power of two and lse come from
+// shared memory, a token's step is its thread's.  Columns that see nothing of a tile are not visited; the
+// columns of a tile are dealt out to as many CTAs as fill the SMs, whose sums a second kernel adds in
+// order, so that results do not depend on timing.
+//
+// Each CTA loads the next 128 queries while the tensor cores work on one half of TMEM and the threads on
+// the other; two CTAs share an SM, so that one's barrier is covered by the other's exponents.
 #include "kv8_internal.h"
 
 using namespace moe;
@@ -14,108 +20,288 @@ namespace {
 
 #include "device_common.cuh"
 #include "kv_operand.cuh"
-#include "kv_rounds.cuh"
+#include "kv_tcgen.cuh"
+
+constexpr int kWeThreads = 256;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct WeighArgs {
+  KvAttnArgs a;
+  float* mass;
+  int per;        // query heads per kv head
+  int tiles;      // token tiles of a sequence, at most
+  int splits;     // CTAs per token tile and kv head
+  float* parts;   // [sequence][head][tile][split][128], splits > 1
+  uint32_t* err;
+};
+
+// Adds sum to the mass of token `pos` of sequence s, head h.
+__device__ __forceinline__ void add_mass(const WeighArgs& w, int s, int h, int pos, float sum) {
+  const int64_t pid = kv_page(w.a.c, w.a.b, s, pos >> w.a.c.page_shift);
+  if (pid >= 0) w.mass[(pid * w.a.c.heads + h) * w.a.c.page_size + (pos & (w.a.c.page_size - 1))] += sum;
+}
+
+struct WeighTile {
+  int s, h, t, len, nx;
+  int64_t first;  // position of row 0
+  KvSeq q;
+  int c0, cn;     // column tiles that see something of the token tile
+
+  __device__ __forceinline__ WeighTile(const WeighArgs& w, int index) {
+    // tiles that the most rows see first
+    h = index % w.a.c.heads;
+    s = index / w.a.c.heads % w.a.b.batch;
+    t = index / w.a.c.heads / w.a.b.batch;
+    q = kv_seq(w.a.b, s);
+    len = min(q.len, kv_capacity(w.a.c, w.a.b));
+    nx = q.rows * w.per;
+    first = (int64_t)q.len - q.rows;
+    cn = c0 = 0;
+    if (t * kPrTile < len && nx > 0) {
+      const int64_t skip = w.a.causal ? max((int64_t)t * kPrTile - first, (int64_t)0) : max(-first, (int64_t)0);
+      if (skip * w.per < nx) {
+        c0 = (int)(skip * w.per / kPrTile);
+        cn = (nx + kPrTile - 1) / kPrTile - c0;
+      }
+    }
+  }
+};
 
 template <typename T, int D>
-__global__ void __launch_bounds__(256) kv8_weigh_kernel(const __grid_constant__ KvAttnArgs a, float* __restrict__ mass, int chunks) {
+__global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_constant__ WeighArgs w) {
   using Geo = Kv8Geom<D>;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
-  const int h = blockIdx.x % a.c.heads, per = a.q_heads / a.c.heads;
-  const int s = blockIdx.x / a.c.heads / chunks;
+  constexpr uint32_t kTileBytes = kPrTile * 128 * (D / 64);
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t done[2];                     // products of a half of TMEM
+  __shared__ uint32_t tmem_base;
+  __shared__ uint32_t sh_gone;
+  // (four of each: threads that are one barrier ahead write a tile's while others read the last but one's)
+  __shared__ float4 sh_col[4][kPrTile / 2];        // two columns' factors and -lse log2 e
+  __shared__ int sh_seen[4][kPrTile];              // tokens that a column sees
+  __shared__ float sh_scale[kPrTile];
+  __shared__ float sh_step[kPrTile], sh_sum[kPrTile];
+  const KvAttnArgs& a = w.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int item = blockIdx.x / w.splits, z = blockIdx.x % w.splits;
+  const WeighTile tile(w, item);
+  const int mine = z < tile.cn ? (tile.cn - z + w.splits - 1) / w.splits : 0;  // column tiles c0 + z, c0 + z + splits, ..
+  const int base = tile.t * kPrTile;
+  float* part = w.parts + ((int64_t)item * w.splits + z) * kPrTile;
+  if (mine == 0) {
+    if (w.splits > 1 && tid < kPrTile) part[tid] = 0.0f;
+    return;
+  }
+  const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  uint8_t* gen = smem_raw + (smem - smem_addr(smem_raw));  // keys, then two query tiles
+  if (tid == 0) {
+    sh_gone = 0;
+    mbar_init(smem_addr(&done[0]), 1);
+    mbar_init(smem_addr(&done[1]), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_base)), "n"(256));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  // ---- the keys: a warp takes a block of 16 tokens
+  {
+    constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+    const int pos = base + 16 * warp, kc = lane % kLanes, kr = lane / kLanes;
+    const int64_t pid = pos < tile.len ? kv_page(a.c, a.b, tile.s, pos >> a.c.page_shift) : -1;
+    const uint8_t* blk = a.c.pages + pid * a.c.page_stride + tile.h * a.c.head_stride +
+                         ((pos & (a.c.page_size - 1)) >> 4) * (int64_t)Geo::kBytes;
+#pragma unroll
+    for (int i = 0; i < 16 / kRows; ++i) {
+      const int r = i * kRows + kr, row = 16 * warp + r;
+      uint4 v = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+      if (pid >= 0) v = *reinterpret_cast<const uint4*>(blk + r * D + Geo::k_piece(r, kc) * 16);
+      auto place = [&](int ch8) {
+        return reinterpret_cast<uint4*>(gen + (ch8 / 8) * (kPrTile * 128) + row * 128 + ((ch8 % 8) ^ (row & 7)) * 16);
+      };
+      *place(2 * kc) = make_uint4(kv8_pair<0>(v.x), kv8_pair<1>(v.x), kv8_pair<0>(v.y), kv8_pair<1>(v.y));
+      *place(2 * kc + 1) = make_uint4(kv8_pair<0>(v.z), kv8_pair<1>(v.z), kv8_pair<0>(v.w), kv8_pair<1>(v.w));
+    }
+    if (lane < 16) sh_step[16 * warp + lane] = pid >= 0 ? *reinterpret_cast<const float*>(blk + Geo::kParams) : 0.0f;
+  }
+  auto column = [&](int i) { return (tile.c0 + z + i * w.splits) * kPrTile; };
+  // the queries of the i-th column tile, zeros where lse is not finite
+  auto fetch = [&](int i_) {
+    const int x0 = column(i_), b = i_ & 1, slot = i_ & 3, r = tid >> 1, x = x0 + r;
+    float ls = __int_as_float(0x7fffffff);
+    int seen = 0;
+    if (x < tile.nx) {
+      const int i = x / w.per;
+      ls = a.lse[kv_row_index(a.b, tile.s, tile.q.row0, i) * a.q_heads + tile.h * w.per + x % w.per];
+      const int64_t p = tile.first + i;
+      seen = p < 0 ? 0 : (int)min(a.causal ? p + 1 : (int64_t)tile.len, (int64_t)tile.len);
+    }
+    const bool fine = fabsf(ls) < __int_as_float(0x7f800000);
+    load_queries<T, D>(gen + kTileBytes * (1 + b), sh_scale, a, tile.s, tile.h, tile.q, w.per, x0, fine ? tile.nx : 0, tid);
+    if (!(tid & 1)) {  // (this thread has written sh_scale[r])
+      float* col = reinterpret_cast<float*>(&sh_col[slot][r >> 1]);
+      col[r & 1] = a.scale * kLog2e * sh_scale[r];
+      col[2 + (r & 1)] = fine ? -ls * kLog2e : -__int_as_float(0x7f800000);
+      sh_seen[slot][r] = seen;
+    }
+  };
+  const uint32_t id = idesc(kPrTile, false);
+  uint32_t tm = 0;
+  auto multiply = [&](int b) {  // by the first warp
+    const uint32_t leader = elect_leader();
+    const uint32_t qa = smem + kTileBytes * (1 + b);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+      mma_ss(leader, tm + b * kPrTile, desc_k(smem + (k / 4) * (kPrTile * 128) + (k % 4) * 32),
+             desc_k(qa + (k / 4) * (kPrTile * 128) + (k % 4) * 32), id, k ? 1u : 0u);
+    commit(leader, &done[b]);
+  };
+  fetch(0);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  fence_before();
+  __syncthreads();
+  fence_after();
+  tm = tmem_base;
+  if (warp == 0) multiply(0);
+
+  const int quad = warp & 3, half = warp >> 2;  // the warp's lanes of TMEM, its columns of a tile
+  const int token = quad * 32 + lane;
+  const float ks = sh_step[token];
+  const uint64_t ks2 = pair2(ks, ks);
+  uint64_t sum[2] = {0, 0};
+  for (int i = 0; i < mine; ++i) {
+    const int b = i & 1, x0 = column(i);
+    if (i + 1 < mine) {  // into the other half, whose products are done
+      fetch(i + 1);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      fence_before();
+      __syncthreads();
+      if (warp == 0) {
+        fence_after();
+        multiply(b ^ 1);
+      }
+    }
+    kv_wait(smem_addr(&done[b]), (uint32_t)(i >> 1) & 1u, &sh_gone, w.err);
+    fence_after();
+    const uint32_t ts = tm + b * kPrTile + half * 64 + ((uint32_t)(quad * 32) << 16);
+    // every column sees the whole token tile?
+    const bool all = tile.first + x0 / w.per >= base + kPrTile - 1 || (!a.causal && tile.first >= 0);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint32_t v[32];
+      tmem_ld32(ts + 32 * k, v);
+      tmem_wait_ld();
+      const float4* col = &sh_col[i & 3][half * 32 + 16 * k];
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) {
+        const float4 f = col[e / 2];
+        uint64_t y = mul2(pair2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), pair2(f.x, f.y));
+        y = fma2(y, ks2, pair2(f.z, f.w));
+        float y0, y1;
+        split2(y, y0, y1);
+        y0 = exp2_fast(y0);
+        y1 = exp2_fast(y1);
+        if (!all) {
+          const int* seen = &sh_seen[i & 3][half * 64 + 32 * k + e];
+          y0 = base + token < seen[0] ? y0 : 0.0f;
+          y1 = base + token < seen[1] ? y1 : 0.0f;
+        }
+        sum[e / 2 & 1] = add2(sum[e / 2 & 1], pair2(y0, y1));
+      }
+    }
+  }
+  float s0, s1;
+  split2(add2(sum[0], sum[1]), s0, s1);
+  if (half) sh_sum[token] = s0 + s1;
+  fence_before();
+  __syncthreads();
+  if (!half) {
+    const float all = (s0 + s1) + sh_sum[token];
+    if (w.splits > 1) part[token] = all;
+    else if (base + token < tile.len) add_mass(w, tile.s, tile.h, base + token, all);
+  }
+  if (warp == 0) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(256));
+  }
+}
+
+// Adds the sums of a token tile's CTAs, in order.
+__global__ void __launch_bounds__(kPrTile) kv8_weigh_join_kernel(const __grid_constant__ WeighArgs w) {
+  const WeighTile tile(w, blockIdx.x);
+  const int pos = tile.t * kPrTile + threadIdx.x;
+  if (tile.cn == 0 || pos >= tile.len) return;
+  const float* part = w.parts + (int64_t)blockIdx.x * w.splits * kPrTile + threadIdx.x;
+  float sum = 0.0f;
+#pragma unroll 8
+  for (int z = 0; z < w.splits; ++z) sum += part[z * kPrTile];
+  add_mass(w, tile.s, tile.h, pos, sum);
+}
+
+// From the scores that the single-token kernel wrote: a thread adds up a token's columns.
+__global__ void __launch_bounds__(256) kv8_weigh_scores_kernel(const __grid_constant__ WeighArgs w, const float* __restrict__ scores,
+                                                               int width, int chunks) {
+  __shared__ float sh_lse[32];
+  const KvAttnArgs& a = w.a;
+  const int h = blockIdx.x % a.c.heads, s = blockIdx.x / a.c.heads / chunks;
+  const int pos = blockIdx.x / a.c.heads % chunks * 256 + threadIdx.x;
   const KvSeq q = kv_seq(a.b, s);
-  const int pos = (blockIdx.x / a.c.heads % chunks * 8 + warp) * 16;
-  if (pos >= min(q.len, kv_capacity(a.c, a.b)) || q.rows == 0) return;
+  const int cols = q.rows * w.per;
+  if (blockIdx.x / a.c.heads % chunks * 256 >= min(q.len, kv_capacity(a.c, a.b))) return;
+  if ((int)threadIdx.x < cols) {
+    const float ls = a.lse[kv_row_index(a.b, s, q.row0, threadIdx.x / w.per) * a.q_heads + h * w.per + threadIdx.x % w.per];
+    sh_lse[threadIdx.x] = fabsf(ls) < __int_as_float(0x7f800000) ? ls * kLog2e : __int_as_float(0x7f800000);
+  }
+  __syncthreads();
+  if (pos >= min(q.len, kv_capacity(a.c, a.b))) return;
   const int64_t pid = kv_page(a.c, a.b, s, pos >> a.c.page_shift);
   if (pid < 0) return;
-  const int off = pos & (a.c.page_size - 1);
-  const uint8_t* blk = a.c.pages + pid * a.c.page_stride + h * a.c.head_stride + (off >> 4) * (int64_t)Geo::kBytes;
-  uint32_t kf[D / 4];  // the codes as operand: D / 16 steps of four registers
+  float* mass = w.mass + (pid * a.c.heads + h) * a.c.page_size + (pos & (a.c.page_size - 1));
+  const float4* y = reinterpret_cast<const float4*>(scores + (((int64_t)s * a.c.heads + h) * kv_capacity(a.c, a.b) + pos) * width);
+  const float had = *mass;
+  float sum = 0.0f;
+  for (int x = 0; x < cols; x += 4) {
+    const float4 v = y[x / 4];
+    const float e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
-    uint32_t lo[4], hi[4];
-    load_words(lo, blk + r * D + Geo::k_piece(r, c + 4 * i) * 16);
-    load_words(hi, blk + (r + 8) * D + Geo::k_piece(r, c + 4 * i) * 16);
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      kf[16 * i + 4 * w] = kv8_pair<0>(lo[w]);
-      kf[16 * i + 4 * w + 1] = kv8_pair<0>(hi[w]);
-      kf[16 * i + 4 * w + 2] = kv8_pair<1>(lo[w]);
-      kf[16 * i + 4 * w + 3] = kv8_pair<1>(hi[w]);
-    }
+    for (int i = 0; i < 4; ++i)
+      if (x + i < cols && sh_lse[x + i] != __int_as_float(0x7f800000)) sum += exp2_fast(e[i] - sh_lse[x + i]);
   }
-  const float ks = *reinterpret_cast<const float*>(blk + Geo::kParams);
-  const int64_t first = (int64_t)q.len - q.rows;  // position of row 0
-  const int64_t skip = a.causal ? max((int64_t)pos - first, (int64_t)0) : max(-first, (int64_t)0);  // rows that see nothing of the block
-  const int64_t cols = (int64_t)q.rows * per;
-  float sum[2] = {0.0f, 0.0f};  // of tokens r and r + 8, columns 2 c, 2 c + 1 of each eight
-  for (int64_t x0 = skip * per / 8 * 8; x0 < cols; x0 += 8) {
-    const int64_t x = x0 + r;
-    const bool real = x < cols;
-    const int i = real ? (int)(x / per) : 0, hq = h * per + (real ? (int)(x % per) : 0);
-    const uint16_t* src = a.q + kv_row_offset(a.b, a.qs, s, q.row0, i) + (int64_t)hq * a.qs.head;
-    uint4 raw[D / 32];
-    uint32_t top = 0;
-#pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
-      raw[w] = real ? *reinterpret_cast<const uint4*>(src + (c + 4 * (w / 2)) * 16 + w % 2 * 8) : make_uint4(0, 0, 0, 0);
-      const uint32_t v[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        top = max(top, max(__float_as_uint(fabsf(KvType<T>::lo(v[e]))), __float_as_uint(fabsf(KvType<T>::hi(v[e])))));
-    }
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const int ex = (int)(top >> 23) - 127;
-    const int by = top == 0u || ex > 127 ? 0 : min(max(14 - ex, -113), 113);
-    const float up = pow2(by);
-    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
-      const uint32_t v[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
-      uint32_t f[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) f[e] = KvType<__half>::pack(KvType<T>::lo(v[e]) * up, KvType<T>::hi(v[e]) * up);
-#pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        const int k = 8 * w + 2 * e;
-        mma_f16(y, kf[k], kf[k + 1], kf[k + 2], kf[k + 3], f[e], f[e + 1]);
-      }
-    }
-    // column x's factor, lse in log2 units (NaN: its weights are not counted) and what it sees
-    const float back = a.scale * 1.4426950408889634f * pow2(-by);
-    const float ls = real ? a.lse[kv_row_index(a.b, s, q.row0, i) * a.q_heads + hq] : __int_as_float(0x7fffffff);
-    const float off2 = fabsf(ls) < __int_as_float(0x7f800000) ? ls * 1.4426950408889634f : __int_as_float(0x7fffffff);
-    const int64_t p = first + i;
-    const int see = !real || p < 0 ? 0 : (int)min(a.causal ? p + 1 : (int64_t)q.len, (int64_t)0x7fffffff);
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float f = __shfl_sync(0xffffffffu, back, 4 * (2 * c + e)), o = __shfl_sync(0xffffffffu, off2, 4 * (2 * c + e));
-      const int n = __shfl_sync(0xffffffffu, see, 4 * (2 * c + e));
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const float w = exp2_fast(y[2 * t + e] * f * ks - o);
-        if (pos + r + 8 * t < n && o == o) sum[t] += w;
-      }
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    sum[t] += __shfl_xor_sync(0xffffffffu, sum[t], 1);
-    sum[t] += __shfl_xor_sync(0xffffffffu, sum[t], 2);
-    if (c == 0 && pos + r + 8 * t < q.len) mass[(pid * a.c.heads + h) * a.c.page_size + off + r + 8 * t] += sum[t];
-  }
+  *mass = had + sum;
 }
 
 }  // namespace
 
-cudaError_t moe::kv8_weigh(Kv8& kv, const KvAttnArgs& a, float* mass, cudaStream_t s) {
-  const int64_t chunks = (((int64_t)a.b.table_pages << a.c.page_shift) + 127) / 128;
-  const int64_t ctas = chunks * a.c.heads * a.b.batch;
-  if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+cudaError_t moe::kv8_weigh(Kv8& kv, const KvAttnArgs& a, float* mass, const float* scores, cudaStream_t s) {
+  WeighArgs w{a, mass, a.q_heads / a.c.heads, 0, 1, kv.parts(), kv.err_dev};
+  const int64_t cap = std::min<int64_t>((int64_t)a.b.table_pages << a.c.page_shift, 0x7ffff000);
+  if (scores) {
+    const int64_t chunks = (cap + 255) / 256, ctas = chunks * a.c.heads * a.b.batch;
+    if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    kv8_weigh_scores_kernel<<<(unsigned)ctas, 256, 0, s>>>(w, scores, score_width(a), (int)chunks);
+    return cudaGetLastError();
+  }
+  const int64_t tiles = (cap + kPrTile - 1) / kPrTile, items = tiles * a.c.heads * a.b.batch;
+  const int64_t columns = ((int64_t)a.b.max_new * w.per + kPrTile - 1) / kPrTile;
+  if (items > 0x7fffffff || columns * kPrTile > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  w.tiles = (int)tiles;
+  // CTAs enough for four rounds of the SMs, which hold two each; their sums have to fit the workspace
+  const int64_t want = std::min<int64_t>((8 * (int64_t)kv.sms + items - 1) / items, columns);
+  const int64_t room = (int64_t)(Kv8::kPartsBytes / (kPrTile * sizeof(float))) / items;
+  w.splits = (int)std::max<int64_t>(std::min(want, room), 1);
+  if (items * w.splits > 0x7fffffff) return cudaErrorInvalidConfiguration;
   cudaError_t e = cudaSuccess;
   KV8_DISPATCH(kv.d, {
-    kv8_weigh_kernel<T, D><<<(unsigned)ctas, 256, 0, s>>>(a, mass, (int)chunks);
-    e = cudaGetLastError();
+    const size_t smem = std::max<size_t>(1024 + (size_t)3 * kPrTile * D * 2, 80 << 10);  // two CTAs an SM, as many as TMEM holds
+    const auto kernel = kv8_weigh_kernel<T, D>;
+    e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
+    if (e == cudaSuccess) {
+      kernel<<<(unsigned)(items * w.splits), kWeThreads, smem, s>>>(w);
+      e = cudaGetLastError();
+    }
   });
+  if (e == cudaSuccess && w.splits > 1) {
+    kv8_weigh_join_kernel<<<(unsigned)items, kPrTile, 0, s>>>(w);
+    e = cudaGetLastError();
+  }
   return e;
 }
