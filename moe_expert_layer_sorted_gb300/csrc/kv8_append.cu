@@ -3,17 +3,13 @@
 // The 16 tokens of a block share a step: s = rn(max |x| / 127) in fp32 over the block's new rows
 // (those without an infinity or a NaN), or the step that its older tokens have where that is larger;
 //     u = x / s to the nearest whole number, ties to even, -127..127,
-// and where the older tokens' step grew, u_old s_old / s likewise.  Both quotients are rounded once: a
-// product with the reciprocal tells all but those within 2e-5 of a half, and there the sign of what
-// is left above the half, which fp32's fma (fp64 for the older ones) gives exactly, decides.
+// and where the older tokens' step grew, u_old s_old / s likewise.  Both are the quotients themselves, rounded
+// once (kv8_common.cuh).
 #include "kv8_internal.h"
 
 using namespace moe;
 
 namespace {
-
-constexpr float kWhole = 12582912.0f;  // 1.5 2^23: added, a number below 2^22 is rounded to a whole one
-constexpr float kNearHalf = 0.49998f;  // a product within 2^-23 127 of the quotient may be on the wrong side beyond
 
 template <typename T>
 struct Limits;
@@ -26,12 +22,11 @@ struct Limits<__half> {
   static constexpr uint32_t kInf = 0x7c00u;
 };
 
-// 1 / s for the quotients, and the power of two that both sides of them are multiplied with first
-// (a tiny step's reciprocal would leave fp32's range).
+// 1 / s for the quotients, and the power of two that both sides of them are multiplied with first.
 struct Step {
   float s, up, inv;
   __device__ __forceinline__ explicit Step(float step) {
-    up = step < 0x1p-60f ? 0x1p80f : 1.0f;
+    up = kv8_lift(step);
     s = step * up;
     inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
   }
@@ -39,28 +34,40 @@ struct Step {
 
 // x / s of eight elements as codes u + 128 in two words.
 __device__ __forceinline__ uint2 quantise8(const float (&x)[8], const Step& st) {
-  float y[8], worst = 0.0f;
+  uint64_t y[4];
+  uint32_t near = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    y[e] = fmaf(x[e], st.inv, kWhole + 128.0f);
-    worst = fmaxf(worst, fabsf(fmaf(x[e], st.inv, (kWhole + 128.0f) - y[e])));
-  }
-  if (worst > kNearHalf) {
+  for (int e = 0; e < 4; ++e) y[e] = kv8_round2(kv8_two(x[2 * e], x[2 * e + 1]), kv8_two(st.inv, st.inv), near);
+  uint32_t lo = kv8_word(y[0], y[1]), hi = kv8_word(y[2], y[3]);
+  while (near) {
+    const int bit = 31 - __clz(near), e = 7 - bit;
+    near ^= 1u << bit;
+    float v = x[0];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float lo = floorf(x[e] * st.inv), d = x[e] * st.inv - lo;
-      if (fabsf(d - 0.5f) < 0.01f) {
-        const float over = fmaf(-(lo + 0.5f), st.s, x[e]);  // its sign is exact
-        y[e] = kWhole + 128.0f + (over > 0.0f ? lo + 1.0f : over < 0.0f ? lo : 2.0f * rintf(0.5f * (lo + 0.5f)));
-      }
-    }
+    for (int i = 1; i < 8; ++i) v = e == i ? x[i] : v;
+    const uint32_t code = (uint32_t)((int)kv8_settle(v, 1.0f, st.s, v * st.inv) + 128), at = 8 * (e & 3);
+    if (e < 4) lo = (lo & ~(0xffu << at)) | code << at;
+    else hi = (hi & ~(0xffu << at)) | code << at;
   }
-  auto word = [&](int e) {
-    const uint32_t a = __byte_perm(__float_as_uint(y[e]), __float_as_uint(y[e + 1]), 0x0040);
-    const uint32_t b = __byte_perm(__float_as_uint(y[e + 2]), __float_as_uint(y[e + 3]), 0x0040);
-    return __byte_perm(a, b, 0x5410);
-  };
-  return make_uint2(word(0), word(4));
+  return make_uint2(lo, hi);
+}
+
+// Codes of two words of the step s, turned to `to` >= s.
+__device__ __forceinline__ uint2 turn8(uint2 w, float s, float to) {
+  const float up = kv8_lift(to);
+  s *= up;
+  to *= up;
+  const float ratio = __fdiv_rn(s, to);
+  uint32_t near = 0;
+  uint32_t lo = kv8_turn(w.x, ratio, near), hi = kv8_turn(w.y, ratio, near);
+  while (near) {
+    const int bit = 31 - __clz(near), e = 7 - bit;
+    near ^= 1u << bit;
+    const uint32_t code = kv8_settle_byte(e < 4 ? w.x : w.y, e & 3, s, to, ratio), at = 8 * (e & 3);
+    if (e < 4) lo = (lo & ~(0xffu << at)) | code << at;
+    else hi = (hi & ~(0xffu << at)) | code << at;
+  }
+  return make_uint2(lo, hi);
 }
 
 // One warp per (sequence, block that its rows touch, head, keys or values).  D / 8 lanes hold a
@@ -133,20 +140,6 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(KvView c, KvBatch b, co
   const float step = fmaxf(fresh, s_old);
   const bool turn = begin > 0 && step > s_old;  // older codes change
   const Step q8(step);
-  // an older code (u + 128 in byte x): u s_old / step to the nearest whole number; the byte
-  const float ratio = turn ? __fdiv_rn(s_old, step) : 0.0f;
-  auto turned = [&](uint32_t word, int i) {
-    const float u = kv8_code(word, i), y = u * ratio, lo = floorf(y);
-    float z = rintf(y);
-    if (fabsf(y - lo - 0.5f) < 1e-3f) {
-      const double over = (double)u * (double)s_old - ((double)lo + 0.5) * (double)step;
-      z = over > 0.0 ? lo + 1.0f : over < 0.0 ? lo : 2.0f * rintf(0.5f * (lo + 0.5f));
-    }
-    return __float_as_uint(z + (kWhole + 128.0f)) & 0xffu;
-  };
-  auto turned_word = [&](uint32_t x) {
-    return turned(x, 0) | turned(x, 1) << 8 | turned(x, 2) << 16 | turned(x, 3) << 24;
-  };
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int t = i * kTok + sub;
@@ -168,8 +161,7 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(KvView c, KvBatch b, co
       uint2* dst = reinterpret_cast<uint2*>(blk + t * D + Geo::k_piece(t, w >> 1) * 16 + (w & 1) * 8);
       if (t < begin) {
         if (!turn) continue;
-        const uint2 old = *dst;
-        code = make_uint2(turned_word(old.x), turned_word(old.y));
+        code = turn8(*dst, s_old, step);
       }
       if (t < end) *dst = code;
     } else {
@@ -184,7 +176,7 @@ __global__ void __launch_bounds__(256) kv8_append_kernel(KvView c, KvBatch b, co
       if (t0 < begin) {  // the first token of the pair, or both, are older
         if (t0 + 1 < begin && !turn) continue;
         uint2 old = *dst;
-        if (turn) old = make_uint2(turned_word(old.x), turned_word(old.y));
+        if (turn) old = turn8(old, s_old, step);
         const uint32_t keep = t0 + 1 < begin ? 0xffffffffu : 0x00ff00ffu;
         both = make_uint2((old.x & keep) | (both.x & ~keep), (old.y & keep) | (both.y & ~keep));
       }
