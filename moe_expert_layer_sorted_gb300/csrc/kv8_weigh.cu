@@ -77,8 +77,7 @@ __global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_c
   __shared__ uint32_t sh_gone;
   // (four of each: threads that are one barrier ahead write a tile's while others read the last but one's)
   __shared__ float4 sh_col[4][kPrTile / 2];        // two columns' factors and -lse log2 e
-  __shared__ int sh_seen[4][kPrTile];              // tokens that a column sees
-  __shared__ float sh_scale[kPrTile];
+  __shared__ __align__(16) int sh_seen[4][kPrTile];              // tokens that a column sees
   __shared__ float sh_step[kPrTile], sh_sum[kPrTile];
   const KvAttnArgs& a = w.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -124,24 +123,70 @@ __global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_c
     if (lane < 16) sh_step[16 * warp + lane] = pid >= 0 ? *reinterpret_cast<const float*>(blk + Geo::kParams) : 0.0f;
   }
   auto column = [&](int i) { return (tile.c0 + z + i * w.splits) * kPrTile; };
-  // the queries of the i-th column tile, zeros where lse is not finite
-  auto fetch = [&](int i_) {
-    const int x0 = column(i_), b = i_ & 1, slot = i_ & 3, r = tid >> 1, x = x0 + r;
-    float ls = __int_as_float(0x7fffffff);
-    int seen = 0;
-    if (x < tile.nx) {
-      const int i = x / w.per;
-      ls = a.lse[kv_row_index(a.b, tile.s, tile.q.row0, i) * a.q_heads + tile.h * w.per + x % w.per];
-      const int64_t p = tile.first + i;
-      seen = p < 0 ? 0 : (int)min(a.causal ? p + 1 : (int64_t)tile.len, (int64_t)tile.len);
+  // the queries of the i-th column tile, zeros where lse is not finite: asked for, and later written.  D / 8 lanes take a
+  // row, a warp sixteen of them.
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kLoads = 16 / kRows;
+  const int qc = lane % kLanes, qr = 16 * warp + lane / kLanes;
+  uint4 raw[kLoads];
+  float row_lse[kLoads];
+  const uint16_t* const head = a.q + kv_row_offset(a.b, a.qs, tile.s, tile.q.row0, 0) + (int64_t)tile.h * w.per * a.qs.head + 8 * qc;
+  const float* const lse = a.lse + kv_row_index(a.b, tile.s, tile.q.row0, 0) * a.q_heads + tile.h * w.per;
+  auto ask = [&](int i_) {
+    const int x = column(i_) + qr, i = x / w.per;
+    int hq = x - i * w.per;
+    const uint16_t* src = head + i * a.qs.row + hq * a.qs.head;
+    const float* ls = lse + (int64_t)i * a.q_heads + hq;
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) {
+      raw[n] = make_uint4(0, 0, 0, 0);
+      row_lse[n] = __int_as_float(0x7fffffff);
+      if (x + n * kRows < tile.nx) {
+        row_lse[n] = *ls;
+        raw[n] = *reinterpret_cast<const uint4*>(src);
+      }
+      hq += kRows;
+      src += kRows * a.qs.head;
+      ls += kRows;
+      while (hq >= w.per) {  // the next row's first head
+        hq -= w.per;
+        src += a.qs.row - w.per * a.qs.head;
+        ls += a.q_heads - w.per;
+      }
     }
-    const bool fine = fabsf(ls) < __int_as_float(0x7f800000);
-    load_queries<T, D>(gen + kTileBytes * (1 + b), sh_scale, a, tile.s, tile.h, tile.q, w.per, x0, fine ? tile.nx : 0, tid);
-    if (!(tid & 1)) {  // (this thread has written sh_scale[r])
-      float* col = reinterpret_cast<float*>(&sh_col[slot][r >> 1]);
-      col[r & 1] = a.scale * kLog2e * sh_scale[r];
-      col[2 + (r & 1)] = fine ? -ls * kLog2e : -__int_as_float(0x7f800000);
-      sh_seen[slot][r] = seen;
+  };
+  auto put = [&](int i_) {
+    uint8_t* to = gen + kTileBytes * (1 + (i_ & 1)) + (qc / 8) * (kPrTile * 128);
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) {
+      const int r = qr + n * kRows;
+      const bool fine = fabsf(row_lse[n]) < __int_as_float(0x7f800000);
+      if (!fine) raw[n] = make_uint4(0, 0, 0, 0);
+      float back = 1.0f;
+      if constexpr (std::is_same<T, __nv_bfloat16>::value) {  // by the power of two that brings the row to 2^14
+        uint32_t v[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
+        uint32_t top = __vmaxu2(__vmaxu2(v[0] & 0x7fff7fffu, v[1] & 0x7fff7fffu), __vmaxu2(v[2] & 0x7fff7fffu, v[3] & 0x7fff7fffu));
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = max(top >> 16, top & 0xffffu);
+        const int ex = (int)(top >> 7) - 127;
+        const int by = top == 0u || ex > 127 ? 0 : min(max(14 - ex, -113), 113);
+        const float up = pow2(by);
+        back = pow2(-by);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = KvType<__half>::pack(KvType<T>::lo(v[e]) * up, KvType<T>::hi(v[e]) * up);
+        raw[n] = make_uint4(v[0], v[1], v[2], v[3]);
+      }
+      *reinterpret_cast<uint4*>(to + r * 128 + ((qc % 8) ^ (r & 7)) * 16) = raw[n];
+      if (qc == 0) {
+        float* col = reinterpret_cast<float*>(&sh_col[i_ & 3][r >> 1]);
+        col[r & 1] = a.scale * kLog2e * back;
+        col[2 + (r & 1)] = fine ? -row_lse[n] * kLog2e : -__int_as_float(0x7f800000);
+      }
+    }
+    if (tid < kPrTile) {
+      const int x = column(i_) + tid;
+      const int64_t p = tile.first + x / w.per;
+      sh_seen[i_ & 3][tid] = x >= tile.nx || p < 0 ? 0 : (int)min(a.causal ? p + 1 : (int64_t)tile.len, (int64_t)tile.len);
     }
   };
   const uint32_t id = idesc(kPrTile, false);
@@ -155,13 +200,15 @@ __global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_c
              desc_k(qa + (k / 4) * (kPrTile * 128) + (k % 4) * 32), id, k ? 1u : 0u);
     commit(leader, &done[b]);
   };
-  fetch(0);
+  ask(0);
+  put(0);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   fence_before();
   __syncthreads();
   fence_after();
   tm = tmem_base;
   if (warp == 0) multiply(0);
+  if (mine > 1) ask(1);
 
   const int quad = warp & 3, half = warp >> 2;  // the warp's lanes of TMEM, its columns of a tile
   const int token = quad * 32 + lane;
@@ -171,7 +218,7 @@ __global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_c
   for (int i = 0; i < mine; ++i) {
     const int b = i & 1, x0 = column(i);
     if (i + 1 < mine) {  // into the other half, whose products are done
-      fetch(i + 1);
+      put(i + 1);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       fence_before();
       __syncthreads();
@@ -179,35 +226,41 @@ __global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_c
         fence_after();
         multiply(b ^ 1);
       }
+      if (i + 2 < mine) ask(i + 2);  // they arrive during the exponents
     }
     kv_wait(smem_addr(&done[b]), (uint32_t)(i >> 1) & 1u, &sh_gone, w.err);
     fence_after();
     const uint32_t ts = tm + b * kPrTile + half * 64 + ((uint32_t)(quad * 32) << 16);
-    // every column sees the whole token tile?
-    const bool all = tile.first + x0 / w.per >= base + kPrTile - 1 || (!a.causal && tile.first >= 0);
+    auto consume = [&](auto masked_) {
+      constexpr bool masked = decltype(masked_)::value;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      uint32_t v[32];
-      tmem_ld32(ts + 32 * k, v);
-      tmem_wait_ld();
-      const float4* col = &sh_col[i & 3][half * 32 + 16 * k];
+      for (int k = 0; k < 2; ++k) {
+        uint32_t v[32];
+        tmem_ld32(ts + 32 * k, v);
+        tmem_wait_ld();
+        const float4* col = &sh_col[i & 3][half * 32 + 16 * k];
+        const int2* seen = reinterpret_cast<const int2*>(&sh_seen[i & 3][half * 64 + 32 * k]);
 #pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        const float4 f = col[e / 2];
-        uint64_t y = mul2(pair2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), pair2(f.x, f.y));
-        y = fma2(y, ks2, pair2(f.z, f.w));
-        float y0, y1;
-        split2(y, y0, y1);
-        y0 = exp2_fast(y0);
-        y1 = exp2_fast(y1);
-        if (!all) {
-          const int* seen = &sh_seen[i & 3][half * 64 + 32 * k + e];
-          y0 = base + token < seen[0] ? y0 : 0.0f;
-          y1 = base + token < seen[1] ? y1 : 0.0f;
+        for (int e = 0; e < 32; e += 2) {
+          const float4 f = col[e / 2];
+          uint64_t y = mul2(pair2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), pair2(f.x, f.y));
+          y = fma2(y, ks2, pair2(f.z, f.w));
+          float y0, y1;
+          split2(y, y0, y1);
+          y0 = exp2_fast(y0);
+          y1 = exp2_fast(y1);
+          if constexpr (masked) {
+            const int2 n = seen[e / 2];
+            y0 = base + token < n.x ? y0 : 0.0f;
+            y1 = base + token < n.y ? y1 : 0.0f;
+          }
+          sum[e / 2 & 1] = add2(sum[e / 2 & 1], pair2(y0, y1));
         }
-        sum[e / 2 & 1] = add2(sum[e / 2 & 1], pair2(y0, y1));
       }
-    }
+    };
+    // every column sees the whole token tile?
+    if (tile.first + x0 / w.per >= base + kPrTile - 1 || (!a.causal && tile.first >= 0)) consume(std::false_type());
+    else consume(std::true_type());
   }
   float s0, s1;
   split2(add2(sum[0], sum[1]), s0, s1);
