@@ -202,6 +202,7 @@ extern "C" moe_status moe_kv8_evict(moe_kv8_cache* h, int layer, const moe_kv_ba
       why = "budget must be >= 1 and hold keep_first >= 0 and keep_last >= 0 tokens";
     if (!why && !kv->d.mass) why = "the cache has no mass";
     if (why) return fail(kv, MOE_ERR_INVALID, why);
+    if (budget > 1 << 30) return fail(kv, MOE_ERR_UNSUPPORTED, "budget above 2^30 tokens");
     if (batch->batch == 0) return MOE_OK;
     if (!kept) return fail(kv, MOE_ERR_INVALID, "kept is NULL");
     const Kv8EvictArgs a{view(kv, layer), batch_of(batch), mass_of(kv, layer), budget, keep_first, keep_last, kept};

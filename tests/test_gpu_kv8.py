@@ -674,3 +674,100 @@ def test_refusals():
     c.close()
     with pytest.raises(MoeError, match="closed"):
         c.check()
+
+
+def test_a_wait_of_a_prompt_that_runs_out_is_reported():
+    from moe_expert_layer_sorted_gb300 import MoeError
+    w = World(128, 64, BF, 2, [700], seed=6).fill()
+    q = w.rand(1, 300, 4, 128)
+    good, out = torch.empty_like(q), torch.empty_like(q)
+    w.cache.attention(q, good, **w.batch)
+    w.cache.debug_fail_next_attention()
+    w.cache.attention(q, out, **w.batch)
+    torch.cuda.synchronize()
+    with pytest.raises(MoeError) as e:
+        w.cache.check()
+    assert e.value.status == 4
+    w.cache.attention(q, out, **w.batch)
+    torch.cuda.synchronize()
+    w.cache.check()
+    assert torch.equal(out, good)
+
+
+@pytest.mark.parametrize("rows", [1, 4, 90])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_queries_that_are_not_finite_harm_no_other_row(rows, dtype):
+    """A query row and head with an infinity or a NaN is NaN and weighs nothing; the others are what they were, within
+    each row's own bound (not to the bit: 32 rows share the moments at which their references rise, and whichever these
+    are, a row is within its bound of the exact value)."""
+    w = World(64, 16, dtype, 2, [150], seed=rows).fill()
+    q = w.rand(rows, 8, 64)
+    bad = q.clone()
+    hit = torch.zeros(rows, 8, dtype=torch.bool, device="cuda")
+    for r, h, x in ((0, 1, math.nan), (rows - 1, 6, math.inf), (rows // 2, 5, -math.inf)):
+        bad[r, h, 7] = x
+        hit[r, h] = True
+    out, ls = run_attention_raw(w, bad, 0.125, weigh=True)
+    assert torch.isnan(out[hit]).all() and not torch.isfinite(ls[hit]).any()
+    full = expected(w, 0, q, 0.125)
+    ref.check(out[~hit], ls[~hit], [x[~hit] for x in full])
+    full[2][hit] = 0
+    add, tol = ref.masses(full, 2)
+    assert ((w.mass_of(0).double() - add).abs() <= tol + 2.0 ** -23 * add).all()
+
+
+@pytest.mark.parametrize("rows,lens", [(1, [70, 0, 33]), (5, [70, 0, 33]), (64, [130, 0, 64])])
+def test_weights_without_room_for_scores(rows, lens):
+    """A table of so many pages that scores would not fit the workspace: made again from the keys, the same sums."""
+    w = World(64, 256, BF, 4, lens, seed=rows).fill()
+    wide = torch.full((3, 1 << 15), -1, dtype=torch.int32, device="cuda")  # 8,388,608 tokens a sequence
+    wide[:, :w.cols] = w.table
+    w.table = wide
+    run_attention(w, [rows] * 3, 8, ragged=False, weigh=True)
+
+
+def test_tables_with_strides_and_lengths_beyond_them():
+    """Rows of a wider table; lens larger than its pages hold: what is there counts, in every call."""
+    w = World(64, 16, BF, 2, [64, 50], seed=2).fill()
+    wide = torch.full((2, 9), 1 << 29, dtype=torch.int32, device="cuda")
+    wide[:, 2:2 + w.cols] = w.table
+    w.table = wide[:, 2:2 + w.cols]
+    q = w.rand(2, 1, 4, 64)
+    out, ls = torch.empty_like(q), torch.empty(2, 4, device="cuda")
+    w.cache.attention(q, out, table=w.table, lens=w.lens_t, lse=ls, weigh=True)
+    for i in range(2):
+        ref.check(out[i], ls[i:i + 1], expected(w, i, q[i]))
+    w.lens_t = ints([1000, 50])
+    kept = torch.empty(2, 2, 40, dtype=torch.int32, device="cuda")
+    masses = [w.mass_of(i).clone() for i in range(2)]
+    w.cache.evict(kept, keep_first=1, keep_last=2, **w.batch)
+    for i, n in enumerate((64, 50)):
+        for h in range(2):
+            assert kept[i, h].tolist() == ref.kept(masses[i][:n, h].tolist(), 40, 1, 2)
+        w.stored[i].keep(kept[i].long())
+    w.holds([40, 40])
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_turned_codes_at_every_ratio_of_steps(dtype):
+    """Steps whose ratios are simple fractions (quotients near and on halves), powers of two, near one and tiny: codes
+    moved by an eviction, and older codes of a block that grows."""
+    n = 16 * 40
+    w = World(64, 16, dtype, 1, [n], seed=1)
+    codes = torch.arange(-127, 128, device="cuda", dtype=torch.float64)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    tops = [127.0, 254.0, 96.0, 192.0, 160.0, 200.0, 128.0, 64.0, 255.0, 253.0, 129.0, 1.0, 0.5, 3.0, 5.0, 6.0, 7.0, 9.0, 2.0 ** -10, 0.0]
+    x = torch.empty(n, 64, dtype=torch.float64, device="cuda")
+    for b in range(40):
+        top = tops[b % len(tops)]
+        pick = codes[torch.randint(0, 255, (16, 64), generator=g, device="cuda")] * (top / 127)
+        pick[0, 0] = top
+        x[16 * b:16 * b + 16] = pick
+    w.k[0] = x[:, None].to(dtype)
+    w.v[0] = x.flip(0)[:, None].to(dtype).contiguous()
+    w.fill([3, 5])
+    w.holds()
+    mass = torch.rand(n, 1, generator=g, device="cuda")
+    run_evict(w, 200, 0, 0, [mass])
+    w.lens, w.lens_t = [200], ints([200])
+    run_evict(w, 77, 1, 1, [mass[:200].contiguous()])
