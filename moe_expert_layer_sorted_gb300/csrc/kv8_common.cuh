@@ -102,6 +102,12 @@ __device__ __forceinline__ uint32_t kv8_word(uint64_t a, uint64_t b) {
   return __byte_perm(__byte_perm((uint32_t)a, (uint32_t)(a >> 32), 0x0040), __byte_perm((uint32_t)b, (uint32_t)(b >> 32), 0x0040),
                      0x5410);
 }
+// Codes of a word (u + 128 in each byte) times ratio, the products rounded to whole numbers.
+__device__ __forceinline__ uint32_t kv8_scale(uint32_t w, float ratio) {
+  const uint64_t f = kv8_two(ratio, ratio), whole = kv8_two(kKv8Whole, kKv8Whole), zero = kv8_two(-8388736.0f, -8388736.0f);
+  auto raw = [&](int i) { return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540 | i)); };
+  return kv8_word(kv8_fma2(kv8_add2(kv8_two(raw(0), raw(1)), zero), f, whole), kv8_fma2(kv8_add2(kv8_two(raw(2), raw(3)), zero), f, whole));
+}
 // Codes of a word (u + 128 in each byte) times ratio, rounded; the bits of those near a half in the mask's lowest
 // four, the first byte's the highest.
 __device__ __forceinline__ uint32_t kv8_turn(uint32_t w, float ratio, uint32_t& mask) {

@@ -61,52 +61,67 @@ __device__ __forceinline__ int cta_scan(int v, int* sh) {
   return v;
 }
 
-// Words of a token's codes, of a step s that is `ratio` (rounded) times the new one, `to`; the token's other words are
-// in the lanes of `group`, with the same numbers.
+// What a token's codes of step s are multiplied with to become codes of step `to` >= s, so that a product rounded to a
+// whole number in fp32 is u s / to to the nearest one; ties: the quotients' halves are to be told apart by turn_words.
 //
-// Of one token, the quotients u s / to that are near a half are all near ties of one fraction: s / to is then within
-// 2e-5 / u of a p / q with q <= 254, and two such fractions are further apart.  So they lie on the same side of their
-// half (mirrored for negative u), and one of them, settled exactly, says on which: a ratio moved by 2^-20 that way rounds
-// all of them rightly, and every other code, which is at least 1 / (2 q) away from a half, as before.  Where s / to is
-// that fraction itself the ties are even ones: right already if ratio is exact, else settled one by one.
+// s / to itself, rounded, is wrong near halves, and these are not rare: steps are 127ths of 16-bit numbers, and the
+// quotients of their codes halves of fractions with small denominators, but for a few 2^-24.  If some u s / to is within
+// 2e-5 of a half, s / to is within 2e-5 / u of a fraction p / q with q <= 254, which is then the last of its continued
+// fraction's convergents with such a q (and the only such fraction).  All quotients near halves then lie on the same
+// side of them, s / to's side of p / q (mirrored for negative u): a ratio moved by 2^-20 that way rounds all of them
+// rightly, and every other code, which is at least 1 / (2 q) from a half, as before.  Where s / to is p / q they are ties.
+struct Ratio {
+  float r;
+  bool ties;  // and r is not exact
+};
+__device__ __forceinline__ Ratio ratio_of(float s, float to) {
+  const float up = kv8_lift(to);
+  s *= up;
+  to *= up;
+  if (!(s < to) || s == 0.0f) return {s < to ? 0.0f : 1.0f, false};
+  const float r = __fdiv_rn(s, to);
+  const uint32_t sb = __float_as_uint(s), tb = __float_as_uint(to);
+  const int d = (int)(tb >> 23) - (int)(sb >> 23);
+  if (d > 8) return {0.0f, false};  // below a half with every code
+  // s / to = S / T in whole numbers of up to 24 and 32 bits
+  const uint32_t S = (sb & 0x7fffffu) | 0x800000u, T = ((tb & 0x7fffffu) | 0x800000u) << d;
+  uint32_t a = T, b = S, p0 = 1, q0 = 0, p = 0, q = 1;
+  while (b != 0) {
+    const uint32_t k = a / b, left = a - k * b;
+    if (k > 254u || k * q + q0 > 254u) break;
+    a = b;
+    b = left;
+    const uint32_t pn = k * p + p0, qn = k * q + q0;
+    p0 = p;
+    q0 = q;
+    p = pn;
+    q = qn;
+  }
+  const int over = (int)(S * q - p * T);  // below T / 254, so 32 bits tell it
+  if (over == 0) return {r, fmaf(-r, to, s) != 0.0f};
+  if ((uint32_t)abs(over) > (T >> 15)) return {r, false};
+  return {fmaf(r, over > 0 ? 0x1p-20f : -0x1p-20f, r), false};
+}
+
+// Words of codes times their ratio.  ties: some lane's are (then rounded up and down, and the even one taken).
 template <int N>
-__device__ __forceinline__ void turn_words(const uint32_t (&w)[N], uint32_t (&o)[N], float s, float to, float ratio, uint32_t group) {
-  if (__all_sync(0xffffffffu, s == to)) {
+__device__ __forceinline__ void turn_words(const uint32_t (&w)[N], uint32_t (&o)[N], float ratio, bool ties) {
+  if (__any_sync(0xffffffffu, ties)) {
+    const float by = ties ? 0x1p-20f : 0.0f;
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+      const float r = fmaf(ratio, side ? by : -by, ratio);
 #pragma unroll
-    for (int n = 0; n < N; ++n) o[n] = w[n];
+      for (int n = 0; n < N; ++n) {
+        const uint32_t x = kv8_scale(w[n], r);
+        const uint32_t odd = (x & 0x01010101u) * 255u;
+        o[n] = side ? (o[n] & odd) | (x & ~odd) : x;
+      }
+    }
     return;
   }
-  uint32_t near = 0;  // a bit per byte, the first one's the highest
 #pragma unroll
-  for (int n = 0; n < N; ++n) o[n] = kv8_turn(w[n], ratio, near);
-  const uint32_t votes = __ballot_sync(0xffffffffu, near != 0);
-  if (votes == 0) return;
-  float side = 0.0f;
-  if (near) {
-    const int at = 4 * N - 1 - (31 - __clz(near));
-    uint32_t x = w[0];
-#pragma unroll
-    for (int n = 1; n < N; ++n) x = at / 4 == n ? w[n] : x;
-    const float u = (float)((int)((x >> (8 * (at & 3))) & 0xffu) - 128), half = floorf(u * ratio) + 0.5f;
-    const float p = u * s, q = half * to, over = (p - q) + (fmaf(u, s, -p) - fmaf(half, to, -q));
-    side = over == 0.0f ? 0.0f : (over > 0.0f) == (u > 0.0f) ? 0x1p-20f : -0x1p-20f;
-  }
-  const uint32_t mine = votes & group;
-  side = __shfl_sync(0xffffffffu, side, mine ? __ffs(mine) - 1 : 0);
-  if (mine && side != 0.0f) {
-    const float moved = fmaf(ratio, side, ratio);
-    uint32_t unused = 0;
-#pragma unroll
-    for (int n = 0; n < N; ++n) o[n] = kv8_turn(w[n], moved, unused);
-  } else if (near && fmaf(-ratio, to, s) != 0.0f) {
-#pragma unroll 1
-    for (; near; near &= near - 1) {
-      const int at = 4 * N - __ffs(near), shift = 8 * (at & 3);
-#pragma unroll
-      for (int n = 0; n < N; ++n)
-        if (at / 4 == n) o[n] = (o[n] & ~(0xffu << shift)) | kv8_settle_byte(w[n], at & 3, s, to, ratio) << shift;
-    }
-  }
+  for (int n = 0; n < N; ++n) o[n] = kv8_scale(w[n], ratio);
 }
 
 template <int D, int kEvThreads>
@@ -341,17 +356,20 @@ __global__ void __launch_bounds__(kEvThreads, 512 / kEvThreads) kv8_evict_kernel
         k_to = fmaxf(k_to, __shfl_xor_sync(0xffffffffu, k_to, o));
         v_to = fmaxf(v_to, __shfl_xor_sync(0xffffffffu, v_to, o));
       }
-      // what every token's codes are multiplied with
-      const float up_k = kv8_lift(k_to), up_v = kv8_lift(v_to), kt = k_to * up_k, vt = v_to * up_v;
-      const float kr = kt > 0.0f ? __fdiv_rn(ks * up_k, kt) : 0.0f, vr = vt > 0.0f ? __fdiv_rn(vs * up_v, vt) : 0.0f;
+      // what the tokens' codes are multiplied with: the keys' in lanes 0 to 15, the values' in 16 to 31
+      const Ratio ratio = ratio_of(lane < 16 ? ks : vs, lane < 16 ? k_to : v_to);
+      if (__all_sync(0xffffffffu, ratio.r == 1.0f)) {  // nothing to turn: of one step, all of them
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int t = (i * 32 + lane) / (D / 16);
-        const uint32_t w[4] = {kw[i].x, kw[i].y, kw[i].z, kw[i].w};
-        uint32_t o[4];
-        turn_words(w, o, __shfl_sync(0xffffffffu, ks * up_k, t), kt, __shfl_sync(0xffffffffu, kr, t),
-                   ((1u << (D / 16)) - 1u) << (lane & ~(D / 16 - 1)));
-        ko[i] = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int i = 0; i < kLoads; ++i) ko[i] = kw[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int t = (i * 32 + lane) / (D / 16);
+          const uint32_t w[4] = {kw[i].x, kw[i].y, kw[i].z, kw[i].w};
+          uint32_t o[4];
+          turn_words(w, o, __shfl_sync(0xffffffffu, ratio.r, t), __shfl_sync(0xffffffffu, (int)ratio.ties, t));
+          ko[i] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
       }
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
@@ -361,8 +379,7 @@ __global__ void __launch_bounds__(kEvThreads, 512 / kEvThreads) kv8_evict_kernel
           const int t = (i * 32 + lane) / (D / 8) * 2 + y;
           const uint32_t sel = __shfl_sync(0xffffffffu, src, t) & 1 ? 0x7531 : 0x6420;  // the token's byte of every pair
           const uint32_t w[2] = {__byte_perm(vw[i][y].x, vw[i][y].y, sel), __byte_perm(vw[i][y].z, vw[i][y].w, sel)};
-          turn_words(w, o[y], __shfl_sync(0xffffffffu, vs * up_v, t), vt, __shfl_sync(0xffffffffu, vr, t),
-                     ((1u << (D / 8)) - 1u) << (lane & ~(D / 8 - 1)));
+          turn_words(w, o[y], __shfl_sync(0xffffffffu, ratio.r, 16 + t), __shfl_sync(0xffffffffu, (int)ratio.ties, 16 + t));
         }
         vo[i] = make_uint4(__byte_perm(o[0][0], o[1][0], 0x5140), __byte_perm(o[0][0], o[1][0], 0x7362),
                            __byte_perm(o[0][1], o[1][1], 0x5140), __byte_perm(o[0][1], o[1][1], 0x7362));
