@@ -19,6 +19,7 @@ namespace cg = cooperative_groups;
 
 namespace {
 
+constexpr int kEvThreads = 256, kEvWarps = kEvThreads / 32;
 constexpr int kEvBins = 2048;
 constexpr int kEvKeys = 16384;  // that a CTA keeps in shared memory; of longer shares they are read again
 constexpr int kEvMaxCluster = 16;
@@ -44,7 +45,6 @@ struct Head {  // a sequence's kv head
 };
 
 // Inclusive prefix sum of v over the CTA.
-template <int kEvWarps>
 __device__ __forceinline__ int cta_scan(int v, int* sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -124,10 +124,9 @@ __device__ __forceinline__ void turn_words(const uint32_t (&w)[N], uint32_t (&o)
   for (int n = 0; n < N; ++n) o[n] = kv8_scale(w[n], ratio);
 }
 
-template <int D, int kEvThreads>
-__global__ void __launch_bounds__(kEvThreads, 512 / kEvThreads) kv8_evict_kernel(const __grid_constant__ Kv8EvictArgs a) {
+template <int D>
+__global__ void __launch_bounds__(kEvThreads, 2) kv8_evict_kernel(const __grid_constant__ Kv8EvictArgs a) {
   using Geo = Kv8Geom<D>;
-  constexpr int kEvWarps = kEvThreads / 32;
   extern __shared__ uint32_t keys[];  // of this CTA's tokens
   __shared__ __align__(16) int hist[2][kEvBins];
   __shared__ int sh_scan[kEvWarps];
@@ -198,7 +197,7 @@ __global__ void __launch_bounds__(kEvThreads, 512 / kEvThreads) kv8_evict_kernel
         mine[y] = hist[buf][kEvBins - 1 - (tid * kMine + y)];
         sum += mine[y];
       }
-      int above = cta_scan<kEvWarps>(sum, sh_scan) - sum;
+      int above = cta_scan(sum, sh_scan) - sum;
 #pragma unroll
       for (int y = 0; y < kMine; ++y) {
         if (above < need && above + mine[y] >= need) {
@@ -409,9 +408,9 @@ __global__ void __launch_bounds__(kEvThreads, 512 / kEvThreads) kv8_evict_kernel
   }
 }
 
-template <int D, int Threads>
+template <int D>
 cudaError_t evict(const Kv8EvictArgs& a, int ctas, cudaStream_t s) {
-  const auto kernel = kv8_evict_kernel<D, Threads>;
+  const auto kernel = kv8_evict_kernel<D>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), kEvKeys * sizeof(uint32_t));
   if (e == cudaSuccess && ctas > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
@@ -421,7 +420,7 @@ cudaError_t evict(const Kv8EvictArgs& a, int ctas, cudaStream_t s) {
   attr.val.clusterDim.x = (unsigned)ctas;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.gridDim = dim3((unsigned)((int64_t)a.b.batch * a.c.heads * ctas));
-  cfg.blockDim = dim3(Threads);
+  cfg.blockDim = dim3(kEvThreads);
   cfg.dynamicSmemBytes = kEvKeys * sizeof(uint32_t);
   cfg.stream = s;
   cfg.attrs = &attr;
@@ -434,10 +433,10 @@ cudaError_t evict(const Kv8EvictArgs& a, int ctas, cudaStream_t s) {
 cudaError_t moe::kv8_evict(const Kv8& kv, const Kv8EvictArgs& a, cudaStream_t s) {
   const int64_t items = (int64_t)a.b.batch * a.c.heads, cap = (int64_t)a.b.table_pages << a.c.page_shift;
   int ctas = kEvMaxCluster;
-  // as many as two a multiprocessor hold at once, and as have some tokens each
+  // as many as two a multiprocessor hold at once, and as have some tokens each.  Measured, one sequence of 131,072
+  // tokens, 8 heads: 16 CTAs of 256 threads 232 us, 16 of 512 (of which half the clusters wait for the others) 254, 8 of
+  // 512 236, 8 of 256 371.
   while (ctas > 1 && (items * ctas > 2 * kv.sms || ctas * 1024 > cap)) ctas >>= 1;
   if (items * ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  const bool wide = items * ctas <= kv.sms;  // a multiprocessor each: twice the warps
-  if (kv.d.head_dim == 64) return wide ? evict<64, 512>(a, ctas, s) : evict<64, 256>(a, ctas, s);
-  return wide ? evict<128, 512>(a, ctas, s) : evict<128, 256>(a, ctas, s);
+  return kv.d.head_dim == 64 ? evict<64>(a, ctas, s) : evict<128>(a, ctas, s);
 }
