@@ -2,7 +2,7 @@
 // query heads that see the token, are added to the token's mass.
 //
 // With lse from the attention a weight is 2^(y - lse log2 e), y the score in log2 units.  Where the
-// single-token kernel has written its scores (kv8_decode.cuh), a thread adds up a token's.  Otherwise the
+// single-token kernel has written its scores (kv8_decode.cuh), a thread adds up four tokens'.  Otherwise the
 // scores are made again, transposed, on the tensor cores, and the sums run along registers:
 //     S^T = U_K Q^T   (128 tokens by 128 columns (row, query head) in TMEM),
 // a thread having a token (a TMEM lane) and half of the columns.  A column's power of two and lse come from
@@ -290,36 +290,48 @@ __global__ void __launch_bounds__(kPrTile) kv8_weigh_join_kernel(const __grid_co
   add_mass(w, tile.s, tile.h, pos, sum);
 }
 
-// From the scores that the single-token kernel wrote: a thread adds up a token's columns.
-__global__ void __launch_bounds__(256) kv8_weigh_scores_kernel(const __grid_constant__ WeighArgs w, const float* __restrict__ scores,
-                                                               int width, int chunks) {
+// From the scores that the single-token kernel wrote: a thread adds up the columns of four tokens (of one page).
+constexpr int kWeTokens = 4 * kWeThreads;
+__global__ void __launch_bounds__(kWeThreads) kv8_weigh_scores_kernel(const __grid_constant__ WeighArgs w, const float* __restrict__ scores,
+                                                                      int width, int chunks) {
   __shared__ float sh_lse[32];
   const KvAttnArgs& a = w.a;
-  const int h = blockIdx.x % a.c.heads, s = blockIdx.x / a.c.heads / chunks;
-  const int pos = blockIdx.x / a.c.heads % chunks * 256 + threadIdx.x;
+  const int h = blockIdx.x % a.c.heads, s = blockIdx.x / a.c.heads / chunks, chunk = blockIdx.x / a.c.heads % chunks;
   const KvSeq q = kv_seq(a.b, s);
-  const int cols = q.rows * w.per;
-  if (blockIdx.x / a.c.heads % chunks * 256 >= min(q.len, kv_capacity(a.c, a.b))) return;
+  const int cols = q.rows * w.per, len = min(q.len, kv_capacity(a.c, a.b));
+  if ((int64_t)chunk * kWeTokens >= len) return;
   if ((int)threadIdx.x < cols) {
     const float ls = a.lse[kv_row_index(a.b, s, q.row0, threadIdx.x / w.per) * a.q_heads + h * w.per + threadIdx.x % w.per];
     sh_lse[threadIdx.x] = fabsf(ls) < __int_as_float(0x7f800000) ? ls * kLog2e : __int_as_float(0x7f800000);
   }
+  const int pos = chunk * kWeTokens + 4 * threadIdx.x, n = min(len - pos, 4);
+  const int64_t pid = n > 0 ? kv_page(a.c, a.b, s, pos >> a.c.page_shift) : -1;
   __syncthreads();
-  if (pos >= min(q.len, kv_capacity(a.c, a.b))) return;
-  const int64_t pid = kv_page(a.c, a.b, s, pos >> a.c.page_shift);
   if (pid < 0) return;
   float* mass = w.mass + (pid * a.c.heads + h) * a.c.page_size + (pos & (a.c.page_size - 1));
   const float4* y = reinterpret_cast<const float4*>(scores + (((int64_t)s * a.c.heads + h) * kv_capacity(a.c, a.b) + pos) * width);
-  const float had = *mass;
-  float sum = 0.0f;
+  const float4 had = *reinterpret_cast<const float4*>(mass);
+  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int x = 0; x < cols; x += 4) {
-    const float4 v = y[x / 4];
-    const float e[4] = {v.x, v.y, v.z, v.w};
+    float4 v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (x + i < cols && sh_lse[x + i] != __int_as_float(0x7f800000)) sum += exp2_fast(e[i] - sh_lse[x + i]);
+    for (int t = 0; t < 4; ++t) v[t] = y[(t * width + x) / 4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float ls = x + i < cols ? sh_lse[x + i] : __int_as_float(0x7f800000);
+      if (ls == __int_as_float(0x7f800000)) continue;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) sum[t] += exp2_fast((i == 0 ? v[t].x : i == 1 ? v[t].y : i == 2 ? v[t].z : v[t].w) - ls);
+    }
   }
-  *mass = had + sum;
+  const float now[4] = {had.x + sum[0], had.y + sum[1], had.z + sum[2], had.w + sum[3]};
+  if (n == 4) {
+    *reinterpret_cast<float4*>(mass) = make_float4(now[0], now[1], now[2], now[3]);
+  } else {
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      if (t < n) mass[t] = now[t];
+  }
 }
 
 }  // namespace
@@ -328,9 +340,9 @@ cudaError_t moe::kv8_weigh(Kv8& kv, const KvAttnArgs& a, float* mass, const floa
   WeighArgs w{a, mass, a.q_heads / a.c.heads, 0, 1, kv.parts(), kv.err_dev};
   const int64_t cap = std::min<int64_t>((int64_t)a.b.table_pages << a.c.page_shift, 0x7ffff000);
   if (scores) {
-    const int64_t chunks = (cap + 255) / 256, ctas = chunks * a.c.heads * a.b.batch;
+    const int64_t chunks = (cap + kWeTokens - 1) / kWeTokens, ctas = chunks * a.c.heads * a.b.batch;
     if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    kv8_weigh_scores_kernel<<<(unsigned)ctas, 256, 0, s>>>(w, scores, score_width(a), (int)chunks);
+    kv8_weigh_scores_kernel<<<(unsigned)ctas, kWeThreads, 0, s>>>(w, scores, score_width(a), (int)chunks);
     return cudaGetLastError();
   }
   const int64_t tiles = (cap + kPrTile - 1) / kPrTile, items = tiles * a.c.heads * a.b.batch;
