@@ -5,15 +5,23 @@ using namespace moe;
 
 // By columns (rows of a sequence times the query heads that share a kv head).  The single-token
 // kernel reads the cache once per 16 columns (8 where there are no more), the prompt kernel
-// once per 256 but turns every code into shared memory first.
+// once per 256 but turns every code into shared memory first.  Measured, both kernels, us (8 kv heads
+// of 128 channels, bf16; single tokens / prompts):
+//     columns                        8         16          32         64
+//     1 sequence of 2,048        12.5 / 21   14.6 / 21   15.1 / 21   - / 21
+//     1 of 131,072                 54 / 131    74 / 131   129 / 131  - / 131
+//     16 of 4,096                  36 / 72     48 / 72     81 / 73   - / 74
+//     64 of 2,048                  57 / 153    90 / 154   158 / 154  - / 155
 //
 // Weights: the single-token kernel leaves its scores behind where the workspace holds them, four
 // bytes a token and column beside the 256 that it reads; otherwise they are made again from the keys.
+// Attention and weights, scores left / made again: 16 columns of 1 sequence of 131,072 108 / 333, of 64 of
+// 2,048 127 / 358.
 cudaError_t moe::kv8_attention(Kv8& kv, const KvAttnArgs& a, float* mass, cudaStream_t s) {
   const bool bf16 = kv.d.dtype == MOE_KV_BF16;
   cudaError_t e;
   float* scores = nullptr;
-  if ((int64_t)a.b.max_new * (a.q_heads / a.c.heads) <= 32) {
+  if ((int64_t)a.b.max_new * (a.q_heads / a.c.heads) <= kKv8Columns) {
     const int64_t cap = std::min<int64_t>((int64_t)a.b.table_pages << a.c.page_shift, 0x7ffff000);
     const double floats = (double)a.b.batch * a.c.heads * (double)cap * score_width(a);
     if (mass && floats * 4 <= (double)Kv8::kScoreBytes) scores = kv.scores();

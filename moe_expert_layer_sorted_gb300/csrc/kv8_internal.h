@@ -48,6 +48,8 @@ cudaError_t kv8_read(const Kv8& kv, const KvView& c, const KvBatch& b, uint16_t*
 // [sequence][kv head][token of the table][score_width] by columns (row, query head), -infinity where not seen.
 cudaError_t kv8_decode_bf16(Kv8& kv, const KvAttnArgs& a, float* scores, cudaStream_t s);
 cudaError_t kv8_decode_f16(Kv8& kv, const KvAttnArgs& a, float* scores, cudaStream_t s);
+// Columns (row, query head) of a kv head that are few.
+constexpr int kKv8Columns = 32;
 inline int score_width(const KvAttnArgs& a) { return (int)(((int64_t)a.b.max_new * (a.q_heads / a.c.heads) + 3) / 4 * 4); }
 // Attention of prompts.
 cudaError_t kv8_prompt_bf16(Kv8& kv, const KvAttnArgs& a, cudaStream_t s);

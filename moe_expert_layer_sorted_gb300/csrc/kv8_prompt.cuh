@@ -30,6 +30,15 @@
 //
 // Masks: a score that its row may not see becomes -infinity.  Tokens that are not finite
 // have codes of zeros; a row that sees one is remembered, and NaN in the end.
+//
+// Measured (bf16, 32 query and 8 kv heads of 128 channels): 8,192 rows at the end of 16,384 tokens 1,301 us, 1,270
+// TFLOP/s (0.65 of the measured rate); with scores that never raise a reference 1,261; 4,096 rows (fp16) 158 us.
+// Bound by two things of about the same length: the chain of a token tile, scores -> weights -> product, of which
+// two row tiles alternate (without the loads of codes and the exponents it takes 1,130 us), and the warps that turn
+// codes (without their loads 1,219).  What paid: a tile's words asked for as soon as the last one's are turned, what
+// the softmax wants to know of a tile worked out a tile ahead (1,446 -> 1,267 us with scores that never raise).  Three
+// ragged prompts of up to 333 rows over up to 2,500 tokens (fp16, 12 heads of 64): 39 us, ten token tiles one
+// after the other, launch and join.
 #pragma once
 
 #include "kv8_internal.h"
