@@ -521,7 +521,7 @@ typedef struct moe_kv8_desc {
 moe_status moe_kv8_sizes(const moe_kv8_desc* desc, int64_t* page_bytes_per_layer, int64_t* mass_bytes_per_layer);
 
 /* As moe_kv_create, moe_kv_destroy, moe_kv_status and
- * moe_kv_debug_fail_next_attention (a workspace of 24 MB, with mass 152 MB). */
+ * moe_kv_debug_fail_next_attention (a workspace of 24 MB, with mass 153 MB). */
 moe_status moe_kv8_create(const moe_kv8_desc* desc, moe_kv8_cache** out);
 moe_status moe_kv8_destroy(moe_kv8_cache* kv);
 moe_status moe_kv8_status(moe_kv8_cache* kv);
@@ -546,7 +546,8 @@ moe_status moe_kv8_read(moe_kv8_cache* kv, int layer, const moe_kv_batch* batch,
  * token of NaN keys or values is NaN.  weigh = 1: after it, every token's softmax
  * weights of this call, summed over the rows and query heads that see it (in fp32,
  * in an order that does not depend on timing), are added to its mass; needs mass and lse.  Rows whose lse is
- * not finite add nothing.
+ * not finite add nothing.  Pages must then not be shared between the sequences of the call (their tokens' mass is
+ * read, added to and written without regard to another's).
  * Accuracy: scores, weights and sums are fp32 and the codes are exact operands; a weight enters the
  * product with the values with 11 bits, relative to the largest weight times step of its row (below 2^-24 of
  * that it loses bits). */

@@ -20,11 +20,16 @@ using namespace moe;
 cudaError_t moe::kv8_attention(Kv8& kv, const KvAttnArgs& a, float* mass, cudaStream_t s) {
   const bool bf16 = kv.d.dtype == MOE_KV_BF16;
   cudaError_t e;
-  float* scores = nullptr;
-  if ((int64_t)a.b.max_new * (a.q_heads / a.c.heads) <= kKv8Columns) {
-    const int64_t cap = std::min<int64_t>((int64_t)a.b.table_pages << a.c.page_shift, 0x7ffff000);
-    const double floats = (double)a.b.batch * a.c.heads * (double)cap * score_width(a);
-    if (mass && floats * 4 <= (double)Kv8::kScoreBytes) scores = kv.scores();
+  Kv8Scores scores{};
+  const int64_t columns = (int64_t)a.b.max_new * (a.q_heads / a.c.heads);
+  if (columns <= kKv8Columns) {
+    if (mass && a.b.batch <= Kv8::kScoreSeqs) {
+      scores.to = kv.scores();
+      scores.base = kv.score_bases();
+      scores.width = std::min((int)(columns + 3) / 4 * 4, 16);
+      scores.ctiles = columns > 16 ? 2 : 1;  // as the kernel has them
+      scores.limit = (int)(Kv8::kScoreBytes / (128 * sizeof(float) * scores.width));
+    }
     e = bf16 ? kv8_decode_bf16(kv, a, scores, s) : kv8_decode_f16(kv, a, scores, s);
   } else {
     e = bf16 ? kv8_prompt_bf16(kv, a, s) : kv8_prompt_f16(kv, a, s);

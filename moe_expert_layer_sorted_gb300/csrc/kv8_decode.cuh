@@ -58,7 +58,7 @@ constexpr int kDec8Slot = D == 128 ? Kv8Geom<D>::kBytes : 2560;
 template <typename T, int D, int NT, bool W>
 __global__ void __launch_bounds__(kDec8Threads, NT == 1 ? 2 : 1)
     kv8_decode_kernel(const __grid_constant__ KvAttnArgs a, const __grid_constant__ DecPlan p, float* __restrict__ ws,
-                      unsigned* __restrict__ counters, uint32_t* err, float* __restrict__ scores, int width) {
+                      unsigned* __restrict__ counters, uint32_t* err, const __grid_constant__ Kv8Scores scores) {
   using Geo = Kv8Geom<D>;
   constexpr int C = 8 * NT, S = kDec8Slots<NT>;
   constexpr int kPart = C * (D + 2);  // floats of one partial result: O [C][D], max [C], sum [C]
@@ -197,6 +197,8 @@ __global__ void __launch_bounds__(kDec8Threads, NT == 1 ? 2 : 1)
         cc.enter(a, p, seg);
         const KvSeq q = kv_seq(a.b, cc.group);
         store(it.at, cc);
+        if constexpr (W)
+          if (cc.item == 0 && cc.item0 == seg) scores.base[cc.group] = cc.end <= scores.limit ? seg : -1;
         it.s = cc.group;
         it.head = cc.item / p.ctiles;
         it.ctile = cc.item % p.ctiles;
@@ -312,14 +314,15 @@ __global__ void __launch_bounds__(kDec8Threads, NT == 1 ? 2 : 1)
               if (pos + r + 8 * (e >> 1) >= seen[nt][e & 1]) y[nt][e] = -__int_as_float(0x7f800000);
         }
         if constexpr (W) {
-          const int col = it.ctile * C + 2 * c;
-          float* to = scores + (((int64_t)it.s * a.c.heads + it.head) * kv_capacity(a.c, a.b) + pos + r) * width + col;
+          if (it.at.end <= scores.limit) {
+            float* to = scores.to + ((int64_t)it.at.item0 * (16 * kDecWarps) + pos + r) * scores.width + 2 * c;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            if (col + 8 * nt < width) {
-              *reinterpret_cast<float2*>(to + 8 * nt) = make_float2(y[nt][0], y[nt][1]);
-              *reinterpret_cast<float2*>(to + 8 * nt + 8 * width) = make_float2(y[nt][2], y[nt][3]);
-            }
+            for (int nt = 0; nt < NT; ++nt)
+              if (2 * c + 8 * nt < scores.width) {
+                *reinterpret_cast<float2*>(to + 8 * nt) = make_float2(y[nt][0], y[nt][1]);
+                *reinterpret_cast<float2*>(to + 8 * nt + 8 * scores.width) = make_float2(y[nt][2], y[nt][3]);
+              }
+          }
         }
         // ---- references
         bool raise = false;
@@ -551,21 +554,21 @@ __global__ void __launch_bounds__(kDec8Threads, NT == 1 ? 2 : 1)
 }
 
 template <typename T, int D, int NT>
-cudaError_t launch_decode8(Kv8& kv, const KvAttnArgs& a, const DecPlan& p, float* scores, cudaStream_t s) {
+cudaError_t launch_decode8(Kv8& kv, const KvAttnArgs& a, const DecPlan& p, const Kv8Scores& scores, cudaStream_t s) {
   constexpr int C = 8 * NT;
   const size_t smem = (size_t)kDecWarps * kDec8Slots<NT> * kDec8Slot<D>;
-  const auto kernel = scores ? kv8_decode_kernel<T, D, NT, true> : kv8_decode_kernel<T, D, NT, false>;
+  const auto kernel = scores.to ? kv8_decode_kernel<T, D, NT, true> : kv8_decode_kernel<T, D, NT, false>;
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
   const int grid = std::min(kv.sms * 2, kDec8MaxParts) / NT;
   static_assert(kDec8MaxParts <= Kv8::kCounters, "a counter per CTA");
   static_assert(2 * (size_t)kDec8MaxParts * C * (D + 2) * sizeof(float) <= Kv8::kPartsBytes, "two partial results per CTA");
-  kernel<<<grid, kDec8Threads, smem, s>>>(a, p, kv.parts(), kv.counters(), kv.err_dev, scores, score_width(a));
+  kernel<<<grid, kDec8Threads, smem, s>>>(a, p, kv.parts(), kv.counters(), kv.err_dev, scores);
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t decode8(Kv8& kv, const KvAttnArgs& a, float* scores, cudaStream_t s) {
+cudaError_t decode8(Kv8& kv, const KvAttnArgs& a, const Kv8Scores& scores, cudaStream_t s) {
   DecPlan p;
   p.per = a.q_heads / a.c.heads;
   const int64_t cols = (int64_t)p.per * a.b.max_new;

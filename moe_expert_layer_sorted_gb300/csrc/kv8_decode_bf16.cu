@@ -1,5 +1,5 @@
 #include "kv8_decode.cuh"
 
-cudaError_t moe::kv8_decode_bf16(Kv8& kv, const KvAttnArgs& a, float* scores, cudaStream_t s) {
+cudaError_t moe::kv8_decode_bf16(Kv8& kv, const KvAttnArgs& a, const Kv8Scores& scores, cudaStream_t s) {
   return decode8<__nv_bfloat16>(kv, a, scores, s);
 }

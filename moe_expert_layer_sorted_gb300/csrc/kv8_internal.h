@@ -17,8 +17,10 @@ struct Kv8 {
   static constexpr int kCounters = 1024;
   static constexpr size_t kCounterBytes = kCounters * sizeof(unsigned);
   static constexpr size_t kScoreBytes = size_t(128) << 20;
-  size_t workspace() const { return kPartsBytes + kCounterBytes + (d.mass ? kScoreBytes : 0); }
+  static constexpr int kScoreSeqs = 1 << 18;  // sequences whose scores are kept
+  size_t workspace() const { return kPartsBytes + kCounterBytes + (d.mass ? kScoreBytes + kScoreSeqs * sizeof(int) : 0); }
   float* scores() const { return reinterpret_cast<float*>(ws + kPartsBytes + kCounterBytes); }
+  int* score_bases() const { return reinterpret_cast<int*>(ws + kPartsBytes + kCounterBytes + kScoreBytes); }
   float* parts() const { return reinterpret_cast<float*>(ws); }
   unsigned* counters() const { return reinterpret_cast<unsigned*>(ws + kPartsBytes); }
   volatile uint32_t* err_host = nullptr;  // mapped pinned word: set by a kernel whose bounded wait gave up
@@ -44,20 +46,29 @@ cudaError_t kv8_append(const Kv8& kv, const KvView& c, const KvBatch& b, const u
                        const uint16_t* v, const KvRows& vs, float* mass, cudaStream_t s);
 cudaError_t kv8_read(const Kv8& kv, const KvView& c, const KvBatch& b, uint16_t* k, const KvRows& ks, uint16_t* v,
                      const KvRows& vs, cudaStream_t s);
-// Attention of few rows.  scores: nullptr, or room for every row's score of every token, log2 units:
-// [sequence][kv head][token of the table][score_width] by columns (row, query head), -infinity where not seen.
-cudaError_t kv8_decode_bf16(Kv8& kv, const KvAttnArgs& a, float* scores, cudaStream_t s);
-cudaError_t kv8_decode_f16(Kv8& kv, const KvAttnArgs& a, float* scores, cudaStream_t s);
 // Columns (row, query head) of a kv head that are few.
 constexpr int kKv8Columns = 32;
-inline int score_width(const KvAttnArgs& a) { return (int)(((int64_t)a.b.max_new * (a.q_heads / a.c.heads) + 3) / 4 * 4); }
+// Where the single-token kernel leaves its scores, log2 units, -infinity where not seen.  They lie in the line of rounds
+// that its work is cut into (kv_rounds.cuh), so that only tokens that are there take room: [round][128 tokens][width], a
+// round being one of a sequence's kv head and column tile.  base[sequence]: its first round, or -1 where there was no
+// room for it (not written for a sequence without rounds).
+struct Kv8Scores {
+  float* to;   // nullptr: scores are not wanted
+  int* base;
+  int width;   // columns of a tile that are kept, a multiple of four
+  int ctiles;  // column tiles of a kv head
+  int limit;   // rounds that there is room for
+};
+// Attention of few rows.
+cudaError_t kv8_decode_bf16(Kv8& kv, const KvAttnArgs& a, const Kv8Scores& scores, cudaStream_t s);
+cudaError_t kv8_decode_f16(Kv8& kv, const KvAttnArgs& a, const Kv8Scores& scores, cudaStream_t s);
 // Attention of prompts.
 cudaError_t kv8_prompt_bf16(Kv8& kv, const KvAttnArgs& a, cudaStream_t s);
 cudaError_t kv8_prompt_f16(Kv8& kv, const KvAttnArgs& a, cudaStream_t s);
 // mass: nullptr, or the layer's, to which the weights of the tokens are added (lse is then given).
 cudaError_t kv8_attention(Kv8& kv, const KvAttnArgs& a, float* mass, cudaStream_t s);
-// The weights of an attention whose lse is written; scores: as written by the single-token kernel, or nullptr.
-cudaError_t kv8_weigh(Kv8& kv, const KvAttnArgs& a, float* mass, const float* scores, cudaStream_t s);
+// The weights of an attention whose lse is written; scores: what the single-token kernel left.
+cudaError_t kv8_weigh(Kv8& kv, const KvAttnArgs& a, float* mass, const Kv8Scores& scores, cudaStream_t s);
 cudaError_t kv8_evict(const Kv8& kv, const Kv8EvictArgs& a, cudaStream_t s);
 
 // Calls f with (T, D) of the cache as compile-time constants.

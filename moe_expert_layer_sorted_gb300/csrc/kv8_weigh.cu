@@ -6,14 +6,16 @@
 // scores are made again, transposed, on the tensor cores, and the sums run along registers:
 //     S^T = U_K Q^T   (128 tokens by 128 columns (row, query head) in TMEM),
 // a thread having a token (a TMEM lane) and half of the columns.  A column's power of two and lse come from
-// shared memory, a token's step is its thread's.  Columns that see nothing of a tile are not visited; the
-// columns of a tile are dealt out to as many CTAs as fill the SMs, whose sums a second kernel adds in
-// order, so that results do not depend on timing.
+// shared memory, a token's step is its thread's.  Columns that see nothing of a tile are not visited.  All the batch's
+// work (sequence, head, token tile, column tile) lies in one line that is cut into equal shares, two CTAs an SM, so that
+// neither the table's size nor uneven sequences matter; a token tile that is cut between CTAs is added up by the one
+// that finishes it last, in the order of the CTAs, so results do not depend on timing.  (A grid over the table's
+// tiles took 159 us for the case below, but 1,500 for 32 single tokens whose table could hold 131,072.)
 //
 // Each CTA loads the next 128 queries while the tensor cores work on one half of TMEM and the threads on
 // the other; two CTAs share an SM, so that one's barrier is covered by the other's exponents.
 //
-// Measured (8 kv heads of 128 channels): 4,096 rows over themselves, 32 query heads, fp16: 159 us for 2.1 million
+// Measured (8 kv heads of 128 channels): 4,096 rows over themselves, 32 query heads, fp16: 162 us for 2.1 million
 // rows and tokens a query head; the exponents alone would take 58.  Bound by the queries' way into shared memory,
 // which every token tile takes again (without it 105 us), and by the columns' constants (133).  From scores: 32 sequences
 // of up to 4,160 tokens 8 us, latency.
@@ -30,13 +32,17 @@ namespace {
 constexpr int kWeThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// A token tile's first products wait for its keys: it counts as so many more pieces of work, behind its own.  Measured,
+// 4,096 rows over themselves: 166 us without, 162 with 1 or 2, 164 with 4.
+constexpr int kWeTurn = 1;
+
 struct WeighArgs {
   KvAttnArgs a;
   float* mass;
-  int per;        // query heads per kv head
-  int tiles;      // token tiles of a sequence, at most
-  int splits;     // CTAs per token tile and kv head
-  float* parts;   // [sequence][head][tile][split][128], splits > 1
+  int per;             // query heads per kv head
+  const int* scored;   // nullptr, or >= 0 for sequences whose scores were left (kv8_weigh_scores_kernel takes those)
+  float* parts;        // [CTA][2][128]
+  unsigned* counters;  // a CTA each, zero between calls
   uint32_t* err;
 };
 
@@ -46,30 +52,51 @@ __device__ __forceinline__ void add_mass(const WeighArgs& w, int s, int h, int p
   if (pid >= 0) w.mass[(pid * w.a.c.heads + h) * w.a.c.page_size + (pos & (w.a.c.page_size - 1))] += sum;
 }
 
-struct WeighTile {
-  int s, h, t, len, nx;
-  int64_t first;  // position of row 0
+// A sequence's pieces of work: for each head and tile of 128 tokens, the tiles of 128 columns that see some of it.  Tile t
+// is seen by column tiles c0(t) .. n - 1, c0(t) = max(0, step t - skip): causal, row i sees it from 128 t - first on, so
+// columns from per (128 t - first) on, and 128 t per / 128 is whole.  Sums of c0 over tiles have a closed form.
+struct WeighSeq {
   KvSeq q;
-  int c0, cn;     // column tiles that see something of the token tile
-
-  __device__ __forceinline__ WeighTile(const WeighArgs& w, int index) {
-    // tiles that the most rows see first
-    h = index % w.a.c.heads;
-    s = index / w.a.c.heads % w.a.b.batch;
-    t = index / w.a.c.heads / w.a.b.batch;
+  int len, tiles, n, step;
+  int64_t first, skip;  // position of row 0
+  WeighSeq() = default;
+  __device__ __forceinline__ WeighSeq(const WeighArgs& w, int s) {
     q = kv_seq(w.a.b, s);
     len = min(q.len, kv_capacity(w.a.c, w.a.b));
-    nx = q.rows * w.per;
     first = (int64_t)q.len - q.rows;
-    cn = c0 = 0;
-    if (t * kPrTile < len && nx > 0) {
-      const int64_t skip = w.a.causal ? max((int64_t)t * kPrTile - first, (int64_t)0) : max(-first, (int64_t)0);
-      if (skip * w.per < nx) {
-        c0 = (int)(skip * w.per / kPrTile);
-        cn = (nx + kPrTile - 1) / kPrTile - c0;
-      }
-    }
+    n = (int)(((int64_t)q.rows * w.per + kPrTile - 1) / kPrTile);
+    tiles = n && !(w.scored && w.scored[s] >= 0) ? (len + kPrTile - 1) / kPrTile : 0;
+    step = w.a.causal ? w.per : 0;
+    const int64_t before = (w.a.causal ? first : min(first, (int64_t)0)) * w.per;  // rounded up, below zero too
+    skip = before >= 0 ? (before + kPrTile - 1) / kPrTile : -(-before / kPrTile);
   }
+  __device__ __forceinline__ int c0(int t) const { return (int)max((int64_t)t * step - skip, (int64_t)0); }
+  __device__ __forceinline__ int64_t before(int t) const {  // column tiles of the token tiles below t
+    int64_t out = 0;
+    if (step == 0) {
+      out = t * max(-skip, (int64_t)0);
+    } else {
+      const int64_t t1 = skip < 0 ? 0 : skip / step + 1;  // the first tile that some do not see
+      if (t > t1) out = step * ((t - 1) * (int64_t)t / 2 - (t1 - 1) * t1 / 2) - skip * (t - t1);
+    }
+    return (int64_t)(n + kWeTurn) * t - out;
+  }
+};
+
+// CTAs that share a line of pieces, a token tile of one column tile each at least.
+__device__ __forceinline__ int weigh_ctas(int64_t total) { return (int)min((int64_t)gridDim.x, total / (1 + kWeTurn)); }
+
+// A place in the line of pieces, which runs over the sequences, their heads, their token tiles and the column tiles.
+struct WeighPlace {
+  int s, h, t;
+  int64_t tile;  // number of the token tile's first piece
+};
+
+// The work at hand: `count` column tiles from c on of a token tile.
+struct WeighItem {
+  WeighPlace at;
+  WeighSeq q;
+  int nx, c, count, pieces;  // columns of the sequence; pieces: of the token tile
 };
 
 template <typename T, int D>
@@ -84,17 +111,60 @@ __global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_c
   __shared__ float4 sh_col[4][kPrTile / 2];        // two columns' factors and -lse log2 e
   __shared__ __align__(16) int sh_seen[4][kPrTile];              // tokens that a column sees
   __shared__ float sh_step[kPrTile], sh_sum[kPrTile];
+  __shared__ WeighItem sh;
+  __shared__ int64_t sh_scan[kWeThreads / 32], sh_base;
+  __shared__ volatile int64_t line[3];  // the share's first piece, its end, the end of all (not in registers)
+  __shared__ int sh_seq;
+  __shared__ unsigned sh_last;
   const KvAttnArgs& a = w.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int item = blockIdx.x / w.splits, z = blockIdx.x % w.splits;
-  const WeighTile tile(w, item);
-  const int mine = z < tile.cn ? (tile.cn - z + w.splits - 1) / w.splits : 0;  // column tiles c0 + z, c0 + z + splits, ..
-  const int base = tile.t * kPrTile;
-  float* part = w.parts + ((int64_t)item * w.splits + z) * kPrTile;
-  if (mine == 0) {
-    if (w.splits > 1 && tid < kPrTile) part[tid] = 0.0f;
-    return;
+
+  // ---- the CTA's share of the line, and the sequence that it begins in
+  int64_t total = 0, first = 0, last = 0;
+  for (int pass = 0; pass < 2; ++pass) {  // the sum; the sequence
+    int64_t before = 0;
+    for (int g0 = 0; g0 < a.b.batch; g0 += kWeThreads) {
+      int64_t mine = 0;
+      if (g0 + tid < a.b.batch) {
+        const WeighSeq q(w, g0 + tid);
+        mine = q.before(q.tiles) * a.c.heads;
+      }
+      int64_t upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      __syncthreads();
+      if (lane == 31) sh_scan[warp] = upto;
+      __syncthreads();
+      int64_t all = 0;
+#pragma unroll
+      for (int y = 0; y < kWeThreads / 32; ++y) {
+        if (y < warp) upto += sh_scan[y];
+        all += sh_scan[y];
+      }
+      upto += before;
+      if (pass && upto - mine <= first && first < upto) {
+        sh_seq = g0 + tid;
+        sh_base = upto - mine;
+      }
+      before += all;
+    }
+    if (pass == 0) {
+      total = before;
+      const int64_t n = weigh_ctas(total);
+      if (blockIdx.x >= n) return;
+      first = total * blockIdx.x / n;
+      last = total * (blockIdx.x + 1) / n;
+    }
   }
+  if (tid == 0) {
+    line[0] = first;
+    line[1] = last;
+    line[2] = total;
+  }
+  __syncthreads();
   const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
   uint8_t* gen = smem_raw + (smem - smem_addr(smem_raw));  // keys, then two query tiles
   if (tid == 0) {
@@ -107,93 +177,6 @@ __global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_c
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_base)), "n"(256));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  // ---- the keys: a warp takes a block of 16 tokens
-  {
-    constexpr int kLanes = D / 16, kRows = 32 / kLanes;
-    const int pos = base + 16 * warp, kc = lane % kLanes, kr = lane / kLanes;
-    const int64_t pid = pos < tile.len ? kv_page(a.c, a.b, tile.s, pos >> a.c.page_shift) : -1;
-    const uint8_t* blk = a.c.pages + pid * a.c.page_stride + tile.h * a.c.head_stride +
-                         ((pos & (a.c.page_size - 1)) >> 4) * (int64_t)Geo::kBytes;
-#pragma unroll
-    for (int i = 0; i < 16 / kRows; ++i) {
-      const int r = i * kRows + kr, row = 16 * warp + r;
-      uint4 v = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-      if (pid >= 0) v = *reinterpret_cast<const uint4*>(blk + r * D + Geo::k_piece(r, kc) * 16);
-      auto place = [&](int ch8) {
-        return reinterpret_cast<uint4*>(gen + (ch8 / 8) * (kPrTile * 128) + row * 128 + ((ch8 % 8) ^ (row & 7)) * 16);
-      };
-      *place(2 * kc) = make_uint4(kv8_pair<0>(v.x), kv8_pair<1>(v.x), kv8_pair<0>(v.y), kv8_pair<1>(v.y));
-      *place(2 * kc + 1) = make_uint4(kv8_pair<0>(v.z), kv8_pair<1>(v.z), kv8_pair<0>(v.w), kv8_pair<1>(v.w));
-    }
-    if (lane < 16) sh_step[16 * warp + lane] = pid >= 0 ? *reinterpret_cast<const float*>(blk + Geo::kParams) : 0.0f;
-  }
-  auto column = [&](int i) { return (tile.c0 + z + i * w.splits) * kPrTile; };
-  // the queries of the i-th column tile, zeros where lse is not finite: asked for, and later written.  D / 8 lanes take a
-  // row, a warp sixteen of them.
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kLoads = 16 / kRows;
-  const int qc = lane % kLanes, qr = 16 * warp + lane / kLanes;
-  uint4 raw[kLoads];
-  float row_lse[kLoads];
-  const uint16_t* const head = a.q + kv_row_offset(a.b, a.qs, tile.s, tile.q.row0, 0) + (int64_t)tile.h * w.per * a.qs.head + 8 * qc;
-  const float* const lse = a.lse + kv_row_index(a.b, tile.s, tile.q.row0, 0) * a.q_heads + tile.h * w.per;
-  auto ask = [&](int i_) {
-    const int x = column(i_) + qr, i = x / w.per;
-    int hq = x - i * w.per;
-    const uint16_t* src = head + i * a.qs.row + hq * a.qs.head;
-    const float* ls = lse + (int64_t)i * a.q_heads + hq;
-#pragma unroll
-    for (int n = 0; n < kLoads; ++n) {
-      raw[n] = make_uint4(0, 0, 0, 0);
-      row_lse[n] = __int_as_float(0x7fffffff);
-      if (x + n * kRows < tile.nx) {
-        row_lse[n] = *ls;
-        raw[n] = *reinterpret_cast<const uint4*>(src);
-      }
-      hq += kRows;
-      src += kRows * a.qs.head;
-      ls += kRows;
-      while (hq >= w.per) {  // the next row's first head
-        hq -= w.per;
-        src += a.qs.row - w.per * a.qs.head;
-        ls += a.q_heads - w.per;
-      }
-    }
-  };
-  auto put = [&](int i_) {
-    uint8_t* to = gen + kTileBytes * (1 + (i_ & 1)) + (qc / 8) * (kPrTile * 128);
-#pragma unroll
-    for (int n = 0; n < kLoads; ++n) {
-      const int r = qr + n * kRows;
-      const bool fine = fabsf(row_lse[n]) < __int_as_float(0x7f800000);
-      if (!fine) raw[n] = make_uint4(0, 0, 0, 0);
-      float back = 1.0f;
-      if constexpr (std::is_same<T, __nv_bfloat16>::value) {  // by the power of two that brings the row to 2^14
-        uint32_t v[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
-        uint32_t top = __vmaxu2(__vmaxu2(v[0] & 0x7fff7fffu, v[1] & 0x7fff7fffu), __vmaxu2(v[2] & 0x7fff7fffu, v[3] & 0x7fff7fffu));
-#pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
-        top = max(top >> 16, top & 0xffffu);
-        const int ex = (int)(top >> 7) - 127;
-        const int by = top == 0u || ex > 127 ? 0 : min(max(14 - ex, -113), 113);
-        const float up = pow2(by);
-        back = pow2(-by);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = KvType<__half>::pack(KvType<T>::lo(v[e]) * up, KvType<T>::hi(v[e]) * up);
-        raw[n] = make_uint4(v[0], v[1], v[2], v[3]);
-      }
-      *reinterpret_cast<uint4*>(to + r * 128 + ((qc % 8) ^ (r & 7)) * 16) = raw[n];
-      if (qc == 0) {
-        float* col = reinterpret_cast<float*>(&sh_col[i_ & 3][r >> 1]);
-        col[r & 1] = a.scale * kLog2e * back;
-        col[2 + (r & 1)] = fine ? -row_lse[n] * kLog2e : -__int_as_float(0x7f800000);
-      }
-    }
-    if (tid < kPrTile) {
-      const int x = column(i_) + tid;
-      const int64_t p = tile.first + x / w.per;
-      sh_seen[i_ & 3][tid] = x >= tile.nx || p < 0 ? 0 : (int)min(a.causal ? p + 1 : (int64_t)tile.len, (int64_t)tile.len);
-    }
-  };
   const uint32_t id = idesc(kPrTile, false);
   uint32_t tm = 0;
   auto multiply = [&](int b) {  // by the first warp
@@ -205,77 +188,236 @@ __global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_c
              desc_k(qa + (k / 4) * (kPrTile * 128) + (k % 4) * 32), id, k ? 1u : 0u);
     commit(leader, &done[b]);
   };
-  ask(0);
-  put(0);
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   fence_before();
   __syncthreads();
   fence_after();
   tm = tmem_base;
-  if (warp == 0) multiply(0);
-  if (mine > 1) ask(1);
-
+  uint32_t parity = 0;  // a bit per half of TMEM
   const int quad = warp & 3, half = warp >> 2;  // the warp's lanes of TMEM, its columns of a tile
   const int token = quad * 32 + lane;
-  const float ks = sh_step[token];
-  const uint64_t ks2 = pair2(ks, ks);
-  uint64_t sum[2] = {0, 0};
-  for (int i = 0; i < mine; ++i) {
-    const int b = i & 1, x0 = column(i);
-    if (i + 1 < mine) {  // into the other half, whose products are done
-      put(i + 1);
+  for (int64_t u = line[0]; u < line[1];) {
+    if (tid == 0) {
+      WeighPlace at = sh.at;
+      if (u == line[0]) {
+        at.s = sh_seq;
+        const WeighSeq q(w, at.s);
+        sh.q = q;
+        const int64_t head = q.before(q.tiles);
+        at.h = (int)((u - sh_base) / head);
+        const int64_t in_head = (u - sh_base) - at.h * head;
+        int t0 = 0, t1 = q.tiles;  // the last tile with before(t) <= in_head lies in t0 .. t1 - 1
+        while (t1 - t0 > 1) {
+          const int mid = (t0 + t1) / 2;
+          if (q.before(mid) <= in_head) t0 = mid;
+          else t1 = mid;
+        }
+        at.t = t0;
+        at.tile = u - (in_head - q.before(t0));
+      } else {  // a token tile's first piece
+        at.tile = u;
+        if (++at.t == sh.q.tiles) {
+          at.t = 0;
+          if (++at.h == a.c.heads) {
+            at.h = 0;
+            do sh.q = WeighSeq(w, ++at.s);
+            while (sh.q.tiles == 0);  // (there is one, the line goes on)
+          }
+        }
+      }
+      sh.at = at;
+      sh.nx = sh.q.q.rows * w.per;
+      const int c0 = sh.q.c0(at.t);
+      sh.pieces = sh.q.n + kWeTurn - c0;
+      sh.c = c0 + (int)(u - at.tile);
+      sh.count = (int)(min(at.tile + sh.pieces, line[1]) - u);
+    }
+    __syncthreads();
+    const int base = sh.at.t * kPrTile, mine = min(sh.count, sh.q.n - sh.c);  // what is not the change to the tile
+    auto column = [&](int i) { return (sh.c + i) * kPrTile; };
+    // the queries of the i-th column tile, zeros where lse is not finite: asked for, and later written.  D / 8 lanes take a
+    // row, a warp sixteen of them.
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kLoads = 16 / kRows;
+    const int qc = lane % kLanes, qr = 16 * warp + lane / kLanes;
+    uint4 raw[kLoads];
+    float row_lse[kLoads];
+    const uint16_t* const head = a.q + kv_row_offset(a.b, a.qs, sh.at.s, sh.q.q.row0, 0) + (int64_t)sh.at.h * w.per * a.qs.head + 8 * qc;
+    const float* const lse = a.lse + kv_row_index(a.b, sh.at.s, sh.q.q.row0, 0) * a.q_heads + sh.at.h * w.per;
+    auto ask = [&](int i_) {
+      const int x = column(i_) + qr, i = x / w.per;
+      int hq = x - i * w.per;
+      const uint16_t* src = head + i * a.qs.row + hq * a.qs.head;
+      const float* ls = lse + (int64_t)i * a.q_heads + hq;
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n) {
+        raw[n] = make_uint4(0, 0, 0, 0);
+        row_lse[n] = __int_as_float(0x7fffffff);
+        if (x + n * kRows < sh.nx) {
+          row_lse[n] = *ls;
+          raw[n] = *reinterpret_cast<const uint4*>(src);
+        }
+        hq += kRows;
+        src += kRows * a.qs.head;
+        ls += kRows;
+        while (hq >= w.per) {  // the next row's first head
+          hq -= w.per;
+          src += a.qs.row - w.per * a.qs.head;
+          ls += a.q_heads - w.per;
+        }
+      }
+    };
+    auto put = [&](int i_) {
+      uint8_t* to = gen + kTileBytes * (1 + (i_ & 1)) + (qc / 8) * (kPrTile * 128);
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n) {
+        const int r = qr + n * kRows;
+        const bool fine = fabsf(row_lse[n]) < __int_as_float(0x7f800000);
+        if (!fine) raw[n] = make_uint4(0, 0, 0, 0);
+        float back = 1.0f;
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) {  // by the power of two that brings the row to 2^14
+          uint32_t v[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
+          uint32_t top = __vmaxu2(__vmaxu2(v[0] & 0x7fff7fffu, v[1] & 0x7fff7fffu), __vmaxu2(v[2] & 0x7fff7fffu, v[3] & 0x7fff7fffu));
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+          top = max(top >> 16, top & 0xffffu);
+          const int ex = (int)(top >> 7) - 127;
+          const int by = top == 0u || ex > 127 ? 0 : min(max(14 - ex, -113), 113);
+          const float up = pow2(by);
+          back = pow2(-by);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = KvType<__half>::pack(KvType<T>::lo(v[e]) * up, KvType<T>::hi(v[e]) * up);
+          raw[n] = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+        *reinterpret_cast<uint4*>(to + r * 128 + ((qc % 8) ^ (r & 7)) * 16) = raw[n];
+        if (qc == 0) {
+          float* col = reinterpret_cast<float*>(&sh_col[i_ & 3][r >> 1]);
+          col[r & 1] = a.scale * kLog2e * back;
+          col[2 + (r & 1)] = fine ? -row_lse[n] * kLog2e : -__int_as_float(0x7f800000);
+        }
+      }
+      if (tid < kPrTile) {
+        const int x = column(i_) + tid;
+        const int64_t p = sh.q.first + x / w.per;
+        sh_seen[i_ & 3][tid] = x >= sh.nx || p < 0 ? 0 : (int)min(a.causal ? p + 1 : (int64_t)sh.q.len, (int64_t)sh.q.len);
+      }
+    };
+    if (mine > 0) {
+      ask(0);
+      // ---- the keys: a warp takes a block of 16 tokens
+      {
+        constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+        const int pos = base + 16 * warp, kc = lane % kLanes, kr = lane / kLanes;
+        const int64_t pid = pos < sh.q.len ? kv_page(a.c, a.b, sh.at.s, pos >> a.c.page_shift) : -1;
+        const uint8_t* blk = a.c.pages + pid * a.c.page_stride + sh.at.h * a.c.head_stride +
+                             ((pos & (a.c.page_size - 1)) >> 4) * (int64_t)Geo::kBytes;
+#pragma unroll
+        for (int i = 0; i < 16 / kRows; ++i) {
+          const int r = i * kRows + kr, row = 16 * warp + r;
+          uint4 v = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+          if (pid >= 0) v = *reinterpret_cast<const uint4*>(blk + r * D + Geo::k_piece(r, kc) * 16);
+          auto place = [&](int ch8) {
+            return reinterpret_cast<uint4*>(gen + (ch8 / 8) * (kPrTile * 128) + row * 128 + ((ch8 % 8) ^ (row & 7)) * 16);
+          };
+          *place(2 * kc) = make_uint4(kv8_pair<0>(v.x), kv8_pair<1>(v.x), kv8_pair<0>(v.y), kv8_pair<1>(v.y));
+          *place(2 * kc + 1) = make_uint4(kv8_pair<0>(v.z), kv8_pair<1>(v.z), kv8_pair<0>(v.w), kv8_pair<1>(v.w));
+        }
+        if (lane < 16) sh_step[16 * warp + lane] = pid >= 0 ? *reinterpret_cast<const float*>(blk + Geo::kParams) : 0.0f;
+      }
+      put(0);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       fence_before();
       __syncthreads();
       if (warp == 0) {
         fence_after();
-        multiply(b ^ 1);
+        multiply(0);
       }
-      if (i + 2 < mine) ask(i + 2);  // they arrive during the exponents
+      if (mine > 1) ask(1);
     }
-    kv_wait(smem_addr(&done[b]), (uint32_t)(i >> 1) & 1u, &sh_gone, w.err);
-    fence_after();
-    const uint32_t ts = tm + b * kPrTile + half * 64 + ((uint32_t)(quad * 32) << 16);
-    auto consume = [&](auto masked_) {
-      constexpr bool masked = decltype(masked_)::value;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t v[32];
-        tmem_ld32(ts + 32 * k, v);
-        tmem_wait_ld();
-        const float4* col = &sh_col[i & 3][half * 32 + 16 * k];
-        const int2* seen = reinterpret_cast<const int2*>(&sh_seen[i & 3][half * 64 + 32 * k]);
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float4 f = col[e / 2];
-          uint64_t y = mul2(pair2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), pair2(f.x, f.y));
-          y = fma2(y, ks2, pair2(f.z, f.w));
-          float y0, y1;
-          split2(y, y0, y1);
-          y0 = exp2_fast(y0);
-          y1 = exp2_fast(y1);
-          if constexpr (masked) {
-            const int2 n = seen[e / 2];
-            y0 = base + token < n.x ? y0 : 0.0f;
-            y1 = base + token < n.y ? y1 : 0.0f;
-          }
-          sum[e / 2 & 1] = add2(sum[e / 2 & 1], pair2(y0, y1));
+
+    const float ks = sh_step[token];
+    const uint64_t ks2 = pair2(ks, ks);
+    uint64_t sum[2] = {0, 0};
+    for (int i = 0; i < mine; ++i) {
+      const int b = i & 1, x0 = column(i);
+      if (i + 1 < mine) {  // into the other half, whose products are done
+        put(i + 1);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        fence_before();
+        __syncthreads();
+        if (warp == 0) {
+          fence_after();
+          multiply(b ^ 1);
         }
+        if (i + 2 < mine) ask(i + 2);  // they arrive during the exponents
       }
-    };
-    // every column sees the whole token tile?
-    if (tile.first + x0 / w.per >= base + kPrTile - 1 || (!a.causal && tile.first >= 0)) consume(std::false_type());
-    else consume(std::true_type());
-  }
-  float s0, s1;
-  split2(add2(sum[0], sum[1]), s0, s1);
-  if (half) sh_sum[token] = s0 + s1;
-  fence_before();
-  __syncthreads();
-  if (!half) {
-    const float all = (s0 + s1) + sh_sum[token];
-    if (w.splits > 1) part[token] = all;
-    else if (base + token < tile.len) add_mass(w, tile.s, tile.h, base + token, all);
+      kv_wait(smem_addr(&done[b]), parity >> b & 1u, &sh_gone, w.err);
+      parity ^= 1u << b;
+      fence_after();
+      const uint32_t ts = tm + b * kPrTile + half * 64 + ((uint32_t)(quad * 32) << 16);
+      auto consume = [&](auto masked_) {
+        constexpr bool masked = decltype(masked_)::value;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t v[32];
+          tmem_ld32(ts + 32 * k, v);
+          tmem_wait_ld();
+          const float4* col = &sh_col[i & 3][half * 32 + 16 * k];
+          const int2* seen = reinterpret_cast<const int2*>(&sh_seen[i & 3][half * 64 + 32 * k]);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float4 f = col[e / 2];
+            uint64_t y = mul2(pair2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), pair2(f.x, f.y));
+            y = fma2(y, ks2, pair2(f.z, f.w));
+            float y0, y1;
+            split2(y, y0, y1);
+            y0 = exp2_fast(y0);
+            y1 = exp2_fast(y1);
+            if constexpr (masked) {
+              const int2 n = seen[e / 2];
+              y0 = base + token < n.x ? y0 : 0.0f;
+              y1 = base + token < n.y ? y1 : 0.0f;
+            }
+            sum[e / 2 & 1] = add2(sum[e / 2 & 1], pair2(y0, y1));
+          }
+        }
+      };
+      // every column sees the whole token tile?
+      if (sh.q.first + x0 / w.per >= base + kPrTile - 1 || (!a.causal && sh.q.first >= 0)) consume(std::false_type());
+      else consume(std::true_type());
+    }
+    float s0, s1;
+    split2(add2(sum[0], sum[1]), s0, s1);
+    if (half) sh_sum[token] = s0 + s1;
+    fence_before();
+    __syncthreads();
+    // a token tile that is cut between CTAs: sums of a CTA's first stretch in slot 0, of its last in slot 1, and who
+    // finishes the tile last adds them in order
+    const bool whole = sh.count == sh.pieces;
+    const int64_t tile = sh.at.tile, tile_end = tile + sh.pieces;
+    if (!half) {
+      const float all = (s0 + s1) + sh_sum[token];
+      if (!whole) w.parts[(int64_t)(2 * blockIdx.x + (u == line[0] ? 0 : 1)) * kPrTile + token] = all;
+      else if (base + token < sh.q.len) add_mass(w, sh.at.s, sh.at.h, base + token, all);
+    }
+    if (!whole) {
+      const int64_t total = line[2];
+      const int n = weigh_ctas(total);
+      const int c0 = (int)(((tile + 1) * n - 1) / total), c1 = (int)((tile_end * n - 1) / total);  // whose shares hold its ends
+      __syncthreads();  // every thread's part is written: one release covers them
+      if (tid == 0) sh_last = add_acq_rel(&w.counters[c0]);
+      __syncthreads();
+      if (sh_last == (unsigned)(c1 - c0)) {
+        if (tid < kPrTile && base + tid < sh.q.len) {
+          float sum_ = 0.0f;
+#pragma unroll 8
+          for (int y = c0; y <= c1; ++y)
+            sum_ += __ldcg(w.parts + (int64_t)(2 * y + (y == c0 && tile != total * c0 / n ? 1 : 0)) * kPrTile + tid);
+          add_mass(w, sh.at.s, sh.at.h, base + tid, sum_);
+        }
+        if (tid == 0) w.counters[c0] = 0;  // for the next call
+      }
+    }
+    u += sh.count;
+    __syncthreads();  // what this tile had in shared memory is the next one's
   }
   if (warp == 0) {
     fence_after();
@@ -283,95 +425,80 @@ __global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_c
   }
 }
 
-// Adds the sums of a token tile's CTAs, in order.
-__global__ void __launch_bounds__(kPrTile) kv8_weigh_join_kernel(const __grid_constant__ WeighArgs w) {
-  const WeighTile tile(w, blockIdx.x);
-  const int pos = tile.t * kPrTile + threadIdx.x;
-  if (tile.cn == 0 || pos >= tile.len) return;
-  const float* part = w.parts + (int64_t)blockIdx.x * w.splits * kPrTile + threadIdx.x;
-  float sum = 0.0f;
-#pragma unroll 8
-  for (int z = 0; z < w.splits; ++z) sum += part[z * kPrTile];
-  add_mass(w, tile.s, tile.h, pos, sum);
-}
-
 // From the scores that the single-token kernel wrote: a thread adds up the columns of four tokens (of one page).
 constexpr int kWeTokens = 4 * kWeThreads;
-__global__ void __launch_bounds__(kWeThreads) kv8_weigh_scores_kernel(const __grid_constant__ WeighArgs w, const float* __restrict__ scores,
-                                                                      int width, int chunks) {
+__global__ void __launch_bounds__(kWeThreads) kv8_weigh_scores_kernel(const __grid_constant__ WeighArgs w, const __grid_constant__ Kv8Scores scores,
+                                                                      int ctas) {
   __shared__ float sh_lse[kKv8Columns];
   const KvAttnArgs& a = w.a;
-  const int h = blockIdx.x % a.c.heads, s = blockIdx.x / a.c.heads / chunks, chunk = blockIdx.x / a.c.heads % chunks;
+  const int h = blockIdx.x % a.c.heads, s = blockIdx.x / a.c.heads / ctas, z = blockIdx.x / a.c.heads % ctas;
   const KvSeq q = kv_seq(a.b, s);
   const int cols = min(q.rows * w.per, kKv8Columns), len = min(q.len, kv_capacity(a.c, a.b));
-  if ((int64_t)chunk * kWeTokens >= len) return;
+  if (q.rows == 0 || (int64_t)z * kWeTokens >= len) return;
+  const int line = scores.base[s], width = scores.width, rounds = (len + kPrTile - 1) / kPrTile;
+  if (line < 0) return;
   if ((int)threadIdx.x < cols) {
     const float ls = a.lse[kv_row_index(a.b, s, q.row0, threadIdx.x / w.per) * a.q_heads + h * w.per + threadIdx.x % w.per];
     sh_lse[threadIdx.x] = fabsf(ls) < __int_as_float(0x7f800000) ? ls * kLog2e : __int_as_float(0x7f800000);
   }
-  const int pos = chunk * kWeTokens + 4 * threadIdx.x, n = min(len - pos, 4);
-  const int64_t pid = n > 0 ? kv_page(a.c, a.b, s, pos >> a.c.page_shift) : -1;
   __syncthreads();
-  if (pid < 0) return;
-  float* mass = w.mass + (pid * a.c.heads + h) * a.c.page_size + (pos & (a.c.page_size - 1));
-  const float4* y = reinterpret_cast<const float4*>(scores + (((int64_t)s * a.c.heads + h) * kv_capacity(a.c, a.b) + pos) * width);
-  const float4 had = *reinterpret_cast<const float4*>(mass);
-  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int x = 0; x < cols; x += 4) {
-    float4 v[4];
+  for (int64_t at = (int64_t)z * kWeTokens; at < len; at += (int64_t)ctas * kWeTokens) {
+    const int pos = (int)at + 4 * threadIdx.x, n = min(len - pos, 4);
+    const int64_t pid = n > 0 ? kv_page(a.c, a.b, s, pos >> a.c.page_shift) : -1;
+    if (pid < 0) continue;
+    float* mass = w.mass + (pid * a.c.heads + h) * a.c.page_size + (pos & (a.c.page_size - 1));
+    const float4 had = *reinterpret_cast<const float4*>(mass);
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int x = 0; x < cols; x += 4) {
+      const int64_t round = line + (int64_t)(h * scores.ctiles + (x >> 4)) * rounds + pos / kPrTile;
+      const float* y = scores.to + (round * kPrTile + (pos & (kPrTile - 1))) * width + (x & 15);
+      float4 v[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) v[t] = y[(t * width + x) / 4];
+      for (int t = 0; t < 4; ++t) v[t] = *reinterpret_cast<const float4*>(y + t * width);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float ls = x + i < cols ? sh_lse[x + i] : __int_as_float(0x7f800000);
-      if (ls == __int_as_float(0x7f800000)) continue;
+      for (int i = 0; i < 4; ++i) {
+        const float ls = x + i < cols ? sh_lse[x + i] : __int_as_float(0x7f800000);
+        if (ls == __int_as_float(0x7f800000)) continue;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) sum[t] += exp2_fast((i == 0 ? v[t].x : i == 1 ? v[t].y : i == 2 ? v[t].z : v[t].w) - ls);
+        for (int t = 0; t < 4; ++t) sum[t] += exp2_fast((i == 0 ? v[t].x : i == 1 ? v[t].y : i == 2 ? v[t].z : v[t].w) - ls);
+      }
     }
-  }
-  const float now[4] = {had.x + sum[0], had.y + sum[1], had.z + sum[2], had.w + sum[3]};
-  if (n == 4) {
-    *reinterpret_cast<float4*>(mass) = make_float4(now[0], now[1], now[2], now[3]);
-  } else {
+    const float now[4] = {had.x + sum[0], had.y + sum[1], had.z + sum[2], had.w + sum[3]};
+    if (n == 4) {
+      *reinterpret_cast<float4*>(mass) = make_float4(now[0], now[1], now[2], now[3]);
+    } else {
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-      if (t < n) mass[t] = now[t];
+      for (int t = 0; t < 4; ++t)
+        if (t < n) mass[t] = now[t];
+    }
   }
 }
 
 }  // namespace
 
-cudaError_t moe::kv8_weigh(Kv8& kv, const KvAttnArgs& a, float* mass, const float* scores, cudaStream_t s) {
-  WeighArgs w{a, mass, a.q_heads / a.c.heads, 0, 1, kv.parts(), kv.err_dev};
+cudaError_t moe::kv8_weigh(Kv8& kv, const KvAttnArgs& a, float* mass, const Kv8Scores& scores, cudaStream_t s) {
+  WeighArgs w{a, mass, a.q_heads / a.c.heads, scores.to ? scores.base : nullptr, kv.parts(), kv.counters(), kv.err_dev};
   const int64_t cap = std::min<int64_t>((int64_t)a.b.table_pages << a.c.page_shift, 0x7ffff000);
-  if (scores) {
-    const int64_t chunks = (cap + kWeTokens - 1) / kWeTokens, ctas = chunks * a.c.heads * a.b.batch;
-    if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    kv8_weigh_scores_kernel<<<(unsigned)ctas, kWeThreads, 0, s>>>(w, scores, score_width(a), (int)chunks);
-    return cudaGetLastError();
+  if (scores.to) {
+    // a CTA for 1,024 tokens that the table could hold; of many, one that goes on to the next ones (an idle CTA takes 0.5 ns)
+    const int64_t items = (int64_t)a.c.heads * a.b.batch;
+    const int64_t ctas = std::min<int64_t>((cap + kWeTokens - 1) / kWeTokens, std::max<int64_t>(8192 / items, 1));
+    if (items * ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    kv8_weigh_scores_kernel<<<(unsigned)(items * ctas), kWeThreads, 0, s>>>(w, scores, (int)ctas);
+    const cudaError_t e = cudaGetLastError();
+    const int64_t rounds = (cap + kPrTile - 1) / kPrTile;
+    if (e != cudaSuccess || items * scores.ctiles <= scores.limit / rounds) return e;  // there was room for all of them
   }
-  const int64_t tiles = (cap + kPrTile - 1) / kPrTile, items = tiles * a.c.heads * a.b.batch;
-  const int64_t columns = ((int64_t)a.b.max_new * w.per + kPrTile - 1) / kPrTile;
-  if (items > 0x7fffffff || columns * kPrTile > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  w.tiles = (int)tiles;
-  // CTAs enough for four rounds of the SMs, which hold two each; their sums have to fit the workspace
-  const int64_t want = std::min<int64_t>((8 * (int64_t)kv.sms + items - 1) / items, columns);
-  const int64_t room = (int64_t)(Kv8::kPartsBytes / (kPrTile * sizeof(float))) / items;
-  w.splits = (int)std::max<int64_t>(std::min(want, room), 1);
-  if (items * w.splits > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  if ((int64_t)a.b.max_new * w.per > 0x7fffffff - kPrTile) return cudaErrorInvalidConfiguration;
   cudaError_t e = cudaSuccess;
   KV8_DISPATCH(kv.d, {
     const size_t smem = std::max<size_t>(1024 + (size_t)3 * kPrTile * D * 2, 80 << 10);  // two CTAs an SM, as many as TMEM holds
     const auto kernel = kv8_weigh_kernel<T, D>;
     e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
     if (e == cudaSuccess) {
-      kernel<<<(unsigned)(items * w.splits), kWeThreads, smem, s>>>(w);
+      kernel<<<(unsigned)std::min(2 * kv.sms, Kv8::kCounters), kWeThreads, smem, s>>>(w);
       e = cudaGetLastError();
     }
   });
-  if (e == cudaSuccess && w.splits > 1) {
-    kv8_weigh_join_kernel<<<(unsigned)items, kPrTile, 0, s>>>(w);
-    e = cudaGetLastError();
-  }
   return e;
 }

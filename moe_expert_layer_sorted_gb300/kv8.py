@@ -102,7 +102,8 @@ class KVCache8(Handle):
                   weigh=False, layer=0, stream=None):
         """out = softmax(scale q k^T) v of the rows q (scale None: 1 / sqrt(head_dim)).
         lse: None, or float32 [rows, heads] for the logarithm of each row's sum of exponentials.
-        weigh: add every token's weights in this call to its mass (needs lse)."""
+        weigh: add every token's weights in this call to its mass (needs lse, and pages that no two
+        sequences of the call share)."""
         self._c.attention(q, out, table, lens, starts, max_new, layer, stream, scale, causal, lse, weigh)
 
     def evict(self, kept, *, table, lens, keep_first=0, keep_last=0, layer=0, stream=None):

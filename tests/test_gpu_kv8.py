@@ -214,7 +214,8 @@ def causal(n, L):
 def expected(w, i, q, scale=None, is_causal=True):
     n, L = len(q), w.stored[i].length
     k, v = w.stored[i].values()
-    seen = causal(n, L) if is_causal else torch.ones(n, L, dtype=torch.bool, device="cuda")
+    real = torch.arange(L - n, L, device="cuda")[:, None] >= 0  # rows before the first token see nothing
+    seen = causal(n, L) if is_causal else real.expand(n, L)
     return ref.attention(q, k, v, w.stored[i].steps()[1], seen, scale if scale is not None else 1 / math.sqrt(w.D))
 
 
@@ -771,3 +772,31 @@ def test_turned_codes_at_every_ratio_of_steps(dtype):
     run_evict(w, 200, 0, 0, [mass])
     w.lens, w.lens_t = [200], ints([200])
     run_evict(w, 77, 1, 1, [mass[:200].contiguous()])
+
+
+def test_weights_of_sequences_with_and_without_room_for_scores():
+    """The workspace holds the scores of 16,256 rounds of 128 tokens at 16 columns: the first sequence's, not the others'."""
+    w = World(64, 64, BF, 64, [9000, 0, 9000, 300], seed=5).fill()
+    run_attention(w, [8] * 4, 256, ragged=False, weigh=True)
+
+
+@pytest.mark.parametrize("rows", [1, 9])
+def test_weights_of_many_sequences_of_one_much_longer(rows):
+    """More sequences than a CTA has threads; a CTA that takes several stretches of one sequence's scores; a table far wider
+    than most of them."""
+    lens = [int(n) for n in torch.randint(0, 40, (300,), generator=torch.Generator().manual_seed(rows))]
+    lens[257] = 5000
+    w = World(64, 16, FP, 8, lens, seed=rows).fill()
+    w.cache.mass.nan_to_num_(0.25)
+    run_attention(w, [rows] * 300, 32, ragged=False, weigh=True)
+
+
+@pytest.mark.parametrize("counts", [[300, 0, 1, 40], [1, 40, 700, 0], [33, 33, 33, 33]])
+@pytest.mark.parametrize("is_causal", [True, False])
+def test_weights_of_uneven_prompts_in_wide_tables(counts, is_causal):
+    """Work of all sizes cut into equal shares: sequences without rows or tokens, rows before their sequence."""
+    w = World(128, 64, BF, 3, [900, 20, 690, 0], seed=sum(counts)).fill()
+    wide = torch.full((4, 2048), -1, dtype=torch.int32, device="cuda")
+    wide[:, :w.cols] = w.table
+    w.table = wide
+    run_attention(w, counts, 15, weigh=True, is_causal=is_causal)
