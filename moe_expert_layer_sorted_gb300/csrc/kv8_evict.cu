@@ -1,20 +1,21 @@
 // Eviction from the 8-bit cache by accumulated weight: of every sequence and kv head the first and
 // the last tokens and those of the largest mass stay, and move together.
 //
-// One cluster per (sequence, kv head), its CTAs sharing the tokens.
-//   Choice: order-preserving 32-bit keys of the masses, kept in shared memory where they fit; the key
-//   of the last token that is taken by three histograms of 11, 11 and 10 bits, added up over the
-//   cluster through distributed shared memory; then one ordered pass counts, and one writes the kept
-//   positions.
-//   Moving: sixteen kept tokens make a new block, whose step is the largest of theirs.  A token moves
-//   to a lower position or stays, so blocks are made in rounds, one per warp of the cluster: all of a
-//   round have been read before any is written, and no later round reads what this one overwrites.  The
-//   next round's words are asked for before this one's barrier is waited for.
+// Choice: one cluster per (sequence, kv head), its CTAs sharing the tokens.  Order-preserving 32-bit keys of the masses,
+//   kept in shared memory where they fit; the key of the last token that is taken by three histograms of 11, 11 and 10
+//   bits, added up over the cluster through distributed shared memory; then one ordered pass counts, and one writes the
+//   kept positions.
+// Moving: one cluster for the keys and one for the values of a (sequence, kv head), which share no byte that either
+//   writes.  Sixteen kept tokens make a new block, whose step is the largest of theirs.  A token moves to a lower
+//   position or stays, so blocks are made in rounds, one per warp of the cluster: all of a round have been read before
+//   any is written, and no later round reads what this one overwrites.  What later rounds need may then be read as early
+//   as one likes: asynchronous copies bring it to shared memory two rounds ahead, and the barrier of a round runs while
+//   its codes are turned.
 //
 // Measured (8 heads of 128 channels, caches whose tokens have not been moved before): 32 sequences of up to 4,608 tokens
-// to 4,096 each 207 us (choice 28), 0.5 GB read and written; one of 131,072 to 65,536 232 us (choice 58), of which half the
-// SMs have no part: the sixteen CTAs of a head's cluster share eight of them.  Bound by the rounds' chain of loads and
-// by the turning of codes (50 us of either).
+// to 4,096 each 131 us (choice 21), 0.5 GB read and written; one of 131,072 to 65,536 183 us (choice 33).  (Keys and values
+// by the same warps: 207 and 232.)  Bound by the turning of codes, one chain a warp with sixteen warps an SM, and for one
+// sequence by the SMs that sixteen clusters leave idle.
 #include <cooperative_groups.h>
 
 #include "kv8_internal.h"
@@ -24,10 +25,13 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kEvThreads = 256, kEvWarps = kEvThreads / 32;
+constexpr int kChThreads = 512, kChWarps = kChThreads / 32;  // that choose
+constexpr int kMvThreads = 256, kMvWarps = kMvThreads / 32;  // that move
 constexpr int kEvBins = 2048;
 constexpr int kEvKeys = 16384;  // that a CTA keeps in shared memory; of longer shares they are read again
 constexpr int kEvMaxCluster = 16;
+constexpr int kMvStages = 3;  // rounds in a ring
+constexpr int kMvPerSm = 2;  // CTAs that move tokens
 
 // Order-preserving key of a mass (-0 and +0 equal), NaN as -infinity.
 __device__ __forceinline__ uint32_t mass_key(float v) {
@@ -61,7 +65,7 @@ __device__ __forceinline__ int cta_scan(int v, int* sh) {
   if (lane == 31) sh[warp] = v;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kEvWarps; ++w)
+  for (int w = 0; w < kChWarps; ++w)
     if (w < warp) v += sh[w];
   return v;
 }
@@ -129,14 +133,12 @@ __device__ __forceinline__ void turn_words(const uint32_t (&w)[N], uint32_t (&o)
   for (int n = 0; n < N; ++n) o[n] = kv8_scale(w[n], ratio);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kEvThreads, 2) kv8_evict_kernel(const __grid_constant__ Kv8EvictArgs a) {
-  using Geo = Kv8Geom<D>;
+__global__ void __launch_bounds__(kChThreads, 2) kv8_choose_kernel(const __grid_constant__ Kv8EvictArgs a) {
   extern __shared__ uint32_t keys[];  // of this CTA's tokens
   __shared__ __align__(16) int hist[2][kEvBins];
-  __shared__ int sh_scan[kEvWarps];
+  __shared__ int sh_scan[kChWarps];
   __shared__ int sh_found[2];  // (the first CTA's) a bin, the count above it
-  __shared__ int sh_gt[kEvWarps], sh_eq[kEvWarps];
+  __shared__ int sh_gt[kChWarps], sh_eq[kChWarps];
   __shared__ int sh_count[2];  // this CTA's tokens above the last key, and equal to it
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) kv8_evict_kernel(const __grid_c
   int32_t* kept = a.kept + (int64_t)item * a.budget;
   const int len = min(max(a.b.lens[head.s], 0), kv_capacity(a.c, a.b));
   if (len <= a.budget) {  // stays as it is (the whole cluster leaves here)
-    for (int j = rank * kEvThreads + tid; j < a.budget; j += ctas * kEvThreads) kept[j] = j < len ? j : -1;
+    for (int j = rank * kChThreads + tid; j < a.budget; j += ctas * kChThreads) kept[j] = j < len ? j : -1;
     return;
   }
   const int lo_tok = (int)((int64_t)len * rank / ctas), n = (int)((int64_t)len * (rank + 1) / ctas) - lo_tok;
@@ -158,16 +160,16 @@ __global__ void __launch_bounds__(kEvThreads, 2) kv8_evict_kernel(const __grid_c
   };
   if (held) {
     constexpr int kAtOnce = 8;
-    for (int x0 = tid; x0 < n; x0 += kAtOnce * kEvThreads) {
+    for (int x0 = tid; x0 < n; x0 += kAtOnce * kChThreads) {
       int64_t pid[kAtOnce];
       float m[kAtOnce];
 #pragma unroll
-      for (int y = 0; y < kAtOnce; ++y) pid[y] = x0 + y * kEvThreads < n ? head.page(lo_tok + x0 + y * kEvThreads) : -1;
+      for (int y = 0; y < kAtOnce; ++y) pid[y] = x0 + y * kChThreads < n ? head.page(lo_tok + x0 + y * kChThreads) : -1;
 #pragma unroll
-      for (int y = 0; y < kAtOnce; ++y) m[y] = pid[y] >= 0 ? *head.mass(pid[y], lo_tok + x0 + y * kEvThreads) : 0.0f;
+      for (int y = 0; y < kAtOnce; ++y) m[y] = pid[y] >= 0 ? *head.mass(pid[y], lo_tok + x0 + y * kChThreads) : 0.0f;
 #pragma unroll
       for (int y = 0; y < kAtOnce; ++y)
-        if (x0 + y * kEvThreads < n) keys[x0 + y * kEvThreads] = pid[y] >= 0 ? mass_key(m[y]) : 0u;
+        if (x0 + y * kChThreads < n) keys[x0 + y * kChThreads] = pid[y] >= 0 ? mass_key(m[y]) : 0u;
     }
   }
   auto key_of = [&](int x) { return held ? keys[x] : read_key(x); };
@@ -179,23 +181,23 @@ __global__ void __launch_bounds__(kEvThreads, 2) kv8_evict_kernel(const __grid_c
   int buf = 0;
   for (int level = 0; any && level < 3; ++level, buf ^= 1) {
     const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bins = level == 2 ? 1024 : kEvBins;
-    for (int x = tid; x < kEvBins; x += kEvThreads) hist[buf][x] = 0;
+    for (int x = tid; x < kEvBins; x += kChThreads) hist[buf][x] = 0;
     __syncthreads();
-    for (int x = max(0, a.first - lo_tok) + tid; x < min(n, last0 - lo_tok); x += kEvThreads) {
+    for (int x = max(0, a.first - lo_tok) + tid; x < min(n, last0 - lo_tok); x += kChThreads) {
       const uint32_t k = key_of(x);
       if (level == 0 || (k >> (shift + (level == 1 ? 11 : 10))) == prefix) atomicAdd(&hist[buf][(k >> shift) & (bins - 1)], 1);
     }
     if (ctas > 1) {  // the others' counts go to the first CTA's
       cluster.sync();
       int* to = cluster.map_shared_rank(&hist[buf][0], 0);
-      for (int x = tid; rank && x < bins; x += kEvThreads)
+      for (int x = tid; rank && x < bins; x += kChThreads)
         if (hist[buf][x]) atomicAdd(to + x, hist[buf][x]);
       cluster.sync();
     } else {
       __syncthreads();
     }
     if (rank == 0) {  // some bins a thread, from the top one down; the bin in which the count reaches `need`
-      constexpr int kMine = kEvBins / kEvThreads;
+      constexpr int kMine = kEvBins / kChThreads;
       int mine[kMine], sum = 0;
 #pragma unroll
       for (int y = 0; y < kMine; ++y) {
@@ -222,7 +224,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) kv8_evict_kernel(const __grid_c
   __syncthreads();  // (the keys, where there were no histograms)
   // tokens above `prefix` are taken, and `need` of those equal to it, the lowest positions first; every
   // warp looks through a run of the CTA's tokens, 32 at a time
-  const int run = (n + kEvThreads - 1) / kEvThreads * 32, w0 = min(warp * run, n), w1 = min(w0 + run, n);
+  const int run = (n + kChThreads - 1) / kChThreads * 32, w0 = min(warp * run, n), w1 = min(w0 + run, n);
   auto looks = [&](int x, bool& equal) {
     const int j = lo_tok + x;
     const bool in = x < w1, always = in && (j < a.first || j >= last0);
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) kv8_evict_kernel(const __grid_c
   __syncthreads();
   int gt_before = 0, eq_before = 0, gt_all = 0, eq_all = 0;
 #pragma unroll
-  for (int y = 0; y < kEvWarps; ++y) {
+  for (int y = 0; y < kChWarps; ++y) {
     if (y == warp) {
       gt_before = gt_all;
       eq_before = eq_all;
@@ -275,148 +277,184 @@ __global__ void __launch_bounds__(kEvThreads, 2) kv8_evict_kernel(const __grid_c
       eq_before += __popc(eqs);
     }
   }
-  __threadfence();
-  cluster.sync();
+  cluster.sync();  // no CTA ends while another reads its counts
+}
 
-  // ---- moving
-  const int blocks = (a.budget + 15) / 16, step = ctas * kEvWarps;
-  constexpr int kLoads = D / 32;  // of 16 bytes a lane, keys and values each
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy4(void* to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+// Bytes of a round in a warp's ring: positions, steps, marks and masses of sixteen tokens, and their values' words.
+template <int D>
+constexpr int kMvStage = 256 + 32 * D;
+
+// The keys' or the values' codes and steps of a sequence's head, and with the keys the masses.
+template <int D, bool kValues>
+__device__ __forceinline__ void move_tokens(const Kv8EvictArgs& a, cg::cluster_group& cluster, int item) {
+  using Geo = Kv8Geom<D>;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const Head head{a, item / a.c.heads, item % a.c.heads};
+  const int32_t* kept = a.kept + (int64_t)item * a.budget;
+  const int len = min(max(a.b.lens[head.s], 0), kv_capacity(a.c, a.b));
+  if (len <= a.budget) return;  // (the whole cluster)
+  const int blocks = (a.budget + 15) / 16, step = ctas * kMvWarps;
+  constexpr int kLoads = kValues ? D / 16 : D / 32;  // of 16 bytes a lane
   constexpr uint32_t kZero = 0x80808080u;
-  // this warp's block of a round: the token that moves to place lane & 15, its page.  Positions are asked for three
-  // rounds ahead, pages two, words one.
-  int src, pid, next_src, next_pid, later;
-  bool moves, next_moves;
+  constexpr int kStep = Geo::kParams + (kValues ? 4 : 0), kMark = Geo::kParams + (kValues ? 10 : 8);
+  // Sources are copied into a ring of the warp's: words as they lie there, every lane's own, and of the sixteen tokens
+  // the position, step, marks and mass.  Positions are asked for two rounds before that, pages one.
+  extern __shared__ __align__(16) uint8_t ring_raw[];
+  constexpr int kStage = kMvStage<D>;
+  uint8_t* ring = ring_raw + warp * kMvStages * kStage;
+  int next_src, next_pid, later, next_blk = rank * kMvWarps + warp;
   auto position = [&](int blk) {
     const int dst = blk * 16 + (lane & 15);
-    return dst < a.budget ? __ldcg(kept + dst) : -1;
+    return dst < a.budget ? __ldg(kept + dst) : -1;
   };
-  auto find = [&](int blk, int j) {  // j: the position as it was asked for (where mass was written to meanwhile: anything)
-    const int dst = blk * 16 + (lane & 15);
-    next_src = j >= dst && j < len ? j : -1;
-    next_moves = __any_sync(0xffffffffu, next_src != dst) && blk < blocks;  // else it is what it is
+  auto find = [&]() {  // the token that moves to place lane & 15 of next_blk, its page
+    const int dst = next_blk * 16 + (lane & 15);
+    next_src = later >= dst && later < len ? later : -1;  // (where mass was written to meanwhile, `later` is anything)
     next_pid = next_src >= 0 ? (int)head.page(next_src) : -1;
   };
-  auto advance = [&]() {
-    src = next_src;
-    pid = next_pid;
-    moves = next_moves;
+  auto moving = [&](int blk, int src) {  // else it is what it is
+    return __any_sync(0xffffffffu, src != blk * 16 + (lane & 15)) && blk < blocks;
   };
-  uint4 kw[kLoads], vw[kLoads][2], par;  // its words as they lie there, and the token's params
-  float m;
-  auto load = [&]() {
-    par = make_uint4(0, 0, 0, 0);
-    m = 0.0f;
-    if (!moves) return;
-    if (pid >= 0) {
-      par = *reinterpret_cast<const uint4*>(head.block(pid, src, Geo::kBytes) + Geo::kParams);
-      m = *head.mass(pid, src);
-    }
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {  // keys: 16 channels of token t
-      const int x = i * 32 + lane, t = x / (D / 16);
-      const int p = __shfl_sync(0xffffffffu, pid, t), j = __shfl_sync(0xffffffffu, src, t);
-      kw[i] = make_uint4(kZero, kZero, kZero, kZero);
-      if (p >= 0)
-        kw[i] = *reinterpret_cast<const uint4*>(head.block(p, j, Geo::kBytes) + (j & 15) * D + Geo::k_piece(j & 15, x % (D / 16)) * 16);
-    }
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i)  // values: 8 channels of the pairs that hold tokens 2 x and 2 x + 1
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int x = i * 32 + lane, t = x / (D / 8) * 2 + y;
-        const int p = __shfl_sync(0xffffffffu, pid, t), j = __shfl_sync(0xffffffffu, src, t), from = (j & 15) >> 1;
-        vw[i][y] = make_uint4(kZero, kZero, kZero, kZero);
-        if (p >= 0)
-          vw[i][y] = *reinterpret_cast<const uint4*>(head.block(p, j, Geo::kBytes) + Geo::kVOff + from * 2 * D +
-                                                     Geo::v_piece(from, x % (D / 8)) * 16);
-      }
-  };
-  const int mine = rank * kEvWarps + warp;
-  later = position(mine);
-  find(mine, later);
-  later = position(mine + step);
-  advance();
-  load();
-  find(mine + step, later);
-  later = position(mine + 2 * step);
-  for (int b0 = 0; b0 < blocks; b0 += step) {
-    const int blk = b0 + mine;
-    const bool moving = moves;
-    const int64_t to_pid = moving ? head.page(blk * 16) : -1;
-    uint4 ko[kLoads], vo[kLoads];
-    float k_to = 0.0f, v_to = 0.0f;
-    uint32_t marks = 0;
-    int have = -1;
-    float mass = 0.0f;
-    if (moving) {
-      const float ks = __uint_as_float(par.x), vs = __uint_as_float(par.y);
-      have = src;
-      mass = m;
-      marks = ((par.z >> (src & 15)) & 1u) | ((par.z >> (16 + (src & 15))) & 1u) << 16;
-      k_to = ks;
-      v_to = vs;
-#pragma unroll
-      for (int o = 1; o < 16; o <<= 1) {
-        k_to = fmaxf(k_to, __shfl_xor_sync(0xffffffffu, k_to, o));
-        v_to = fmaxf(v_to, __shfl_xor_sync(0xffffffffu, v_to, o));
-      }
-      // what the tokens' codes are multiplied with: the keys' in lanes 0 to 15, the values' in 16 to 31
-      const Ratio ratio = ratio_of(lane < 16 ? ks : vs, lane < 16 ? k_to : v_to);
-      if (__all_sync(0xffffffffu, ratio.r == 1.0f)) {  // nothing to turn: of one step, all of them
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) ko[i] = kw[i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const int t = (i * 32 + lane) / (D / 16);
-          const uint32_t w[4] = {kw[i].x, kw[i].y, kw[i].z, kw[i].w};
-          uint32_t o[4];
-          turn_words(w, o, __shfl_sync(0xffffffffu, ratio.r, t), __shfl_sync(0xffffffffu, (int)ratio.ties, t));
-          ko[i] = make_uint4(o[0], o[1], o[2], o[3]);
+  // Keys: 16 channels of a token; values: 8 channels of the pairs that hold tokens 2 x and 2 x + 1, one after the other
+  auto fetch = [&](int stage) {
+    uint8_t* to = ring + stage * kStage;
+    if (lane < 16) reinterpret_cast<int*>(to)[lane] = next_src;
+    if (moving(next_blk, next_src)) {
+      if (lane < 16) {
+        uint32_t* par = reinterpret_cast<uint32_t*>(to) + 16 + lane;
+        if (next_pid >= 0) {
+          const uint8_t* from = head.block(next_pid, next_src, Geo::kBytes) + Geo::kParams;
+          copy4(par, from + (kValues ? 4 : 0));
+          copy4(par + 16, from + 8);
+          if constexpr (!kValues) copy4(par + 32, head.mass(next_pid, next_src));
+        } else {
+          par[0] = par[16] = par[32] = 0;
         }
       }
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        uint32_t o[2][2];
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const int t = (i * 32 + lane) / (D / 8) * 2 + y;
-          const uint32_t sel = __shfl_sync(0xffffffffu, src, t) & 1 ? 0x7531 : 0x6420;  // the token's byte of every pair
-          const uint32_t w[2] = {__byte_perm(vw[i][y].x, vw[i][y].y, sel), __byte_perm(vw[i][y].z, vw[i][y].w, sel)};
-          turn_words(w, o[y], __shfl_sync(0xffffffffu, ratio.r, 16 + t), __shfl_sync(0xffffffffu, (int)ratio.ties, 16 + t));
+        const int x = (kValues ? i / 2 : i) * 32 + lane, piece = x % (kValues ? D / 8 : D / 16);
+        const int t = kValues ? x / (D / 8) * 2 + i % 2 : x / (D / 16);
+        const int p = __shfl_sync(0xffffffffu, next_pid, t), j = __shfl_sync(0xffffffffu, next_src, t);
+        uint4* dst = reinterpret_cast<uint4*>(to + 256) + i * 32 + lane;
+        if (p >= 0) {
+          const int row = kValues ? (j & 15) >> 1 : j & 15;
+          const int at = kValues ? Geo::kVOff + row * 2 * D + Geo::v_piece(row, piece) * 16 : row * D + Geo::k_piece(row, piece) * 16;
+          copy16(dst, head.block(p, j, Geo::kBytes) + at);
+        } else {
+          *dst = make_uint4(kZero, kZero, kZero, kZero);
         }
-        vo[i] = make_uint4(__byte_perm(o[0][0], o[1][0], 0x5140), __byte_perm(o[0][0], o[1][0], 0x7362),
-                           __byte_perm(o[0][1], o[1][1], 0x5140), __byte_perm(o[0][1], o[1][1], 0x7362));
       }
     }
-    auto token = cluster.barrier_arrive();  // this warp has read its part of the round
-    advance();
-    load();
-    find(blk + 2 * step, later);
-    later = position(blk + 3 * step);
-    cluster.barrier_wait(std::move(token));
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    next_blk += step;
+    find();
+    later = position(next_blk + step);
+  };
+  later = position(next_blk);
+  find();
+  later = position(next_blk + step);
+#pragma unroll 1
+  for (int y = 0; y < kMvStages - 1; ++y) fetch(y);
+  int stage = 0;
+  for (int b0 = 0; b0 < blocks; b0 += step) {
+    const int blk = b0 + rank * kMvWarps + warp;
+    asm volatile("cp.async.wait_group %0;" ::"n"(kMvStages - 2) : "memory");
+    __syncwarp();
+    // This warp has its part of the round: nothing is handed over but that, so the barrier does not wait for its writes.
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    fetch(stage == 0 ? kMvStages - 1 : stage - 1);  // (the one before this)
+    const uint8_t* from = ring + stage * kStage;
+    const int src = reinterpret_cast<const int*>(from)[lane & 15];
+    const int64_t to_pid = moving(blk, src) ? head.page(blk * 16) : -1;
+    uint4 out[D / 32];
+    float s_new = 0.0f;
+    bool marked = false;
+    if (to_pid >= 0) {
+      const uint32_t* par = reinterpret_cast<const uint32_t*>(from) + 16 + (lane & 15);
+      const uint4* words = reinterpret_cast<const uint4*>(from + 256) + lane;
+      const float s_old = __uint_as_float(par[0]);
+      marked = (par[16] >> ((kValues ? 16 : 0) + (src & 15))) & 1u;
+      s_new = s_old;
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) s_new = fmaxf(s_new, __shfl_xor_sync(0xffffffffu, s_new, o));
+      const Ratio ratio = ratio_of(s_old, s_new);  // what the codes of token lane & 15 are multiplied with
+      if constexpr (!kValues) {
+        if (__all_sync(0xffffffffu, ratio.r == 1.0f)) {  // nothing to turn: of one step, all of them
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) out[i] = words[32 * i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) {
+            const int t = (i * 32 + lane) / (D / 16);
+            const uint4 v = words[32 * i];
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t o[4];
+            turn_words(w, o, __shfl_sync(0xffffffffu, ratio.r, t), __shfl_sync(0xffffffffu, (int)ratio.ties, t));
+            out[i] = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t o[2][2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint4 v = words[32 * (2 * i + y)];
+            const int t = (i * 32 + lane) / (D / 8) * 2 + y;
+            const uint32_t sel = __shfl_sync(0xffffffffu, src, t) & 1 ? 0x7531 : 0x6420;  // the token's byte of every pair
+            const uint32_t w[2] = {__byte_perm(v.x, v.y, sel), __byte_perm(v.z, v.w, sel)};
+            turn_words(w, o[y], __shfl_sync(0xffffffffu, ratio.r, t), __shfl_sync(0xffffffffu, (int)ratio.ties, t));
+          }
+          out[i] = make_uint4(__byte_perm(o[0][0], o[1][0], 0x5140), __byte_perm(o[0][0], o[1][0], 0x7362),
+                              __byte_perm(o[0][1], o[1][1], 0x5140), __byte_perm(o[0][1], o[1][1], 0x7362));
+        }
+      }
+    }
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     if (to_pid >= 0) {
       uint8_t* to = head.block(to_pid, blk * 16, Geo::kBytes);
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int x = i * 32 + lane, t = x / (D / 16), pair = x / (D / 8);
-        *reinterpret_cast<uint4*>(to + t * D + Geo::k_piece(t, x % (D / 16)) * 16) = ko[i];
-        *reinterpret_cast<uint4*>(to + Geo::kVOff + pair * 2 * D + Geo::v_piece(pair, x % (D / 8)) * 16) = vo[i];
+      for (int i = 0; i < D / 32; ++i) {
+        const int x = i * 32 + lane, row = x / (kValues ? D / 8 : D / 16), piece = x % (kValues ? D / 8 : D / 16);
+        const int at = kValues ? Geo::kVOff + row * 2 * D + Geo::v_piece(row, piece) * 16 : row * D + Geo::k_piece(row, piece) * 16;
+        *reinterpret_cast<uint4*>(to + at) = out[i];
       }
-      const uint32_t bits_k = __ballot_sync(0xffffffffu, lane < 16 && (marks & 1u));
-      const uint32_t bits_v = __ballot_sync(0xffffffffu, lane < 16 && (marks >> 16));
-      if (lane == 0)
-        *reinterpret_cast<uint4*>(to + Geo::kParams) =
-            make_uint4(__float_as_uint(k_to), __float_as_uint(v_to), bits_k | bits_v << 16, 0);
-      if (lane < 16 && have >= 0) *head.mass(to_pid, blk * 16 + lane) = mass;
+      const uint32_t marks = __ballot_sync(0xffffffffu, lane < 16 && marked);
+      if (lane == 0) {
+        *reinterpret_cast<float*>(to + kStep) = s_new;
+        *reinterpret_cast<uint16_t*>(to + kMark) = (uint16_t)marks;
+        if constexpr (!kValues) *reinterpret_cast<uint32_t*>(to + Geo::kParams + 12) = 0;
+      }
+      if constexpr (!kValues)
+        if (lane < 16 && src >= 0) *head.mass(to_pid, blk * 16 + lane) = reinterpret_cast<const float*>(from)[48 + lane];
     }
+    stage = stage + 1 == kMvStages ? 0 : stage + 1;
   }
 }
 
+// Clusters of the values first (they have more to do), then those of the keys: the two share no byte that either writes.
 template <int D>
-cudaError_t evict(const Kv8EvictArgs& a, int ctas, cudaStream_t s) {
-  const auto kernel = kv8_evict_kernel<D>;
-  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), kEvKeys * sizeof(uint32_t));
+__global__ void __launch_bounds__(kMvThreads, kMvPerSm) kv8_move_kernel(const __grid_constant__ Kv8EvictArgs a) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int item = blockIdx.x / cluster.num_blocks(), items = a.b.batch * a.c.heads;
+  if (item < items) move_tokens<D, true>(a, cluster, item);
+  else move_tokens<D, false>(a, cluster, item - items);
+}
+
+using Kernel = void (*)(Kv8EvictArgs);
+
+// Calls f with the launch of `clusters` clusters.
+template <typename F>
+cudaError_t with_launch(Kernel kernel, int64_t clusters, int ctas, int threads, size_t smem, cudaStream_t s, F f) {
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
   if (e == cudaSuccess && ctas > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -424,24 +462,47 @@ cudaError_t evict(const Kv8EvictArgs& a, int ctas, cudaStream_t s) {
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = (unsigned)ctas;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)((int64_t)a.b.batch * a.c.heads * ctas));
-  cfg.blockDim = dim3(kEvThreads);
-  cfg.dynamicSmemBytes = kEvKeys * sizeof(uint32_t);
+  cfg.gridDim = dim3((unsigned)(clusters * ctas));
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  return f(cfg);
 }
 
 }  // namespace
 
 cudaError_t moe::kv8_evict(const Kv8& kv, const Kv8EvictArgs& a, cudaStream_t s) {
   const int64_t items = (int64_t)a.b.batch * a.c.heads, cap = (int64_t)a.b.table_pages << a.c.page_shift;
-  int ctas = kEvMaxCluster;
-  // as many as two a multiprocessor hold at once, and as have some tokens each.  Measured, one sequence of 131,072
-  // tokens, 8 heads: 16 CTAs of 256 threads 232 us, 16 of 512 (of which half the clusters wait for the others) 254, 8 of
-  // 512 236, 8 of 256 371.
-  while (ctas > 1 && (items * ctas > 2 * kv.sms || ctas * 1024 > cap)) ctas >>= 1;
-  if (items * ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  return kv.d.head_dim == 64 ? evict<64>(a, ctas, s) : evict<128>(a, ctas, s);
+  // to choose: as many CTAs as two a multiprocessor hold at once, and as have some tokens each
+  int choose = kEvMaxCluster;
+  while (choose > 1 && (items * choose > 2 * kv.sms || choose * 1024 > cap)) choose >>= 1;
+  // to move: as many as have a block for each warp, and as let all clusters run at once (the parts of the chip that a
+  // cluster has to lie in are not of one size, so the driver is asked, once a cache); where clusters outnumber what
+  // runs at once, enough for some waves, since those of the values take longer.  Measured: 32 sequences of up to 4,608
+  // tokens, 8 heads, 512 clusters of one CTA 142 us, of two 131; one of 131,072, 16 clusters of 16, of which some wait
+  // for others, 255, of as many as all run 183.
+  const Kernel mover = kv.d.head_dim == 64 ? kv8_move_kernel<64> : kv8_move_kernel<128>;
+  const size_t ring = kMvWarps * kMvStages * (kv.d.head_dim == 64 ? kMvStage<64> : kMvStage<128>);
+  const bool waves = 2 * items > kMvPerSm * kv.sms;
+  int move = kEvMaxCluster;
+  for (; move > 1; --move) {
+    if (2 * items * move > (waves ? 7 : kMvPerSm) * kv.sms || move * kMvWarps * 16 > a.budget) continue;
+    if (waves) break;
+    int& fit = kv.move_clusters[move];
+    if (fit < 0) {
+      const cudaError_t e = with_launch(mover, 1, move, kMvThreads, ring, s, [&](const cudaLaunchConfig_t& cfg) {
+        return cudaOccupancyMaxActiveClusters(&fit, mover, &cfg);
+      });
+      if (e != cudaSuccess) return e;
+    }
+    if (fit >= 2 * items) break;
+  }
+  if (items * choose > 0x7fffffff || 2 * items * move > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  const cudaError_t e = with_launch(kv8_choose_kernel, items, choose, kChThreads, kEvKeys * sizeof(uint32_t), s,
+                                    [&](const cudaLaunchConfig_t& cfg) { return cudaLaunchKernelEx(&cfg, kv8_choose_kernel, a); });
+  if (e != cudaSuccess) return e;
+  return with_launch(mover, 2 * items, move, kMvThreads, ring, s,
+                     [&](const cudaLaunchConfig_t& cfg) { return cudaLaunchKernelEx(&cfg, mover, a); });
 }

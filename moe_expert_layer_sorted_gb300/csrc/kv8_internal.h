@@ -29,6 +29,8 @@ struct Kv8 {
   cudaEvent_t ev_done = nullptr;  // end of the last call that used the workspace
   unsigned long long last_stream = 0;  // its identity
   bool have_last = false;
+  // of 2, 3, .. CTAs, as many as run at once (kv8_evict.cu), -1: not asked yet
+  mutable int move_clusters[17] = {-1, -1, -1, -1, -1, -1, -1, -1, -1, -1, -1, -1, -1, -1, -1, -1, -1};
   std::atomic<int> busy{0};
   std::string last_error;
 };

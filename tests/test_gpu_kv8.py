@@ -800,3 +800,20 @@ def test_weights_of_uneven_prompts_in_wide_tables(counts, is_causal):
     wide[:, :w.cols] = w.table
     w.table = wide
     run_attention(w, counts, 15, weigh=True, is_causal=is_causal)
+
+
+@pytest.mark.parametrize("heads,lens,budget", [(8, [700, 0, 273, 272] * 8, 272), (4, [3000, 2500, 2100, 1999, 4000], 2000)])
+def test_evict_in_clusters_of_other_sizes(heads, lens, budget):
+    """More clusters than run at once; clusters of a number of CTAs that is no power of two.  Blocks of far steps, marks."""
+    w = World(64, 32, FP, heads, lens, seed=budget)
+    for k, v in zip(w.k, w.v):
+        n = len(k)
+        far = torch.exp2(torch.randint(-6, 3, (-(-n // 16), 1, 1), generator=w.g, device="cuda").float())
+        far = far.repeat_interleave(16, 0)[:n]
+        k.copy_((k.float() * far).to(k.dtype))
+        v.copy_((v.float() * far.flip(0)).to(v.dtype))
+        k[5::97] = math.nan
+        v[11::89, ..., 3] = math.inf
+    w.fill()
+    masses = [torch.exp(2 * torch.randn(n, heads, generator=w.g, device="cuda")) for n in lens]
+    run_evict(w, budget, 4, 50, masses)
