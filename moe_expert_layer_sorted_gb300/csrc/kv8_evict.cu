@@ -9,13 +9,13 @@
 //   writes.  Sixteen kept tokens make a new block, whose step is the largest of theirs.  A token moves to a lower
 //   position or stays, so blocks are made in rounds, one per warp of the cluster: all of a round have been read before
 //   any is written, and no later round reads what this one overwrites.  What later rounds need may then be read as early
-//   as one likes: asynchronous copies bring it to shared memory two rounds ahead, and the barrier of a round runs while
+//   as one likes: asynchronous copies bring it to shared memory a round ahead, and the barrier of a round runs while
 //   its codes are turned.
 //
 // Measured (8 heads of 128 channels, caches whose tokens have not been moved before): 32 sequences of up to 4,608 tokens
-// to 4,096 each 131 us (choice 21), 0.5 GB read and written; one of 131,072 to 65,536 183 us (choice 33).  (Keys and values
-// by the same warps: 207 and 232.)  Bound by the turning of codes, one chain a warp with sixteen warps an SM, and for one
-// sequence by the SMs that sixteen clusters leave idle.
+// to 4,096 each 106 us (choice 21), 0.5 GB read and written; one of 131,072 to 65,536 161 us (choice 33).  Keys and values
+// by the same warps: 207 and 232; rings of three rounds and two CTAs an SM: 117 and 167.  Bound by the chain of a block (ratios,
+// 10 us and 20, and turning, 10 and 17) at 24 warps an SM, and for one sequence by the SMs that sixteen clusters leave idle.
 #include <cooperative_groups.h>
 
 #include "kv8_internal.h"
@@ -30,8 +30,8 @@ constexpr int kMvThreads = 256, kMvWarps = kMvThreads / 32;  // that move
 constexpr int kEvBins = 2048;
 constexpr int kEvKeys = 16384;  // that a CTA keeps in shared memory; of longer shares they are read again
 constexpr int kEvMaxCluster = 16;
-constexpr int kMvStages = 3;  // rounds in a ring
-constexpr int kMvPerSm = 2;  // CTAs that move tokens
+constexpr int kMvStages = 2;  // rounds in a ring
+constexpr int kMvPerSm = 3;  // CTAs that move tokens
 
 // Order-preserving key of a mass (-0 and +0 equal), NaN as -infinity.
 __device__ __forceinline__ uint32_t mass_key(float v) {
@@ -88,28 +88,26 @@ __device__ __forceinline__ Ratio ratio_of(float s, float to) {
   s *= up;
   to *= up;
   if (!(s < to) || s == 0.0f) return {s < to ? 0.0f : 1.0f, false};
+  if (s * 256.0f < to) return {0.0f, false};  // below a half with every code
   const float r = __fdiv_rn(s, to);
-  const uint32_t sb = __float_as_uint(s), tb = __float_as_uint(to);
-  const int d = (int)(tb >> 23) - (int)(sb >> 23);
-  if (d > 8) return {0.0f, false};  // below a half with every code
-  // s / to = S / T in whole numbers of up to 24 and 32 bits
-  const uint32_t S = (sb & 0x7fffffu) | 0x800000u, T = ((tb & 0x7fffffu) | 0x800000u) << d;
-  uint32_t a = T, b = S, p0 = 1, q0 = 0, p = 0, q = 1;
-  while (b != 0) {
-    const uint32_t k = a / b, left = a - k * b;
-    if (k > 254u || k * q + q0 > 254u) break;
+  // Euclid's steps on to and s: whole multiples of s's last place of up to 24 bits, so every remainder is exact.  The
+  // remainder is also how far s q is from to p, on the one side and the other in turn.
+  float a = to, b = s, q0 = 0.0f, q = 1.0f, side = 0x1p-20f;
+  while (b != 0.0f) {
+    float k = (__fdividef(a, b) - 0.5f + 12582912.0f) - 12582912.0f, left = fmaf(-k, b, a);
+    if (left < 0.0f) left = fmaf(-(k -= 1.0f), b, a);
+    if (left >= b) left = fmaf(-(k += 1.0f), b, a);
+    const float qn = fmaf(k, q, q0);
+    if (qn > 254.0f) break;
     a = b;
     b = left;
-    const uint32_t pn = k * p + p0, qn = k * q + q0;
-    p0 = p;
     q0 = q;
-    p = pn;
     q = qn;
+    side = -side;
   }
-  const int over = (int)(S * q - p * T);  // below T / 254, so 32 bits tell it
-  if (over == 0) return {r, fmaf(-r, to, s) != 0.0f};
-  if ((uint32_t)abs(over) > (T >> 15)) return {r, false};
-  return {fmaf(r, over > 0 ? 0x1p-20f : -0x1p-20f, r), false};
+  if (b == 0.0f) return {r, fmaf(-r, to, s) != 0.0f};
+  if (b > to * 0x1p-15f) return {r, false};
+  return {fmaf(r, side, r), false};
 }
 
 // Words of codes times their ratio.  ties: some lane's are (then rounded up and down, and the even one taken).
@@ -327,10 +325,13 @@ __device__ __forceinline__ void move_tokens(const Kv8EvictArgs& a, cg::cluster_g
     uint8_t* to = ring + stage * kStage;
     if (lane < 16) reinterpret_cast<int*>(to)[lane] = next_src;
     if (moving(next_blk, next_src)) {
+      // where the token's block lies, a multiple of 16, and the token's place in it
+      const int64_t block = next_pid >= 0 ? head.block(next_pid, next_src, Geo::kBytes) - a.c.pages : -16;
+      const uint32_t lo = (uint32_t)block | (next_src & 15), hi = (uint32_t)(block >> 32);
       if (lane < 16) {
         uint32_t* par = reinterpret_cast<uint32_t*>(to) + 16 + lane;
         if (next_pid >= 0) {
-          const uint8_t* from = head.block(next_pid, next_src, Geo::kBytes) + Geo::kParams;
+          const uint8_t* from = a.c.pages + block + Geo::kParams;
           copy4(par, from + (kValues ? 4 : 0));
           copy4(par + 16, from + 8);
           if constexpr (!kValues) copy4(par + 32, head.mass(next_pid, next_src));
@@ -342,12 +343,12 @@ __device__ __forceinline__ void move_tokens(const Kv8EvictArgs& a, cg::cluster_g
       for (int i = 0; i < kLoads; ++i) {
         const int x = (kValues ? i / 2 : i) * 32 + lane, piece = x % (kValues ? D / 8 : D / 16);
         const int t = kValues ? x / (D / 8) * 2 + i % 2 : x / (D / 16);
-        const int p = __shfl_sync(0xffffffffu, next_pid, t), j = __shfl_sync(0xffffffffu, next_src, t);
+        const uint32_t l = __shfl_sync(0xffffffffu, lo, t), h = __shfl_sync(0xffffffffu, hi, t);
         uint4* dst = reinterpret_cast<uint4*>(to + 256) + i * 32 + lane;
-        if (p >= 0) {
-          const int row = kValues ? (j & 15) >> 1 : j & 15;
+        if ((int)h >= 0) {
+          const int row = kValues ? (l & 15u) >> 1 : l & 15u;
           const int at = kValues ? Geo::kVOff + row * 2 * D + Geo::v_piece(row, piece) * 16 : row * D + Geo::k_piece(row, piece) * 16;
-          copy16(dst, head.block(p, j, Geo::kBytes) + at);
+          copy16(dst, a.c.pages + ((int64_t)h << 32 | (l & ~15u)) + at);
         } else {
           *dst = make_uint4(kZero, kZero, kZero, kZero);
         }
@@ -481,14 +482,14 @@ cudaError_t moe::kv8_evict(const Kv8& kv, const Kv8EvictArgs& a, cudaStream_t s)
   // to move: as many as have a block for each warp, and as let all clusters run at once (the parts of the chip that a
   // cluster has to lie in are not of one size, so the driver is asked, once a cache); where clusters outnumber what
   // runs at once, enough for some waves, since those of the values take longer.  Measured: 32 sequences of up to 4,608
-  // tokens, 8 heads, 512 clusters of one CTA 142 us, of two 131; one of 131,072, 16 clusters of 16, of which some wait
-  // for others, 255, of as many as all run 183.
+  // tokens, 8 heads, 512 clusters of one CTA 160 us, of two 117, of four 110; one of 131,072, 16 clusters of 16 CTAs, of
+  // which some wait for others, 187, of as many as all run 178.
   const Kernel mover = kv.d.head_dim == 64 ? kv8_move_kernel<64> : kv8_move_kernel<128>;
   const size_t ring = kMvWarps * kMvStages * (kv.d.head_dim == 64 ? kMvStage<64> : kMvStage<128>);
   const bool waves = 2 * items > kMvPerSm * kv.sms;
   int move = kEvMaxCluster;
   for (; move > 1; --move) {
-    if (2 * items * move > (waves ? 7 : kMvPerSm) * kv.sms || move * kMvWarps * 16 > a.budget) continue;
+    if (2 * items * move > (waves ? 14 : kMvPerSm) * kv.sms || move * kMvWarps * 16 > a.budget) continue;
     if (waves) break;
     int& fit = kv.move_clusters[move];
     if (fit < 0) {
