@@ -817,3 +817,29 @@ def test_evict_in_clusters_of_other_sizes(heads, lens, budget):
     w.fill()
     masses = [torch.exp(2 * torch.randn(n, heads, generator=w.g, device="cuda")) for n in lens]
     run_evict(w, budget, 4, 50, masses)
+
+
+def test_first_calls_of_a_cache_are_captured():
+    """Nothing that a cache does once is in the way of a capture."""
+    w = World(64, 64, BF, 4, [1500, 900], seed=7).fill()
+    masses = [torch.rand(n, 4, generator=w.g, device="cuda") for n in w.lens]
+    for i, m in enumerate(masses):
+        w.set_mass(i, m)
+    kept = torch.empty(2, 4, 1000, dtype=torch.int32, device="cuda")
+    q = w.rand(2, 1, 8, 64)
+    out, ls = torch.empty_like(q), torch.empty(2, 8, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        w.cache.attention(q, out, lse=ls, weigh=True, **w.batch)
+        w.cache.evict(kept, keep_first=4, keep_last=16, **w.batch)
+    graph.replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        want = expected(w, i, q[i])
+        ref.check(out[i], ls[i:i + 1], want)
+        n = w.lens[i]
+        assert (kept[i, :, :min(n, 1000)].diff(dim=1) > 0).all() and (kept[i, :, n:] == -1).all()
+        if n > 1000:
+            w.stored[i].keep(kept[i].long())
+    w.holds([1000, 900])
