@@ -15,8 +15,8 @@ using namespace moe;
 //
 // Weights: the single-token kernel leaves its scores behind where the workspace holds them, four
 // bytes a token and column beside the 256 that it reads; otherwise they are made again from the keys.
-// Attention and weights, scores left / made again: 16 columns of 1 sequence of 131,072 110 / 333, of 64 of
-// 2,048 128 / 358.
+// What weights add, us: scores left, 16 columns of 1 sequence of 131,072 37, of 64 of 2,048 38; made again, of any number of
+// columns up to 128, 177 and 178.
 cudaError_t moe::kv8_attention(Kv8& kv, const KvAttnArgs& a, float* mass, cudaStream_t s) {
   const bool bf16 = kv.d.dtype == MOE_KV_BF16;
   cudaError_t e;

@@ -4,21 +4,21 @@
 // With lse from the attention a weight is 2^(y - lse log2 e), y the score in log2 units.  Where the
 // single-token kernel has written its scores (kv8_decode.cuh), a thread adds up four tokens'.  Otherwise the
 // scores are made again, transposed, on the tensor cores, and the sums run along registers:
-//     S^T = U_K Q^T   (128 tokens by 128 columns (row, query head) in TMEM),
+//     S^T = U_K Q^T   (twice 128 tokens by 128 columns (row, query head) in TMEM),
 // a thread having a token (a TMEM lane) and half of the columns.  A column's power of two and lse come from
 // shared memory, a token's step is its thread's.  Columns that see nothing of a tile are not visited.  All the batch's
-// work (sequence, head, token tile, column tile) lies in one line that is cut into equal shares, two CTAs an SM, so that
+// work (sequence, head, 256 tokens, 128 columns) lies in one line that is cut into equal shares, a CTA each SM, so that
 // neither the table's size nor uneven sequences matter; a token tile that is cut between CTAs is added up by the one
 // that finishes it last, in the order of the CTAs, so results do not depend on timing.  (A grid over the table's
-// tiles took 159 us for the case below, but 1,500 for 32 single tokens whose table could hold 131,072.)
+// tiles took 1,500 us for 32 single tokens whose table could hold 131,072.)
 //
 // Each CTA loads the next 128 queries while the tensor cores work on one half of TMEM and the threads on
-// the other; two CTAs share an SM, so that one's barrier is covered by the other's exponents.
+// the other.
 //
-// Measured (8 kv heads of 128 channels): 4,096 rows over themselves, 32 query heads, fp16: 162 us for 2.1 million
-// rows and tokens a query head; the exponents alone would take 58.  Bound by the queries' way into shared memory,
-// which every token tile takes again (without it 105 us), and by the columns' constants (133).  From scores: 32 sequences
-// of up to 4,160 tokens 8 us, latency.
+// Measured (8 kv heads of 128 channels): 4,096 rows over themselves, 32 query heads, fp16: 143 us for 2.1 million
+// rows and tokens a query head; the exponents alone would take 58.  Bound by instructions, those that bring the queries to
+// shared memory among them: 128 tokens a CTA and two CTAs an SM, which did that twice as often, took 162.  From scores: 32
+// sequences of up to 4,160 tokens 8 us, latency.
 #include "kv8_internal.h"
 
 using namespace moe;
@@ -29,11 +29,12 @@ namespace {
 #include "kv_operand.cuh"
 #include "kv_tcgen.cuh"
 
-constexpr int kWeThreads = 256;
+constexpr int kWeThreads = 512, kWeWarps = kWeThreads / 32;
+constexpr int kWeTile = 256;  // tokens of a CTA at a time, two tiles of the tensor cores
 constexpr float kLog2e = 1.4426950408889634f;
 
 // A token tile's first products wait for its keys: it counts as so many more pieces of work, behind its own.  Measured,
-// 4,096 rows over themselves: 166 us without, 162 with 1 or 2, 164 with 4.
+// 4,096 rows over themselves, tiles of 128 tokens: 166 us without, 162 with 1 or 2, 164 with 4.
 constexpr int kWeTurn = 1;
 
 struct WeighArgs {
@@ -65,8 +66,8 @@ struct WeighSeq {
     len = min(q.len, kv_capacity(w.a.c, w.a.b));
     first = (int64_t)q.len - q.rows;
     n = (int)(((int64_t)q.rows * w.per + kPrTile - 1) / kPrTile);
-    tiles = n && !(w.scored && w.scored[s] >= 0) ? (len + kPrTile - 1) / kPrTile : 0;
-    step = w.a.causal ? w.per : 0;
+    tiles = n && !(w.scored && w.scored[s] >= 0) ? (len + kWeTile - 1) / kWeTile : 0;
+    step = w.a.causal ? kWeTile / kPrTile * w.per : 0;
     const int64_t before = (w.a.causal ? first : min(first, (int64_t)0)) * w.per;  // rounded up, below zero too
     skip = before >= 0 ? (before + kPrTile - 1) / kPrTile : -(-before / kPrTile);
   }
@@ -100,7 +101,7 @@ struct WeighItem {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_constant__ WeighArgs w) {
+__global__ void __launch_bounds__(kWeThreads, 1) kv8_weigh_kernel(const __grid_constant__ WeighArgs w) {
   using Geo = Kv8Geom<D>;
   constexpr uint32_t kTileBytes = kPrTile * 128 * (D / 64);
   extern __shared__ uint8_t smem_raw[];
@@ -110,9 +111,9 @@ __global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_c
   // (four of each: threads that are one barrier ahead write a tile's while others read the last but one's)
   __shared__ float4 sh_col[4][kPrTile / 2];        // two columns' factors and -lse log2 e
   __shared__ __align__(16) int sh_seen[4][kPrTile];              // tokens that a column sees
-  __shared__ float sh_step[kPrTile], sh_sum[kPrTile];
+  __shared__ float sh_step[kWeTile], sh_sum[kWeTile];
   __shared__ WeighItem sh;
-  __shared__ int64_t sh_scan[kWeThreads / 32], sh_base;
+  __shared__ int64_t sh_scan[kWeWarps], sh_base;
   __shared__ volatile int64_t line[3];  // the share's first piece, its end, the end of all (not in registers)
   __shared__ int sh_seq;
   __shared__ unsigned sh_last;
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_c
       __syncthreads();
       int64_t all = 0;
 #pragma unroll
-      for (int y = 0; y < kWeThreads / 32; ++y) {
+      for (int y = 0; y < kWeWarps; ++y) {
         if (y < warp) upto += sh_scan[y];
         all += sh_scan[y];
       }
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_c
   }
   __syncthreads();
   const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  uint8_t* gen = smem_raw + (smem - smem_addr(smem_raw));  // keys, then two query tiles
+  uint8_t* gen = smem_raw + (smem - smem_addr(smem_raw));  // two tiles of keys, then two of queries
   if (tid == 0) {
     sh_gone = 0;
     mbar_init(smem_addr(&done[0]), 1);
@@ -174,18 +175,20 @@ __global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_c
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_base)), "n"(256));
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_base)), "n"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   const uint32_t id = idesc(kPrTile, false);
   uint32_t tm = 0;
   auto multiply = [&](int b) {  // by the first warp
     const uint32_t leader = elect_leader();
-    const uint32_t qa = smem + kTileBytes * (1 + b);
+    const uint32_t qa = smem + kTileBytes * (2 + b);
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k)
-      mma_ss(leader, tm + b * kPrTile, desc_k(smem + (k / 4) * (kPrTile * 128) + (k % 4) * 32),
-             desc_k(qa + (k / 4) * (kPrTile * 128) + (k % 4) * 32), id, k ? 1u : 0u);
+    for (int y = 0; y < kWeTile / kPrTile; ++y)
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        mma_ss(leader, tm + b * kWeTile + y * kPrTile, desc_k(smem + y * kTileBytes + (k / 4) * (kPrTile * 128) + (k % 4) * 32),
+               desc_k(qa + (k / 4) * (kPrTile * 128) + (k % 4) * 32), id, k ? 1u : 0u);
     commit(leader, &done[b]);
   };
   fence_before();
@@ -193,8 +196,9 @@ __global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_c
   fence_after();
   tm = tmem_base;
   uint32_t parity = 0;  // a bit per half of TMEM
-  const int quad = warp & 3, half = warp >> 2;  // the warp's lanes of TMEM, its columns of a tile
-  const int token = quad * 32 + lane;
+  // the warp's lanes of TMEM, its columns of a tile, its tile of tokens
+  const int quad = warp & 3, half = warp >> 2 & 1, part = warp >> 3;
+  const int token = part * kPrTile + quad * 32 + lane;
   for (int64_t u = line[0]; u < line[1];) {
     if (tid == 0) {
       WeighPlace at = sh.at;
@@ -232,12 +236,12 @@ __global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_c
       sh.count = (int)(min(at.tile + sh.pieces, line[1]) - u);
     }
     __syncthreads();
-    const int base = sh.at.t * kPrTile, mine = min(sh.count, sh.q.n - sh.c);  // what is not the change to the tile
+    const int base = sh.at.t * kWeTile, mine = min(sh.count, sh.q.n - sh.c);  // what is not the change to the tile
     auto column = [&](int i) { return (sh.c + i) * kPrTile; };
     // the queries of the i-th column tile, zeros where lse is not finite: asked for, and later written.  D / 8 lanes take a
-    // row, a warp sixteen of them.
-    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kLoads = 16 / kRows;
-    const int qc = lane % kLanes, qr = 16 * warp + lane / kLanes;
+    // row, a warp eight of them.
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kLoads = kPrTile / kWeWarps / kRows;
+    const int qc = lane % kLanes, qr = kPrTile / kWeWarps * warp + lane / kLanes;
     uint4 raw[kLoads];
     float row_lse[kLoads];
     const uint16_t* const head = a.q + kv_row_offset(a.b, a.qs, sh.at.s, sh.q.q.row0, 0) + (int64_t)sh.at.h * w.per * a.qs.head + 8 * qc;
@@ -266,7 +270,7 @@ __global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_c
       }
     };
     auto put = [&](int i_) {
-      uint8_t* to = gen + kTileBytes * (1 + (i_ & 1)) + (qc / 8) * (kPrTile * 128);
+      uint8_t* to = gen + kTileBytes * (2 + (i_ & 1)) + (qc / 8) * (kPrTile * 128);
 #pragma unroll
       for (int n = 0; n < kLoads; ++n) {
         const int r = qr + n * kRows;
@@ -315,7 +319,8 @@ __global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_c
           uint4 v = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
           if (pid >= 0) v = *reinterpret_cast<const uint4*>(blk + r * D + Geo::k_piece(r, kc) * 16);
           auto place = [&](int ch8) {
-            return reinterpret_cast<uint4*>(gen + (ch8 / 8) * (kPrTile * 128) + row * 128 + ((ch8 % 8) ^ (row & 7)) * 16);
+            return reinterpret_cast<uint4*>(gen + part * kTileBytes + (ch8 / 8) * (kPrTile * 128) + (row & (kPrTile - 1)) * 128 +
+                                          ((ch8 % 8) ^ (row & 7)) * 16);
           };
           *place(2 * kc) = make_uint4(kv8_pair<0>(v.x), kv8_pair<1>(v.x), kv8_pair<0>(v.y), kv8_pair<1>(v.y));
           *place(2 * kc + 1) = make_uint4(kv8_pair<0>(v.z), kv8_pair<1>(v.z), kv8_pair<0>(v.w), kv8_pair<1>(v.w));
@@ -352,7 +357,7 @@ __global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_c
       kv_wait(smem_addr(&done[b]), parity >> b & 1u, &sh_gone, w.err);
       parity ^= 1u << b;
       fence_after();
-      const uint32_t ts = tm + b * kPrTile + half * 64 + ((uint32_t)(quad * 32) << 16);
+      const uint32_t ts = tm + b * kWeTile + part * kPrTile + half * 64 + ((uint32_t)(quad * 32) << 16);
       auto consume = [&](auto masked_) {
         constexpr bool masked = decltype(masked_)::value;
 #pragma unroll
@@ -380,8 +385,10 @@ __global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_c
           }
         }
       };
-      // every column sees the whole token tile?
-      if (sh.q.first + x0 / w.per >= base + kPrTile - 1 || (!a.causal && sh.q.first >= 0)) consume(std::false_type());
+      // no column sees any of these tokens?  every column all of them?
+      const int low = base + part * kPrTile;
+      if (a.causal && sh.q.first + (x0 + kPrTile - 1) / w.per < low) continue;
+      if (sh.q.first + x0 / w.per >= low + kPrTile - 1 || (!a.causal && sh.q.first >= 0)) consume(std::false_type());
       else consume(std::true_type());
     }
     float s0, s1;
@@ -395,7 +402,7 @@ __global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_c
     const int64_t tile = sh.at.tile, tile_end = tile + sh.pieces;
     if (!half) {
       const float all = (s0 + s1) + sh_sum[token];
-      if (!whole) w.parts[(int64_t)(2 * blockIdx.x + (u == line[0] ? 0 : 1)) * kPrTile + token] = all;
+      if (!whole) w.parts[(int64_t)(2 * blockIdx.x + (u == line[0] ? 0 : 1)) * kWeTile + token] = all;
       else if (base + token < sh.q.len) add_mass(w, sh.at.s, sh.at.h, base + token, all);
     }
     if (!whole) {
@@ -406,11 +413,11 @@ __global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_c
       if (tid == 0) sh_last = add_acq_rel(&w.counters[c0]);
       __syncthreads();
       if (sh_last == (unsigned)(c1 - c0)) {
-        if (tid < kPrTile && base + tid < sh.q.len) {
+        if (tid < kWeTile && base + tid < sh.q.len) {
           float sum_ = 0.0f;
 #pragma unroll 8
           for (int y = c0; y <= c1; ++y)
-            sum_ += __ldcg(w.parts + (int64_t)(2 * y + (y == c0 && tile != total * c0 / n ? 1 : 0)) * kPrTile + tid);
+            sum_ += __ldcg(w.parts + (int64_t)(2 * y + (y == c0 && tile != total * c0 / n ? 1 : 0)) * kWeTile + tid);
           add_mass(w, sh.at.s, sh.at.h, base + tid, sum_);
         }
         if (tid == 0) w.counters[c0] = 0;  // for the next call
@@ -421,13 +428,13 @@ __global__ void __launch_bounds__(kWeThreads, 2) kv8_weigh_kernel(const __grid_c
   }
   if (warp == 0) {
     fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(256));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(512));
   }
 }
 
 // From the scores that the single-token kernel wrote: a thread adds up the columns of four tokens (of one page).
-constexpr int kWeTokens = 4 * kWeThreads;
-__global__ void __launch_bounds__(kWeThreads) kv8_weigh_scores_kernel(const __grid_constant__ WeighArgs w, const __grid_constant__ Kv8Scores scores,
+constexpr int kScThreads = 256, kWeTokens = 4 * kScThreads;
+__global__ void __launch_bounds__(kScThreads) kv8_weigh_scores_kernel(const __grid_constant__ WeighArgs w, const __grid_constant__ Kv8Scores scores,
                                                                       int ctas) {
   __shared__ float sh_lse[kKv8Columns];
   const KvAttnArgs& a = w.a;
@@ -484,7 +491,7 @@ cudaError_t moe::kv8_weigh(Kv8& kv, const KvAttnArgs& a, float* mass, const Kv8S
     const int64_t items = (int64_t)a.c.heads * a.b.batch;
     const int64_t ctas = std::min<int64_t>((cap + kWeTokens - 1) / kWeTokens, std::max<int64_t>(8192 / items, 1));
     if (items * ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    kv8_weigh_scores_kernel<<<(unsigned)(items * ctas), kWeThreads, 0, s>>>(w, scores, (int)ctas);
+    kv8_weigh_scores_kernel<<<(unsigned)(items * ctas), kScThreads, 0, s>>>(w, scores, (int)ctas);
     const cudaError_t e = cudaGetLastError();
     const int64_t rounds = (cap + kPrTile - 1) / kPrTile;
     if (e != cudaSuccess || items * scores.ctiles <= scores.limit / rounds) return e;  // there was room for all of them
@@ -492,11 +499,11 @@ cudaError_t moe::kv8_weigh(Kv8& kv, const KvAttnArgs& a, float* mass, const Kv8S
   if ((int64_t)a.b.max_new * w.per > 0x7fffffff - kPrTile) return cudaErrorInvalidConfiguration;
   cudaError_t e = cudaSuccess;
   KV8_DISPATCH(kv.d, {
-    const size_t smem = std::max<size_t>(1024 + (size_t)3 * kPrTile * D * 2, 80 << 10);  // two CTAs an SM, as many as TMEM holds
+    const size_t smem = std::max<size_t>(1024 + (size_t)4 * kPrTile * D * 2, 120 << 10);  // one CTA an SM, as many as TMEM holds
     const auto kernel = kv8_weigh_kernel<T, D>;
     e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
     if (e == cudaSuccess) {
-      kernel<<<(unsigned)std::min(2 * kv.sms, Kv8::kCounters), kWeThreads, smem, s>>>(w);
+      kernel<<<(unsigned)std::min(kv.sms, Kv8::kCounters), kWeThreads, smem, s>>>(w);
       e = cudaGetLastError();
     }
   });
