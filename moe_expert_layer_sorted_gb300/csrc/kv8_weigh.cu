@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kWeThreads, 1) kv8_weigh_kernel(const __grid_c
         *reinterpret_cast<uint4*>(to + r * 128 + ((qc % 8) ^ (r & 7)) * 16) = raw[n];
         if (qc == 0) {
           float* col = reinterpret_cast<float*>(&sh_col[i_ & 3][r >> 1]);
-          col[r & 1] = a.scale * kLog2e * back;
+          col[r & 1] = fine ? a.scale * kLog2e * back : 0.0f;  // (the scale may be so large that the product is not finite)
           col[2 + (r & 1)] = fine ? -row_lse[n] * kLog2e : -__int_as_float(0x7f800000);
         }
       }

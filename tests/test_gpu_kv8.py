@@ -843,3 +843,12 @@ def test_first_calls_of_a_cache_are_captured():
         if n > 1000:
             w.stored[i].keep(kept[i].long())
     w.holds([1000, 900])
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_rows_beyond_fp32_weigh_nothing(rows):
+    """A scale that takes every score out of fp32's range: no row is finite, and mass stays what it was."""
+    w = World(64, 64, BF, 2, [130], seed=rows).fill()
+    out, ls = run_attention_raw(w, w.rand(rows, 4, 64), 3e38, weigh=True)
+    assert not torch.isfinite(ls).any()
+    assert (w.mass_of(0) == 0).all()
