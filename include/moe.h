@@ -548,9 +548,10 @@ moe_status moe_kv8_read(moe_kv8_cache* kv, int layer, const moe_kv_batch* batch,
  * in an order that does not depend on timing), are added to its mass; needs mass and lse.  Rows whose lse is
  * not finite add nothing.  Pages must then not be shared between the sequences of the call (their tokens' mass is
  * read, added to and written without regard to another's).
- * Accuracy: scores, weights and sums are fp32 and the codes are exact operands; a weight enters the
- * product with the values with 11 bits, relative to the largest weight times step of its row (below 2^-24 of
- * that it loses bits). */
+ * Accuracy: scores, weights and sums are fp32 and the codes are exact operands.  A weight times its block's step enters the
+ * product with the values with 11 bits, or, where it is small beside others, is off by up to 2^-17 of the sum of these
+ * products over 128 tokens that lie together (with up to 32 rows times query heads of a kv head: 2^-25 of the largest
+ * of the row), and never by more than itself; what is below 2^-48 of the row's largest loses bits beyond that. */
 moe_status moe_kv8_attention(moe_kv8_cache* kv, int layer, const moe_kv_batch* batch, const moe_kv_tensor* q,
                              int q_heads, float scale, int causal, const moe_kv_tensor* out, float* lse, int weigh,
                              void* stream);

@@ -22,7 +22,9 @@
 // far from what the row's references are made for, take two exponentials per score, one for
 // the sum and one for P, so that values of any size take nothing from the sum, nor weights
 // from the values.  A row's references are raised, and O rescaled in TMEM, only where a
-// tile's P would outgrow fp16 (or its sum fp32).
+// tile's P would outgrow fp16 (or its sum fp32), and rz is lowered, O scaled up, where a tile's P
+// are all small: a token that takes most of a row's weight may have next to no value (a block's
+// step says nothing of a single token of it), and what the others weigh then makes up the result.
 //
 // Where there are fewer tiles of rows than half the SMs, the tokens are cut into as
 // many stretches as fill them, and a second kernel joins a tile's parts, in the order
@@ -31,8 +33,8 @@
 // Masks: a score that its row may not see becomes -infinity.  Tokens that are not finite
 // have codes of zeros; a row that sees one is remembered, and NaN in the end.
 //
-// Measured (bf16, 32 query and 8 kv heads of 128 channels): 8,192 rows at the end of 16,384 tokens 1,301 us, 1,270
-// TFLOP/s (0.65 of the measured rate); with scores that never raise a reference 1,261; 4,096 rows (fp16) 158 us.
+// Measured (bf16, 32 query and 8 kv heads of 128 channels): 8,192 rows at the end of 16,384 tokens 1,325 us, 1,245
+// TFLOP/s (0.63 of the measured rate); with scores that never raise a reference 1,288; 4,096 rows (fp16) 158 us.
 // Bound by two things of about the same length: the chain of a token tile, scores -> weights -> product, of which
 // two row tiles alternate (without the loads of codes and the exponents it takes 1,130 us), and the warps that turn
 // codes (without their loads 1,219).  What paid: a tile's words asked for as soon as the last one's are turned, what
@@ -57,10 +59,18 @@ constexpr int kPrThreads = 512;  // four warpgroups; warps 13-15 only fill their
 // 128 threads x (176 + 176 + 112 + 48) = 512 x 128.
 constexpr int kPrRegs = 128, kPrSoftRegs = 176, kPrDequantRegs = 112, kPrMmaRegs = 48;
 static_assert(2 * kPrSoftRegs + kPrDequantRegs + kPrMmaRegs == 4 * kPrRegs, "a split above the launch's registers never ends");
-// rz is set kPrDrop below the largest weight times step and raised when a tile's sum to kPrLimit: no P passes fp16's
-// range, which holds those 2^-26 of the largest.  (A raise costs a tile twice its time; 7 and 2^15, 4 and 2^15, 2 and
-// 60,000: 1,542, 1,379 and 1,301 us for the chunk below, whose scores have a standard deviation of 2.)
-constexpr float kPrDrop = 2.0f, kPrLimit = 60000.0f;
+// rz is set kPrDrop below the largest weight times step and raised when a tile's sum comes to kPrLimit, so that this is 2^kPrAim:
+// no P passes fp16's range.  Where the sum passes kPrFar, the scores are looked through again, which takes a tile three times as
+// long (every raise so, 7 and 2^15, 4 and 2^15, 2 and 60,000: 1,542, 1,379 and 1,301 us for the chunk below, whose scores have a
+// standard deviation of 2).
+constexpr float kPrDrop = 2.0f, kPrLimit = 60000.0f, kPrAim = 5.0f, kPrFar = 0x1p60f;
+// rz is lowered, the sum 2^kPrAim again, where the P of the tokens that a row sees of a tile are below kPrLow on average: fp16's
+// last place below 2^-14 is 2^-24, so such a P is off by 2^-25 at most, and 128 of them by twice what 11 bits would be beside
+// their sum.  By no more than 2^kPrFall since it was raised, which keeps O within fp32 (tiles' sums of 2^16 times 127, by 2^24
+// tiles: 2^103); falls of less than kPrStep and what is below kPrGone are left alone.  Measured, never lowered / lowered, us: the
+// 8,192 rows below 1,308 / 1,325, with scores that never raise a reference 1,271 / 1,288, the ragged prompts 39.3 / 39.3 (50 where
+// the scores are looked through).
+constexpr float kPrLow = 0x1p-15f, kPrGone = 0x1p-64f, kPrFall = 56.0f, kPrStep = 8.0f;
 constexpr float kPrApart = 30.0f;       // log2 of how far an ordinary tile's steps may lie apart,
 constexpr float kPrNear = 60.0f;        // and of how far they may be from the row's 2^-dz
 constexpr float kPrMaxSum = 0x1p60f;    // ry is raised when a tile's weights sum to this
@@ -160,6 +170,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv8_prompt_kernel(const __grid_
     if (tid == 0) mbar_arrive(smem_addr(&qFull));
     const float kappa = a.scale * 1.4426950408889634f * sh_qscale[t * kPrTile + quad * 32 + lane];
     float ry = kNone, dz = kNoProduct, l = 0.0f;
+    float fell = 0.0f;    // how far rz has been lowered since it was raised
     bool vnan = false;    // the row sees values that are not finite
     bool coarse = false;  // a row's scores are as large as kCoarse
     for (int j = 0; j < (t == 0 || two ? ntiles : 0); ++j) {
@@ -224,33 +235,39 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv8_prompt_kernel(const __grid_
           if constexpr (plain) whole = fma2(part, pair2(b.z, b.z), whole);
         }
       };
-      // P against the references as they stand, and once more where they have to rise: for the first
-      // tile, or where a P or a weight is above its limit, which shows in the sum (that may reach the
-      // limit without one: no harm)
-      bool raise = j == 0;
+      // P against the references as they stand, and once more where they have to move: for the first tile, or where
+      // a P or a weight is above its limit, which shows in the sum (that may reach the limit without one: no harm), or where
+      // the row's P are all small.  Mostly the sum tells by how much, otherwise the scores are looked through.
+      enum { kStay, kShift, kScan } move = j == 0 ? kScan : kStay;
+      float by = 0.0f;
       while (true) {
-        if (raise) {
-          float top = kNone, most_z = -__int_as_float(0x7f800000);
+        if (move != kStay) {
+          float cur = dz, next = dz + by;
+          if (move == kScan) {
+            float top = kNone, most_z = -__int_as_float(0x7f800000);
 #pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            load(k, v[0]);
+            for (int k = 0; k < 4; ++k) {
+              load(k, v[0]);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(v[0][i]));
-          }
-          const float now = fmaxf(ry, top);
+              for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(v[0][i]));
+            }
+            const float now = fmaxf(ry, top);
 #pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            load(k, v[0]);
-            const float lv[2] = {load_block(blocks + 32 * k).y, load_block(blocks + 32 * k + 16).y};
+            for (int k = 0; k < 4; ++k) {
+              load(k, v[0]);
+              const float lv[2] = {load_block(blocks + 32 * k).y, load_block(blocks + 32 * k + 16).y};
 #pragma unroll
-            for (int i = 0; i < 32; ++i) most_z = fmaxf(most_z, (__uint_as_float(v[0][i]) - now) + lv[i / 16]);
+              for (int i = 0; i < 32; ++i) most_z = fmaxf(most_z, (__uint_as_float(v[0][i]) - now) + lv[i / 16]);
+            }
+            l *= exp2_fast(ry - now);
+            cur = fminf(dz - (ry - now), kNoProduct);
+            next = fminf(kPrDrop - most_z, cur);
+            ry = now;
+            coarse = coarse || __any_sync(0xffffffffu, ry != kNone && fabsf(ry) >= kCoarse);
           }
-          l *= exp2_fast(ry - now);
-          const float cur = fminf(dz - (ry - now), kNoProduct), want = kPrDrop - most_z;
-          const float fo = want < cur ? exp2_fast(want - cur) : 1.0f;
-          ry = now;
-          dz = fminf(want, cur);
-          coarse = coarse || __any_sync(0xffffffffu, ry != kNone && fabsf(ry) >= kCoarse);
+          const float fo = next != cur ? exp2_fast(next - cur) : 1.0f;
+          dz = next;
+          fell = fmaxf(fell + (next - cur), 0.0f);
           plain = ordinary();
           if (j > 0 && __any_sync(0xffffffffu, fo != 1.0f)) {
 #pragma unroll 1
@@ -281,12 +298,22 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv8_prompt_kernel(const __grid_
             weights(v[0], k, load_block(blocks + 32 * k), load_block(blocks + 32 * k + 16), std::false_type());
           }
         }
-        if (raise) break;
+        if (move == kScan) break;
         float s0, s1, w0, w1;
         split2(sum, s0, s1);
         split2(whole, w0, w1);
-        raise = __any_sync(0xffffffffu, fmaxf(s0, s1) > kPrLimit || (!plain && w0 + w1 > kPrMaxSum));
-        if (!raise) break;
+        s0 += s1;
+        const bool large = !plain && w0 + w1 > kPrMaxSum;
+        if (!__any_sync(0xffffffffu, s0 > kPrLimit || s0 < kPrLow * kPrTile || large)) break;
+        if (__any_sync(0xffffffffu, s0 > kPrFar || large)) {
+          move = kScan;
+          continue;
+        }
+        if (move == kShift) break;
+        const bool low = s0 < kPrLow * (float)min(seen - j * kPrTile, kPrTile) && s0 > kPrGone && fell <= kPrFall - kPrStep;
+        by = s0 > kPrLimit || low ? fminf(kPrAim - log2_fast(s0), kPrFall - fell) : 0.0f;
+        if (!__any_sync(0xffffffffu, by != 0.0f)) break;
+        move = kShift;
       }
       {
         float w0, w1;
