@@ -261,7 +261,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv8_prompt_kernel(const __grid_
             }
             l *= exp2_fast(ry - now);
             cur = fminf(dz - (ry - now), kNoProduct);
-            next = fminf(kPrDrop - most_z, cur);
+            const float want = kPrDrop - most_z;  // (infinite where there is nothing)
+            next = want >= cur + kPrStep && want <= cur + 64.0f && fell <= kPrFall - kPrStep ? fminf(want, cur + (kPrFall - fell)) : fminf(want, cur);
             ry = now;
             coarse = coarse || __any_sync(0xffffffffu, ry != kNone && fabsf(ry) >= kCoarse);
           }

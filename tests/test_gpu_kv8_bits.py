@@ -11,14 +11,17 @@ BF, FP = torch.bfloat16, torch.float16
 HALF = {BF: 2.0 ** -8, FP: 2.0 ** -11}  # half a step, relative
 
 
-def cache_of(level, v, heads, dtype, D=64, P=64):
+def cache_of(level, v, heads, dtype, D=64, P=64, far=None):
     """Tokens whose scores are their `level` (whole numbers up to 127) times the queries' first channel, and whose
-    values v [N, D] are whole numbers of 0..127, all of them stored as they are (127 in every block: steps of 1)."""
+    values v [N, D] are whole numbers of 0..127, all of them stored as they are (127 in every block: steps of 1).  far: the
+    keys' third channel."""
     from moe_expert_layer_sorted_gb300 import KVCache8
     n = len(level)
     cache = KVCache8.allocate(-(-n // P), kv_heads=heads, head_dim=D, page_size=P, dtype=dtype)
     k = torch.zeros(n, D, device="cuda")
     k[:, 0], k[:, 1] = level.float(), 127.0
+    if far is not None:
+        k[:, 2] = far
     v = v.clone()
     v[15::16, 0] = 127.0
     table = torch.arange(-(-n // P), dtype=torch.int32, device="cuda")[None]
@@ -95,3 +98,28 @@ def test_weights_that_fall_and_rise(shape, order):
     v[stairs > 0] = 0
     cache, table, v = cache_of(25 * stairs.int(), v, 8, BF)
     run(cache, table, v, 25 * stairs.int(), 9.4 / 25, dtype=BF, **shape)
+
+
+def test_weights_that_fall_where_another_row_rises_far():
+    """Rows that share a warp: of some, the second 128 tokens are little beside the first one (which has no value); of the
+    others, they are 2^70 of all before."""
+    n, rows, per, unit = 384, 640, 4, 22.912 / 127
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    v = torch.randint(64, 128, (n, 64), generator=gen, device="cuda").float()
+    level = torch.zeros(n, dtype=torch.int32, device="cuda")
+    level[3] = 127
+    v[3] = 0
+    far = torch.zeros(n, device="cuda")
+    far[128:] = 127
+    cache, table, v = cache_of(level, v, 8, FP, far=far)
+    q = torch.zeros(1, rows, 8 * per, 64, device="cuda")
+    q[:, :, ::2, 0] = 1
+    q[:, :, 1::2, 2] = 70 / 22.912
+    q = q.to(FP)
+    out = torch.empty_like(q)
+    cache.attention(q, out, table=table, causal=False, scale=unit * math.log(2), lens=torch.tensor([n], dtype=torch.int32, device="cuda"))
+    for h, y in ((0, level.double() * unit), (1, far.double() * unit * q[0, 0, 1, 2].double())):
+        want, tol = wanted(y, v, 128, 2.0 ** -27, 2.0 ** -17)
+        off = ((out[0, -n:, h::2].double() - want).abs() / (tol + 1.01 * HALF[FP] * want + 2.0 ** -24)).max().item()
+        assert off <= 1, (h, off)
+    assert (out[0, :-n] == 0).all()  # rows before the first token
