@@ -12,8 +12,10 @@
 // output's, independent from token to token).  Two references per column: ry of the
 // sum of weights 2^(y - ry), and rz of the weights times steps, so that values of any
 // size beside each other take nothing from the sum, nor weights from the values.
-// They are raised only where a block passes them far (by 2^60, by 2^12): hardly any
-// block rescales anything.
+// They are raised only where a block passes them far (by 2^60, by 2^12), and rz is
+// lowered where it is 2^8 above all of a block: a token that takes most of a row's weight may
+// have next to no value (a block's step says nothing of a single token of it), and the
+// result is then the others'.  Hardly any block rescales anything.
 //
 // Work split: as in the 4-bit cache's kernel (kv_rounds.cuh), rounds of 8 blocks of 16
 // tokens cut into equal shares, one per CTA; each warp takes one block of a round and
@@ -24,10 +26,10 @@
 // the CTA that finishes last, in the order of the CTAs, so results do not depend on
 // timing.
 //
-// Measured (8 kv heads of 128 channels): 64 sequences of up to 8,191 tokens, 32 query heads, bf16: 112 us, 5.8 TB/s,
-// 0.87 of the measured copy rate; 2 of 131,072, 64 query heads, fp16: 95 us, 5.6 TB/s; one of 777: 12 us.  Bound by
+// Measured (8 kv heads of 128 channels): 64 sequences of up to 8,191 tokens, 32 query heads, bf16: 115 us, 5.7 TB/s,
+// 0.85 of the measured copy rate (112 with an rz that only rises); 2 of 131,072, 64 query heads, fp16: 94 us, 5.7 TB/s; one of 777: 12 us.  Bound by
 // the memory, and some 12 us of launch, shares, first round and joins (one token of 2,048 takes 13 us, 64 sequences of
-// 2,048 57).  A block takes about 200 instructions where the memory's rate leaves 700 issue slots, so that codes
+// 2,048 59).  A block takes about 200 instructions where the memory's rate leaves 700 issue slots, so that codes
 // can be turned to exact fp16 numbers one by one.  Shares of at least 2 or 4 rounds: one sequence of 777 tokens
 // 15.3 and 17.8 us, of 4,096 14.2 and 14.8 (against 15.1), of 16,384 20.7 and 18.8 (against 21.0).
 #pragma once
@@ -46,6 +48,10 @@ constexpr int kDec8Threads = kDecWarps * 32;
 constexpr int kDec8MaxParts = 304;        // CTAs, so parts of an item
 constexpr float kRaiseSum = 60.0f, kRaiseProduct = 12.0f;  // weights reach 2^60, weights times steps 2^12
 constexpr float kNoProduct = 1e38f;       // ry - rz of a column that has seen no value
+// rz is lowered where a block's largest weight times step is below 2^kLower (fp16's last place below 2^-14 is 2^-24: of such a
+// block all sixteen together are off by 2^-13 of the largest), by no more than kLowerMost since it was raised, which keeps O
+// within fp32; what is 2^kGone below rz is left alone, as are the last eight of kLowerMost.
+constexpr float kLower = -8.0f, kLowerMost = 56.0f, kGone = -64.0f;
 
 // Slots of a warp's ring: two CTAs share an SM for 8 columns, one takes it for 16 (whose O takes two slots).
 template <int NT>
@@ -256,6 +262,7 @@ __global__ void __launch_bounds__(kDec8Threads, NT == 1 ? 2 : 1)
 
       float acc[D / 16][NT][4];  // O^T: channel tiles by columns
       float ry[NT][2], l[NT][2], dz[NT][2];  // reference, sum of weights, ry - rz
+      float fell[NT][2];         // how far rz has been lowered since it was raised
       float bad[NT][2];          // NaN where the column sees a token of NaN values
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -267,7 +274,7 @@ __global__ void __launch_bounds__(kDec8Threads, NT == 1 ? 2 : 1)
         for (int e = 0; e < 2; ++e) {
           ry[nt][e] = kNone;
           dz[nt][e] = kNoProduct;
-          l[nt][e] = bad[nt][e] = 0.0f;
+          l[nt][e] = bad[nt][e] = fell[nt][e] = 0.0f;
         }
       }
 
@@ -326,14 +333,19 @@ __global__ void __launch_bounds__(kDec8Threads, NT == 1 ? 2 : 1)
         }
         // ---- references
         bool raise = false;
+        uint32_t all = ~0u;  // columns (a bit of four) of which some token is not small
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float t = fmaxf(y[nt][x], y[nt][2 + x]) - ry[nt][x];
-            raise |= t > kRaiseSum || t + (lv + dz[nt][x]) > kRaiseProduct;
+            const float t = fmaxf(y[nt][x], y[nt][2 + x]) - ry[nt][x], z = t + (lv + dz[nt][x]);
+            raise |= t > kRaiseSum || z > kRaiseProduct;
+            uint32_t some = __ballot_sync(0xffffffffu, z > kLower);
+            some |= some >> 16;
+            some |= some >> 8;
+            all &= some | some >> 4;
           }
-        if (__any_sync(0xffffffffu, raise)) {
+        if (__any_sync(0xffffffffu, raise) || (all & 15u) != 15u) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -346,9 +358,11 @@ __global__ void __launch_bounds__(kDec8Threads, NT == 1 ? 2 : 1)
               l[nt][x] *= exp2_fast(up);
               float to = fminf(dz[nt][x] - up, kNoProduct);  // rz as it is, from the new ry
               const float most = -((t - now) + lv);          // rz at this block's largest product
-              if (most < to && t != kNone) {
-                const float by = exp2_fast(most - to);
-                to = most;
+              const bool lower = most > to - kLower && most < to - kGone && fell[nt][x] <= kLowerMost - 8.0f;
+              if ((most < to || lower) && t != kNone) {
+                const float next = fminf(most, to + (kLowerMost - fell[nt][x])), by = exp2_fast(next - to);
+                fell[nt][x] = fmaxf(fell[nt][x] + (next - to), 0.0f);
+                to = next;
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) {
                   acc[j][nt][x] *= by;

@@ -67,11 +67,11 @@ def run(cache, table, v, level, unit, rows, per, batch, dtype):
         assert off <= 1, f"{s}: {off} of the bound, {((got - want).abs().norm() / want.norm() / len(got) ** 0.5).item():.1e} of the result"
 
 
-# 80 pairs of row tiles, so that none is cut
-MANY = dict(rows=640, per=4, batch=1)
+# 320 items of single tokens, so that one CTA takes the whole of most; 80 pairs of row tiles, so that none is cut
+FEW, MANY = dict(rows=1, per=4, batch=40), dict(rows=640, per=4, batch=1)
 
 
-@pytest.mark.parametrize("shape", [MANY], ids=["many"])
+@pytest.mark.parametrize("shape", [FEW, MANY], ids=["few", "many"])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("apart,dtype", [(12.0, FP), (18.3, FP), (20.9, FP), (22.912, FP), (30.2, BF), (41.7, BF), (52.0, BF)])
 def test_one_token_of_much_weight_and_no_value(shape, D, apart, dtype):
@@ -85,7 +85,7 @@ def test_one_token_of_much_weight_and_no_value(shape, D, apart, dtype):
     run(cache, table, v, level, apart / 127, dtype=dtype, **shape)
 
 
-@pytest.mark.parametrize("shape", [MANY], ids=["many"])
+@pytest.mark.parametrize("shape", [FEW, MANY], ids=["few", "many"])
 @pytest.mark.parametrize("order", ["down", "up", "both", "last"])
 def test_weights_that_fall_and_rise(shape, order):
     """Steps of 2^-9.4 and less every 256 tokens, values in the lightest steps alone; the same upwards, and down and up."""
