@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kDec8Threads, NT == 1 ? 2 : 1)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) y[nt][e] = y[nt][e] * factor[nt][e & 1] * ks;
+          for (int e = 0; e < 4; ++e) y[nt][e] *= factor[nt][e & 1] * ks;  // (together first: they may lie far apart)
         if (par.z != 0) {  // tokens that read as NaN
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)

@@ -370,8 +370,8 @@ __global__ void __launch_bounds__(kWeThreads, 1) kv8_weigh_kernel(const __grid_c
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             const float4 f = col[e / 2];
-            uint64_t y = mul2(pair2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), pair2(f.x, f.y));
-            y = fma2(y, ks2, pair2(f.z, f.w));
+            const uint64_t by = mul2(pair2(f.x, f.y), ks2);  // (together first: they may lie far apart)
+            const uint64_t y = fma2(pair2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), by, pair2(f.z, f.w));
             float y0, y1;
             split2(y, y0, y1);
             y0 = exp2_fast(y0);
