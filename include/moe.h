@@ -546,7 +546,8 @@ moe_status moe_kv8_read(moe_kv8_cache* kv, int layer, const moe_kv_batch* batch,
  * token of NaN keys or values is NaN.  weigh = 1: after it, every token's softmax
  * weights of this call, summed over the rows and query heads that see it (in fp32,
  * in an order that does not depend on timing), are added to its mass; needs mass and lse.  Rows whose lse is
- * not finite add nothing.  Pages must then not be shared between the sequences of the call (their tokens' mass is
+ * not finite add nothing, among them those whose results a wait that gave up has spoiled: these are NaN, lse too.
+ * Pages must then not be shared between the sequences of the call (their tokens' mass is
  * read, added to and written without regard to another's).
  * Accuracy: scores, weights and sums are fp32 and the codes are exact operands.  A weight times its block's step enters the
  * product with the values with 11 bits, or, where it is small beside others, is off by up to 2^-17 of the sum of these

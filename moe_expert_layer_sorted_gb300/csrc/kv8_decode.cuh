@@ -453,6 +453,8 @@ __global__ void __launch_bounds__(kDec8Threads, NT == 1 ? 2 : 1)
         }
       }
       __syncthreads();
+      // Where a wait gave up, the rows whose blocks are missing are NaN, their lse too, so that they add nothing to mass.
+      const bool gone = *static_cast<volatile uint32_t*>(&sh_gone);
       const int item0 = it.at.item0, item_end = it.at.item_end;
       const bool whole = seg == item0 && seg_end == item_end;
       // partial results: a CTA's first stretch in slot 0, its last in slot 1
@@ -481,6 +483,7 @@ __global__ void __launch_bounds__(kDec8Threads, NT == 1 ? 2 : 1)
           Z = fmaxf(Z, d - mz[w * C + col]);
           L = fmaf(exp2_fast(d), ml[w * C + col], L);
         }
+        if (gone) L = __int_as_float(0x7fffffff);
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < kDecWarps; ++w) {

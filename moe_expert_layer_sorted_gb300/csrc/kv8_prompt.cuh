@@ -340,6 +340,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv8_prompt_kernel(const __grid_
       kv_wait(smem_addr(&oFull), 0, &sh_gone, p.err);
       fence_after();
     }
+    // where a wait gave up, rows are NaN, their lse too, so that they add nothing to mass
+    if (*static_cast<volatile uint32_t*>(&sh_gone)) l = __int_as_float(0x7fffffff);
     const int row = t * kPrTile + quad * 32 + lane;
     const bool has = t == 0 || two;
     auto sums = [&](int k, uint32_t (&v)[32]) {  // 32 channels of the row's O
