@@ -521,7 +521,8 @@ typedef struct moe_kv8_desc {
 moe_status moe_kv8_sizes(const moe_kv8_desc* desc, int64_t* page_bytes_per_layer, int64_t* mass_bytes_per_layer);
 
 /* As moe_kv_create, moe_kv_destroy, moe_kv_status and
- * moe_kv_debug_fail_next_attention (a workspace of 24 MB, with mass 153 MB). */
+ * moe_kv_debug_fail_next_attention (a workspace of 24 MB, with mass 153 MB; where weights are counted from the keys,
+ * a wait of that runs out as well). */
 moe_status moe_kv8_create(const moe_kv8_desc* desc, moe_kv8_cache** out);
 moe_status moe_kv8_destroy(moe_kv8_cache* kv);
 moe_status moe_kv8_status(moe_kv8_cache* kv);

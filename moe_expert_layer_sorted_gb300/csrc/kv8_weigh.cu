@@ -42,10 +42,12 @@ struct WeighArgs {
   float* mass;
   int per;             // query heads per kv head
   const int* scored;   // nullptr, or >= 0 for sequences whose scores were left (kv8_weigh_scores_kernel takes those)
-  float* parts;        // [CTA][2][128]
+  float* parts;        // [CTA][2][kWeTile]
   unsigned* counters;  // a CTA each, zero between calls
   uint32_t* err;
+  int fail;            // test hook: the first CTA's first products are not announced
 };
+static_assert(2 * size_t(Kv8::kCounters) * kWeTile * sizeof(float) <= Kv8::kPartsBytes, "two partial results per CTA");
 
 // Adds sum to the mass of token `pos` of sequence s, head h.
 __device__ __forceinline__ void add_mass(const WeighArgs& w, int s, int h, int pos, float sum) {
@@ -53,9 +55,9 @@ __device__ __forceinline__ void add_mass(const WeighArgs& w, int s, int h, int p
   if (pid >= 0) w.mass[(pid * w.a.c.heads + h) * w.a.c.page_size + (pos & (w.a.c.page_size - 1))] += sum;
 }
 
-// A sequence's pieces of work: for each head and tile of 128 tokens, the tiles of 128 columns that see some of it.  Tile t
-// is seen by column tiles c0(t) .. n - 1, c0(t) = max(0, step t - skip): causal, row i sees it from 128 t - first on, so
-// columns from per (128 t - first) on, and 128 t per / 128 is whole.  Sums of c0 over tiles have a closed form.
+// A sequence's pieces of work: for each head and tile of kWeTile tokens, the tiles of 128 columns that see some of it.  Tile t
+// is seen by column tiles c0(t) .. n - 1, c0(t) = max(0, step t - skip): causal, row i sees it from i = kWeTile t - first on, so
+// columns from per (kWeTile t - first) on, and kWeTile t per / 128 is whole.  Sums of c0 over tiles have a closed form.
 struct WeighSeq {
   KvSeq q;
   int len, tiles, n, step;
@@ -106,8 +108,9 @@ __global__ void __launch_bounds__(kWeThreads, 1) kv8_weigh_kernel(const __grid_c
   constexpr uint32_t kTileBytes = kPrTile * 128 * (D / 64);
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t done[2];                     // products of a half of TMEM
+  __shared__ uint64_t drained;                     // all of them, after a wait that gave up
   __shared__ uint32_t tmem_base;
-  __shared__ uint32_t sh_gone;
+  __shared__ uint32_t sh_gone;                     // a wait gave up: nothing more is multiplied or added to mass
   // (four of each: threads that are one barrier ahead write a tile's while others read the last but one's)
   __shared__ float4 sh_col[4][kPrTile / 2];        // two columns' factors and -lse log2 e
   __shared__ __align__(16) int sh_seen[4][kPrTile];              // tokens that a column sees
@@ -172,6 +175,7 @@ __global__ void __launch_bounds__(kWeThreads, 1) kv8_weigh_kernel(const __grid_c
     sh_gone = 0;
     mbar_init(smem_addr(&done[0]), 1);
     mbar_init(smem_addr(&done[1]), 1);
+    mbar_init(smem_addr(&drained), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
@@ -180,7 +184,9 @@ __global__ void __launch_bounds__(kWeThreads, 1) kv8_weigh_kernel(const __grid_c
   }
   const uint32_t id = idesc(kPrTile, false);
   uint32_t tm = 0;
-  auto multiply = [&](int b) {  // by the first warp
+  auto gone = [&]() { return *static_cast<volatile uint32_t*>(&sh_gone) != 0; };
+  auto multiply = [&](int b, bool announce = true) {  // by the first warp
+    if (__any_sync(0xffffffffu, gone())) return;
     const uint32_t leader = elect_leader();
     const uint32_t qa = smem + kTileBytes * (2 + b);
 #pragma unroll
@@ -189,7 +195,7 @@ __global__ void __launch_bounds__(kWeThreads, 1) kv8_weigh_kernel(const __grid_c
       for (int k = 0; k < D / 16; ++k)
         mma_ss(leader, tm + b * kWeTile + y * kPrTile, desc_k(smem + y * kTileBytes + (k / 4) * (kPrTile * 128) + (k % 4) * 32),
                desc_k(qa + (k / 4) * (kPrTile * 128) + (k % 4) * 32), id, k ? 1u : 0u);
-    commit(leader, &done[b]);
+    if (announce) commit(leader, &done[b]);
   };
   fence_before();
   __syncthreads();
@@ -333,7 +339,7 @@ __global__ void __launch_bounds__(kWeThreads, 1) kv8_weigh_kernel(const __grid_c
       __syncthreads();
       if (warp == 0) {
         fence_after();
-        multiply(0);
+        multiply(0, !(w.fail && blockIdx.x == 0 && u == line[0]));
       }
       if (mine > 1) ask(1);
     }
@@ -397,13 +403,13 @@ __global__ void __launch_bounds__(kWeThreads, 1) kv8_weigh_kernel(const __grid_c
     fence_before();
     __syncthreads();
     // a token tile that is cut between CTAs: sums of a CTA's first stretch in slot 0, of its last in slot 1, and who
-    // finishes the tile last adds them in order
+    // finishes the tile last adds them in order; sums of a CTA of which a wait gave up are NaN, and are added to nothing
     const bool whole = sh.count == sh.pieces;
     const int64_t tile = sh.at.tile, tile_end = tile + sh.pieces;
     if (!half) {
-      const float all = (s0 + s1) + sh_sum[token];
+      const float all = gone() ? __int_as_float(0x7fffffff) : (s0 + s1) + sh_sum[token];
       if (!whole) w.parts[(int64_t)(2 * blockIdx.x + (u == line[0] ? 0 : 1)) * kWeTile + token] = all;
-      else if (base + token < sh.q.len) add_mass(w, sh.at.s, sh.at.h, base + token, all);
+      else if (base + token < sh.q.len && all == all) add_mass(w, sh.at.s, sh.at.h, base + token, all);
     }
     if (!whole) {
       const int64_t total = line[2];
@@ -418,7 +424,7 @@ __global__ void __launch_bounds__(kWeThreads, 1) kv8_weigh_kernel(const __grid_c
 #pragma unroll 8
           for (int y = c0; y <= c1; ++y)
             sum_ += __ldcg(w.parts + (int64_t)(2 * y + (y == c0 && tile != total * c0 / n ? 1 : 0)) * kWeTile + tid);
-          add_mass(w, sh.at.s, sh.at.h, base + tid, sum_);
+          if (sum_ == sum_) add_mass(w, sh.at.s, sh.at.h, base + tid, sum_);
         }
         if (tid == 0) w.counters[c0] = 0;  // for the next call
       }
@@ -428,6 +434,10 @@ __global__ void __launch_bounds__(kWeThreads, 1) kv8_weigh_kernel(const __grid_c
   }
   if (warp == 0) {
     fence_after();
+    if (gone()) {  // products that nobody waited for end before their operands, their barriers and TMEM do
+      commit(elect_leader(), &drained);
+      mbar_drain(smem_addr(&drained), 0);
+    }
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(512));
   }
 }
@@ -484,7 +494,7 @@ __global__ void __launch_bounds__(kScThreads) kv8_weigh_scores_kernel(const __gr
 }  // namespace
 
 cudaError_t moe::kv8_weigh(Kv8& kv, const KvAttnArgs& a, float* mass, const Kv8Scores& scores, cudaStream_t s) {
-  WeighArgs w{a, mass, a.q_heads / a.c.heads, scores.to ? scores.base : nullptr, kv.parts(), kv.counters(), kv.err_dev};
+  WeighArgs w{a, mass, a.q_heads / a.c.heads, scores.to ? scores.base : nullptr, kv.parts(), kv.counters(), kv.err_dev, kv.fail_next};
   const int64_t cap = std::min<int64_t>((int64_t)a.b.table_pages << a.c.page_shift, 0x7ffff000);
   if (scores.to) {
     // a CTA for 1,024 tokens that the table could hold; of many, one that goes on to the next ones (an idle CTA takes 0.5 ns)

@@ -47,3 +47,30 @@ def test_a_wait_that_runs_out_leaves_no_mass_that_is_wrong(rows):
     assert (late >= 0.5).all() and (late <= mass * (1 + 2.0 ** -20)).all()
     assert torch.equal(call(out), mass) and torch.equal(out, good)
     w.cache.check()
+
+
+@pytest.mark.parametrize("rows", [40, 2000])
+def test_a_wait_of_the_weighing_that_runs_out_is_reported(rows):
+    """The first tokens of the first head get nothing then, the others all that they should or less; the next call is right."""
+    from moe_expert_layer_sorted_gb300 import MoeError
+    w = World(64, 64, BF, 2, [5000], seed=7).fill()
+    q = w.rand(1, rows, 8, 64)
+    out, ls = torch.empty_like(q), torch.empty(rows, 8, device="cuda")
+
+    def call():
+        w.cache.mass.fill_(0.5)
+        w.cache.attention(q, out, lse=ls, weigh=True, **w.batch)
+        torch.cuda.synchronize()
+        return w.mass_of(0).clone()
+
+    mass = call()
+    assert (mass > 0.5).all()
+    w.cache.debug_fail_next_attention()
+    late = call()
+    with pytest.raises(MoeError) as e:
+        w.cache.check()
+    assert e.value.status == 4
+    assert (late[:256, 0] == 0.5).all() and (late >= 0.5).all() and (late <= mass * (1 + 2.0 ** -20)).all()
+    assert torch.equal(late[:, 1], mass[:, 1])
+    assert torch.equal(call(), mass)
+    w.cache.check()
