@@ -546,7 +546,10 @@ moe_status moe_kv8_read(moe_kv8_cache* kv, int layer, const moe_kv_batch* batch,
  * h / (q_heads / kv_heads), causal, lse, rows that see nothing).  A row that sees a
  * token of NaN keys or values is NaN.  weigh = 1: after it, every token's softmax
  * weights of this call, summed over the rows and query heads that see it (in fp32,
- * in an order that does not depend on timing), are added to its mass; needs mass and lse.  Rows whose lse is
+ * in an order that does not depend on timing), are added to its mass; needs mass and lse.  They are the weights that
+ * the attention itself takes, of which a row's come to 1 within 2^-14, whatever the size of its scores (beyond the first
+ * 2^24 rows times query heads of a call, and where the scores of up to 32 of them a kv head find no room, within
+ * 2^-14 + |lse| 2^-20).  Rows whose lse is
  * not finite add nothing, among them those whose results a wait that gave up has spoiled: these are NaN, lse too.
  * Pages must then not be shared between the sequences of the call (their tokens' mass is
  * read, added to and written without regard to another's).

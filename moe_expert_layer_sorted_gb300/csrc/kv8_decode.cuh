@@ -60,7 +60,7 @@ constexpr int kDec8Slots = NT == 1 ? 3 : 6;
 template <int D>
 constexpr int kDec8Slot = D == 128 ? Kv8Geom<D>::kBytes : 2560;
 
-// W: the scores are written down too.
+// W: references, sums and scores are written down too.
 template <typename T, int D, int NT, bool W>
 __global__ void __launch_bounds__(kDec8Threads, NT == 1 ? 2 : 1)
     kv8_decode_kernel(const __grid_constant__ KvAttnArgs a, const __grid_constant__ DecPlan p, float* __restrict__ ws,
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kDec8Threads, NT == 1 ? 2 : 1)
         const KvSeq q = kv_seq(a.b, cc.group);
         store(it.at, cc);
         if constexpr (W)
-          if (cc.item == 0 && cc.item0 == seg) scores.base[cc.group] = cc.end <= scores.limit ? seg : -1;
+          if (scores.base && cc.item == 0 && cc.item0 == seg) scores.base[cc.group] = cc.end <= scores.limit ? seg : -1;
         it.s = cc.group;
         it.head = cc.item / p.ctiles;
         it.ctile = cc.item % p.ctiles;
@@ -466,9 +466,10 @@ __global__ void __launch_bounds__(kDec8Threads, NT == 1 ? 2 : 1)
         const KvSeq q = it.seq();
         *reinterpret_cast<uint2*>(a.out + kv_row_offset(a.b, a.os, s, q.row0, i) + (int64_t)hq * a.os.head + 4 * d4) =
             make_uint2(KvType<T>::pack(o.x, o.y), KvType<T>::pack(o.z, o.w));
-        if (a.lse && d4 == 0)
-          a.lse[kv_row_index(a.b, s, q.row0, i) * a.q_heads + hq] =
-              L == 0.0f ? -__int_as_float(0x7f800000) : (M + log2f(L)) * 0.6931471805599453f;
+        const int64_t row = kv_row_index(a.b, s, q.row0, i) * a.q_heads + hq;
+        if (a.lse && d4 == 0) a.lse[row] = L == 0.0f ? -__int_as_float(0x7f800000) : (M + log2f(L)) * 0.6931471805599453f;
+        if constexpr (W)
+          if (d4 == 0 && row < scores.refs_limit) scores.refs[row] = make_float2(M, 1.0f / L);
       };
       for (int x = tid; x < C * (D / 4); x += kDec8Threads) {
         const int col = x / (D / 4), d4 = x % (D / 4), nt = col / 8, cc = col % 8;
@@ -574,12 +575,12 @@ template <typename T, int D, int NT>
 cudaError_t launch_decode8(Kv8& kv, const KvAttnArgs& a, const DecPlan& p, const Kv8Scores& scores, cudaStream_t s) {
   constexpr int C = 8 * NT;
   const size_t smem = (size_t)kDecWarps * kDec8Slots<NT> * kDec8Slot<D>;
-  const auto kernel = scores.to ? kv8_decode_kernel<T, D, NT, true> : kv8_decode_kernel<T, D, NT, false>;
+  const auto kernel = scores.refs ? kv8_decode_kernel<T, D, NT, true> : kv8_decode_kernel<T, D, NT, false>;
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
   const int grid = std::min(kv.sms * 2, kDec8MaxParts) / NT;
   static_assert(kDec8MaxParts <= Kv8::kCounters, "a counter per CTA");
-  static_assert(2 * (size_t)kDec8MaxParts * C * (D + 2) * sizeof(float) <= Kv8::kPartsBytes, "two partial results per CTA");
+  static_assert(2 * (size_t)kDec8MaxParts * C * (D + 2) * sizeof(float) <= Kv8::kFewPartsBytes, "two partial results per CTA");
   kernel<<<grid, kDec8Threads, smem, s>>>(a, p, kv.parts(), kv.counters(), kv.err_dev, scores);
   return cudaGetLastError();
 }

@@ -94,12 +94,21 @@ __device__ __forceinline__ uint32_t load_word(uint32_t at) {
   return v;
 }
 
+struct Prompt8Args : PromptArgs {
+  float2* refs;        // see Kv8Scores
+  int64_t refs_limit;
+};
+// What a row leaves for its weights to be counted.
+__device__ __forceinline__ void leave(const Prompt8Args& p, int64_t row, float reference, float sum) {
+  if (row < p.refs_limit) p.refs[row] = make_float2(reference, 1.0f / sum);
+}
+
 // Floats of a stretch's part: results [D / 4][row] of four channels, then references, sums, 1 where a row is NaN.
 template <int D>
 constexpr int64_t kPr8Part = 2 * kPrTile * (D + 3);
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kPrThreads, 1) kv8_prompt_kernel(const __grid_constant__ PromptArgs p) {
+__global__ void __launch_bounds__(kPrThreads, 1) kv8_prompt_kernel(const __grid_constant__ Prompt8Args p) {
   using Geo = Kv8Geom<D>;
   constexpr uint32_t kSlab = kPrTile * 128;          // 128 rows of 64 channels
   constexpr uint32_t kTileBytes = kSlab * (D / 64);  // a Q, K or V tile
@@ -172,7 +181,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv8_prompt_kernel(const __grid_
     float ry = kNone, dz = kNoProduct, l = 0.0f;
     float fell = 0.0f;    // how far rz has been lowered since it was raised
     bool vnan = false;    // the row sees values that are not finite
-    bool coarse = false;  // a row's scores are as large as kCoarse
+    bool coarse = false;  // a row's scores are as large as kKv8Coarse
     for (int j = 0; j < (t == 0 || two ? ntiles : 0); ++j) {
       kv_wait(smem_addr(&sFull[t]), (uint32_t)j & 1u, &sh_gone, p.err);
       fence_after();
@@ -264,7 +273,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv8_prompt_kernel(const __grid_
             const float want = kPrDrop - most_z;  // (infinite where there is nothing)
             next = want >= cur + kPrStep && want <= cur + 64.0f && fell <= kPrFall - kPrStep ? fminf(want, cur + (kPrFall - fell)) : fminf(want, cur);
             ry = now;
-            coarse = coarse || __any_sync(0xffffffffu, ry != kNone && fabsf(ry) >= kCoarse);
+            coarse = coarse || __any_sync(0xffffffffu, ry != kNone && fabsf(ry) >= kKv8Coarse);
           }
           const float fo = next != cur ? exp2_fast(next - cur) : 1.0f;
           dz = next;
@@ -382,9 +391,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv8_prompt_kernel(const __grid_
           }
         }
       }
-      if (dst && a.lse)
-        a.lse[kv_row_index(a.b, end.s, end.q.row0, i) * a.q_heads + hq] =
-            l == 0.0f ? -__int_as_float(0x7f800000) : (ry + log2f(l)) * 0.6931471805599453f;
+      if (dst && a.lse) {
+        const int64_t at = kv_row_index(a.b, end.s, end.q.row0, i) * a.q_heads + hq;
+        a.lse[at] = l == 0.0f ? -__int_as_float(0x7f800000) : (ry + log2f(l)) * 0.6931471805599453f;
+        leave(p, at, ry, l);
+      }
     } else if (has) {  // a stretch's part
       float* part = p.ws + ((int64_t)blockIdx.x * p.splits + z) * kPr8Part<D>;
       const float g0 = l == 0.0f ? 0.0f : f1 / l;
@@ -603,7 +614,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) kv8_prompt_kernel(const __grid_
 // Joins the stretches' parts of a pair of row tiles: a CTA takes 32 rows, lane by lane, a warp
 // every eighth four channels.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ PromptArgs p) {
+__global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ Prompt8Args p) {
   const KvAttnArgs& a = p.a;
   const PromptTile tile(p);
   const int row = blockIdx.y * 32 + (threadIdx.x & 31);
@@ -644,13 +655,15 @@ __global__ void __launch_bounds__(256) kv8_join_kernel(const __grid_constant__ P
     const int d4 = (threadIdx.x >> 5) * kQuads + k;
     *reinterpret_cast<uint2*>(dst + 4 * d4) = make_uint2(KvType<T>::pack(o[k].x, o[k].y), KvType<T>::pack(o[k].z, o[k].w));
   }
-  if (a.lse && threadIdx.x < 32)
-    a.lse[kv_row_index(a.b, tile.s, tile.q.row0, i) * a.q_heads + hq] =
-        l == 0.0f ? -__int_as_float(0x7f800000) : (m + log2f(l)) * 0.6931471805599453f;
+  if (a.lse && threadIdx.x < 32) {
+    const int64_t at = kv_row_index(a.b, tile.s, tile.q.row0, i) * a.q_heads + hq;
+    a.lse[at] = l == 0.0f ? -__int_as_float(0x7f800000) : (m + log2f(l)) * 0.6931471805599453f;
+    leave(p, at, m, l);
+  }
 }
 
 template <typename T, int D>
-cudaError_t launch_prompt8(const PromptArgs& p, unsigned ctas, cudaStream_t s) {
+cudaError_t launch_prompt8(const Prompt8Args& p, unsigned ctas, cudaStream_t s) {
   const size_t smem = 1024 + (size_t)6 * kPrTile * D * 2;
   const auto kernel = kv8_prompt_kernel<T, D>;
   static const bool registers_fit = brings_registers(reinterpret_cast<const void*>(kernel), kPrRegs);
@@ -663,8 +676,8 @@ cudaError_t launch_prompt8(const PromptArgs& p, unsigned ctas, cudaStream_t s) {
 }
 
 template <typename T>
-cudaError_t prompt8(Kv8& kv, const KvAttnArgs& a, cudaStream_t s) {
-  PromptArgs p{a, a.q_heads / a.c.heads, 0, 1, kv.parts(), kv.err_dev, kv.fail_next};
+cudaError_t prompt8(Kv8& kv, const KvAttnArgs& a, const Kv8Scores& scores, cudaStream_t s) {
+  Prompt8Args p{{a, a.q_heads / a.c.heads, 0, 1, kv.parts(), kv.err_dev, kv.fail_next}, scores.refs, scores.refs_limit};
   const int64_t tiles = ((int64_t)a.b.max_new * p.per + 2 * kPrTile - 1) / (2 * kPrTile);
   const int64_t ctas = tiles * a.c.heads * a.b.batch;
   if (ctas > 0x7fffffff || (int64_t)a.c.heads * a.b.batch > 0x7fffffff || tiles * 2 * kPrTile > 0x7fffffff)

@@ -1,12 +1,14 @@
 // The weight of every token: the softmax weights of an attention's rows, summed over the rows and
 // query heads that see the token, are added to the token's mass.
 //
-// With lse from the attention a weight is 2^(y - lse log2 e), y the score in log2 units.  Where the
+// With the reference r of a row and its sum of weights l from the attention (Kv8Scores) a weight is 2^(y - r) / l, y the
+// score in log2 units, rounded as there: whatever the size of the scores, a row's weights are those that the attention took, and
+// come to 1.  (Or 2^(y - lse log2 e), which is off by |lse| 2^-23, for rows of scores below kKv8Coarse.)  Where the
 // single-token kernel has written its scores (kv8_decode.cuh), a thread adds up four tokens'.  Otherwise the
 // scores are made again, transposed, on the tensor cores, and the sums run along registers:
 //     S^T = U_K Q^T   (twice 128 tokens by 128 columns (row, query head) in TMEM),
-// a thread having a token (a TMEM lane) and half of the columns.  A column's power of two and lse come from
-// shared memory, a token's step is its thread's.  Columns that see nothing of a tile are not visited.  All the batch's
+// a thread having a token (a TMEM lane) and half of the columns.  A column's power of two, reference and sum come
+// from shared memory, a token's step is its thread's.  Columns that see nothing of a tile are not visited.  All the batch's
 // work (sequence, head, 256 tokens, 128 columns) lies in one line that is cut into equal shares, a CTA each SM, so that
 // neither the table's size nor uneven sequences matter; a token tile that is cut between CTAs is added up by the one
 // that finishes it last, in the order of the CTAs, so results do not depend on timing.  (A grid over the table's
@@ -15,7 +17,7 @@
 // Each CTA loads the next 128 queries while the tensor cores work on one half of TMEM and the threads on
 // the other.
 //
-// Measured (8 kv heads of 128 channels): 4,096 rows over themselves, 32 query heads, fp16: 143 us for 2.1 million
+// Measured (8 kv heads of 128 channels): 4,096 rows over themselves, 32 query heads, fp16: 149 us for 2.1 million
 // rows and tokens a query head; the exponents alone would take 58.  Bound by instructions, those that bring the queries to
 // shared memory among them: 128 tokens a CTA and two CTAs an SM, which did that twice as often, took 162.  From scores: 32
 // sequences of up to 4,160 tokens 8 us, latency.
@@ -41,18 +43,31 @@ struct WeighArgs {
   KvAttnArgs a;
   float* mass;
   int per;             // query heads per kv head
+  const float2* refs;  // of the first refs_limit rows and query heads
+  int64_t refs_limit;
   const int* scored;   // nullptr, or >= 0 for sequences whose scores were left (kv8_weigh_scores_kernel takes those)
   float* parts;        // [CTA][2][kWeTile]
   unsigned* counters;  // a CTA each, zero between calls
   uint32_t* err;
   int fail;            // test hook: the first CTA's first products are not announced
 };
-static_assert(2 * size_t(Kv8::kCounters) * kWeTile * sizeof(float) <= Kv8::kPartsBytes, "two partial results per CTA");
+static_assert(2 * size_t(Kv8::kCounters) * kWeTile * sizeof(float) <= Kv8::kFewPartsBytes, "two partial results per CTA");
 
 // Adds sum to the mass of token `pos` of sequence s, head h.
 __device__ __forceinline__ void add_mass(const WeighArgs& w, int s, int h, int pos, float sum) {
   const int64_t pid = kv_page(w.a.c, w.a.b, s, pos >> w.a.c.page_shift);
   if (pid >= 0) w.mass[(pid * w.a.c.heads + h) * w.a.c.page_size + (pos & (w.a.c.page_size - 1))] += sum;
+}
+
+// Reference and 1 / sum of a row and query head, and whether it adds anything (rows whose results are not finite do not).
+__device__ __forceinline__ float2 reference(const WeighArgs& w, int64_t row) {
+  if (row < w.refs_limit) return w.refs[row];
+  const float lse = w.a.lse[row];
+  return make_float2(lse * kLog2e, 1.0f);
+}
+__device__ __forceinline__ bool adds(float2 ref) {
+  constexpr uint32_t kInf = 0x7f800000u;
+  return fabsf(ref.x) < __uint_as_float(kInf) && ref.y > 0.0f && ref.y < __uint_as_float(kInf);
 }
 
 // A sequence's pieces of work: for each head and tile of kWeTile tokens, the tiles of 128 columns that see some of it.  Tile t
@@ -102,6 +117,29 @@ struct WeighItem {
   int nx, c, count, pieces;  // columns of the sequence; pieces: of the token tile
 };
 
+// The weights of 64 columns from x0 on for token `pos` of step ks, with the rows' own references and sums, and the scores as the
+// attention rounds them.  (A call, so that the ordinary tiles' registers stay what they are.)
+__device__ __noinline__ float coarse_weights(const WeighArgs& w, const WeighItem& it, uint32_t ts, int x0, const float4* col, const int* seen,
+                                             int pos, float ks) {
+  const int64_t row0 = kv_row_index(w.a.b, it.at.s, it.q.q.row0, 0) * w.a.q_heads + it.at.h * w.per;
+  float sum = 0.0f;
+#pragma unroll 1
+  for (int k = 0; k < 64; k += 32) {
+    uint32_t v[32];
+    tmem_ld32(ts + k, v);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const int x = x0 + k + e, row = x / w.per;
+      const float2 ref = x < it.nx ? reference(w, row0 + (int64_t)row * w.a.q_heads + (x - row * w.per)) : make_float2(0.0f, 0.0f);
+      if (!adds(ref) || pos >= seen[k + e]) continue;
+      const float f = reinterpret_cast<const float*>(col + (k + e) / 2)[e & 1] * ks;
+      sum = fmaf(exp2_fast(__fadd_rn(__fmul_rn(__uint_as_float(v[e]), f), -ref.x)), ref.y, sum);
+    }
+  }
+  return sum;
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kWeThreads, 1) kv8_weigh_kernel(const __grid_constant__ WeighArgs w) {
   using Geo = Kv8Geom<D>;
@@ -111,8 +149,10 @@ __global__ void __launch_bounds__(kWeThreads, 1) kv8_weigh_kernel(const __grid_c
   __shared__ uint64_t drained;                     // all of them, after a wait that gave up
   __shared__ uint32_t tmem_base;
   __shared__ uint32_t sh_gone;                     // a wait gave up: nothing more is multiplied or added to mass
+  enum : uint32_t { kNothing, kSome, kEvery };
   // (four of each: threads that are one barrier ahead write a tile's while others read the last but one's)
   __shared__ float4 sh_col[4][kPrTile / 2];        // two columns' factors and -lse log2 e
+  __shared__ uint4 sh_mode[4];                     // what its columns see of either half of the tokens; whether coarse_weights takes it
   __shared__ __align__(16) int sh_seen[4][kPrTile];              // tokens that a column sees
   __shared__ float sh_step[kWeTile], sh_sum[kWeTile];
   __shared__ WeighItem sh;
@@ -172,7 +212,7 @@ __global__ void __launch_bounds__(kWeThreads, 1) kv8_weigh_kernel(const __grid_c
   const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
   uint8_t* gen = smem_raw + (smem - smem_addr(smem_raw));  // two tiles of keys, then two of queries
   if (tid == 0) {
-    sh_gone = 0;
+    sh_gone = sh_mode[0].z = 0;
     mbar_init(smem_addr(&done[0]), 1);
     mbar_init(smem_addr(&done[1]), 1);
     mbar_init(smem_addr(&drained), 1);
@@ -184,9 +224,10 @@ __global__ void __launch_bounds__(kWeThreads, 1) kv8_weigh_kernel(const __grid_c
   }
   const uint32_t id = idesc(kPrTile, false);
   uint32_t tm = 0;
+  uint32_t parity = 0;  // a bit per half of TMEM; the next one: a wait of this thread gave up
   auto gone = [&]() { return *static_cast<volatile uint32_t*>(&sh_gone) != 0; };
   auto multiply = [&](int b, bool announce = true) {  // by the first warp
-    if (__any_sync(0xffffffffu, gone())) return;
+    if (__any_sync(0xffffffffu, parity & 4u)) return;
     const uint32_t leader = elect_leader();
     const uint32_t qa = smem + kTileBytes * (2 + b);
 #pragma unroll
@@ -201,7 +242,6 @@ __global__ void __launch_bounds__(kWeThreads, 1) kv8_weigh_kernel(const __grid_c
   __syncthreads();
   fence_after();
   tm = tmem_base;
-  uint32_t parity = 0;  // a bit per half of TMEM
   // the warp's lanes of TMEM, its columns of a tile, its tile of tokens
   const int quad = warp & 3, half = warp >> 2 & 1, part = warp >> 3;
   const int token = part * kPrTile + quad * 32 + lane;
@@ -299,8 +339,10 @@ __global__ void __launch_bounds__(kWeThreads, 1) kv8_weigh_kernel(const __grid_c
         }
         *reinterpret_cast<uint4*>(to + r * 128 + ((qc % 8) ^ (r & 7)) * 16) = raw[n];
         if (qc == 0) {
+          const float f = a.scale * kLog2e * back;
+          if (fine && (fabsf(row_lse[n]) * kLog2e >= kKv8Coarse || !(fabsf(f) >= 0x1p-64f && fabsf(f) <= 0x1p64f))) sh_mode[i_ & 3].z = 1;
           float* col = reinterpret_cast<float*>(&sh_col[i_ & 3][r >> 1]);
-          col[r & 1] = fine ? a.scale * kLog2e * back : 0.0f;  // (the scale may be so large that the product is not finite)
+          col[r & 1] = fine ? f : 0.0f;  // (the scale may be so large that the product is not finite)
           col[2 + (r & 1)] = fine ? -row_lse[n] * kLog2e : -__int_as_float(0x7f800000);
         }
       }
@@ -308,6 +350,13 @@ __global__ void __launch_bounds__(kWeThreads, 1) kv8_weigh_kernel(const __grid_c
         const int x = column(i_) + tid;
         const int64_t p = sh.q.first + x / w.per;
         sh_seen[i_ & 3][tid] = x >= sh.nx || p < 0 ? 0 : (int)min(a.causal ? p + 1 : (int64_t)sh.q.len, (int64_t)sh.q.len);
+      }
+      if (tid < kWeTile / kPrTile) {
+        const int low = base + tid * kPrTile, x0 = column(i_);
+        const bool none = a.causal && sh.q.first + (x0 + kPrTile - 1) / w.per < low;
+        const bool every = sh.q.first + x0 / w.per >= low + kPrTile - 1 || (!a.causal && sh.q.first >= 0);
+        reinterpret_cast<uint32_t*>(&sh_mode[i_ & 3])[tid] = none ? kNothing : every ? kEvery : kSome;
+        if (tid == 0) sh_mode[(i_ + 1) & 3].z = 0;  // (of three column tiles ago)
       }
     };
     if (mine > 0) {
@@ -360,7 +409,7 @@ __global__ void __launch_bounds__(kWeThreads, 1) kv8_weigh_kernel(const __grid_c
         }
         if (i + 2 < mine) ask(i + 2);  // they arrive during the exponents
       }
-      kv_wait(smem_addr(&done[b]), parity >> b & 1u, &sh_gone, w.err);
+      if (!kv_wait(smem_addr(&done[b]), parity >> b & 1u, &sh_gone, w.err)) parity |= 4u;
       parity ^= 1u << b;
       fence_after();
       const uint32_t ts = tm + b * kWeTile + part * kPrTile + half * 64 + ((uint32_t)(quad * 32) << 16);
@@ -376,8 +425,8 @@ __global__ void __launch_bounds__(kWeThreads, 1) kv8_weigh_kernel(const __grid_c
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             const float4 f = col[e / 2];
-            const uint64_t by = mul2(pair2(f.x, f.y), ks2);  // (together first: they may lie far apart)
-            const uint64_t y = fma2(pair2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), by, pair2(f.z, f.w));
+            uint64_t y = mul2(pair2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), pair2(f.x, f.y));
+            y = fma2(y, ks2, pair2(f.z, f.w));
             float y0, y1;
             split2(y, y0, y1);
             y0 = exp2_fast(y0);
@@ -391,10 +440,12 @@ __global__ void __launch_bounds__(kWeThreads, 1) kv8_weigh_kernel(const __grid_c
           }
         }
       };
-      // no column sees any of these tokens?  every column all of them?
-      const int low = base + part * kPrTile;
-      if (a.causal && sh.q.first + (x0 + kPrTile - 1) / w.per < low) continue;
-      if (sh.q.first + x0 / w.per >= low + kPrTile - 1 || (!a.causal && sh.q.first >= 0)) consume(std::false_type());
+      const uint4 modes = sh_mode[i & 3];
+      const uint32_t mode = part ? modes.y : modes.x;
+      if (mode == kNothing) continue;
+      if (modes.z)
+        sum[0] = add2(sum[0], pair2(coarse_weights(w, sh, ts, x0 + half * 64, &sh_col[i & 3][half * 32], &sh_seen[i & 3][half * 64], base + token, ks), 0.0f));
+      else if (mode == kEvery) consume(std::false_type());
       else consume(std::true_type());
     }
     float s0, s1;
@@ -430,6 +481,7 @@ __global__ void __launch_bounds__(kWeThreads, 1) kv8_weigh_kernel(const __grid_c
       }
     }
     u += sh.count;
+    if (tid == 0) sh_mode[0].z = 0;
     __syncthreads();  // what this tile had in shared memory is the next one's
   }
   if (warp == 0) {
@@ -446,7 +498,7 @@ __global__ void __launch_bounds__(kWeThreads, 1) kv8_weigh_kernel(const __grid_c
 constexpr int kScThreads = 256, kWeTokens = 4 * kScThreads;
 __global__ void __launch_bounds__(kScThreads) kv8_weigh_scores_kernel(const __grid_constant__ WeighArgs w, const __grid_constant__ Kv8Scores scores,
                                                                       int ctas) {
-  __shared__ float sh_lse[kKv8Columns];
+  __shared__ float2 sh_col[kKv8Columns];
   const KvAttnArgs& a = w.a;
   const int h = blockIdx.x % a.c.heads, s = blockIdx.x / a.c.heads / ctas, z = blockIdx.x / a.c.heads % ctas;
   const KvSeq q = kv_seq(a.b, s);
@@ -455,8 +507,8 @@ __global__ void __launch_bounds__(kScThreads) kv8_weigh_scores_kernel(const __gr
   const int line = scores.base[s], width = scores.width, rounds = (len + kPrTile - 1) / kPrTile;
   if (line < 0) return;
   if ((int)threadIdx.x < cols) {
-    const float ls = a.lse[kv_row_index(a.b, s, q.row0, threadIdx.x / w.per) * a.q_heads + h * w.per + threadIdx.x % w.per];
-    sh_lse[threadIdx.x] = fabsf(ls) < __int_as_float(0x7f800000) ? ls * kLog2e : __int_as_float(0x7f800000);
+    const float2 ref = reference(w, kv_row_index(a.b, s, q.row0, threadIdx.x / w.per) * a.q_heads + h * w.per + threadIdx.x % w.per);
+    sh_col[threadIdx.x] = adds(ref) ? ref : make_float2(0.0f, 0.0f);
   }
   __syncthreads();
   for (int64_t at = (int64_t)z * kWeTokens; at < len; at += (int64_t)ctas * kWeTokens) {
@@ -474,10 +526,11 @@ __global__ void __launch_bounds__(kScThreads) kv8_weigh_scores_kernel(const __gr
       for (int t = 0; t < 4; ++t) v[t] = *reinterpret_cast<const float4*>(y + t * width);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float ls = x + i < cols ? sh_lse[x + i] : __int_as_float(0x7f800000);
-        if (ls == __int_as_float(0x7f800000)) continue;
+        const float2 ref = x + i < cols ? sh_col[x + i] : make_float2(0.0f, 0.0f);
+        if (ref.y == 0.0f) continue;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) sum[t] += exp2_fast((i == 0 ? v[t].x : i == 1 ? v[t].y : i == 2 ? v[t].z : v[t].w) - ls);
+        for (int t = 0; t < 4; ++t)
+          sum[t] = fmaf(exp2_fast((i == 0 ? v[t].x : i == 1 ? v[t].y : i == 2 ? v[t].z : v[t].w) - ref.x), ref.y, sum[t]);
       }
     }
     const float now[4] = {had.x + sum[0], had.y + sum[1], had.z + sum[2], had.w + sum[3]};
@@ -494,9 +547,9 @@ __global__ void __launch_bounds__(kScThreads) kv8_weigh_scores_kernel(const __gr
 }  // namespace
 
 cudaError_t moe::kv8_weigh(Kv8& kv, const KvAttnArgs& a, float* mass, const Kv8Scores& scores, cudaStream_t s) {
-  WeighArgs w{a, mass, a.q_heads / a.c.heads, scores.to ? scores.base : nullptr, kv.parts(), kv.counters(), kv.err_dev, kv.fail_next};
+  WeighArgs w{a, mass, a.q_heads / a.c.heads, scores.refs, scores.refs_limit, scores.base, kv.parts(), kv.counters(), kv.err_dev, kv.fail_next};
   const int64_t cap = std::min<int64_t>((int64_t)a.b.table_pages << a.c.page_shift, 0x7ffff000);
-  if (scores.to) {
+  if (scores.base) {
     // a CTA for 1,024 tokens that the table could hold; of many, one that goes on to the next ones (an idle CTA takes 0.5 ns)
     const int64_t items = (int64_t)a.c.heads * a.b.batch;
     const int64_t ctas = std::min<int64_t>((cap + kWeTokens - 1) / kWeTokens, std::max<int64_t>(8192 / items, 1));
