@@ -332,20 +332,16 @@ __global__ void __launch_bounds__(kDec8Threads, NT == 1 ? 2 : 1)
           }
         }
         // ---- references
-        bool raise = false;
-        uint32_t all = ~0u;  // columns (a bit of four) of which some token is not small
+        uint32_t some = 0, raise = 0;  // columns (a bit each) of which some token is not small; the highest bit: one is too large
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const float t = fmaxf(y[nt][x], y[nt][2 + x]) - ry[nt][x], z = t + (lv + dz[nt][x]);
-            raise |= t > kRaiseSum || z > kRaiseProduct;
-            uint32_t some = __ballot_sync(0xffffffffu, z > kLower);
-            some |= some >> 16;
-            some |= some >> 8;
-            all &= some | some >> 4;
+            if (t > kRaiseSum || z > kRaiseProduct) raise = 1u << 31;
+            if (z > kLower) some |= 1u << (8 * nt + 4 * x);
           }
-        if (__any_sync(0xffffffffu, raise) || (all & 15u) != 15u) {
+        if (__reduce_or_sync(0xffffffffu, some << c | raise) != (1u << C) - 1u) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
