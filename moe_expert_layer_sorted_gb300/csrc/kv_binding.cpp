@@ -27,7 +27,7 @@
 namespace {
 
 // The C entry points of the two caches.  The 8-bit cache's are weak: the host tests put a library in
-// the real one's place that has the 4-bit cache's only.
+// the real one's place that has the 4-bit cache's only (over such a one no Cache8 is made).
 struct Kv {
   using Handle = moe_kv_cache;
   static constexpr auto append = moe_kv_append;
@@ -297,6 +297,15 @@ int cache_init(PyObject* self, PyObject* args, PyObject*) {
   return 0;
 }
 
+int cache8_init(PyObject* self, PyObject* args, PyObject* kw) {
+  if (!(moe_kv8_append && moe_kv8_read && moe_kv8_attention && moe_kv8_evict && moe_kv8_status &&
+        moe_kv8_debug_fail_next_attention && moe_kv8_destroy && moe_kv8_last_error)) {
+    PyErr_SetString(PyExc_ImportError, "the library has no 8-bit key/value cache");
+    return -1;
+  }
+  return cache_init(self, args, kw);
+}
+
 // A function of METH_FASTCALL's signature as the table holds it.
 template <typename F>
 PyCFunction fast(F* f) {
@@ -401,8 +410,8 @@ PyMethodDef cache8_methods[] = {
     {"close", close<Kv8>, METH_NOARGS, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
-PyObject* type_of(const char* name, PyMethodDef* methods) {
-  PyType_Slot slots[] = {{Py_tp_init, reinterpret_cast<void*>(&cache_init)},
+PyObject* type_of(const char* name, initproc init, PyMethodDef* methods) {
+  PyType_Slot slots[] = {{Py_tp_init, reinterpret_cast<void*>(init)},
                          {Py_tp_new, reinterpret_cast<void*>(&PyType_GenericNew)},
                          {Py_tp_methods, methods},
                          {0, nullptr}};
@@ -419,11 +428,12 @@ PyMODINIT_FUNC PyInit__kv_binding() {
   if (!m) return nullptr;
   const struct {
     const char *name, *full;
+    initproc init;
     PyMethodDef* methods;
-  } types[] = {{"Cache", "moe_expert_layer_sorted_gb300._kv_binding.Cache", cache_methods},
-               {"Cache8", "moe_expert_layer_sorted_gb300._kv_binding.Cache8", cache8_methods}};
+  } types[] = {{"Cache", "moe_expert_layer_sorted_gb300._kv_binding.Cache", cache_init, cache_methods},
+               {"Cache8", "moe_expert_layer_sorted_gb300._kv_binding.Cache8", cache8_init, cache8_methods}};
   for (const auto& t : types) {
-    PyObject* type = type_of(t.full, t.methods);
+    PyObject* type = type_of(t.full, t.init, t.methods);
     if (!type || PyModule_AddObject(m, t.name, type) < 0) {
       Py_XDECREF(type);
       Py_DECREF(m);
