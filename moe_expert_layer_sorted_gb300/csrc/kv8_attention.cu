@@ -8,10 +8,10 @@ using namespace moe;
 // once per 256 but turns every code into shared memory first.  Measured, both kernels, us (8 kv heads
 // of 128 channels, bf16; single tokens / prompts):
 //     columns                        8         16          32         64
-//     1 sequence of 2,048        12.5 / 21   14.6 / 21   15.1 / 21   - / 21
-//     1 of 131,072                 54 / 131    74 / 131   129 / 131  - / 131
-//     16 of 4,096                  36 / 72     48 / 72     81 / 73   - / 74
-//     64 of 2,048                  57 / 153    90 / 154   158 / 154  - / 155
+//     1 sequence of 2,048        12.4 / 21   14.7 / 21   16.3 / 21   - / 21
+//     1 of 131,072                 55 / 131    74 / 131   131 / 131  - / 131
+//     16 of 4,096                  37 / 72     49 / 72     82 / 73   - / 73
+//     64 of 2,048                  58 / 153    92 / 154   162 / 154  - / 154
 //
 // Weights: the single-token kernel leaves its scores behind where the workspace holds them, four
 // bytes a token and column beside the 256 that it reads; otherwise they are made again from the keys.

@@ -33,8 +33,8 @@
 // Masks: a score that its row may not see becomes -infinity.  Tokens that are not finite
 // have codes of zeros; a row that sees one is remembered, and NaN in the end.
 //
-// Measured (bf16, 32 query and 8 kv heads of 128 channels): 8,192 rows at the end of 16,384 tokens 1,325 us, 1,245
-// TFLOP/s (0.63 of the measured rate); with scores that never raise a reference 1,288; 4,096 rows (fp16) 158 us.
+// Measured (bf16, 32 query and 8 kv heads of 128 channels): 8,192 rows at the end of 16,384 tokens 1,314 us, 1,255
+// TFLOP/s (0.64 of the measured rate); with scores that never raise a reference 1,274; 4,096 rows (fp16) 158 us.
 // Bound by two things of about the same length: the chain of a token tile, scores -> weights -> product, of which
 // two row tiles alternate (without the loads of codes and the exponents it takes 1,130 us), and the warps that turn
 // codes (without their loads 1,219).  What paid: a tile's words asked for as soon as the last one's are turned, what
@@ -68,8 +68,8 @@ constexpr float kPrDrop = 2.0f, kPrLimit = 60000.0f, kPrAim = 5.0f, kPrFar = 0x1
 // last place below 2^-14 is 2^-24, so such a P is off by 2^-25 at most, and 128 of them by twice what 11 bits would be beside
 // their sum.  By no more than 2^kPrFall since it was raised, which keeps O within fp32 (tiles' sums of 2^16 times 127, by 2^24
 // tiles: 2^103); falls of less than kPrStep and what is below kPrGone are left alone.  Measured, never lowered / lowered, us: the
-// 8,192 rows below 1,308 / 1,325, with scores that never raise a reference 1,271 / 1,288, the ragged prompts 39.3 / 39.3 (50 where
-// the scores are looked through).
+// 8,192 rows below 1,308 / 1,314, with scores that never raise a reference 1,271 / 1,274, the ragged prompts 39.3 / 39.3 (50 where
+// the scores are looked through for it).
 constexpr float kPrLow = 0x1p-15f, kPrGone = 0x1p-64f, kPrFall = 56.0f, kPrStep = 8.0f;
 constexpr float kPrApart = 30.0f;       // log2 of how far an ordinary tile's steps may lie apart,
 constexpr float kPrNear = 60.0f;        // and of how far they may be from the row's 2^-dz

@@ -92,7 +92,8 @@ class Handle:
         self._c.debug_fail_next_attention()
 
     def append(self, k, v, *, table, lens, starts=None, max_new=None, layer=0, stream=None):
-        """Quantise the rows k, v into the sequences' pages."""
+        """Quantise the rows k, v into the sequences' pages, and update the pages' bounds (KVCache) or set the
+        rows' mass to 0 (KVCache8) where the cache has them."""
         self._c.append(k, v, table, lens, starts, max_new, layer, stream)
 
     def read(self, k, v, *, table, lens, starts=None, max_new=None, layer=0, stream=None):
