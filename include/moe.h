@@ -554,9 +554,11 @@ moe_status moe_kv8_read(moe_kv8_cache* kv, int layer, const moe_kv_batch* batch,
  * Pages must then not be shared between the sequences of the call (their tokens' mass is
  * read, added to and written without regard to another's).
  * Accuracy: scores, weights and sums are fp32 and the codes are exact operands.  A weight times its block's step enters the
- * product with the values with 11 bits, or, where it is small beside others, is off by up to 2^-17 of the sum of these
- * products over 128 tokens that lie together (with up to 32 rows times query heads of a kv head: of the largest of 16),
- * and never by more than itself; what is below 2^-48 of the row's largest loses bits beyond that. */
+ * product with the values with 11 bits; those that are small beside others may have fewer, so that of 128 tokens that lie
+ * together (those that the row sees) all are off by up to 2^-10 of their sum (with up to 32 rows times query heads of a kv
+ * head: of 16 tokens by 2^-13 of the largest), none by more than itself.  What is below 2^-48 of the row's largest loses
+ * bits beyond that.  (The largest weight times step, not weight times value: a token may weigh much and have next to no
+ * value, and the result is then the others'.) */
 moe_status moe_kv8_attention(moe_kv8_cache* kv, int layer, const moe_kv_batch* batch, const moe_kv_tensor* q,
                              int q_heads, float scale, int causal, const moe_kv_tensor* out, float* lse, int weigh,
                              void* stream);
