@@ -7,8 +7,8 @@
 // single-token kernel has written its scores (kv8_decode.cuh), a thread adds up four tokens'.  Otherwise the
 // scores are made again, transposed, on the tensor cores, and the sums run along registers:
 //     S^T = U_K Q^T   (twice 128 tokens by 128 columns (row, query head) in TMEM),
-// a thread having a token (a TMEM lane) and half of the columns.  A column's power of two, reference and sum come
-// from shared memory, a token's step is its thread's.  Columns that see nothing of a tile are not visited.  All the batch's
+// a thread having a token (a TMEM lane) and half of the columns.  A column's power of two and lse come from
+// shared memory, a token's step is its thread's.  Columns that see nothing of a tile are not visited.  All the batch's
 // work (sequence, head, 256 tokens, 128 columns) lies in one line that is cut into equal shares, a CTA each SM, so that
 // neither the table's size nor uneven sequences matter; a token tile that is cut between CTAs is added up by the one
 // that finishes it last, in the order of the CTAs, so results do not depend on timing.  (A grid over the table's
